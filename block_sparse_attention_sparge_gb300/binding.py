@@ -9,7 +9,9 @@ raise.
 
 from __future__ import annotations
 
+import array
 import ctypes
+import math
 import os
 
 import torch
@@ -27,6 +29,12 @@ __all__ = [
     "sparge_mask_from_prob",
     "sparge_attn_fwd",
     "sparge_attn_bwd",
+    "RopeAxes",
+    "sparge_heads_fwd",
+    "sparge_heads_bwd",
+    "sparge_resnorm_fwd",
+    "sparge_resnorm_bwd",
+    "sparge_clip_grads",
     "sparge_debug_wait_probe",
     "num_blocks",
     "SPARGE_OK",
@@ -61,6 +69,43 @@ class Shape(ctypes.Structure):
                 ("d", ctypes.c_int32), ("block_q", ctypes.c_int32), ("block_kv", ctypes.c_int32)]
 
 
+class Rope(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("turn", ctypes.c_uint64 * 64), ("axis", ctypes.c_uint8 * 64)]
+
+
+class HeadsPart(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64 * 3),
+                ("weight", ctypes.c_void_p), ("y", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("dx_stride", ctypes.c_int64 * 3), ("dweight", ctypes.c_void_p),
+                ("H", ctypes.c_int32), ("plain", ctypes.c_int32)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("x_type", ctypes.c_int32), ("weight_type", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("n_parts", ctypes.c_int32),
+                ("rope", ctypes.c_void_p), ("grid", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("pos_batch", ctypes.c_int32), ("part", HeadsPart * 3)]
+
+
+class Resnorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("C", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("branch_type", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("unit_offset", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("x", ctypes.c_void_p), ("branch", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p),
+                ("gate_groups", ctypes.c_int32), ("scale_groups", ctypes.c_int32),
+                ("shift_groups", ctypes.c_int32),
+                ("gate_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
+                ("shift_stride", ctypes.c_int64), ("post_weight", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("h", ctypes.c_void_p), ("stats", ctypes.c_void_p),
+                ("dy", ctypes.c_void_p), ("dh", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("dbranch", ctypes.c_void_p), ("dgate", ctypes.c_void_p),
+                ("dscale", ctypes.c_void_p), ("dshift", ctypes.c_void_p),
+                ("dpost", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
@@ -79,6 +124,16 @@ _SIGNATURES = {
     "sparge_attn_bwd_workspace_bytes": ([_SHP, ctypes.POINTER(_SZ)], _I),
     "sparge_attn_bwd": ([_SHP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P, _SZ,
                          _P, _P], _I),
+    "sparge_rope_init": ([ctypes.POINTER(Rope), ctypes.c_int32, ctypes.POINTER(ctypes.c_int32),
+                          ctypes.c_double, ctypes.POINTER(ctypes.c_double), ctypes.c_int32], _I),
+    "sparge_heads_fwd": ([ctypes.POINTER(Heads), _P], _I),
+    "sparge_heads_bwd_workspace_bytes": ([ctypes.POINTER(Heads), ctypes.POINTER(_SZ)], _I),
+    "sparge_heads_bwd": ([ctypes.POINTER(Heads), _P, _SZ, _P], _I),
+    "sparge_resnorm_fwd": ([ctypes.POINTER(Resnorm), _P], _I),
+    "sparge_resnorm_bwd_workspace_bytes": ([ctypes.POINTER(Resnorm), ctypes.POINTER(_SZ)], _I),
+    "sparge_resnorm_bwd": ([ctypes.POINTER(Resnorm), _P, _SZ, _P], _I),
+    "sparge_clip_workspace_bytes": ([ctypes.c_int32, ctypes.POINTER(_SZ)], _I),
+    "sparge_clip_grads": ([_P, _P, ctypes.c_int32, _F, _F, _P, _P, _SZ, _P], _I),
     "sparge_status_copy_async": ([_P, _P, _P], _I),
     "sparge_read_status": ([_P, _P, ctypes.POINTER(ctypes.c_int32)], _I),
     "sparge_debug_wait_probe": ([_P, ctypes.c_uint64, _P], _I),
@@ -282,6 +337,409 @@ def sparge_attn_bwd(q, k, v, o, lse, dout, row_idx, row_cnt, col_idx, col_cnt,
            "sparge_attn_bwd")
     _finish(st, check_status, "sparge_attn_bwd")
     return dq, dk, dv
+
+
+# ------------------------------------------------- around the attention
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+_HEADS_NORMS = {None: 0, "token": 1, "head": 2}
+_NORMS = {None: 0, "layer": 1, "rms": 2}
+
+
+def _type_of(t: torch.Tensor, what: str) -> int:
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be bf16 or fp32")
+    return code
+
+
+def _same_device(device, *ts):
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError("expected CUDA tensors on one device")
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors on one device")
+
+
+def _call(fn, where: str, device, *args):
+    """One library call on the device's current stream."""
+    if device.index == torch.cuda.current_device():
+        code = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, _stream(device))
+    if code != SPARGE_OK:
+        raise SpargeError(code, where)
+
+
+def _workspace(fn, where: str, args, device, given):
+    nbytes = _SZ(0)
+    _check(fn(ctypes.byref(args), ctypes.byref(nbytes)), where + "_workspace_bytes")
+    if given is None and nbytes.value:
+        given = torch.empty(nbytes.value, dtype=torch.uint8, device=device)
+    if given is None:
+        return None, 0
+    _same_device(device, given)
+    return given, given.numel() * given.element_size()
+
+
+class RopeAxes:
+    """Rotary positions over up to three axes (time, height, width): the first
+    ``pairs[0]`` channel pairs of a head turn with axis 0, the next with axis 1,
+    then axis 2; pairs behind them do not turn.  Pair i of an axis with n pairs
+    turns by ``scale * theta ** (-i / n)`` radians per unit of position.  Pairs
+    are channels (2j, 2j + 1), or (j, j + d / 2) if not ``interleaved``."""
+
+    def __init__(self, d: int, pairs, theta: float = 10000.0, scale=(1.0, 1.0, 1.0),
+                 interleaved: bool = True):
+        pairs, scale = tuple(pairs), tuple(scale)
+        if not (1 <= len(pairs) <= 3 and len(scale) >= len(pairs)):
+            raise ValueError("expected pairs (and a scale) for one to three axes")
+        self.d, self.pairs, self.theta = int(d), pairs, float(theta)
+        self.scale, self.interleaved = scale[:len(pairs)], bool(interleaved)
+        pad = 3 - len(pairs)
+        self.plan = Rope()
+        _check(load_library().sparge_rope_init(
+            ctypes.byref(self.plan), self.d, (ctypes.c_int32 * 3)(*pairs, *[0] * pad),
+            self.theta, (ctypes.c_double * 3)(*self.scale, *[1.0] * pad), int(self.interleaved)),
+            "sparge_rope_init")
+
+
+def _token_strides(t, B, N, H):
+    sb, sn, sh, sc = t.stride()
+    if sc != 1:
+        raise ValueError("the channels of a head must be contiguous")
+    return sb if B > 1 else 0, sn if N > 1 else 0, sh if H > 1 else 0
+
+
+def _heads_args(B, N, d, x_type, rope, grid, pos, norm, weights, eps, device):
+    if norm not in _HEADS_NORMS:
+        raise ValueError("norm must be None, 'token' or 'head'")
+    a = Heads()
+    a.B, a.N, a.d, a.x_type, a.norm, a.eps = B, N, d, x_type, _HEADS_NORMS[norm], eps
+    if rope is not None:
+        if rope.d != d:
+            raise ValueError("the rope's head width differs from the tensors'")
+        a.rope = ctypes.addressof(rope.plan)
+    if grid is not None:
+        if grid.dtype != torch.int32 or grid.shape != (B, 3) or not grid.is_contiguous():
+            raise ValueError("grid must be a contiguous int32 [B, 3] tensor")
+        a.grid = grid.data_ptr()
+    if pos is not None:
+        if (pos.dtype != torch.int32 or pos.dim() != 3 or pos.shape[0] not in (1, B)
+                or pos.shape[1:] != (N, 3) or not pos.is_contiguous()):
+            raise ValueError("pos must be a contiguous int32 [B, N, 3] or [1, N, 3] tensor")
+        a.pos, a.pos_batch = pos.data_ptr(), pos.shape[0]
+    if (rope is None) != (grid is None and pos is None) or (grid is not None and pos is not None):
+        raise ValueError("a rope needs grid or pos, one of the two")
+    _same_device(device, grid, pos, *weights)
+    given = [w for w in weights if w is not None]
+    if given:
+        a.weight_type = _type_of(given[0], "a norm weight")
+        if norm is None or any(w.dtype != given[0].dtype for w in given):
+            raise ValueError("norm weights need a norm and share one type")
+    return a
+
+
+def _norm_weight(w, norm, H, d):
+    if w is None:
+        return None
+    if w.shape != ((H * d,) if norm == "token" else (d,)) or not w.is_contiguous():
+        raise ValueError("a norm weight is contiguous, [H * d] for 'token' and [d] for 'head'")
+    return w.data_ptr()
+
+
+def sparge_heads_fwd(q=None, k=None, v=None, rope: RopeAxes | None = None, grid=None, pos=None,
+                     norm: str | None = None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                     out=None):
+    """Projections to the attention's layout: each of q, k and v is bf16 or
+    fp32 [B, N, H, d] of any batch, token and head stride (slices of a fused
+    projection need no copy) and comes back as bf16 [B, H, N, d].  Q and K pass
+    an RMS norm over the token's H * d channels (``"token"``) or over each head
+    (``"head"``), then ``rope``: with ``grid`` (int32 [B, 3]: frames, height,
+    width of each sample; tokens behind them do not turn) or ``pos`` (int32
+    [B, N, 3]).  Returns (q, k, v), None for what was not given."""
+    parts = [t for t in (q, k, v) if t is not None]
+    if not parts:
+        raise ValueError("nothing to lay out")
+    first = parts[0]
+    device = first.device
+    _same_device(device, q, k, v)
+    if first.dim() != 4:
+        raise ValueError("expected [B, N, H, d] tensors")
+    B, N, _, d = first.shape
+    a = _heads_args(B, N, d, _type_of(first, "q, k and v"), rope, grid, pos, norm,
+                    (q_weight, k_weight), eps, device)
+    res, n = [None, None, None], 0
+    for i, (t, w) in enumerate(((q, q_weight), (k, k_weight), (v, None))):
+        if t is None:
+            if w is not None:
+                raise ValueError("a norm weight without its tensor")
+            continue
+        H = t.shape[2] if t.dim() == 4 else 0
+        if t.shape != (B, N, H, d) or t.dtype != first.dtype:
+            raise ValueError("q, k and v share their type, batch, length and head width")
+        y = out[i] if out is not None and out[i] is not None else None
+        if y is None:
+            y = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=device)
+        else:
+            _same_device(device, y)
+            if y.shape != (B, H, N, d) or y.dtype != torch.bfloat16 or not y.is_contiguous():
+                raise ValueError("out must be contiguous bf16 [B, H, N, d] tensors")
+        p = a.part[n]
+        p.x, p.x_stride = t.data_ptr(), _token_strides(t, B, N, H)
+        p.weight, p.y, p.H, p.plain = _norm_weight(w, norm, H, d), y.data_ptr(), H, i == 2
+        res[i], n = y, n + 1
+    a.n_parts = n
+    _call(load_library().sparge_heads_fwd, "sparge_heads_fwd", device, ctypes.byref(a))
+    return tuple(res)
+
+
+def sparge_heads_bwd(dq=None, dk=None, dv=None, q=None, k=None, rope: RopeAxes | None = None,
+                     grid=None, pos=None, norm: str | None = None, q_weight=None, k_weight=None,
+                     eps: float = 1e-6, out=None, dtype=None, workspace=None):
+    """Gradients of ``sparge_heads_fwd`` from those of its results (bf16
+    [B, H, N, d]); q and k are the forward's inputs, needed under a norm.
+    Returns (dq, dk, dv, dq_weight, dk_weight): [B, N, H, d] in the inputs'
+    type (``dtype`` where neither q nor k is given), written into ``out`` where
+    that is given (slices of one buffer, say), and the weights' gradients."""
+    parts = [t for t in (dq, dk, dv) if t is not None]
+    if not parts:
+        raise ValueError("no gradient given")
+    first = parts[0]
+    device = first.device
+    _same_device(device, dq, dk, dv, q, k)
+    if first.dim() != 4:
+        raise ValueError("expected [B, H, N, d] gradients")
+    B, _, N, d = first.shape
+    outs = out if out is not None else (None, None, None)
+    typed = [t for t in (q, k, *outs) if t is not None]
+    dtype = typed[0].dtype if typed else (dtype or torch.bfloat16)
+    if dtype not in _TYPES or any(t.dtype != dtype for t in typed):
+        raise ValueError("q, k and out share one type, bf16 or fp32")
+    a = _heads_args(B, N, d, _TYPES[dtype], rope, grid, pos, norm, (q_weight, k_weight), eps,
+                    device)
+    res, n = [None] * 5, 0
+    for i, (g, x, w) in enumerate(((dq, q, q_weight), (dk, k, k_weight), (dv, None, None))):
+        if g is None:
+            if w is not None:
+                raise ValueError("a norm weight without its gradient")
+            continue
+        H = g.shape[1] if g.dim() == 4 else 0
+        if g.shape != (B, H, N, d) or g.dtype != torch.bfloat16 or not g.is_contiguous():
+            raise ValueError("gradients are contiguous bf16 [B, H, N, d] tensors")
+        p = a.part[n]
+        p.y, p.H, p.plain = g.data_ptr(), H, i == 2
+        if norm is not None and i < 2:
+            if x is None or x.shape != (B, N, H, d):
+                raise ValueError("a norm's gradient needs its input, [B, N, H, d]")
+            p.x, p.x_stride = x.data_ptr(), _token_strides(x, B, N, H)
+            p.weight = _norm_weight(w, norm, H, d)
+            if w is not None:
+                res[3 + i] = torch.empty_like(w)
+                p.dweight = res[3 + i].data_ptr()
+        dx = outs[i]
+        if dx is None:
+            dx = torch.empty((B, N, H, d), dtype=dtype, device=device)
+        else:
+            _same_device(device, dx)
+            if dx.shape != (B, N, H, d):
+                raise ValueError("out must be [B, N, H, d] tensors")
+            if any(st == 0 and n_ > 1 for st, n_ in zip(dx.stride(), dx.shape)):
+                raise ValueError("out must not repeat elements")
+        p.dx, p.dx_stride = dx.data_ptr(), _token_strides(dx, B, N, H)
+        res[i], n = dx, n + 1
+    a.n_parts = n
+    lib = load_library()
+    ws, size = _workspace(lib.sparge_heads_bwd_workspace_bytes, "sparge_heads_bwd", a, device,
+                          workspace)
+    _call(lib.sparge_heads_bwd, "sparge_heads_bwd", device, ctypes.byref(a), _ptr(ws), size)
+    return tuple(res)
+
+
+def _modulation(m, what, B, N, C):
+    """(pointer, groups, stride) of a gate, scale or shift: [C] for all tokens,
+    or [B, F, C] with a row for each run of N / F tokens of a sample."""
+    if m is None:
+        return None, 1, 0
+    if m.dtype != torch.float32 or m.stride(-1) != 1:
+        raise ValueError(f"{what} must be fp32 with contiguous channels")
+    if m.shape == (C,):
+        return m.data_ptr(), 1, 0
+    if m.dim() != 3 or m.shape[2] != C or m.shape[0] not in (1, B):
+        raise ValueError(f"{what} must be [C] or [B, F, C]")
+    b, f = m.shape[:2]
+    if b * f == 1:
+        return m.data_ptr(), 1, 0
+    if b != B or f < 1 or N % f:
+        raise ValueError(f"{what} [B, F, C]: F must divide the tokens of a sample")
+    if f == 1:
+        return m.data_ptr(), b, m.stride(0)
+    if b > 1 and m.stride(0) != f * m.stride(1):
+        raise ValueError(f"the rows of {what} must be evenly spaced")
+    return m.data_ptr(), b * f, m.stride(1)
+
+
+def _resnorm_args(x, branch, gate, scale, shift, norm, unit_offset, post_weight, eps, h_type):
+    if norm not in _NORMS:
+        raise ValueError("norm must be None, 'layer' or 'rms'")
+    if x.dim() not in (2, 3) or not x.is_contiguous():
+        raise ValueError("x must be a contiguous [B, N, C] or [N, C] tensor")
+    _same_device(x.device, branch, gate, scale, shift, post_weight)
+    C = x.shape[-1]
+    B, N = (1, x.shape[0]) if x.dim() == 2 else x.shape[:2]
+    a = Resnorm()
+    a.rows, a.C, a.x_type = B * N, C, _type_of(x, "x")
+    if branch is not None and (branch.shape != x.shape or not branch.is_contiguous()):
+        raise ValueError("branch must be contiguous, of x's shape")
+    a.branch_type, a.norm, a.unit_offset, a.eps = h_type, _NORMS[norm], bool(unit_offset), eps
+    a.x = x.data_ptr()
+    a.branch = branch.data_ptr() if branch is not None else None
+    a.gate, a.gate_groups, a.gate_stride = _modulation(gate, "gate", B, N, C)
+    a.scale, a.scale_groups, a.scale_stride = _modulation(scale, "scale", B, N, C)
+    a.shift, a.shift_groups, a.shift_stride = _modulation(shift, "shift", B, N, C)
+    if post_weight is not None:
+        if (post_weight.shape != (C,) or post_weight.dtype != torch.float32
+                or not post_weight.is_contiguous()):
+            raise ValueError("post_weight must be contiguous fp32 [C]")
+        a.post_weight = post_weight.data_ptr()
+    return a
+
+
+def sparge_resnorm_fwd(x, branch=None, gate=None, scale=None, shift=None,
+                       norm: str | None = "layer", unit_offset: bool = True, post_weight=None,
+                       eps: float = 1e-6, h_dtype=None, want_stats: bool = True):
+    """Residual join and norm: y = x + gate * branch, h = norm(y) * (1 + scale)
+    + shift (``scale`` itself without ``unit_offset``); with ``post_weight`` the
+    branch passes an RMS norm first.  x and branch are contiguous [B, N, C]
+    (bf16 x: bf16 branch); gate, scale and shift fp32, [C] for all tokens or
+    [B, F, C] with a row for each run of N / F tokens.  Returns (y, h, stats):
+    y is x where there is no branch, h (of the branch's type, or ``h_dtype``)
+    is None without a norm, stats (fp32 [3, tokens]) is what the backward
+    needs."""
+    if branch is not None:
+        h_type = _type_of(branch, "branch")
+        if h_dtype is not None and h_dtype != branch.dtype:
+            raise ValueError("h has the branch's type")
+        h_dtype = branch.dtype
+    else:
+        h_dtype = h_dtype or x.dtype
+        if h_dtype not in _TYPES:
+            raise ValueError("h must be bf16 or fp32")
+        h_type = _TYPES[h_dtype]
+    a = _resnorm_args(x, branch, gate, scale, shift, norm, unit_offset, post_weight, eps, h_type)
+    y, h, stats = x, None, None
+    if branch is not None:
+        y = torch.empty_like(x)
+        a.y = y.data_ptr()
+    if norm is not None:
+        h = torch.empty_like(x, dtype=h_dtype)
+        a.h = h.data_ptr()
+    if want_stats and (norm is not None or post_weight is not None):
+        stats = torch.empty((3, a.rows), dtype=torch.float32, device=x.device)
+        a.stats = stats.data_ptr()
+    _call(load_library().sparge_resnorm_fwd, "sparge_resnorm_fwd", x.device, ctypes.byref(a))
+    return y, h, stats
+
+
+def sparge_resnorm_bwd(dy, dh, x, branch=None, gate=None, scale=None, shift=None, stats=None,
+                       norm: str | None = "layer", unit_offset: bool = True, post_weight=None,
+                       want_mods: bool = True, workspace=None):
+    """Gradients of ``sparge_resnorm_fwd``: returns (dx, dbranch, dgate, dscale,
+    dshift, dpost), None for what was not given.  ``dy`` or ``dh`` may be None
+    (zero).  ``want_mods=False`` leaves the four sums out."""
+    like = branch if branch is not None else dh if dh is not None else x
+    a = _resnorm_args(x, branch, gate, scale, shift, norm, unit_offset, post_weight, 0.0,
+                      _type_of(like, "branch and dh"))
+    device = x.device
+    _same_device(device, dy, dh, stats)
+    for t, ref, what in ((dy, x, "dy"), (dh, like, "dh")):
+        if t is not None and (t.shape != x.shape or t.dtype != ref.dtype
+                              or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous, of x's shape and its own result's type")
+    if stats is not None:
+        if stats.dtype != torch.float32 or stats.numel() != 3 * a.rows or not stats.is_contiguous():
+            raise ValueError("stats must be the forward's fp32 [3, tokens]")
+        a.stats = stats.data_ptr()
+    a.dy, a.dh = (t.data_ptr() if t is not None else None for t in (dy, dh))
+    dx = torch.empty_like(x)
+    a.dx = dx.data_ptr()
+    dbranch = None
+    if branch is not None:
+        dbranch = torch.empty_like(branch)
+        a.dbranch = dbranch.data_ptr()
+    sums = [None] * 4
+    if want_mods:
+        for i, (m, name) in enumerate(((gate, "dgate"), (scale, "dscale"), (shift, "dshift"),
+                                       (post_weight, "dpost"))):
+            if m is not None:
+                sums[i] = torch.empty(m.shape, dtype=torch.float32, device=device)
+                setattr(a, name, sums[i].data_ptr())
+    lib = load_library()
+    ws, size = _workspace(lib.sparge_resnorm_bwd_workspace_bytes, "sparge_resnorm_bwd", a, device,
+                          workspace)
+    _call(lib.sparge_resnorm_bwd, "sparge_resnorm_bwd", device, ctypes.byref(a), _ptr(ws), size)
+    return (dx, dbranch, *sums)
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill its memory without gaps or repeats."""
+    step = 1
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size != 1:
+            if stride != step:
+                return False
+            step *= size
+    return True
+
+
+def _tensor_list(tensors, device, what):
+    rows = []
+    for t in tensors:
+        if t.layout is not torch.strided or t.dtype not in _TYPES or t.device != device:
+            raise ValueError(f"{what} must be dense bf16 or fp32 CUDA tensors on one device")
+        if not (t.is_contiguous() or t.numel() == 0 or _dense(t)):
+            raise ValueError(f"{what} must have no gaps or repeated elements")
+        rows += (t.data_ptr(), t.numel(), _TYPES[t.dtype])
+    return array.array("q", rows)  # sparge_tensor: pointer, int64, int32 and padding
+
+
+def sparge_clip_grads(grads, max_norm: float | None, out=None, eps: float = 1e-6, workspace=None):
+    """Global 2-norm of a list of gradients (fp32 scalar tensor, returned
+    without waiting for the GPU), and g * min(1, max_norm / (norm + eps)) in
+    place or into ``out``.  ``max_norm=None``: the norm alone.  Tensors may mix
+    bf16 and fp32; a tensor must not be listed twice or overlap another."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("expected at least one gradient")
+    if max_norm is not None and not (math.isfinite(max_norm) and max_norm >= 0):
+        raise ValueError("max_norm must be finite and not negative")
+    device = grads[0].device
+    _same_device(device)
+    table = _tensor_list(grads, device, "gradients")
+    n = len(grads)
+    outs = None
+    if out is not None:
+        out = list(out)
+        if len(out) != n or any(o.shape != g.shape or o.dtype != g.dtype or o.stride() != g.stride()
+                                for o, g in zip(out, grads)):
+            raise ValueError("out must match the gradients in shape, type and strides")
+        _same_device(device, *out)
+        outs = array.array("q", [o.data_ptr() for o in out])
+    lib = load_library()
+    if workspace is None:
+        nbytes = _SZ(0)
+        _check(lib.sparge_clip_workspace_bytes(n, ctypes.byref(nbytes)),
+               "sparge_clip_workspace_bytes")
+        workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=device)
+    _same_device(device, workspace)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    _call(lib.sparge_clip_grads, "sparge_clip_grads", device, table.buffer_info()[0],
+          outs.buffer_info()[0] if outs is not None else None, n,
+          -1.0 if max_norm is None else float(max_norm), eps, norm.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if max_norm is not None:
+        torch.autograd.graph.increment_version(grads if out is None else out)
+    return norm
 
 
 def sparge_debug_wait_probe(timeout_ns: int = 10_000_000, device="cuda") -> int:

@@ -236,6 +236,188 @@ int sparge_attn_bwd(const sparge_shape* shape, const void* q, const void* k, con
                     float softmax_scale, void* dq, void* dk, void* dv, void* workspace,
                     size_t ws_bytes, int32_t* status, sparge_stream_t stream);
 
+/*
+ * Operators of the transformer block around the attention
+ * -------------------------------------------------------
+ * They keep the conventions above, with these additions: inputs and outputs
+ * must not overlap unless a comment allows it; channels are innermost; all
+ * arithmetic and all sums are fp32 (the gradient norm: fp64), results are
+ * rounded once; repeated calls give the same bits (no atomics).
+ */
+
+/* Element types. */
+enum sparge_type { SPARGE_BF16 = 0, SPARGE_F32 = 1 };
+
+/* Rotary positions with up to three axes (time, height, width): a host-side
+ * plan, filled by sparge_rope_init and kept by the caller. */
+typedef struct sparge_rope {
+  int32_t d;            /* head width: 64 or 128 */
+  int32_t interleaved;  /* pairs (2j, 2j+1); 0: pairs (j, j + d/2) */
+  uint64_t turn[64];    /* pair j's turns per unit of position, times 2^64 */
+  uint8_t axis[64];     /* the axis whose position turns pair j */
+} sparge_rope;
+
+/*
+ * sparge_rope_init -- the first pairs[0] pairs follow axis 0, the next
+ * pairs[1] axis 1, then pairs[2] axis 2; pairs behind them do not turn.  Pair i
+ * of an axis with n pairs turns by scale * theta^(-i/n) radians per unit of
+ * position.  Host only.
+ *   pairs : int32 [3], each >= 0, at most d/2 in all.  scale : double [3]
+ *           (position interpolation); NULL = 1.
+ */
+int sparge_rope_init(sparge_rope* rope, int32_t d, const int32_t* pairs, double theta,
+                     const double* scale, int32_t interleaved);
+
+enum sparge_heads_norm {
+  SPARGE_HEADS_NORM_NONE = 0,
+  SPARGE_HEADS_NORM_TOKEN = 1, /* RMS over all H*d channels of a token */
+  SPARGE_HEADS_NORM_HEAD = 2   /* RMS over the d channels of each head */
+};
+
+/* Q, K or V on its way between a projection and the attention. */
+typedef struct sparge_heads_part {
+  const void* x;         /* [B,N,H,d] of x_type, strides below.  sparge_heads_bwd
+                            reads it only under a norm (else NULL is fine) */
+  int64_t x_stride[3];   /* elements between samples, tokens and heads of x */
+  const void* weight;    /* norm weight, dense: [H*d] (token) or [d] (head), of
+                            weight_type; NULL = 1 */
+  void* y;               /* bf16 [B,H,N,d]: the result; sparge_heads_bwd reads
+                            the gradient of it here */
+  void* dx;              /* sparge_heads_bwd: gradient of x, of x_type (out) */
+  int64_t dx_stride[3];
+  void* dweight;         /* sparge_heads_bwd: gradient of weight, of weight_type
+                            (out); NULL: not wanted */
+  int32_t H;             /* heads; H * d <= 8192 */
+  int32_t plain;         /* nonzero: neither norm nor rotation (V) */
+} sparge_heads_part;
+
+typedef struct sparge_heads {
+  int32_t B, N, d;       /* d in {64, 128}; B * N < 2^31 */
+  int32_t x_type, weight_type;
+  int32_t norm;          /* enum sparge_heads_norm */
+  float eps;
+  int32_t n_parts;       /* 1 to 3 of `part` are used */
+  const sparge_rope* rope; /* host; NULL: no rotation */
+  /* Positions, exactly one of the two with a rope:
+   *   grid : int32 [B,3] (device): token n < t*h*w of a sample has the
+   *          positions (n / (h*w), n / w % h, n % w); later tokens (padding,
+   *          text) and samples with an extent below 1 do not turn;
+   *   pos  : int32 [pos_batch,N,3] (device), any values; pos_batch 1 or B. */
+  const int32_t* grid;
+  const int32_t* pos;
+  int32_t pos_batch;
+  sparge_heads_part part[3];
+} sparge_heads;
+
+/*
+ * sparge_heads_fwd -- projections to the attention's layout, one launch for
+ * all parts:  u = x * weight / sqrt(mean(x^2) + eps) (under a norm), each pair
+ * of channels turned by its position's angle, rounded to bf16 and written
+ * head-major.  Pointers and strides are multiples of 16 bytes; channels of a
+ * head are contiguous.  A slice of a fused projection needs no copy.
+ */
+int sparge_heads_fwd(const sparge_heads* args, sparge_stream_t stream);
+
+/* Workspace of sparge_heads_bwd (partial sums of the weight gradients; 0
+ * without them).  `args` as in the call. */
+int sparge_heads_bwd_workspace_bytes(const sparge_heads* args, size_t* bytes);
+
+/*
+ * sparge_heads_bwd -- gradients of sparge_heads_fwd.  x, weight, norm, eps and
+ * positions as in the forward.  The parts' dx may interleave in one buffer
+ * (the gradient of a fused projection).
+ */
+int sparge_heads_bwd(const sparge_heads* args, void* workspace, size_t ws_bytes,
+                     sparge_stream_t stream);
+
+enum sparge_norm { SPARGE_NORM_NONE = 0, SPARGE_NORM_LAYER = 1, SPARGE_NORM_RMS = 2 };
+
+/*
+ * The residual join of one half-block and the norm before the next:
+ *   n = branch, or with post_weight: branch * post_weight / sqrt(mean(branch^2) + eps)
+ *   y = x + gate * n;   h = norm(y) * gain + shift,
+ * gain = scale, or 1 + scale with unit_offset; the norm subtracts the mean and
+ * divides by sqrt(var + eps) (LAYER) or divides by sqrt(mean(y^2) + eps) (RMS).
+ *
+ * gate, scale and shift have one row of C fp32 values for all tokens
+ * (groups 1), or `groups` rows, each for rows / groups consecutive tokens (the
+ * same count for all that have more than one); row r starts r * stride values
+ * on.  NULL gate or scale = 1 (gain 1), NULL shift = 0.
+ */
+typedef struct sparge_resnorm {
+  int64_t rows;          /* tokens of all samples */
+  int32_t C;             /* channels: a multiple of 8, at most 8192 */
+  int32_t x_type;        /* x, y, dy, dx */
+  int32_t branch_type;   /* branch, h, dbranch, dh; with a bf16 x: bf16 */
+  int32_t norm;          /* enum sparge_norm */
+  int32_t unit_offset;
+  float eps;
+  const void* x;         /* [rows, C] */
+  const void* branch;    /* [rows, C]; NULL: y = x and y is not written */
+  const float* gate;     /* needs a branch */
+  const float* scale;    /* need a norm */
+  const float* shift;
+  int32_t gate_groups, scale_groups, shift_groups;
+  int64_t gate_stride, scale_stride, shift_stride;
+  const float* post_weight; /* [C]; needs a branch */
+  void* y;               /* out */
+  void* h;               /* out; not written without a norm */
+  float* stats;          /* [3, rows]: mean (0 for RMS) and 1/deviation of y, 1/rms
+                            of the branch (with post_weight).  Forward: out,
+                            NULL if no backward follows.  Backward: in */
+  /* sparge_resnorm_bwd only */
+  const void* dy;        /* NULL = 0, but not both */
+  const void* dh;        /* NULL = 0 */
+  void* dx;              /* out */
+  void* dbranch;         /* out, with a branch */
+  float* dgate;          /* out, dense [groups, C]; NULL: not wanted */
+  float* dscale;
+  float* dshift;
+  float* dpost;          /* out, [C] */
+} sparge_resnorm;
+
+/* One launch; any of y's and h's readers may follow on the stream. */
+int sparge_resnorm_fwd(const sparge_resnorm* args, sparge_stream_t stream);
+
+/* Workspace of sparge_resnorm_bwd (partial column sums; may be 0).  `args` as
+ * in the call. */
+int sparge_resnorm_bwd_workspace_bytes(const sparge_resnorm* args, size_t* bytes);
+
+/* Gradients.  Reads x, branch, gate, scale, post_weight and the forward's
+ * stats (y is recomputed); shift only for its shape. */
+int sparge_resnorm_bwd(const sparge_resnorm* args, void* workspace, size_t ws_bytes,
+                       sparge_stream_t stream);
+
+/* A dense tensor of a list; data aligned to its element size. */
+typedef struct sparge_tensor {
+  void* data;
+  int64_t numel;         /* 0 is fine (data may be NULL then) */
+  int32_t type;
+} sparge_tensor;
+
+#define SPARGE_MAX_TENSORS 65536
+
+/* Workspace of sparge_clip_grads for a list of n tensors. */
+int sparge_clip_workspace_bytes(int32_t n, size_t* bytes);
+
+/*
+ * sparge_clip_grads -- global norm of a list of gradients, and clipping:
+ *   norm = sqrt(sum of g^2 over all tensors);   g *= min(1, max_norm / (norm + eps)).
+ *   grads : n tensors (host array; copied by the call).
+ *   out   : host array of n device pointers for the clipped tensors, of the
+ *           inputs' types; NULL: in place (nothing is written if the factor
+ *           is 1).  out[i] may be grads[i].data.  Tensors that are written
+ *           must not overlap, with one another or with another input (a tensor
+ *           listed twice included): SPARGE_ERR_INVALID_ARG.
+ *   max_norm : finite; below 0: the norm alone, nothing is written to a tensor.
+ *   norm  : fp32 [1] out (device).
+ * A gradient that holds NaN makes the norm and every result NaN; one that
+ * holds an infinity makes the norm infinite and the factor 0.
+ */
+int sparge_clip_grads(const sparge_tensor* grads, void* const* out, int32_t n, float max_norm,
+                      float eps, float* norm, void* workspace, size_t ws_bytes,
+                      sparge_stream_t stream);
+
 /* Enqueues on `stream` a copy of the device status word into *host_status
  * (caller-owned, page-locked host memory for the copy to be asynchronous) and
  * returns without waiting; the value is valid once the stream has reached the
