@@ -53,70 +53,226 @@ struct HeadsParams {
   uint8_t axis[64];
 };
 
-// Cosines and sines of T tokens in shared memory: [T][D / 2].
-template <int T, int D>
-SPARGE_DEV void token_angles(const HeadsParams& p, const Slot& s, const uint64_t* turn,
-                             const uint8_t* axis, int row0, float2* out) {
-  constexpr int P = D / 2;
-  for (int i = s.tid; i < T * P; i += s.W * 32) {
-    const int j = i % P, row = row0 + i / P;
-    int pos = 0;
-    if (row < p.M) {
-      const int b = row / p.N, n = row - b * p.N;
-      const int a = axis[j];
-      if (p.pos != nullptr) {
-        pos = p.pos[b * p.pos_ld + static_cast<int64_t>(n) * 3 + a];
-      } else {
-        // Token n of a (t, h, w) grid; tokens behind it stay at position 0.
-        const int t = p.grid[3 * b], h = p.grid[3 * b + 1], w = p.grid[3 * b + 2];
-        if (t > 0 && h > 0 && w > 0) {
-          const int64_t hw = static_cast<int64_t>(h) * w;
-          const int it = hw > n ? 0 : n / static_cast<int>(hw);
-          const int rest = n - static_cast<int>(it * hw);
-          const int ih = rest / w;
-          if (it < t) pos = a == 0 ? it : a == 1 ? ih : rest - ih * w;
-        }
-      }
+// Frequencies in shared memory: indexed by lane, they would be replayed 32
+// times out of the parameter bank.
+struct Turns {
+  uint64_t turn[64];
+  uint8_t axis[64];
+  SPARGE_DEV void fill(const HeadsParams& p) {
+    if (threadIdx.x < 64) {
+      turn[threadIdx.x] = p.turn[threadIdx.x];
+      axis[threadIdx.x] = p.axis[threadIdx.x];
     }
-    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turn[j];
-    const float half_turns =
-        static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
-    float sn, cs;
-    sincospif(half_turns, &sn, &cs);
-    out[i] = make_float2(cs, sn);
+  }
+};
+
+// The cosines and sines of a slot's tokens, T at a time, each computed once for
+// all heads of its parts: [T][cos | sin][D / 2] floats of shared memory.
+// Thread i of the slot owns pair i % (D / 2) of token i / (D / 2) (and more of
+// them where the slot is narrow).  Coordinates are counted on from token to
+// token, so the divisions are done once a sample; a thread whose coordinate did
+// not change keeps its values, which for time and height is nearly always.
+template <int T, int D>
+struct Angles {
+  static constexpr int P = D / 2;
+  int n, b;        // the next token
+  int it, ih, iw;  // its coordinates on the grid
+  int t, h, w;     // the sample's grid; t = 0: nothing turns
+  int last;        // position behind cs, sn
+  float cs, sn;
+
+  SPARGE_DEV void open(const HeadsParams& p, int sample, int token) {
+    b = sample;
+    n = token;
+    it = ih = iw = t = 0;
+    if (p.grid == nullptr || b * static_cast<int64_t>(p.N) >= p.M) return;
+    t = p.grid[3 * b], h = p.grid[3 * b + 1], w = p.grid[3 * b + 2];
+    if (t < 1 || h < 1 || w < 1) {
+      t = 0;
+      return;
+    }
+    const int64_t hw = static_cast<int64_t>(h) * w;
+    it = hw > n ? 0 : n / static_cast<int>(hw);
+    const int rest = n - static_cast<int>(it * hw);
+    ih = rest / w;
+    iw = rest - ih * w;
+  }
+  // The position of the token `on` (0 or 1) tokens on along axis a.
+  SPARGE_DEV int position(const HeadsParams& p, int on, int a) const {
+    if (p.pos != nullptr)
+      return n + on < p.N && b * static_cast<int64_t>(p.N) < p.M
+                 ? p.pos[b * p.pos_ld + static_cast<int64_t>(n + on) * 3 + a]
+                 : 0;
+    int ct = it, ch = ih, cw = iw;
+    if (T > 1 && on != 0) step(ct, ch, cw);
+    if (ct >= t) return 0;  // behind the grid, or no grid
+    return a == 0 ? ct : a == 1 ? ch : cw;
+  }
+  SPARGE_DEV void step(int& ct, int& ch, int& cw) const {
+    if (++cw == w) {
+      cw = 0;
+      if (++ch == h) ch = 0, ++ct;
+    }
+  }
+  SPARGE_DEV void fill(const HeadsParams& p, const Slot& s, const Turns& turns, float* out) {
+    for (int i = s.tid; i < T * P; i += s.W * 32) {
+      const int j = i % P;
+      const int pos = position(p, i / P, turns.axis[j]);
+      const bool first = i == s.tid;
+      float c = cs, q = sn;
+      if (!(first && pos == last)) {
+        const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns.turn[j];
+        sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f,
+                  &q, &c);  // 2^-31: half turns
+      }
+      if (first) last = pos, cs = c, sn = q;
+      out[(i / P) * D + j] = c;
+      out[(i / P) * D + P + j] = q;
+    }
+  }
+  // On to the next unit of at most T tokens of a sample.
+  SPARGE_DEV void next(const HeadsParams& p) {
+    n += T;
+    if (n >= p.N) {
+      open(p, b + 1, 0);
+    } else if (t > 0) {
+#pragma unroll
+      for (int k = 0; k < T; ++k) step(it, ih, iw);
+    }
+  }
+  SPARGE_DEV void start(const HeadsParams& p, int sample, int token) {
+    open(p, sample, token);
+    last = 0, cs = 1.f, sn = 0.f;  // position 0 turns nothing
+  }
+};
+
+// Four pairs (a, b) of a thread as packed halves: a[0] holds the first members
+// of pairs 0 and 1.  Both channel orders unpack into it and pack out of it
+// without a move, and every step below is a packed operation.
+struct Pairs {
+  uint64_t a[2], b[2];
+};
+
+template <bool INTER>
+SPARGE_DEV Pairs to_pairs(const float (&f)[8]) {
+  if constexpr (INTER)
+    return {{f32x2(f[0], f[2]), f32x2(f[4], f[6])}, {f32x2(f[1], f[3]), f32x2(f[5], f[7])}};
+  else
+    return {{f32x2(f[0], f[1]), f32x2(f[2], f[3])}, {f32x2(f[4], f[5]), f32x2(f[6], f[7])}};
+}
+template <bool INTER>
+SPARGE_DEV void from_pairs(const Pairs& v, float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float a = j & 1 ? f32x2_hi(v.a[j / 2]) : f32x2_lo(v.a[j / 2]);
+    const float b = j & 1 ? f32x2_hi(v.b[j / 2]) : f32x2_lo(v.b[j / 2]);
+    f[INTER ? 2 * j : j] = a;
+    f[INTER ? 2 * j + 1 : j + 4] = b;
   }
 }
 
-// This thread's eight channels of one token of a token-major tensor: eight in
-// a row when pairs are adjacent, four and their four partners otherwise.
-template <typename T, bool INTER, int D>
-SPARGE_DEV Raw8<T> load_row(const T* p) {
-  if constexpr (INTER)
-    return load8(p);
-  else
-    return load4x2(p, p + D / 2);
+SPARGE_DEV float dot(const Pairs& x, const Pairs& y) {
+  const uint64_t s = ffma2(x.a[0], y.a[0], fmul2(x.b[0], y.b[0]));
+  const uint64_t t = ffma2(x.a[1], y.a[1], fmul2(x.b[1], y.b[1]));
+  const uint64_t u = fadd2(s, t);
+  return f32x2_lo(u) + f32x2_hi(u);
 }
-template <typename T, bool INTER, int D>
+SPARGE_DEV Pairs mul(const Pairs& x, const Pairs& y) {
+  return {{fmul2(x.a[0], y.a[0]), fmul2(x.a[1], y.a[1])},
+          {fmul2(x.b[0], y.b[0]), fmul2(x.b[1], y.b[1])}};
+}
+SPARGE_DEV Pairs mul(const Pairs& x, float f) {
+  const uint64_t r = f32x2(f, f);
+  return {{fmul2(x.a[0], r), fmul2(x.a[1], r)}, {fmul2(x.b[0], r), fmul2(x.b[1], r)}};
+}
+SPARGE_DEV Pairs fma(const Pairs& x, const Pairs& y, const Pairs& z) {
+  return {{ffma2(x.a[0], y.a[0], z.a[0]), ffma2(x.a[1], y.a[1], z.a[1])},
+          {ffma2(x.b[0], y.b[0], z.b[0]), ffma2(x.b[1], y.b[1], z.b[1])}};
+}
+SPARGE_DEV Pairs fma(const Pairs& x, float f, const Pairs& z) {
+  const uint64_t r = f32x2(f, f);
+  return {{ffma2(x.a[0], r, z.a[0]), ffma2(x.a[1], r, z.a[1])},
+          {ffma2(x.b[0], r, z.b[0]), ffma2(x.b[1], r, z.b[1])}};
+}
+
+// A thread's four angles of a token: pairs c / 2 on where its channels are eight
+// in a row from c, pairs c on where they are partners, else c / 2 and c / 2 + 1
+// and the same a quarter of a head on.
+template <bool INTER, bool SPLIT, int D>
+SPARGE_DEV float4 four_of(const float* row, int c) {
+  if constexpr (!SPLIT) {
+    return *reinterpret_cast<const float4*>(row + c / 2);
+  } else if constexpr (!INTER) {
+    return *reinterpret_cast<const float4*>(row + c);
+  } else {
+    const float2 a = *reinterpret_cast<const float2*>(row + c / 2);
+    const float2 b = *reinterpret_cast<const float2*>(row + c / 2 + D / 4);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+}
+
+// Turns the pairs by the angles at cs (BACK: by their negatives).
+template <bool BACK, bool INTER, bool SPLIT, int D>
+SPARGE_DEV Pairs rotate(const Pairs& v, const float* cs, int at) {
+  const float4 c4 = four_of<INTER, SPLIT, D>(cs, at);
+  const float4 s4 = four_of<INTER, SPLIT, D>(cs + D / 2, at);
+  const uint64_t c[2] = {f32x2(c4.x, c4.y), f32x2(c4.z, c4.w)};
+  const uint64_t s[2] = {f32x2(s4.x, s4.y), f32x2(s4.z, s4.w)};
+  const uint64_t n[2] = {f32x2(-s4.x, -s4.y), f32x2(-s4.z, -s4.w)};
+  Pairs r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    r.a[i] = ffma2(v.a[i], c[i], fmul2(v.b[i], BACK ? s[i] : n[i]));
+    r.b[i] = ffma2(v.a[i], BACK ? n[i] : s[i], fmul2(v.b[i], c[i]));
+  }
+  return r;
+}
+
+// A thread's eight channels of one token: eight in a row for bf16 with adjacent
+// pairs, else four and the four that lie half a head further: their partners,
+// or two more pairs, so that fp32 rows too are read in whole sectors.
+template <typename TX, bool INTER>
+constexpr bool split() {
+  return !INTER || sizeof(TX) == 4;
+}
+template <typename T, bool SPLIT, int D>
+SPARGE_DEV void stage_row(Ring dst, const T* p) {
+  if constexpr (!SPLIT)
+    stage8(dst, p);
+  else
+    stage4x2(dst, p, p + D / 2);
+}
+template <bool SPLIT, int D>
+SPARGE_DEV void store_row_raw(__nv_bfloat16* p, const Raw8<__nv_bfloat16>& r) {
+  if constexpr (!SPLIT) {
+    store_raw8(p, r);
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(r.v[0].x, r.v[0].y);
+    *reinterpret_cast<uint2*>(p + D / 2) = make_uint2(r.v[0].z, r.v[0].w);
+  }
+}
+template <typename T, bool SPLIT, int D>
 SPARGE_DEV void store_row(T* p, const float (&f)[8]) {
-  if constexpr (INTER)
+  if constexpr (!SPLIT)
     store8(p, f);
   else
     store4x2(p, p + D / 2, f);
 }
-
-// Turns the four pairs by (cos, sin); sgn = -1 turns them back.
-template <bool INTER>
-SPARGE_DEV void rotate8(float (&f)[8], const float4* cs, float sgn) {
-  const float4 c0 = cs[0], c1 = cs[1];
-  const float c[4] = {c0.x, c0.z, c1.x, c1.z};
-  const float n[4] = {sgn * c0.y, sgn * c0.w, sgn * c1.y, sgn * c1.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int ia = INTER ? 2 * j : j, ib = INTER ? 2 * j + 1 : j + 4;
-    const float a = f[ia], b = f[ib];
-    f[ia] = a * c[j] - b * n[j];
-    f[ib] = a * n[j] + b * c[j];
-  }
+template <typename T, bool INTER>
+SPARGE_DEV Pairs unstage_pairs(Ring src) {
+  float f[8];
+  unpack8(unstage8<T>(src), f);
+  return to_pairs<INTER>(f);
+}
+// The weights lie in the ring in the order of the pairs.
+SPARGE_DEV Pairs unstage_weight(Ring src) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2&>(src[0]);
+  const ulonglong2 b = reinterpret_cast<const ulonglong2&>(src[1]);
+  return {{a.x, a.y}, {b.x, b.y}};
+}
+SPARGE_DEV void keep_weight(Ring dst, const Pairs& w) {
+  reinterpret_cast<ulonglong2&>(dst[0]) = make_ulonglong2(w.a[0], w.a[1]);
+  reinterpret_cast<ulonglong2&>(dst[1]) = make_ulonglong2(w.b[0], w.b[1]);
 }
 
 // Sums over the lanes of one head (D / 8 of them, aligned).
@@ -129,250 +285,591 @@ SPARGE_DEV void head_sum(float (&v)[K]) {
   }
 }
 
-// The eight weights of this thread's channels (1 without a weight).
-template <bool INTER, int D>
-SPARGE_DEV void load_weight(const HeadsParams& p, const void* w, bool active, int c, float (&f)[8]) {
+// The weights of this thread's eight channels (1 without a weight).
+template <bool INTER, bool SPLIT, int D>
+SPARGE_DEV Pairs load_weight(const HeadsParams& p, const void* w, bool active, int c) {
+  float f[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = 1.f;
-  if (w == nullptr || !active) return;
-  if (p.w_bf16)
-    unpack8(load_row<__nv_bfloat16, INTER, D>(static_cast<const __nv_bfloat16*>(w) + c), f);
-  else
-    unpack8(load_row<float, INTER, D>(static_cast<const float*>(w) + c), f);
+  for (int i = 0; i < 8; ++i) {
+    const int at = c + (!SPLIT || i < 4 ? i : i - 4 + D / 2);
+    f[i] = 1.f;
+    if (w != nullptr && active)
+      f[i] = p.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[at])
+                      : static_cast<const float*>(w)[at];
+  }
+  return to_pairs<INTER>(f);
 }
 
-// What a thread keeps of its place: its head, and its first channel in it.
-template <bool INTER, int D>
+// A thread's place in the rows of a part: vector v of V covers eight channels
+// of head `head + v * head_step`, from channel c of the head.
+template <bool SPLIT, int D, int V>
 struct Place {
-  bool active;
-  int head, c;  // c: first channel within the head
+  bool active[V];
+  int head, head_step, c;
   SPARGE_DEV Place(const Slot& s, int C) {
     constexpr int L = D / 8;  // threads of one head
-    active = s.tid * 8 < C;
+#pragma unroll
+    for (int v = 0; v < V; ++v) active[v] = (s.tid + v * s.W * 32) * 8 < C;
     head = s.tid / L;
-    c = (s.tid % L) * (INTER ? 8 : 4);
+    head_step = s.W * 256 / D;
+    c = (s.tid % L) * (SPLIT ? 4 : 8);
   }
 };
 
-template <typename TX, bool INTER, int D, int T, int THREADS>
-__global__ void __launch_bounds__(THREADS) heads_fwd_kernel(const __grid_constant__ HeadsParams p) {
-  __shared__ float red[kSlotRedFloats];
-  __shared__ __align__(16) float2 angles[kMaxSlots * 2 * T * 64];
-  __shared__ uint64_t turn[64];
-  __shared__ uint8_t axis[64];
-  const HeadsPart& part = p.part[blockIdx.y];
-  const bool rot = p.rotate && !part.plain;
-  const int norm = part.plain ? 0 : p.norm;
-  if (threadIdx.x < 64) {
-    turn[threadIdx.x] = p.turn[threadIdx.x];
-    axis[threadIdx.x] = p.axis[threadIdx.x];
-  }
-  __syncthreads();
-  const int per_cta = slots_per_cta(part.W);
-  Slot s = make_slot(part.W, red);
-  if (s.index >= per_cta) return;
-  const Place<INTER, D> at(s, part.C);
-  const int wc = norm == 1 ? at.head * D + at.c : at.c;
-  float w[8];
-  load_weight<INTER, D>(p, norm ? part.w : nullptr, at.active, wc, w);
+// One kernel for each direction, in two forms: JOINT takes Q, K and V (parts
+// 0, 1 and 2, any but one of which may be absent) of a token together, so the
+// angles are computed once for both and one barrier serves both sums; else a
+// part to each blockIdx.y, for parts of different head counts.
+template <bool JOINT>
+constexpr int turned_parts() {
+  return JOINT ? 2 : 1;
+}
+template <bool JOINT>
+constexpr int all_parts() {
+  return JOINT ? 3 : 1;
+}
 
-  const TX* x = static_cast<const TX*>(part.x) + at.head * part.xs[2] + at.c;
-  const int H = part.C / D;
-  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(part.y) + static_cast<int64_t>(at.head) * p.N * D + at.c;
-  const int nslots = gridDim.x * per_cta;
-  float2* ang = angles + s.index * 2 * T * 64;
-  int buf = 0;
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x * per_cta + s.index) * T; row0 < p.M;
-       row0 += static_cast<int64_t>(nslots) * T, buf ^= 1) {
-    Raw8<TX> raw[T];
-    int b = static_cast<int>(row0) / p.N, n = static_cast<int>(row0) - b * p.N;
-    int64_t yo[T];
+#ifndef HF_S
+#define HF_S 3
+#endif
+#ifndef HF_T
+#define HF_T 2
+#endif
+#ifndef HF_B
+#define HF_B 2
+#endif
+#ifndef HB_S
+#define HB_S 4
+#endif
+#ifndef HB_B
+#define HB_B 2
+#endif
+// Stages of the ring.
+template <typename TX>
+constexpr int fwd_stages() {
+  return sizeof(TX) == 2 ? HF_S : 2;
+}
+template <typename TX>
+constexpr int bwd_stages() {
+  return sizeof(TX) == 2 ? HB_S : 3;
+}
+template <int V>
+constexpr int fwd_rows() {
+  return HF_T >= V ? HF_T / V : 1;
+}
+// Pieces of one stage, and of a thread's whole ring with the weights behind it.
+template <typename TX, bool JOINT, int V>
+constexpr int fwd_pieces() {
+  return all_parts<JOINT>() * fwd_rows<V>() * V * pieces8<TX>();
+}
+template <typename TX, bool JOINT, int V>
+constexpr int bwd_pieces() {
+  return all_parts<JOINT>() * V + turned_parts<JOINT>() * V * pieces8<TX>();
+}
+template <typename TX, bool JOINT, int V>
+constexpr int fwd_ring() {
+  return fwd_stages<TX>() * fwd_pieces<TX, JOINT, V>() + turned_parts<JOINT>() * V * 2;
+}
+template <typename TX, bool JOINT, int V>
+constexpr int bwd_ring() {
+  return bwd_stages<TX>() * bwd_pieces<TX, JOINT, V>() + turned_parts<JOINT>() * V * 2;
+}
+constexpr int kAngleBuffers = 2;  // of T tokens (D floats each), for every slot
+
+// A slot's share of the units (at most T tokens of one sample), in a row.
+struct Share {
+  int left, b, n;  // units, and the first one's sample and token
+  SPARGE_DEV Share(const HeadsParams& p, int T, int64_t slot, int64_t nslots) {
+    const int per_sample = (p.N + T - 1) / T;
+    const int64_t units = static_cast<int64_t>(p.M / p.N) * per_sample;
+    const int begin = static_cast<int>(units * slot / nslots);
+    left = static_cast<int>(units * (slot + 1) / nslots) - begin;
+    b = begin / per_sample;
+    n = (begin - b * per_sample) * T;
+  }
+};
+
+template <typename TX, bool INTER, int D, int V, bool JOINT>
+__global__ void __launch_bounds__(row_threads(V), V == 1 ? HF_B : 1) heads_fwd_kernel(
+    const __grid_constant__ HeadsParams p) {
+  constexpr int T = fwd_rows<V>(), S = fwd_stages<TX>(), Q8 = pieces8<TX>();
+  constexpr int NT = turned_parts<JOINT>(), NP = all_parts<JOINT>();
+  constexpr int STAGE = fwd_pieces<TX, JOINT, V>(), RING = fwd_ring<TX, JOINT, V>();
+  constexpr bool SPLIT = split<TX, INTER>();
+  extern __shared__ uint4 smem[];
+  __shared__ __align__(16) float red[kSlotRedFloats];
+  __shared__ Turns turns;
+  const int part0 = JOINT ? 0 : blockIdx.y;
+  const HeadsPart& any = p.part[part0];
+  const bool plain = !JOINT && any.plain;
+  const bool rot = p.rotate && !plain;
+  const int norm = plain ? 0 : p.norm;
+  turns.fill(p);
+  __syncthreads();
+  const int per_cta = slots_per_cta(any.W);
+  Slot s = make_slot(any.W, red);
+  if (s.index >= per_cta) return;
+  const Place<SPLIT, D, V> at(s, any.C);
+  const int H = any.C / D;
+  Share mine(p, T, static_cast<int64_t>(blockIdx.x) * per_cta + s.index,
+             static_cast<int64_t>(gridDim.x) * per_cta);
+  if (mine.left == 0) return;
+
+  // Shared memory: the threads' rings, then the slots' angles.
+  const Ring ring = {smem + threadIdx.x, static_cast<int>(blockDim.x)};
+  const Ring weights = ring + S * STAGE;
+  float* ang = reinterpret_cast<float*>(smem + blockDim.x * RING) + s.index * kAngleBuffers * T * D;
+  const TX* xp[NP];
+  int64_t xs[NP];  // elements from one unit to the next
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const bool ok = at.active && row0 + t < p.M;
-      raw[t] = ok ? load_row<TX, INTER, D>(x + b * part.xs[0] + n * part.xs[1]) : zero8<TX>();
-      yo[t] = ok ? (static_cast<int64_t>(b) * H * p.N + n) * D : -1;
-      if (++n == p.N) n = 0, ++b;
+  for (int i = 0; i < NP; ++i) {
+    const HeadsPart& part = p.part[part0 + i];
+    xp[i] = static_cast<const TX*>(part.x) + at.head * part.xs[2] + at.c + mine.b * part.xs[0] +
+            mine.n * part.xs[1];
+    xs[i] = T * part.xs[1];
+  }
+  int ahead_b = mine.b, ahead_n = mine.n, ahead_left = mine.left;
+  const auto issue = [&](Ring stage) {
+    if (ahead_left > 0) {
+      --ahead_left;
+      const bool second = T == 1 || ahead_n + 1 < p.N;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const HeadsPart& part = p.part[part0 + i];
+        if (!JOINT || part.x != nullptr) {
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+              if (at.active[v] && (t == 0 || second))
+                stage_row<TX, SPLIT, D>(stage + ((i * T + t) * V + v) * Q8,
+                                        xp[i] + t * part.xs[1] + v * at.head_step * part.xs[2]);
+          }
+        }
+        xp[i] += xs[i];
+      }
+      ahead_n += T;
+      if (ahead_n >= p.N) {
+        ahead_n = 0;
+        ++ahead_b;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const HeadsPart& part = p.part[part0 + i];
+          xp[i] = static_cast<const TX*>(part.x) + at.head * part.xs[2] + at.c + ahead_b * part.xs[0];
+        }
+      }
     }
-    float2* cs = ang + buf * T * 64;
-    if (rot) token_angles<T, D>(p, s, turn, axis, static_cast<int>(row0), cs);
-    float v[T][8], ss[T];
+    cp_async_commit();
+  };
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      unpack8(raw[t], v[t]);
-      ss[t] = 0.f;
+  for (int k = 0; k < S; ++k) issue(ring + k * STAGE);
+
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss[t] += v[t][i] * v[t][i];
+  for (int i = 0; i < NT; ++i) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int wc = at.c + (norm == 1 ? (at.head + v * at.head_step) * D : 0);
+      keep_weight(weights + (i * V + v) * 2,
+                  load_weight<INTER, SPLIT, D>(p, norm ? p.part[part0 + i].w : nullptr, at.active[v], wc));
+      if (!at.active[v]) {
+        // Threads behind the last channel add zeros to the sums.
+        for (int k = 0; k < S; ++k) {
+          for (int t = 0; t < T; ++t) {
+            for (int q = 0; q < Q8; ++q)
+              ring[k * STAGE + ((i * T + t) * V + v) * Q8 + q] = make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
     }
-    if (norm == 1 && s.W > 1) {
-      slot_sum(s, ss);  // its barrier also publishes the angles
+  }
+
+  const float inv = 1.f / (norm == 1 ? any.C : D);
+  Angles<T, D> angles;
+  angles.start(p, mine.b, mine.n);
+  int n = mine.n;
+  int64_t out = ((static_cast<int64_t>(mine.b) * H + at.head) * p.N + n) * D + at.c;
+  const int64_t far = static_cast<int64_t>(at.head_step) * p.N * D;
+  int buf = 0, k = 0;
+  for (; mine.left > 0; --mine.left) {
+    float* cs = ang + buf * T * D;
+    buf ^= 1;
+    if (rot) {
+      angles.fill(p, s, turns, cs);
+      angles.next(p);
+    }
+    cp_async_wait<S - 1>();
+    const Ring stage = ring + k * STAGE;
+    Pairs x[NT * T * V];
+    float sums[NT * T * V];
+#pragma unroll
+    for (int i = 0; i < NT * T * V; ++i) {
+      x[i] = unstage_pairs<TX, INTER>(stage + i * Q8);
+      sums[i] = dot(x[i], x[i]);
+    }
+    if (norm == 1) {
+      float ts[NT * T];
+#pragma unroll
+      for (int i = 0; i < NT * T; ++i) {
+        ts[i] = sums[i * V];
+#pragma unroll
+        for (int v = 1; v < V; ++v) ts[i] += sums[i * V + v];
+      }
+      slot_sum(s, ts);  // its barrier also publishes the angles
+#pragma unroll
+      for (int i = 0; i < NT * T * V; ++i) sums[i] = ts[i / V];
+      if (s.W == 1) slot_sync(s);
     } else {
-      if (norm == 1) slot_sum(s, ss);
-      if (norm == 2) head_sum<D>(ss);
+      if (norm == 2) head_sum<D>(sums);
       if (rot) slot_sync(s);
     }
-    const float inv = 1.f / (norm == 1 ? part.C : D);
+    const bool second = T == 1 || n + 1 < p.N;
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      if (norm) {
-        const float r = 1.f / sqrtf(ss[t] * inv + p.eps);
+    for (int i = 0; i < NP; ++i) {
+      const HeadsPart& part = p.part[part0 + i];
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(part.y) + out;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[t][i] *= r * w[i];
+      for (int t = 0; t < T; ++t) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const bool ok = at.active[v] && (t == 0 || second) && (!JOINT || part.x != nullptr);
+          const int q = (i * T + t) * V + v;
+          if (i < NT) {
+            Pairs u = x[q];
+            if (norm) {
+              const float r = rsqrtf(sums[q] * inv + p.eps);
+              u = mul(mul(u, r), unstage_weight(weights + (i * V + v) * 2));
+            }
+            if (rot) u = rotate<false, INTER, SPLIT, D>(u, cs + t * D, at.c);
+            float f[8];
+            from_pairs<INTER>(u, f);
+            if (ok) store_row<__nv_bfloat16, SPLIT, D>(y + t * D + v * far, f);
+          } else {
+            const Raw8<TX> r = unstage8<TX>(stage + q * Q8);
+            if (ok) {
+              if constexpr (sizeof(TX) == 2) {
+                store_row_raw<SPLIT, D>(y + t * D + v * far, r);
+              } else {
+                float f[8];
+                unpack8(r, f);
+                store_row<__nv_bfloat16, SPLIT, D>(y + t * D + v * far, f);
+              }
+            }
+          }
+        }
       }
-      if (rot)
-        rotate8<INTER>(v[t], reinterpret_cast<const float4*>(
-                                 cs + t * (D / 2) + (INTER ? at.c / 2 : at.c)), 1.f);
-      if (yo[t] >= 0) store_row<__nv_bfloat16, INTER, D>(y + yo[t], v[t]);
+    }
+    issue(stage);
+    k = k + 1 == S ? 0 : k + 1;
+    n += T;
+    out += T * D;
+    if (n >= p.N) {
+      // Token 0 of the next sample.
+      out += (static_cast<int64_t>(H) * p.N - n) * D;
+      n = 0;
     }
   }
 }
 
-template <typename TX, bool INTER, int D, int T, int THREADS>
-__global__ void __launch_bounds__(THREADS) heads_bwd_kernel(const __grid_constant__ HeadsParams p) {
-  __shared__ float red[kSlotRedFloats];
-  __shared__ __align__(16) float2 angles[kMaxSlots * 2 * T * 64];
-  __shared__ uint64_t turn[64];
-  __shared__ uint8_t axis[64];
+template <typename TX, bool INTER, int D, int V, bool JOINT>
+__global__ void __launch_bounds__(row_threads(V), V == 1 ? HB_B : 1) heads_bwd_kernel(
+    const __grid_constant__ HeadsParams p) {
+  constexpr int S = bwd_stages<TX>(), Q8 = pieces8<TX>();
+  constexpr int NT = turned_parts<JOINT>(), NP = all_parts<JOINT>();
+  constexpr int STAGE = bwd_pieces<TX, JOINT, V>(), RING = bwd_ring<TX, JOINT, V>();
+  constexpr bool SPLIT = split<TX, INTER>();
+  constexpr int XAT = NP * V;  // the inputs' rows, behind the gradients' rows
+  extern __shared__ uint4 smem[];
+  __shared__ __align__(16) float red[kSlotRedFloats];
+  __shared__ Turns turns;
   grid_launch_dependents();
-  const HeadsPart& part = p.part[blockIdx.y];
-  const bool rot = p.rotate && !part.plain;
-  const int norm = part.plain ? 0 : p.norm;
-  if (threadIdx.x < 64) {
-    turn[threadIdx.x] = p.turn[threadIdx.x];
-    axis[threadIdx.x] = p.axis[threadIdx.x];
-  }
+  const int part0 = JOINT ? 0 : blockIdx.y;
+  const HeadsPart& any = p.part[part0];
+  const bool plain = !JOINT && any.plain;
+  const bool rot = p.rotate && !plain;
+  const int norm = plain ? 0 : p.norm;
+  turns.fill(p);
   __syncthreads();
-  const int per_cta = slots_per_cta(part.W);
-  Slot s = make_slot(part.W, red);
+  const int per_cta = slots_per_cta(any.W);
+  Slot s = make_slot(any.W, red);
   if (s.index >= per_cta) return;
-  const Place<INTER, D> at(s, part.C);
-  const int wc = norm == 1 ? at.head * D + at.c : at.c;
-  float w[8], dw[8];
-  load_weight<INTER, D>(p, norm ? part.w : nullptr, at.active, wc, w);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i] = 0.f;
+  const Place<SPLIT, D, V> at(s, any.C);
+  const int H = any.C / D;
+  const int64_t slot = static_cast<int64_t>(blockIdx.x) * per_cta + s.index;
+  Share mine(p, 1, slot, static_cast<int64_t>(gridDim.x) * per_cta);
 
-  const TX* x = static_cast<const TX*>(part.x) + at.head * part.xs[2] + at.c;
-  TX* dx = static_cast<TX*>(part.dx) + at.head * part.ds[2] + at.c;
-  const int H = part.C / D;
-  const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(part.y) +
-                            static_cast<int64_t>(at.head) * p.N * D + at.c;
-  const int nslots = gridDim.x * per_cta;
-  const int slot = blockIdx.x * per_cta + s.index;
-  float2* ang = angles + s.index * 2 * T * 64;
-  int buf = 0;
-  for (int64_t row0 = static_cast<int64_t>(slot) * T; row0 < p.M;
-       row0 += static_cast<int64_t>(nslots) * T, buf ^= 1) {
-    Raw8<TX> raw[T];
-    Raw8<__nv_bfloat16> rawg[T];
-    int b = static_cast<int>(row0) / p.N, n = static_cast<int>(row0) - b * p.N;
-    TX* out[T];
+  const Ring ring = {smem + threadIdx.x, static_cast<int>(blockDim.x)};
+  const Ring weights = ring + S * STAGE;
+  float* ang = reinterpret_cast<float*>(smem + blockDim.x * RING) + s.index * kAngleBuffers * D;
+  const int64_t far = static_cast<int64_t>(at.head_step) * p.N * D;
+  int64_t in = ((static_cast<int64_t>(mine.b) * H + at.head) * p.N + mine.n) * D + at.c;
+  const TX* xp[NT];
+  TX* dx[NP];
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const bool ok = at.active && row0 + t < p.M;
-      rawg[t] = ok ? load_row<__nv_bfloat16, INTER, D>(
-                         dy + (static_cast<int64_t>(b) * H * p.N + n) * D)
-                   : zero8<__nv_bfloat16>();
-      raw[t] = ok && norm ? load_row<TX, INTER, D>(x + b * part.xs[0] + n * part.xs[1])
-                          : zero8<TX>();
-      out[t] = ok ? dx + b * part.ds[0] + n * part.ds[1] : nullptr;
-      if (++n == p.N) n = 0, ++b;
-    }
-    const float2* cs = ang + buf * T * 64;
-    if (rot) {
-      token_angles<T, D>(p, s, turn, axis, static_cast<int>(row0), ang + buf * T * 64);
-      slot_sync(s);
-    }
-    float g[T][8], v[T][8], sums[2 * T];
+  for (int i = 0; i < NP; ++i) {
+    const HeadsPart& part = p.part[part0 + i];
+    if (i < NT)
+      xp[i] = static_cast<const TX*>(part.x) + at.head * part.xs[2] + at.c + mine.b * part.xs[0] +
+              mine.n * part.xs[1];
+    dx[i] = static_cast<TX*>(part.dx) + at.head * part.ds[2] + at.c + mine.b * part.ds[0] +
+            mine.n * part.ds[1];
+  }
+  int ahead_b = mine.b, ahead_n = mine.n, ahead_left = mine.left;
+  const auto issue = [&](Ring stage) {
+    if (ahead_left > 0) {
+      --ahead_left;
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      unpack8(rawg[t], g[t]);
-      if (rot)
-        rotate8<INTER>(g[t], reinterpret_cast<const float4*>(
-                                 cs + t * (D / 2) + (INTER ? at.c / 2 : at.c)), -1.f);
-      if (norm) {
-        unpack8(raw[t], v[t]);
-        sums[2 * t] = sums[2 * t + 1] = 0.f;
+      for (int i = 0; i < NP; ++i) {
+        const HeadsPart& part = p.part[part0 + i];
+        const bool here = !JOINT || part.y != nullptr;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sums[2 * t] += v[t][i] * v[t][i];
-          sums[2 * t + 1] += v[t][i] * (g[t][i] * w[i]);
+        for (int v = 0; v < V; ++v) {
+          if (here && at.active[v]) {
+            stage_row<__nv_bfloat16, SPLIT, D>(
+                stage + i * V + v, static_cast<const __nv_bfloat16*>(part.y) + in + v * far);
+            if (i < NT && norm)
+              stage_row<TX, SPLIT, D>(stage + XAT + (i * V + v) * Q8,
+                                      xp[i < NT ? i : 0] + v * at.head_step * part.xs[2]);
+          }
+        }
+        if (i < NT) xp[i < NT ? i : 0] += part.xs[1];
+      }
+      in += D;
+      if (++ahead_n == p.N) {
+        ahead_n = 0;
+        ++ahead_b;
+        in += static_cast<int64_t>(H - 1) * p.N * D;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const HeadsPart& part = p.part[part0 + i];
+          xp[i] = static_cast<const TX*>(part.x) + at.head * part.xs[2] + at.c + ahead_b * part.xs[0];
         }
       }
     }
-    if (norm == 1) slot_sum(s, sums);
-    if (norm == 2) head_sum<D>(sums);
-    const float inv = 1.f / (norm == 1 ? part.C : D);
+    cp_async_commit();
+  };
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      if (norm) {
-        const float r = 1.f / sqrtf(sums[2 * t] * inv + p.eps);
-        const float m = sums[2 * t + 1] * inv * r * r;
+  for (int k = 0; k < S; ++k) issue(ring + k * STAGE);
+
+  Pairs dw[NT * V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dw[i] += g[t][i] * (v[t][i] * r);
-          g[t][i] = r * (g[t][i] * w[i] - v[t][i] * m);
+  for (int i = 0; i < NT; ++i) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int wc = at.c + (norm == 1 ? (at.head + v * at.head_step) * D : 0);
+      keep_weight(weights + (i * V + v) * 2,
+                  load_weight<INTER, SPLIT, D>(p, norm ? p.part[part0 + i].w : nullptr, at.active[v], wc));
+      dw[i * V + v] = {{0, 0}, {0, 0}};
+      if (!at.active[v]) {
+        for (int k = 0; k < S; ++k) {
+          ring[k * STAGE + i * V + v] = make_uint4(0, 0, 0, 0);
+          for (int q = 0; q < Q8; ++q)
+            ring[k * STAGE + XAT + (i * V + v) * Q8 + q] = make_uint4(0, 0, 0, 0);
         }
       }
-      if (out[t] != nullptr) store_row<TX, INTER, D>(out[t], g[t]);
     }
   }
-  if (norm && part.dw_part != nullptr && at.active)
-    store_row<float, INTER, D>(
-        part.dw_part + static_cast<int64_t>(slot) * part.C + at.head * D + at.c, dw);
-}
 
-// Slots of one part: a CTA per resident place of the machine, shared by the
-// parts, and no more than there are row groups.
-int heads_ctas(int M, int T, int n_parts, int per_cta, int per_sm) {
-  const int64_t units = (static_cast<int64_t>(M) + T - 1) / T;
-  const int64_t need = (units + per_cta - 1) / per_cta;
-  const int64_t most = (kSMs * per_sm + n_parts - 1) / n_parts;
-  return static_cast<int>(std::max<int64_t>(1, std::min(need, most)));
+  const float inv = 1.f / (norm == 1 ? any.C : D);
+  Angles<1, D> angles;
+  int b = mine.b, n = mine.n, buf = 0;
+  if (rot && mine.left > 0) {
+    angles.start(p, b, n);
+    angles.fill(p, s, turns, ang);
+    slot_sync(s);
+  }
+  int k = 0;
+  for (; mine.left > 0; --mine.left) {
+    cp_async_wait<S - 1>();
+    const Ring stage = ring + k * STAGE;
+    const float* cs = ang + buf * D;
+    Pairs g[NT * V];
+    float sums[2 * NT * V];
+#pragma unroll
+    for (int i = 0; i < NT * V; ++i) {
+      g[i] = unstage_pairs<__nv_bfloat16, INTER>(stage + i);
+      if (rot) g[i] = rotate<true, INTER, SPLIT, D>(g[i], cs, at.c);
+      if (norm) {
+        const Pairs x = unstage_pairs<TX, INTER>(stage + XAT + i * Q8);
+        sums[2 * i] = dot(x, x);
+        sums[2 * i + 1] = dot(x, mul(g[i], unstage_weight(weights + i * 2)));
+      }
+    }
+    // The next token's angles, into the buffer that every warp has read before
+    // the barrier of the token before; this token's barrier publishes them.
+    buf ^= 1;
+    if (rot) {
+      angles.next(p);
+      angles.fill(p, s, turns, ang + buf * D);
+    }
+    if (norm == 1) {
+      float ts[2 * NT];
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) {
+        ts[i] = sums[(i / 2) * 2 * V + i % 2];
+#pragma unroll
+        for (int v = 1; v < V; ++v) ts[i] += sums[((i / 2) * V + v) * 2 + i % 2];
+      }
+      slot_sum(s, ts);
+#pragma unroll
+      for (int i = 0; i < 2 * NT * V; ++i) sums[i] = ts[(i / (2 * V)) * 2 + i % 2];
+      if (s.W == 1) slot_sync(s);
+    } else {
+      if (norm == 2) head_sum<D>(sums);
+      if (rot) slot_sync(s);
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const HeadsPart& part = p.part[part0 + i];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const bool ok = at.active[v] && (!JOINT || part.y != nullptr);
+        TX* out = dx[i] + v * at.head_step * part.ds[2];
+        if (i < NT) {
+          const int q = i < NT ? i * V + v : 0;
+          Pairs o = g[q];
+          if (norm) {
+            const Pairs xh = mul(unstage_pairs<TX, INTER>(stage + XAT + q * Q8),
+                                 rsqrtf(sums[2 * q] * inv + p.eps));
+            const float r = rsqrtf(sums[2 * q] * inv + p.eps);
+            dw[q] = fma(o, xh, dw[q]);
+            // r (g w - xh mean(g w xh))
+            o = mul(fma(xh, -(sums[2 * q + 1] * inv * r), mul(o, unstage_weight(weights + q * 2))), r);
+          }
+          float f[8];
+          from_pairs<INTER>(o, f);
+          if (ok) store_row<TX, SPLIT, D>(out, f);
+        } else {
+          const Raw8<__nv_bfloat16> r = unstage8<__nv_bfloat16>(stage + i * V + v);
+          if (ok) {
+            if constexpr (sizeof(TX) == 2) {
+              store_row_raw<SPLIT, D>(out, r);
+            } else {
+              float f[8];
+              unpack8(r, f);
+              store_row<TX, SPLIT, D>(out, f);
+            }
+          }
+        }
+      }
+      dx[i] += part.ds[1];
+    }
+    issue(stage);
+    k = k + 1 == S ? 0 : k + 1;
+    if (++n == p.N) {
+      n = 0;
+      ++b;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const HeadsPart& part = p.part[part0 + i];
+        dx[i] = static_cast<TX*>(part.dx) + at.head * part.ds[2] + at.c + b * part.ds[0];
+      }
+    }
+  }
+  if (!norm) return;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    float* out = p.part[part0 + i].dw_part;
+    if (out == nullptr) continue;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!at.active[v]) continue;
+      float f[8];
+      from_pairs<INTER>(dw[i * V + v], f);
+      store_row<float, SPLIT, D>(out + slot * any.C + (at.head + v * at.head_step) * D + at.c, f);
+    }
+  }
 }
 
 struct HeadsPlan {
-  int ctas, threads, tier;
-  int n;             // parts
+  bool joint;
+  int V, ctas, threads, slots;  // slots: of a CTA, at most
+  int n;             // parts beside one another in the grid
+  int at[3];         // the place of each of the call's parts
+  int smem;          // dynamic, of a CTA
   size_t dw_off[3];  // into the workspace
   size_t bytes;
 };
 
+template <typename TX>
+int ring_bytes(const HeadsPlan& pl, bool bwd) {
+  if (pl.V == 1) {
+    if (pl.joint) return bwd ? bwd_ring<TX, true, 1>() : fwd_ring<TX, true, 1>();
+    return bwd ? bwd_ring<TX, false, 1>() : fwd_ring<TX, false, 1>();
+  }
+  if (pl.joint) return bwd ? bwd_ring<TX, true, 2>() : fwd_ring<TX, true, 2>();
+  return bwd ? bwd_ring<TX, false, 2>() : fwd_ring<TX, false, 2>();
+}
+int heads_smem(const HeadsPlan& pl, bool f32, int d, bool bwd) {
+  const int ring = f32 ? ring_bytes<float>(pl, bwd) : ring_bytes<__nv_bfloat16>(pl, bwd);
+  const int rows = bwd ? 1 : (HF_T >= pl.V ? HF_T / pl.V : 1);
+  return 16 * ring * pl.threads + pl.slots * kAngleBuffers * rows * d * static_cast<int>(sizeof(float));
+}
+
 HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
   HeadsPlan pl = {};
-  int threads = 32, slots_min = kMaxSlots;
-  pl.n = a.n_parts;
+  int turned = 0, plain = 0, widest = 0;
+  bool same = true;
   for (int i = 0; i < a.n_parts; ++i) {
-    const int W = slot_warps(a.part[i].H * a.d);
-    threads = std::max(threads, W * slots_per_cta(W) * 32);
-    slots_min = std::min(slots_min, slots_per_cta(W));
+    const sparge_heads_part& s = a.part[i];
+    same = same && s.H == a.part[0].H;
+    widest = std::max(widest, s.H * a.d);
+    pl.at[i] = s.plain ? 2 : turned;
+    (s.plain ? plain : turned)++;
   }
-  pl.threads = threads;
-  pl.tier = tier_of(threads);
-  const int per_sm = std::max(1, 1280 / threads);
-  const int rows = bwd ? kTiers[pl.tier].bwd_rows : kTiers[pl.tier].fwd_rows;
-  pl.ctas = heads_ctas(a.B * a.N, rows, a.n_parts, slots_min, per_sm);
+  // Together when the rows are alike: angles and barriers are shared, so 480p
+  // takes less time than with a part to each blockIdx.y.
+  // Wide rows only where a CTA's ring still fits the shared memory.
+  pl.V = row_vectors(widest);
+  pl.joint = a.n_parts > 1 && same && turned <= 2 && plain <= 1 && turned > 0 &&
+             (pl.V == 1 || (!bwd && a.x_type == SPARGE_BF16));
+  pl.n = pl.joint ? 1 : a.n_parts;
+  int slots_min = kMaxSlots;
+  for (int i = 0; i < a.n_parts; ++i) {
+    if (!pl.joint) pl.at[i] = i;
+    const int W = slot_warps(a.part[i].H * a.d, pl.V);
+    pl.threads = std::max(pl.threads, W * slots_per_cta(W) * 32);
+    slots_min = std::min(slots_min, slots_per_cta(W));
+    pl.slots = std::max(pl.slots, slots_per_cta(W));
+  }
+  // A grid that is resident as a whole: every CTA stays for its share of the
+  // rows.  Shared memory limits it, or registers (at most 64 a thread forward,
+  // 128 backward).
+  pl.smem = heads_smem(pl, a.x_type == SPARGE_F32, a.d, bwd);
+  const int rows = bwd ? 1 : (HF_T >= pl.V ? HF_T / pl.V : 1);
+  const int per_sm = std::max(1, std::min(65536 / ((bwd ? 65536 / 256 / HB_B / 8 * 8 : 65536 / 256 / HF_B / 8 * 8) * pl.threads),
+                                          kSmemPerSm / (pl.smem + kSmemOfCta)));
+  const int64_t units = static_cast<int64_t>(a.B) * ((a.N + rows - 1) / rows);
+  const int64_t need = (units + slots_min - 1) / slots_min;
+  const int64_t most = (kSMs * per_sm + pl.n - 1) / pl.n;
+  pl.ctas = static_cast<int>(std::max<int64_t>(1, std::min(need, most)));
   for (int i = 0; i < a.n_parts; ++i) {
     if (!bwd || a.norm == 0 || a.part[i].plain || a.part[i].dweight == nullptr) continue;
     const int C = a.part[i].H * a.d;
     pl.dw_off[i] = pl.bytes;
-    pl.bytes += static_cast<size_t>(pl.ctas) * slots_per_cta(slot_warps(C)) * C * sizeof(float);
+    pl.bytes += static_cast<size_t>(pl.ctas) * slots_per_cta(slot_warps(C, pl.V)) * C * sizeof(float);
   }
   return pl;
 }
 
-HeadsParams heads_params(const sparge_heads& a) {
+HeadsParams heads_params(const sparge_heads& a, const HeadsPlan& pl) {
   HeadsParams p = {};
+  if (pl.joint) {
+    // An absent part still gives the row its size.
+    for (int i = 0; i < 3; ++i) {
+      p.part[i].C = a.part[0].H * a.d;
+      p.part[i].W = slot_warps(p.part[i].C, pl.V);
+    }
+  }
   for (int i = 0; i < a.n_parts; ++i) {
     const sparge_heads_part& s = a.part[i];
-    HeadsPart& o = p.part[i];
+    HeadsPart& o = p.part[pl.at[i]];
     o.x = s.x;
     o.w = s.weight;
     o.y = s.y;
     o.dx = s.dx;
     for (int k = 0; k < 3; ++k) o.xs[k] = s.x_stride[k], o.ds[k] = s.dx_stride[k];
     o.C = s.H * a.d;
-    o.W = slot_warps(o.C);
+    o.W = slot_warps(o.C, pl.V);
     o.plain = s.plain;
   }
   p.grid = a.grid;
@@ -390,22 +887,28 @@ HeadsParams heads_params(const sparge_heads& a) {
   return p;
 }
 
-template <typename TX, bool INTER, int D, int I>
-void launch_tier(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cudaStream_t st) {
-  constexpr Tier t = kTiers[I];
-  const dim3 grid(pl.ctas, pl.n);
-  if (bwd)
-    heads_bwd_kernel<TX, INTER, D, t.bwd_rows, t.threads><<<grid, pl.threads, 0, st>>>(p);
-  else
-    heads_fwd_kernel<TX, INTER, D, t.fwd_rows, t.threads><<<grid, pl.threads, 0, st>>>(p);
+template <typename TX, bool INTER, int D, int V, bool JOINT>
+cudaError_t launch_form(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cudaStream_t st) {
+  auto* kernel = bwd ? heads_bwd_kernel<TX, INTER, D, V, JOINT> : heads_fwd_kernel<TX, INTER, D, V, JOINT>;
+  if (pl.smem > 47 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
+    if (e != cudaSuccess) {
+      cudaGetLastError();  // the next launch must not report it
+      return e;
+    }
+  }
+  kernel<<<dim3(pl.ctas, pl.n), pl.threads, pl.smem, st>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename TX, bool INTER, int D>
 cudaError_t launch_heads(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cudaStream_t st) {
-  if (pl.tier == 0) launch_tier<TX, INTER, D, 0>(p, pl, bwd, st);
-  if (pl.tier == 1) launch_tier<TX, INTER, D, 1>(p, pl, bwd, st);
-  if (pl.tier == 2) launch_tier<TX, INTER, D, 2>(p, pl, bwd, st);
-  return cudaGetLastError();
+  if (pl.V == 1)
+    return pl.joint ? launch_form<TX, INTER, D, 1, true>(p, pl, bwd, st)
+                    : launch_form<TX, INTER, D, 1, false>(p, pl, bwd, st);
+  return pl.joint ? launch_form<TX, INTER, D, 2, true>(p, pl, bwd, st)
+                  : launch_form<TX, INTER, D, 2, false>(p, pl, bwd, st);
 }
 
 cudaError_t dispatch_heads(const sparge_heads& a, const HeadsParams& p, const HeadsPlan& pl,
@@ -531,8 +1034,8 @@ int sparge_rope_init(sparge_rope* rope, int32_t d, const int32_t* pairs, double 
 
 int sparge_heads_fwd(const sparge_heads* args, sparge_stream_t stream) {
   HEADS_TRY(check_heads(args, false));
-  return status_of(dispatch_heads(*args, heads_params(*args), heads_plan(*args, false), false,
-                                  stream));
+  const HeadsPlan pl = heads_plan(*args, false);
+  return status_of(dispatch_heads(*args, heads_params(*args, pl), pl, false, stream));
 }
 
 int sparge_heads_bwd_workspace_bytes(const sparge_heads* args, size_t* bytes) {
@@ -550,20 +1053,21 @@ int sparge_heads_bwd(const sparge_heads* args, void* workspace, size_t ws_bytes,
     if (workspace == nullptr || ws_bytes < pl.bytes) return SPARGE_ERR_WORKSPACE;
     HEADS_TRY(check_aligned(workspace, 16));
   }
-  HeadsParams p = heads_params(*args);
+  HeadsParams p = heads_params(*args, pl);
   ReduceJobs jobs = {};
   for (int i = 0; i < args->n_parts; ++i) {
     const sparge_heads_part& s = args->part[i];
     if (args->norm == SPARGE_HEADS_NORM_NONE || s.plain || s.dweight == nullptr) continue;
     const int C = s.H * args->d;
-    p.part[i].dw_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.dw_off[i]);
+    float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.dw_off[i]);
+    p.part[pl.at[i]].dw_part = part;
     // One row of C sums a slot; with a norm over each head, H rows of d.
     const bool token = args->norm == SPARGE_HEADS_NORM_TOKEN;
     ReduceJob& j = jobs.job[jobs.n++];
-    j.src = p.part[i].dw_part;
+    j.src = part;
     j.C = token ? C : args->d;
     j.ld = j.C;
-    j.nrow = pl.ctas * slots_per_cta(slot_warps(C)) * (token ? 1 : s.H);
+    j.nrow = pl.ctas * slots_per_cta(slot_warps(C, pl.V)) * (token ? 1 : s.H);
     j.nout = 1;
     j.out = s.dweight;
     j.out_bf16 = args->weight_type == SPARGE_BF16;

@@ -54,374 +54,696 @@ struct ResnormParams {
   // backward: column sums in the order gate, scale, shift, post
   float* sum[4];      // null: not wanted
   int by_group[4];    // written at the end of each item, else at the slot's end
-  int items, parts, part_rows;  // items = groups * parts
+  int items, parts;  // items = groups * parts
 };
 
+// Eight channels as packed pairs: every elementwise step is a packed operation.
+struct F8 {
+  uint64_t v[4];
+};
+SPARGE_DEV F8 f8(const float (&f)[8]) {
+  return {{f32x2(f[0], f[1]), f32x2(f[2], f[3]), f32x2(f[4], f[5]), f32x2(f[6], f[7])}};
+}
+SPARGE_DEV F8 f8(float f) {
+  const uint64_t u = f32x2(f, f);
+  return {{u, u, u, u}};
+}
+SPARGE_DEV F8 fma(const F8& a, const F8& b, const F8& c) {
+  return {{ffma2(a.v[0], b.v[0], c.v[0]), ffma2(a.v[1], b.v[1], c.v[1]),
+           ffma2(a.v[2], b.v[2], c.v[2]), ffma2(a.v[3], b.v[3], c.v[3])}};
+}
+SPARGE_DEV F8 mul(const F8& a, const F8& b) {
+  return {{fmul2(a.v[0], b.v[0]), fmul2(a.v[1], b.v[1]), fmul2(a.v[2], b.v[2]),
+           fmul2(a.v[3], b.v[3])}};
+}
+SPARGE_DEV F8 add(const F8& a, const F8& b) {
+  return {{fadd2(a.v[0], b.v[0]), fadd2(a.v[1], b.v[1]), fadd2(a.v[2], b.v[2]),
+           fadd2(a.v[3], b.v[3])}};
+}
+SPARGE_DEV float total(const F8& a) {
+  const uint64_t s = fadd2(fadd2(a.v[0], a.v[1]), fadd2(a.v[2], a.v[3]));
+  return f32x2_lo(s) + f32x2_hi(s);
+}
+SPARGE_DEV float dot(const F8& a, const F8& b) {
+  const uint64_t s = fadd2(ffma2(a.v[0], b.v[0], fmul2(a.v[1], b.v[1])),
+                           ffma2(a.v[2], b.v[2], fmul2(a.v[3], b.v[3])));
+  return f32x2_lo(s) + f32x2_hi(s);
+}
+SPARGE_DEV F8 f8(const Raw8<float>& r) {
+  return {{f32x2(__uint_as_float(r.v[0].x), __uint_as_float(r.v[0].y)),
+           f32x2(__uint_as_float(r.v[0].z), __uint_as_float(r.v[0].w)),
+           f32x2(__uint_as_float(r.v[1].x), __uint_as_float(r.v[1].y)),
+           f32x2(__uint_as_float(r.v[1].z), __uint_as_float(r.v[1].w))}};
+}
+SPARGE_DEV F8 f8(const Raw8<__nv_bfloat16>& r) {
+  float f[8];
+  unpack8(r, f);
+  return f8(f);
+}
 template <typename T>
-SPARGE_DEV void load_f32x8(const T* p, float (&f)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+SPARGE_DEV F8 unstage(Ring src) {
+  return f8(unstage8<T>(src));
 }
 
-// Mean and sum of squares about it, of each of T rows, over the slot.  `cnt`
-// channels of this warp are in use (a multiple of 8).
-template <int T>
-SPARGE_DEV void slot_moments(Slot& s, const float (&y)[T][8], bool active, int cnt, float inv_c,
-                             float (&mean)[T], float (&m2)[T]) {
-  const float inv = cnt > 0 ? 1.f / cnt : 0.f;
+// Eight channels of a thread are two fours: side by side when every tensor is
+// bf16, 128 channels apart (32 lanes on) when one is fp32, so that a warp reads
+// and writes whole sectors of it.
+template <typename TX>
+constexpr int four_step() {
+  return sizeof(TX) == 2 ? 4 : 128;
+}
+template <int F, typename T>
+SPARGE_DEV void stage_fours(Ring dst, const T* p, bool lo, bool hi) {
+  if constexpr (F == 4) {
+    if (lo) stage8(dst, p);
+  } else if constexpr (sizeof(T) == 4) {
+    if (lo) cp_async16(&dst[0], p);
+    if (hi) cp_async16(&dst[1], p + F);
+  } else {
+    if (lo) cp_async8(&dst[0], p);
+    if (hi) cp_async8(reinterpret_cast<uint2*>(&dst[0]) + 1, p + F);
+  }
+}
+template <int F, typename T>
+SPARGE_DEV void put(T* p, const F8& a, bool lo, bool hi) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[2 * i] = f32x2_lo(a.v[i]), f[2 * i + 1] = f32x2_hi(a.v[i]);
+  const Raw8<T> r = pack8(f, T());
+  if constexpr (F == 4) {
+    if (lo) store_raw8(p, r);
+  } else if constexpr (sizeof(T) == 4) {
+    if (lo) *reinterpret_cast<uint4*>(p) = r.v[0];
+    if (hi) *reinterpret_cast<uint4*>(p + F) = r.v[1];
+  } else {
+    if (lo) *reinterpret_cast<uint2*>(p) = make_uint2(r.v[0].x, r.v[0].y);
+    if (hi) *reinterpret_cast<uint2*>(p + F) = make_uint2(r.v[0].z, r.v[0].w);
+  }
+}
+
+// What stands for an absent gate, scale or shift: read like one, it keeps
+// null checks out of the row loops (an absent gate or gain is 0 + 1).
+__device__ float g_zeros[kMaxRowChannels];
+
+// Eight channels of a gate, scale, shift or weight; `step` between the fours.
+SPARGE_DEV F8 load_mod(const float* m, int step) {
+  Raw8<float> r;
+  r.v[0] = __ldg(reinterpret_cast<const uint4*>(m));
+  r.v[1] = __ldg(reinterpret_cast<const uint4*>(m + step));
+  return f8(r);
+}
+
+// One such row as a thread sees it: in registers from row to row where it
+// covers eight channels (V = 1), read again from L1 (which the rows bypass)
+// where it covers sixteen.
+template <int V>
+struct Mod {
+  const float* at;
+  F8 kept;
+  SPARGE_DEV void open(const float* row, float plus, const int (&off)[V][2]) {
+    at = row;
+    if constexpr (V == 1) kept = add(load_mod(row + off[0][0], off[0][1]), f8(plus));
+  }
+  SPARGE_DEV F8 get(int v, const int (&off)[V][2], float plus) const {
+    if constexpr (V == 1) return kept;
+    return add(load_mod(at + off[v][0], off[v][1]), f8(plus));
+  }
+  SPARGE_DEV F8 get(int v, const int (&off)[V][2]) const {
+    if constexpr (V == 1) return kept;
+    return load_mod(at + off[v][0], off[v][1]);
+  }
+};
+
+// Mean and sum of squares about it of each of T rows over the slot.  `cnt`:
+// channels of this warp, `full` of every warp but the last, `last` of that.
+template <int T, int V>
+SPARGE_DEV void slot_moments(Slot& s, const F8 (&y)[T * V], const bool (&lo)[V], const bool (&hi)[V], float inv_cnt,
+                             const float* counts, float inv_c, float (&mean)[T], float (&m2)[T]) {
+  float part[T];
 #pragma unroll
   for (int t = 0; t < T; ++t) {
-    float sum = 0.f;
+    part[t] = total(y[t * V]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += y[t][i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    mean[t] = sum * inv;
-    float sq = 0.f;
-    if (active) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sq += (y[t][i] - mean[t]) * (y[t][i] - mean[t]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    m2[t] = sq;
+    for (int v = 1; v < V; ++v) part[t] += total(y[t * V + v]);
   }
-  if (s.W == 1) return;
+  const float mine = warp_sums(part, s.lane) * inv_cnt;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    mean[t] = __shfl_sync(0xffffffffu, mine, t * (32 / T));
+    part[t] = 0.f;
+    const F8 m = f8(-mean[t]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      F8 d = add(y[t * V + v], m);
+      if (!lo[v]) d.v[0] = d.v[1] = 0;
+      if (!hi[v]) d.v[2] = d.v[3] = 0;
+      part[t] += dot(d, d);
+    }
+  }
+  const float square = warp_sums(part, s.lane);
+  if (s.W == 1) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) m2[t] = __shfl_sync(0xffffffffu, square, t * (32 / T));
+    return;
+  }
   static_assert(2 * T <= kSlotRed, "reduction buffer");
   float* red = s.red + s.phase * s.W * kSlotRed;
   s.phase ^= 1;
-  if (s.lane == 0) {
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      red[s.warp * kSlotRed + 2 * t] = mean[t];
-      red[s.warp * kSlotRed + 2 * t + 1] = m2[t];
-    }
-  }
+  if (s.lane % (32 / T) == 0)
+    *reinterpret_cast<float2*>(red + s.warp * kSlotRed + 2 * (s.lane / (32 / T))) =
+        make_float2(mine, square);
   slot_sync(s);
-  // Every warp but the last has 256 channels.
-  const int last = static_cast<int>(1.f / inv_c + 0.5f) - (s.W - 1) * 256;
 #pragma unroll
   for (int t = 0; t < T; ++t) mean[t] = m2[t] = 0.f;
   for (int w = 0; w < s.W; ++w) {
-    const float n = w + 1 < s.W ? 256.f : static_cast<float>(last);
+    const float n = counts[w];
 #pragma unroll
-    for (int t = 0; t < T; ++t) mean[t] += n * red[w * kSlotRed + 2 * t];
+    for (int t = 0; t < T; ++t) mean[t] = fmaf(n, red[w * kSlotRed + 2 * t], mean[t]);
   }
 #pragma unroll
   for (int t = 0; t < T; ++t) mean[t] *= inv_c;
   for (int w = 0; w < s.W; ++w) {
-    const float n = w + 1 < s.W ? 256.f : static_cast<float>(last);
+    const float n = counts[w];
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-      const float d = red[w * kSlotRed + 2 * t] - mean[t];
-      m2[t] += red[w * kSlotRed + 2 * t + 1] + n * d * d;
+      const float2 r = *reinterpret_cast<const float2*>(red + w * kSlotRed + 2 * t);
+      const float d = r.x - mean[t];
+      m2[t] += fmaf(n * d, d, r.y);
     }
   }
 }
 
-template <typename TX, typename TB, int T, int THREADS>
-__global__ void __launch_bounds__(THREADS) resnorm_fwd_kernel(
+#ifndef RF_S
+#define RF_S 3
+#endif
+#ifndef RF_T
+#define RF_T 2
+#endif
+#ifndef RF_B
+#define RF_B 2
+#endif
+#ifndef RB_S
+#define RB_S 3
+#endif
+#ifndef RB_T
+#define RB_T 1
+#endif
+#ifndef RB_B
+#define RB_B 2
+#endif
+// Rows a slot takes at once, and pieces of one stage.
+template <int V>
+constexpr int fwd_rows() {
+  return RF_T >= V ? RF_T / V : 1;
+}
+template <typename TX, typename TB, int V>
+constexpr int fwd_pieces() {
+  return fwd_rows<V>() * V * (pieces8<TX>() + pieces8<TB>());
+}
+template <int V>
+constexpr int bwd_rows() {
+  return V == 1 ? RB_T : 1;
+}
+template <typename TX, typename TB, int V>
+constexpr int bwd_pieces() {
+  return bwd_rows<V>() * V * 2 * (pieces8<TX>() + pieces8<TB>());
+}
+// Stages of the ring; wide rows have as many as a CTA of 512 threads can hold.
+constexpr int kFwdStages = RF_S;
+template <typename TX, typename TB, int V>
+constexpr int bwd_stages() {
+  return V == 1 ? RB_S : 24 / bwd_pieces<TX, TB, V>();
+}
+
+// A thread's channels (vector v: fours at c + v * far and F further) and its
+// part of the ring.
+template <int V, int F>
+struct Lane {
+  int c, far;
+  bool lo[V], hi[V], all;
+  int mod[V][2];  // where it reads a row that is kept: inside also behind the end
+  Ring ring;
+  SPARGE_DEV Lane(const Slot& s, int C, uint4* smem) {
+    c = F == 4 ? s.tid * 8 : s.warp * 256 + s.lane * 4;
+    far = s.W * 256;
+    all = true;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      lo[v] = c + v * far < C;
+      hi[v] = c + v * far + F < C;
+      all = all && lo[v] && hi[v];
+      mod[v][0] = lo[v] ? c + v * far : 0;
+      mod[v][1] = hi[v] ? F : 0;
+    }
+    ring = {smem + threadIdx.x, static_cast<int>(blockDim.x)};
+  }
+};
+
+// The rows of a slot's items.  An item is one of the `parts` interleaved
+// shares of a group's rows: T rows of every parts * T, so that the slots of the
+// machine read neighbouring rows at any time.
+struct ItemWalk {
+  int item, row, end, g;
+  SPARGE_DEV void open(const ResnormParams& p, int T) {
+    if (item >= p.items) return;
+    g = item / p.parts;
+    row = g * p.R + (item - g * p.parts) * T;
+    end = (g + 1) * p.R;
+  }
+  SPARGE_DEV void next(const ResnormParams& p, int T, int nslots) {
+    row += p.parts * T;
+    if (row >= end) {
+      item += nslots;
+      open(p, T);
+    }
+  }
+};
+
+template <typename TX, typename TB, int V>
+__global__ void __launch_bounds__(row_threads(V), V == 1 ? RF_B : 1) resnorm_fwd_kernel(
     const __grid_constant__ ResnormParams p) {
-  __shared__ float red[kSlotRedFloats];
+  constexpr int T = fwd_rows<V>(), S = kFwdStages, XQ = pieces8<TX>(), BQ = pieces8<TB>();
+  constexpr int PIECES = fwd_pieces<TX, TB, V>(), STAGE = PIECES;
+  extern __shared__ uint4 smem[];
+  __shared__ __align__(16) float red[kSlotRedFloats];
+  __shared__ float counts[16];
   Slot s = make_slot(p.W, red);
   const int per_cta = slots_per_cta(p.W);
+  if (threadIdx.x < p.W) {
+    int n = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      n += max(0, min(256, p.C - (v * p.W + static_cast<int>(threadIdx.x)) * 256));
+    counts[threadIdx.x] = static_cast<float>(n);
+  }
+  __syncthreads();
   if (s.index >= per_cta) return;
-  const int c = s.tid * 8;
-  const bool active = c < p.C;
-  const int cnt = max(0, min(256, p.C - s.warp * 256));
-  const TX* x = static_cast<const TX*>(p.x) + c;
-  const TB* b = static_cast<const TB*>(p.b) + c;
-  TX* y_out = static_cast<TX*>(p.y) + c;
-  TB* h_out = static_cast<TB*>(p.h) + c;
+  const float inv_cnt = 1.f / counts[s.warp];
+  constexpr int F = four_step<TX>();
+  const Lane<V, F> at(s, p.C, smem);
+  // What is never loaded is zero: threads behind the last channel add zeros.
+  if (!at.all) {
+    for (int k = 0; k < S * PIECES; ++k) at.ring[k] = make_uint4(0, 0, 0, 0);
+  }
 
-  float gate[8], gain[8], shift[8], post[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) gate[i] = gain[i] = post[i] = 1.f, shift[i] = 0.f;
-  if (p.post != nullptr && active) load_f32x8(p.post + c, post);
+  const int nslots = static_cast<int>(gridDim.x) * per_cta;
+  ItemWalk ahead = {static_cast<int>(blockIdx.x) * per_cta + s.index, 0, 0, 0};
+  ahead.open(p, T);
+  ItemWalk now = ahead;
 
-  const int units_per_group = (p.R + T - 1) / T;
-  const int units = (p.M / p.R) * units_per_group;
-  const int nslots = gridDim.x * per_cta;
-  int group = -1;
-  for (int u = blockIdx.x * per_cta + s.index; u < units; u += nslots) {
-    const int g = u / units_per_group, first = (u - g * units_per_group) * T;
-    const int rows = min(T, p.R - first);
-    const int64_t row0 = static_cast<int64_t>(g) * p.R + first;
-    Raw8<TX> rx[T];
-    Raw8<TB> rb[T];
+  const TX* x = static_cast<const TX*>(p.x) + at.c;
+  const TB* b = static_cast<const TB*>(p.b) + at.c;
+  const bool has_b = p.b != nullptr, has_post = p.post != nullptr;
+  const auto issue = [&](Ring stage) {
+    if (ahead.item < p.items) {
+      int64_t o = static_cast<int64_t>(ahead.row) * p.C;
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const bool ok = active && t < rows;
-      rx[t] = ok ? load8(x + (row0 + t) * p.C) : zero8<TX>();
-      rb[t] = ok && p.b != nullptr ? load8(b + (row0 + t) * p.C) : zero8<TB>();
-    }
-    if (g != group) {
-      if (active && p.gate != nullptr && (group < 0 || p.gate_ld != 0))
-        load_f32x8(p.gate + g * p.gate_ld + c, gate);
-      if (active && p.scale != nullptr && (group < 0 || p.scale_ld != 0)) {
-        load_f32x8(p.scale + g * p.scale_ld + c, gain);
-        if (p.unit) {
+      for (int t = 0; t < T; ++t) {
+        if (ahead.row + t < ahead.end) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) gain[i] += 1.f;
+          for (int v = 0; v < V; ++v) {
+            const Ring dst = stage + (t * V + v) * (XQ + BQ);
+            stage_fours<F>(dst, x + o + v * at.far, at.lo[v], at.hi[v]);
+            if (has_b) stage_fours<F>(dst + XQ, b + o + v * at.far, at.lo[v], at.hi[v]);
+          }
         }
+        o += p.C;
       }
-      if (active && p.shift != nullptr && (group < 0 || p.shift_ld != 0))
-        load_f32x8(p.shift + g * p.shift_ld + c, shift);
-      group = g;
+      ahead.next(p, T, nslots);
     }
-    float y[T][8];
-    float rbs[T];
-    if (p.b != nullptr) {
+    cp_async_commit();
+  };
 #pragma unroll
-      for (int t = 0; t < T; ++t) unpack8(rb[t], y[t]);
-      if (p.post != nullptr) {
+  for (int k = 0; k < S; ++k) issue(at.ring + k * STAGE);
+
+  const float* gate_row = (p.gate != nullptr ? p.gate : g_zeros);
+  const float* scale_row = (p.scale != nullptr ? p.scale : g_zeros);
+  const float* shift_row = (p.shift != nullptr ? p.shift : g_zeros);
+  const float plus = p.unit || p.scale == nullptr ? 1.f : 0.f;
+  const float gate_plus = p.gate == nullptr ? 1.f : 0.f;
+  Mod<V> gate, gain, shift;
+  int group = -1;
+  int k = 0;
+  while (now.item < p.items) {
+    const int rows = min(T, now.end - now.row), row = now.row;
+    if (now.g != group) {
+      group = now.g;
+      gate.open(gate_row + group * p.gate_ld, gate_plus, at.mod);
+      gain.open(scale_row + group * p.scale_ld, plus, at.mod);
+      shift.open(shift_row + group * p.shift_ld, 0.f, at.mod);
+    }
+    now.next(p, T, nslots);
+    // The stage is read out at once and filled again, so its bytes are in
+    // flight while the rows are computed.
+    cp_async_wait<S - 1>();
+    const Ring stage = at.ring + k * STAGE;
+    k = k + 1 == S ? 0 : k + 1;
+    Raw8<TX> rx[T * V];
+    Raw8<TB> rb[T * V];
+#pragma unroll
+    for (int i = 0; i < T * V; ++i) {
+      rx[i] = unstage8<TX>(stage + i * (XQ + BQ));
+      rb[i] = unstage8<TB>(stage + i * (XQ + BQ) + XQ);
+    }
+    issue(stage);
+    F8 y[T * V];
+    float rbs[T];
+    if (has_b) {
+      F8 b8[T * V];
+#pragma unroll
+      for (int i = 0; i < T * V; ++i) b8[i] = f8(rb[i]);
+      if (has_post) {
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-          rbs[t] = 0.f;
+          rbs[t] = dot(b8[t * V], b8[t * V]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) rbs[t] += y[t][i] * y[t][i];
+          for (int v = 1; v < V; ++v) rbs[t] += dot(b8[t * V + v], b8[t * V + v]);
         }
         slot_sum(s, rbs);
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-          rbs[t] = 1.f / sqrtf(rbs[t] * p.inv_c + p.eps);
+          rbs[t] = rsqrtf(rbs[t] * p.inv_c + p.eps);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[t][i] *= rbs[t] * post[i];
+          for (int v = 0; v < V; ++v)
+            b8[t * V + v] = mul(mul(b8[t * V + v], f8(rbs[t])), load_mod(p.post + at.mod[v][0], at.mod[v][1]));
         }
       }
+      int64_t o = static_cast<int64_t>(row) * p.C + at.c;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        float xv[8];
-        unpack8(rx[t], xv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[t][i] = fmaf(gate[i], y[t][i], xv[i]);
-        if (active && t < rows) store8(y_out + (row0 + t) * p.C, y[t]);
+        for (int v = 0; v < V; ++v) {
+          const int i = t * V + v;
+          y[i] = fma(gate.get(v, at.mod, gate_plus), b8[i], f8(rx[i]));
+          if (t < rows) put<F>(static_cast<TX*>(p.y) + o + v * at.far, y[i], at.lo[v], at.hi[v]);
+        }
+        o += p.C;
       }
     } else {
 #pragma unroll
-      for (int t = 0; t < T; ++t) unpack8(rx[t], y[t]);
+      for (int i = 0; i < T * V; ++i) y[i] = f8(rx[i]);
     }
-    float mean[T], sq[T];
-    if (p.norm == SPARGE_NORM_LAYER) {
-      slot_moments(s, y, active, cnt, p.inv_c, mean, sq);
-    } else if (p.norm == SPARGE_NORM_RMS) {
+    float mean[T], rstd[T];
+    if (p.norm != SPARGE_NORM_NONE) {
+      if (p.norm == SPARGE_NORM_LAYER) {
+        slot_moments<T, V>(s, y, at.lo, at.hi, inv_cnt, counts, p.inv_c, mean, rstd);
+      } else {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          mean[t] = 0.f;
+          rstd[t] = dot(y[t * V], y[t * V]);
+#pragma unroll
+          for (int v = 1; v < V; ++v) rstd[t] += dot(y[t * V + v], y[t * V + v]);
+        }
+        slot_sum(s, rstd);
+      }
+      int64_t o = static_cast<int64_t>(row) * p.C + at.c;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        mean[t] = sq[t] = 0.f;
+        rstd[t] = rsqrtf(rstd[t] * p.inv_c + p.eps);
+        const F8 m = f8(-mean[t]), r = f8(rstd[t]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sq[t] += y[t][i] * y[t][i];
-      }
-      slot_sum(s, sq);
-    }
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      float rstd = 0.f;
-      if (p.norm != SPARGE_NORM_NONE) {
-        rstd = 1.f / sqrtf(sq[t] * p.inv_c + p.eps);
-        float h[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = fmaf((y[t][i] - mean[t]) * rstd, gain[i], shift[i]);
-        if (active && t < rows) store8(h_out + (row0 + t) * p.C, h);
-      }
-      if (s.tid == 0 && t < rows && p.stats != nullptr) {
-        if (p.norm != SPARGE_NORM_NONE) {
-          p.stats[row0 + t] = mean[t];
-          p.stats[p.M + row0 + t] = rstd;
+        for (int v = 0; v < V; ++v) {
+          const F8 h = fma(mul(add(y[t * V + v], m), r), gain.get(v, at.mod, plus), shift.get(v, at.mod));
+          if (t < rows) put<F>(static_cast<TB*>(p.h) + o + v * at.far, h, at.lo[v], at.hi[v]);
         }
-        if (p.post != nullptr) p.stats[2 * static_cast<int64_t>(p.M) + row0 + t] = rbs[t];
+        o += p.C;
+      }
+    }
+    if (s.tid == 0 && p.stats != nullptr) {
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        if (t >= rows) continue;
+        if (p.norm != SPARGE_NORM_NONE) {
+          p.stats[row + t] = mean[t];
+          p.stats[p.M + row + t] = rstd[t];
+        }
+        if (has_post) p.stats[2 * static_cast<int64_t>(p.M) + row + t] = rbs[t];
       }
     }
   }
 }
 
-template <typename TX, typename TB, int T, int THREADS>
-__global__ void __launch_bounds__(THREADS) resnorm_bwd_kernel(
+template <typename TX, typename TB, int V, bool POST>
+__global__ void __launch_bounds__(row_threads(V), V == 1 ? RB_B : 1) resnorm_bwd_kernel(
     const __grid_constant__ ResnormParams p) {
-  __shared__ float red[kSlotRedFloats];
+  constexpr int T = bwd_rows<V>(), S = bwd_stages<TX, TB, V>(), XQ = pieces8<TX>(),
+                BQ = pieces8<TB>();
+  constexpr int PIECES = bwd_pieces<TX, TB, V>(), ROW = 2 * (XQ + BQ), STAGE = PIECES;
+  constexpr int SUMS = POST ? 4 : 3;
+  extern __shared__ uint4 smem[];
+  __shared__ __align__(16) float red[kSlotRedFloats];
   grid_launch_dependents();
   Slot s = make_slot(p.W, red);
   const int per_cta = slots_per_cta(p.W);
   if (s.index >= per_cta) return;
-  const int c = s.tid * 8;
-  const bool active = c < p.C;
-  const TX* x = static_cast<const TX*>(p.x) + c;
-  const TB* b = static_cast<const TB*>(p.b) + c;
-  const TX* dy = static_cast<const TX*>(p.dy) + c;
-  const TB* dh = static_cast<const TB*>(p.dh) + c;
-  TX* dx = static_cast<TX*>(p.dx) + c;
-  TB* db = static_cast<TB*>(p.db) + c;
-
-  float gate[8], gain[8], post[8], acc[4][8];
+  constexpr int F = four_step<TX>();
+  const Lane<V, F> at(s, p.C, smem);
+  const bool normed = p.norm != SPARGE_NORM_NONE, has_b = p.b != nullptr;
+  const bool has_dy = p.dy != nullptr, has_dh = p.dh != nullptr;
+  F8 acc[SUMS][V];  // gate, scale, shift, post
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    gate[i] = gain[i] = post[i] = 1.f;
+  for (int k = 0; k < SUMS; ++k) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k][i] = 0.f;
+    for (int v = 0; v < V; ++v) acc[k][v] = f8(0.f);
   }
-  if (p.post != nullptr && active) load_f32x8(p.post + c, post);
+  // What is never loaded is zero: absent inputs, threads behind the last channel.
+  if (!(at.all && normed && has_b && has_dy && has_dh)) {
+    for (int k = 0; k < S * PIECES; ++k) at.ring[k] = make_uint4(0, 0, 0, 0);
+  }
 
   const int nslots = gridDim.x * per_cta, slot = blockIdx.x * per_cta + s.index;
-  bool first_item = true;
-  for (int item = slot; item < p.items; item += nslots) {
-    const int g = item / p.parts, part = item - g * p.parts;
-    const int begin = min(p.R, part * p.part_rows), end = min(p.R, begin + p.part_rows);
-    if (active && p.gate != nullptr && (first_item || p.gate_ld != 0))
-      load_f32x8(p.gate + g * p.gate_ld + c, gate);
-    if (active && p.scale != nullptr && (first_item || p.scale_ld != 0)) {
-      load_f32x8(p.scale + g * p.scale_ld + c, gain);
-      if (p.unit) {
+  ItemWalk ahead = {slot, 0, 0, 0};
+  ahead.open(p, T);
+  ItemWalk now = ahead;
+  const TX* x = static_cast<const TX*>(p.x) + at.c;
+  const TB* b = static_cast<const TB*>(p.b) + at.c;
+  const TX* dy = static_cast<const TX*>(p.dy) + at.c;
+  const TB* dh = static_cast<const TB*>(p.dh) + at.c;
+  const auto issue = [&](Ring stage) {
+    if (ahead.item < p.items) {
+      int64_t o = static_cast<int64_t>(ahead.row) * p.C;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) gain[i] += 1.f;
+      for (int t = 0; t < T; ++t) {
+        if (ahead.row + t < ahead.end) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const Ring dst = stage + (t * V + v) * ROW;
+            const int64_t ov = o + v * at.far;
+            if (normed) stage_fours<F>(dst, x + ov, at.lo[v], at.hi[v]);
+            if (has_b) stage_fours<F>(dst + XQ, b + ov, at.lo[v], at.hi[v]);
+            if (has_dy) stage_fours<F>(dst + XQ + BQ, dy + ov, at.lo[v], at.hi[v]);
+            if (has_dh) stage_fours<F>(dst + 2 * XQ + BQ, dh + ov, at.lo[v], at.hi[v]);
+          }
+        }
+        o += p.C;
+      }
+      ahead.next(p, T, nslots);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < S; ++k) issue(at.ring + k * STAGE);
+
+  // The row's mean, 1/deviation and branch 1/rms, one step ahead.
+  float mean_n[T], rstd_n[T], rb_n[T];
+  const auto fetch = [&](const ItemWalk& w) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      mean_n[t] = rstd_n[t] = 0.f;
+      rb_n[t] = 1.f;
+      if (w.item < p.items && w.row + t < w.end) {
+        if (p.norm == SPARGE_NORM_LAYER) mean_n[t] = p.stats[w.row + t];
+        if (normed) rstd_n[t] = p.stats[p.M + w.row + t];
+        if (POST) rb_n[t] = p.stats[2 * static_cast<int64_t>(p.M) + w.row + t];
       }
     }
-    first_item = false;
-    for (int first = begin; first < end; first += T) {
-      const int rows = min(T, end - first);
-      const int64_t row0 = static_cast<int64_t>(g) * p.R + first;
-      Raw8<TX> rx[T], rdy[T];
-      Raw8<TB> rb[T], rdh[T];
-      float mean[T], rstd[T], rbs[T];
+  };
+  fetch(now);
+
+  const float* gate_row = (p.gate != nullptr ? p.gate : g_zeros);
+  const float* scale_row = (p.scale != nullptr ? p.scale : g_zeros);
+  const float plus = p.unit || p.scale == nullptr ? 1.f : 0.f;
+  const float gate_plus = p.gate == nullptr ? 1.f : 0.f;
+  const float one_mean = p.norm == SPARGE_NORM_LAYER ? p.inv_c : 0.f;
+  Mod<V> gate, gain, post;
+  if (POST) post.open(p.post, 0.f, at.mod);
+  int group = -1;
+  int k = 0;
+  while (now.item < p.items) {
+    const int item = now.item, rows = min(T, now.end - now.row), row = now.row;
+    if (now.g != group) {
+      group = now.g;
+      gate.open(gate_row + group * p.gate_ld, gate_plus, at.mod);
+      gain.open(scale_row + group * p.scale_ld, plus, at.mod);
+    }
+    float mean[T], rstd[T], rb[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) mean[t] = mean_n[t], rstd[t] = rstd_n[t], rb[t] = rb_n[t];
+    now.next(p, T, nslots);
+    fetch(now);
+    cp_async_wait<S - 1>();
+    const Ring stage = at.ring + k * STAGE;
+    k = k + 1 == S ? 0 : k + 1;
+
+    F8 z[T * V], d[T * V];
+    float sums[2 * T] = {};
+    if (normed) {
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        const bool ok = active && t < rows;
-        const int64_t at = (row0 + t) * p.C;
-        rx[t] = ok && p.norm ? load8(x + at) : zero8<TX>();
-        rb[t] = ok && p.b != nullptr ? load8(b + at) : zero8<TB>();
-        rdy[t] = ok && p.dy != nullptr ? load8(dy + at) : zero8<TX>();
-        rdh[t] = ok && p.dh != nullptr ? load8(dh + at) : zero8<TB>();
-        mean[t] = rstd[t] = rbs[t] = 0.f;
-        if (t < rows) {
-          if (p.norm == SPARGE_NORM_LAYER) mean[t] = p.stats[row0 + t];
-          if (p.norm) rstd[t] = p.stats[p.M + row0 + t];
-          if (p.post != nullptr) rbs[t] = p.stats[2 * static_cast<int64_t>(p.M) + row0 + t];
+        const F8 m = f8(-mean[t]), r = f8(rstd[t]);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int i = t * V + v;
+          const Ring src = stage + i * ROW;
+          F8 y = unstage<TX>(src);
+          if (has_b) {
+            F8 n = unstage<TB>(src + XQ);
+            if (POST) n = mul(mul(n, f8(rb[t])), post.get(v, at.mod));
+            y = fma(gate.get(v, at.mod, gate_plus), n, y);
+          }
+          z[i] = mul(add(y, m), r);
+          const F8 h = unstage<TB>(src + 2 * XQ + BQ);
+          d[i] = mul(h, gain.get(v, at.mod, plus));
+          if (t < rows) {
+            acc[1][v] = fma(h, z[i], acc[1][v]);
+            acc[2][v] = add(acc[2][v], h);
+          }
+          sums[2 * t] += total(d[i]);
+          sums[2 * t + 1] += dot(d[i], z[i]);
         }
       }
-      float z[T][8], d[T][8], sums[2 * T];
+      slot_sum(s, sums);
+    }
+    float e[T];
+    int64_t o = static_cast<int64_t>(row) * p.C + at.c;
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
-        float n[8], q[8];
-        unpack8(rx[t], z[t]);
-        unpack8(rb[t], n);
-        unpack8(rdh[t], q);
-        const float scale_b = p.post != nullptr ? rbs[t] : 1.f;
-        sums[2 * t] = sums[2 * t + 1] = 0.f;
+    for (int t = 0; t < T; ++t) {
+      e[t] = 0.f;
+      if (t < rows) {
+        const F8 c1 = f8(-sums[2 * t] * one_mean), c2 = f8(-sums[2 * t + 1] * p.inv_c);
+        const F8 r = f8(rstd[t]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y = p.b != nullptr ? fmaf(gate[i], n[i] * (scale_b * post[i]), z[t][i]) : z[t][i];
-          z[t][i] = p.norm ? (y - mean[t]) * rstd[t] : 0.f;
-          d[t][i] = q[i] * gain[i];
-          acc[1][i] += q[i] * z[t][i];
-          acc[2][i] += q[i];
-          sums[2 * t] += d[t][i];
-          sums[2 * t + 1] += d[t][i] * z[t][i];
-        }
-      }
-      if (p.norm) slot_sum(s, sums);
-      float e[T];
-#pragma unroll
-      for (int t = 0; t < T; ++t) {
-        const float c1 = p.norm == SPARGE_NORM_LAYER ? sums[2 * t] * p.inv_c : 0.f;
-        const float c2 = sums[2 * t + 1] * p.inv_c;
-        float v[8];
-        unpack8(rdy[t], v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[t][i] = fmaf(rstd[t], d[t][i] - c1 - z[t][i] * c2, v[i]);
-        if (active && t < rows) store8(dx + (row0 + t) * p.C, d[t]);
-        if (p.b != nullptr) {
-          unpack8(rb[t], v);
-          e[t] = 0.f;
-          if (p.post != nullptr) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float bh = v[i] * rbs[t];
-              acc[0][i] += d[t][i] * (bh * post[i]);
-              const float en = d[t][i] * gate[i];
-              acc[3][i] += en * bh;
-              d[t][i] = en * post[i];
-              e[t] += d[t][i] * bh;
-            }
+        for (int v = 0; v < V; ++v) {
+          const int i = t * V + v;
+          const Ring src = stage + i * ROW;
+          const F8 g = unstage<TX>(src + XQ + BQ);
+          d[i] = normed ? fma(r, fma(z[i], c2, add(d[i], c1)), g) : g;
+          put<F>(static_cast<TX*>(p.dx) + o + v * at.far, d[i], at.lo[v], at.hi[v]);
+          if (!has_b) continue;
+          const F8 b8 = unstage<TB>(src + XQ);
+          if (POST) {
+            const F8 bh = mul(b8, f8(rb[t])), w = post.get(v, at.mod);
+            acc[0][v] = fma(d[i], mul(bh, w), acc[0][v]);
+            d[i] = mul(d[i], gate.get(v, at.mod, gate_plus));
+            acc[SUMS - 1][v] = fma(d[i], bh, acc[SUMS - 1][v]);
+            d[i] = mul(d[i], w);
+            e[t] += dot(d[i], bh);  // bh is 0 behind the last channel
           } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              acc[0][i] += d[t][i] * v[i];
-              d[t][i] *= gate[i];
-            }
-            if (active && t < rows) store8(db + (row0 + t) * p.C, d[t]);
+            acc[0][v] = fma(d[i], b8, acc[0][v]);
+            d[i] = mul(d[i], gate.get(v, at.mod, gate_plus));
+            put<F>(static_cast<TB*>(p.db) + o + v * at.far, d[i], at.lo[v], at.hi[v]);
           }
         }
       }
-      if (p.post != nullptr) {
-        slot_sum(s, e);
+      o += p.C;
+    }
+    if (POST) {
+      slot_sum(s, e);
+      o = static_cast<int64_t>(row) * p.C + at.c;
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-          float v[8];
-          unpack8(rb[t], v);
+      for (int t = 0; t < T; ++t) {
+        if (t < rows) {
+          const F8 r = f8(rb[t]), c3 = f8(-e[t] * p.inv_c * rb[t]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            d[t][i] = rbs[t] * (d[t][i] - v[i] * rbs[t] * (e[t] * p.inv_c));
-          if (active && t < rows) store8(db + (row0 + t) * p.C, d[t]);
+          for (int v = 0; v < V; ++v) {
+            const int i = t * V + v;
+            const F8 b8 = unstage<TB>(stage + i * ROW + XQ);
+            put<F>(static_cast<TB*>(p.db) + o + v * at.far, mul(fma(b8, c3, d[i]), r), at.lo[v],
+                   at.hi[v]);
+          }
+        }
+        o += p.C;
+      }
+    }
+    issue(stage);
+
+    if (now.item != item) {  // the item's last rows
+#pragma unroll
+      for (int j = 0; j < SUMS; ++j) {
+        if (!p.by_group[j]) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (p.sum[j] != nullptr)
+            put<F>(p.sum[j] + static_cast<int64_t>(item) * p.C + at.c + v * at.far, acc[j][v],
+                   at.lo[v], at.hi[v]);
+          acc[j][v] = f8(0.f);
         }
       }
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (!p.by_group[k]) continue;
-      if (active && p.sum[k] != nullptr)
-        store8(p.sum[k] + static_cast<int64_t>(item) * p.C + c, acc[k]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[k][i] = 0.f;
-    }
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (!p.by_group[k] && active && p.sum[k] != nullptr)
-      store8(p.sum[k] + static_cast<int64_t>(slot) * p.C + c, acc[k]);
+  for (int j = 0; j < SUMS; ++j) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!p.by_group[j] && p.sum[j] != nullptr)
+        put<F>(p.sum[j] + static_cast<int64_t>(slot) * p.C + at.c + v * at.far, acc[j][v],
+               at.lo[v], at.hi[v]);
+    }
   }
 }
 
 struct ResnormPlan {
-  int W, per_cta, threads, ctas, slots;
-  int tier;
+  int V, W, per_cta, threads, ctas, slots, smem;
   int groups, R;
-  int items, parts, part_rows;
+  int items, parts;  // items = groups * parts
   // backward: a sum is written per item straight to the output (one part a
   // group), per item to the workspace, or per slot to the workspace
   bool wanted[4], by_group[4];
   size_t off[4], bytes;
 };
 
+template <typename TX, typename TB, int V>
+int ring_bytes(bool bwd) {
+  return 16 * (bwd ? bwd_stages<TX, TB, V>() * bwd_pieces<TX, TB, V>()
+                              : kFwdStages * fwd_pieces<TX, TB, V>());
+}
+template <typename TX, typename TB>
+int ring_bytes_of(int V, bool bwd) {
+  return V == 1 ? ring_bytes<TX, TB, 1>(bwd) : ring_bytes<TX, TB, 2>(bwd);
+}
+
 ResnormPlan resnorm_plan(const sparge_resnorm& a, bool bwd) {
   ResnormPlan pl = {};
   const int64_t M = a.rows;
-  pl.W = slot_warps(a.C);
+  pl.V = row_vectors(a.C);
+  pl.W = slot_warps(a.C, pl.V);
   pl.per_cta = slots_per_cta(pl.W);
   pl.threads = pl.W * pl.per_cta * 32;
-  pl.tier = tier_of(pl.threads);
+  const int ring = a.x_type == SPARGE_BF16 ? ring_bytes_of<__nv_bfloat16, __nv_bfloat16>(pl.V, bwd)
+                   : a.branch_type == SPARGE_BF16 ? ring_bytes_of<float, __nv_bfloat16>(pl.V, bwd)
+                                                  : ring_bytes_of<float, float>(pl.V, bwd);
+  pl.smem = ring * pl.threads;
   int groups = 1;
   if (a.gate) groups = std::max(groups, a.gate_groups);
   if (a.scale) groups = std::max(groups, a.scale_groups);
   if (a.shift) groups = std::max(groups, a.shift_groups);
   pl.groups = groups;
   pl.R = static_cast<int>(M / groups);
-  const int T = bwd ? kTiers[pl.tier].bwd_rows : kTiers[pl.tier].fwd_rows;
-  const int per_sm = std::max(1, 1024 / pl.threads);
+  const int T = bwd ? (pl.V == 1 ? RB_T : 1) : (RF_T >= pl.V ? RF_T / pl.V : 1);
+  // A grid that is resident as a whole: shared memory limits it, or registers
+  // (at most 80 a thread forward, 128 backward).
+  const int per_sm = std::max(1, std::min(65536 / ((bwd ? 65536 / 256 / RB_B / 8 * 8 > 128 ? 128 : 65536 / 256 / RB_B / 8 * 8 : 65536 / 256 / RF_B / 8 * 8 > 128 ? 128 : 65536 / 256 / RF_B / 8 * 8) * pl.threads),
+                                          kSmemPerSm / (pl.smem + kSmemOfCta)));
   const int64_t most = static_cast<int64_t>(kSMs) * per_sm;
-  if (!bwd) {
-    const int64_t units = static_cast<int64_t>(groups) * ((pl.R + T - 1) / T);
-    pl.ctas = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>(most, (units + pl.per_cta - 1) / pl.per_cta)));
-    return pl;
-  }
   const int64_t target = most * pl.per_cta;  // slots that fill the machine
   const int64_t units = (pl.R + T - 1) / T;
-  int64_t parts = std::max<int64_t>(1, std::min<int64_t>(units, target / groups));
-  pl.part_rows = static_cast<int>((units + parts - 1) / parts) * T;
-  pl.parts = (pl.R + pl.part_rows - 1) / pl.part_rows;
+  pl.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(units, target / groups)));
   pl.items = groups * pl.parts;
   pl.ctas = static_cast<int>(std::max<int64_t>(
       1, std::min<int64_t>(most, (static_cast<int64_t>(pl.items) + pl.per_cta - 1) / pl.per_cta)));
   pl.slots = pl.ctas * pl.per_cta;
+  if (!bwd) return pl;
   const void* const out[4] = {a.dgate, a.dscale, a.dshift, a.dpost};
   const int out_groups[4] = {a.gate_groups, a.scale_groups, a.shift_groups, 1};
   for (int k = 0; k < 4; ++k) {
@@ -465,26 +787,30 @@ ResnormParams resnorm_params(const sparge_resnorm& a, const ResnormPlan& pl, boo
   p.inv_c = 1.f / a.C;
   p.items = pl.items;
   p.parts = pl.parts;
-  p.part_rows = pl.part_rows;
   return p;
 }
 
-template <typename TX, typename TB, int I>
-void launch_tier(const ResnormParams& p, const ResnormPlan& pl, bool bwd, cudaStream_t st) {
-  constexpr Tier t = kTiers[I];
-  if (bwd)
-    resnorm_bwd_kernel<TX, TB, t.bwd_rows, t.threads><<<pl.ctas, pl.threads, 0, st>>>(p);
-  else
-    resnorm_fwd_kernel<TX, TB, t.fwd_rows, t.threads><<<pl.ctas, pl.threads, 0, st>>>(p);
+template <typename TX, typename TB, int V>
+cudaError_t launch_form(const ResnormParams& p, const ResnormPlan& pl, bool bwd, cudaStream_t st) {
+  auto* kernel = !bwd                ? resnorm_fwd_kernel<TX, TB, V>
+                 : p.post != nullptr ? resnorm_bwd_kernel<TX, TB, V, true>
+                                     : resnorm_bwd_kernel<TX, TB, V, false>;
+  if (pl.smem > 47 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
+    if (e != cudaSuccess) {
+      cudaGetLastError();  // the next launch must not report it
+      return e;
+    }
+  }
+  kernel<<<pl.ctas, pl.threads, pl.smem, st>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename TX, typename TB>
 cudaError_t launch_resnorm(const ResnormParams& p, const ResnormPlan& pl, bool bwd,
                            cudaStream_t st) {
-  if (pl.tier == 0) launch_tier<TX, TB, 0>(p, pl, bwd, st);
-  if (pl.tier == 1) launch_tier<TX, TB, 1>(p, pl, bwd, st);
-  if (pl.tier == 2) launch_tier<TX, TB, 2>(p, pl, bwd, st);
-  return cudaGetLastError();
+  return pl.V == 1 ? launch_form<TX, TB, 1>(p, pl, bwd, st) : launch_form<TX, TB, 2>(p, pl, bwd, st);
 }
 
 cudaError_t dispatch_resnorm(const sparge_resnorm& a, const ResnormParams& p,

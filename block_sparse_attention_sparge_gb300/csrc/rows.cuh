@@ -2,11 +2,16 @@
 // layout kernels and the residual norm kernels).
 //
 // A slot is a group of W warps that owns one row (token) of C channels at a
-// time, eight consecutive channels to a thread, so per-channel operands
-// (weights, gates, scales) and per-channel sums stay in its registers from row
-// to row.  A slot takes T rows at once: their loads are all in flight together
-// and one barrier serves the sums of all T.  Slots of one CTA are independent
-// of one another: each has its own named barrier, or none when W is 1.
+// time, V times eight consecutive channels to a thread, so per-channel
+// operands (weights, gates, scales) and per-channel sums stay with the thread
+// from row to row.  A slot takes T rows at once: one barrier serves the sums of
+// all T.  Slots of one CTA are independent of one another: each has its own
+// named barrier, or none when W is 1.
+//
+// Rows come in through a ring of shared-memory stages that every thread fills
+// for itself (cp.async of its own channels) and alone reads: bytes stay in
+// flight while earlier rows are computed, without registers to hold them and
+// without a barrier.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -18,23 +23,19 @@
 namespace sparge {
 
 constexpr int kSMs = 152;              // of a GB300: sizes grids and workspaces
-constexpr int kMaxRowChannels = 8192;  // 32 warps of 8 channels a thread
+constexpr int kSmemPerSm = 228 * 1024;  // shared memory of an SM
+constexpr int kSmemOfCta = 3 * 1024;    // of it a row kernel's CTA takes beside its ring, at most
+constexpr int kMaxRowChannels = 8192;
 constexpr int kMaxSlots = 8;           // per CTA; named barriers 1 .. 8
 
+// Channels of a thread, in eights: 1 up to 2048 channels (CTAs of at most 256
+// threads), 2 above (at most 512), so a wide row keeps several CTAs on an SM.
+inline int row_vectors(int C) { return C <= 2048 ? 1 : 2; }
+constexpr int row_threads(int V) { return V == 1 ? 256 : 512; }
 // Warps of one slot, and slots of one CTA: enough to make 8 warps of a CTA
 // where a row needs fewer.
-__host__ __device__ inline int slot_warps(int C) { return (C + 255) / 256; }
+__host__ __device__ inline int slot_warps(int C, int V) { return (C + 256 * V - 1) / (256 * V); }
 __host__ __device__ inline int slots_per_cta(int W) { return W >= kMaxSlots ? 1 : kMaxSlots / W; }
-
-// A kernel is built for three sizes of CTA (threads, rows a slot takes at
-// once): the registers of a thread shrink as rows get wider.
-struct Tier {
-  int threads, fwd_rows, bwd_rows;
-};
-constexpr Tier kTiers[3] = {{256, 4, 2}, {640, 2, 1}, {1024, 1, 1}};
-inline int tier_of(int threads) {
-  return threads <= kTiers[0].threads ? 0 : threads <= kTiers[1].threads ? 1 : 2;
-}
 
 struct Slot {
   int index;    // in the CTA
@@ -45,12 +46,14 @@ struct Slot {
 };
 
 // Floats one warp contributes to a slot reduction, at most.
-constexpr int kSlotRed = 8;
-constexpr int kSlotRedFloats = 2 * 32 * kSlotRed;  // of a CTA of at most 32 warps
+constexpr int kSlotRed = 4;
+constexpr int kSlotRedFloats = 2 * 16 * kSlotRed;  // of a CTA of at most 16 warps
 
 SPARGE_DEV Slot make_slot(int W, float* red) {
   Slot s;
-  const int warp = threadIdx.x >> 5;
+  // The shuffle tells the compiler that the warp's index is the same in all
+  // lanes, so what follows from it is computed once for the warp.
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
   s.lane = threadIdx.x & 31;
   s.index = warp / W;
   s.W = W;
@@ -68,31 +71,95 @@ SPARGE_DEV void slot_sync(const Slot& s) {
     named_barrier_sync(1 + s.index, s.W * 32);
 }
 
-// Sums v[0..K) over the slot's threads; every thread gets the sums.  The two
-// halves of `red` alternate, so one barrier a call is enough: a warp cannot
-// reach the next but one call before every warp has read this one's sums.
+// Sums v[0..K) over the warp, K a power of two: each step halves the values a
+// lane carries while it doubles the lanes behind each, so K sums take K + 4 or
+// so shuffles instead of 5 K.  The sum of v[k] ends in the lanes l with
+// l / (32 / K) == k.
 template <int K>
-SPARGE_DEV void slot_sum(Slot& s, float (&v)[K]) {
-  static_assert(K <= kSlotRed, "reduction buffer");
+SPARGE_DEV float warp_sums(const float (&in)[K], int lane) {
+  static_assert(K == 1 || K == 2 || K == 4 || K == 8, "power of two");
+  float v[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
+  for (int k = 0; k < K; ++k) v[k] = in[k];
+  int o = 16;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  for (int m = K / 2; m >= 1; m /= 2, o /= 2) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int k = 0; k < m; ++k) {
+      const float keep = upper ? v[m + k] : v[k], send = upper ? v[k] : v[m + k];
+      v[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
   }
-  if (s.W == 1) return;
+#pragma unroll
+  for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
+}
+
+// K floats of every warp of the slot, from the lanes that warp_sums leaves them
+// in, to every thread: out[w * kSlotRed + k].  The two halves of `red`
+// alternate, so one barrier a call is enough: a warp cannot reach the next but
+// one call before every warp has read this one's values.
+template <int K>
+SPARGE_DEV const float* slot_exchange(Slot& s, float mine) {
+  static_assert(K <= kSlotRed, "reduction buffer");
   float* red = s.red + s.phase * s.W * kSlotRed;
   s.phase ^= 1;
-  if (s.lane == 0) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) red[s.warp * kSlotRed + k] = v[k];
-  }
+  if (s.lane % (32 / K) == 0) red[s.warp * kSlotRed + s.lane / (32 / K)] = mine;
   slot_sync(s);
+  return red;
+}
+
+// Sums v[0..K) over the slot's threads; every thread gets the sums.
+template <int K>
+SPARGE_DEV void slot_sum(Slot& s, float (&v)[K]) {
+  const float mine = warp_sums(v, s.lane);
+  if (s.W == 1) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, mine, k * (32 / K));
+    return;
+  }
+  const float* red = slot_exchange<K>(s, mine);
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = 0.f;
   for (int w = 0; w < s.W; ++w) {
+    if constexpr (K == 4) {
+      const float4 r = *reinterpret_cast<const float4*>(red + w * kSlotRed);
+      v[0] += r.x, v[1] += r.y, v[2] += r.z, v[3] += r.w;
+    } else if constexpr (K == 2) {
+      const float2 r = *reinterpret_cast<const float2*>(red + w * kSlotRed);
+      v[0] += r.x, v[1] += r.y;
+    } else {
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += red[w * kSlotRed + k];
+      for (int k = 0; k < K; ++k) v[k] += red[w * kSlotRed + k];
+    }
   }
+}
+
+// ------------------------------------------------------ stages of a thread
+SPARGE_DEV void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+SPARGE_DEV void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+SPARGE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+SPARGE_DEV void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// A thread's pieces of 16 bytes, `pitch` (the threads of the CTA) apart, so the
+// pieces that a warp copies lie side by side.  (Laid out thread by thread
+// instead, a copy of two bf16 tensors into a third runs at 4.1 TB/s, not 6.3.)
+struct Ring {
+  uint4* p;
+  int pitch;
+  SPARGE_DEV Ring operator+(int k) const { return {p + k * pitch, pitch}; }
+  SPARGE_DEV uint4& operator[](int k) const { return p[k * pitch]; }
+};
+template <typename T>
+constexpr int pieces8() {  // pieces of eight values
+  return static_cast<int>(sizeof(T)) / 2;
 }
 
 // ------------------------------------------------- eight values of a thread
@@ -107,39 +174,12 @@ struct Raw8<float> {
   uint4 v[2];
 };
 
-SPARGE_DEV uint2 ldg8_no_l1(const void* ptr) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(ptr));
-  return v;
-}
-
 // Eight consecutive values (16-byte aligned), read once.
 template <typename T>
 SPARGE_DEV Raw8<T> load8(const T* p) {
   Raw8<T> r;
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-    r.v[i] = ldg_no_l1(reinterpret_cast<const uint4*>(p) + i);
-  return r;
-}
-
-// Four values at p and four at q.
-SPARGE_DEV Raw8<__nv_bfloat16> load4x2(const __nv_bfloat16* p, const __nv_bfloat16* q) {
-  const uint2 a = ldg8_no_l1(p), b = ldg8_no_l1(q);
-  return {{make_uint4(a.x, a.y, b.x, b.y)}};
-}
-SPARGE_DEV Raw8<float> load4x2(const float* p, const float* q) {
-  return {{ldg_no_l1(reinterpret_cast<const uint4*>(p)),
-           ldg_no_l1(reinterpret_cast<const uint4*>(q))}};
-}
-
-template <typename T>
-SPARGE_DEV Raw8<T> zero8() {
-  Raw8<T> r;
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) r.v[i] = make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < pieces8<T>(); ++i) r.v[i] = ldg_no_l1(reinterpret_cast<const uint4*>(p) + i);
   return r;
 }
 
@@ -170,10 +210,13 @@ SPARGE_DEV Raw8<float> pack8(const float (&f)[8], float) {
 }
 
 template <typename T>
-SPARGE_DEV void store8(T* p, const float (&f)[8]) {
-  const Raw8<T> r = pack8(f, T());
+SPARGE_DEV void store_raw8(T* p, const Raw8<T>& r) {
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = r.v[i];
+  for (int i = 0; i < pieces8<T>(); ++i) reinterpret_cast<uint4*>(p)[i] = r.v[i];
+}
+template <typename T>
+SPARGE_DEV void store8(T* p, const float (&f)[8]) {
+  store_raw8(p, pack8(f, T()));
 }
 SPARGE_DEV void store4x2(__nv_bfloat16* p, __nv_bfloat16* q, const float (&f)[8]) {
   const Raw8<__nv_bfloat16> r = pack8(f, __nv_bfloat16());
@@ -184,6 +227,29 @@ SPARGE_DEV void store4x2(float* p, float* q, const float (&f)[8]) {
   const Raw8<float> r = pack8(f, 0.f);
   *reinterpret_cast<uint4*>(p) = r.v[0];
   *reinterpret_cast<uint4*>(q) = r.v[1];
+}
+
+// Eight values into the ring at dst, and back out: in a row at p, or four at p
+// and four at q.
+template <typename T>
+SPARGE_DEV void stage8(Ring dst, const T* p) {
+#pragma unroll
+  for (int i = 0; i < pieces8<T>(); ++i) cp_async16(&dst[i], reinterpret_cast<const uint4*>(p) + i);
+}
+SPARGE_DEV void stage4x2(Ring dst, const __nv_bfloat16* p, const __nv_bfloat16* q) {
+  cp_async8(&dst[0], p);
+  cp_async8(reinterpret_cast<uint2*>(&dst[0]) + 1, q);
+}
+SPARGE_DEV void stage4x2(Ring dst, const float* p, const float* q) {
+  cp_async16(&dst[0], p);
+  cp_async16(&dst[1], q);
+}
+template <typename T>
+SPARGE_DEV Raw8<T> unstage8(Ring src) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < pieces8<T>(); ++i) r.v[i] = src[i];
+  return r;
 }
 
 // ------------------------------------------------------- sums of partial rows
