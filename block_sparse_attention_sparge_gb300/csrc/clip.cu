@@ -10,10 +10,11 @@
 //
 // A thread squares and adds 32 values in fp32, then adds that to an fp64 sum.
 // Where the fp32 sum left the range in which no square that matters over- or
-// underflows (below 2^-90 or above 2^126), those 32 values are done again in
-// fp64, so gradients of any size that fp32 holds give a finite norm of full
-// precision.  An fp64 operation for every value instead would cap the pass
-// below the memory's rate (fp64 runs at 1/60 of the fp32 rate here).
+// underflows (below 2^-90 or above 2^126), those values are read again and done
+// in fp64, so gradients of any size that fp32 holds give a norm of full
+// precision.  fp64 runs at 1/60 of the fp32 rate here (a warp's addition takes
+// the pipe some 15 cycles): an operation for every value would cap the pass
+// below the memory's rate, and even the last sums are left to single warps.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -30,9 +31,9 @@ namespace sparge {
 
 namespace {
 
-constexpr int kClipThreads = 512;
+constexpr int kClipThreads = 256;
 constexpr int kChunk = kClipThreads * 32;  // values a CTA takes at a time
-constexpr int kClipCtas = kSMs * 4;        // sums of one launch in the workspace
+constexpr int kClipCtas = kSMs * 6;        // sums of one launch in the workspace
 constexpr int kSmallList = 48, kLargeList = 1024;  // tensors of one launch
 
 // A list of tensors as a kernel parameter (27.7 KB of the 32 KB there is for
@@ -55,148 +56,177 @@ struct ClipArgs {
   int in_place;
 };
 
-// The tensor that owns chunk c, by bisection of the chunk starts.
+// A chunk: values [base, base + left) of tensor i, or the first kChunk of them.
+struct Chunk {
+  int i;
+  int64_t base, left;
+};
+
+// Finds chunk c by bisection of the chunk starts, among tensors [lo, hi).
 template <int MAX>
-SPARGE_DEV int owner(const ClipList<MAX>& l, uint32_t c) {
-  int lo = 0, hi = l.n;
+SPARGE_DEV Chunk find(const ClipList<MAX>& l, uint32_t c, int lo, int hi) {
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (l.chunk[mid] <= c) lo = mid;
     else hi = mid;
   }
-  return lo;
+  const int64_t base = static_cast<int64_t>(c - l.chunk[lo]) * kChunk;
+  return {lo, base, l.numel[lo] - base};
 }
 
-SPARGE_DEV double sum_squares(const float (&v)[32]) {
-  uint64_t a = 0, b = 0;
+// Sum of the squares of eight values.
+SPARGE_DEV void square8(const float (&f)[8], uint64_t& a, uint64_t& b) {
+  const uint64_t p = f32x2(f[0], f[1]), q = f32x2(f[2], f[3]);
+  const uint64_t r = f32x2(f[4], f[5]), s = f32x2(f[6], f[7]);
+  a = ffma2(p, p, a);
+  b = ffma2(q, q, b);
+  a = ffma2(r, r, a);
+  b = ffma2(s, s, b);
+}
+
+// Eight values of the chunk from place `at`, zeros behind its end.
+template <typename T>
+SPARGE_DEV void load_edge(const T* in, int at, int64_t left, float (&f)[8]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const uint64_t p = f32x2(v[i], v[i + 1]), q = f32x2(v[i + 2], v[i + 3]);
-    a = ffma2(p, p, a);
-    b = ffma2(q, q, b);
+  for (int i = 0; i < 8; ++i) f[i] = at + i < left ? static_cast<float>(in[at + i]) : 0.f;
+}
+
+// This thread's 32 values of a chunk: four groups of eight consecutive ones.
+// `ahead` runs while the loads are in flight.
+template <typename T, typename Ahead>
+SPARGE_DEV double chunk_squares(const T* in, int64_t left, const Ahead& ahead) {
+  uint64_t a = 0, b = 0;
+  if (left >= kChunk && (reinterpret_cast<uintptr_t>(in) & 15) == 0) {
+    Raw8<T> r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = load8(in + (k * kClipThreads + threadIdx.x) * 8);
+    ahead();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float f[8];
+      unpack8(r[k], f);
+      square8(f, a, b);
+    }
+  } else {
+    ahead();
+    for (int k = 0; k < 4; ++k) {
+      float f[8];
+      load_edge(in, (k * kClipThreads + threadIdx.x) * 8, left, f);
+      square8(f, a, b);
+    }
   }
   a = fadd2(a, b);
   const float s = f32x2_lo(a) + f32x2_hi(a);
   if (s > 8.0779357e-28f && s < 8.5070592e37f) return s;  // 2^-90, 2^126
-  uint32_t any = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) any |= __float_as_uint(v[i]) & 0x7fffffffu;
-  if (any == 0) return 0.0;
+  // All zeros need no second look; squares that vanished do.
   double d = 0.0;
-#pragma unroll 1
-  for (int i = 0; i < 32; ++i) {
-    // a dynamic index would send v to local memory
-    float x = 0.f;
-#pragma unroll
-    for (int k = 0; k < 32; ++k) x = k == i ? v[k] : x;
-    d += static_cast<double>(x) * static_cast<double>(x);
+  for (int k = 0; k < 4; ++k) {
+    float f[8];
+    load_edge(in, (k * kClipThreads + threadIdx.x) * 8, left, f);
+    for (int i = 0; i < 8; ++i) {
+      if (f[i] != 0.f) d += static_cast<double>(f[i]) * static_cast<double>(f[i]);
+    }
   }
   return d;
 }
 
-// 32 values of this thread from the chunk that starts at `base`: four groups
-// of eight consecutive ones, zeros behind the end.
-template <typename T>
-SPARGE_DEV void load_chunk(const T* in, int64_t left, bool wide, float (&v)[32]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int at = (k * kClipThreads + threadIdx.x) * 8;
-    float f[8];
-    if (wide && at + 8 <= left) {
-      unpack8(load8(in + at), f);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = at + i < left ? static_cast<float>(in[at + i]) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[8 * k + i] = f[i];
-  }
-}
-
-// Sum over the CTA's threads, the same bits in every thread.
-SPARGE_DEV double cta_sum(double v, double* red) {
+SPARGE_DEV double warp_sum(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = 0.0;
-#pragma unroll
-  for (int w = 0; w < kClipThreads / 32; ++w) s += red[w];
-  return s;
+  return v;
 }
 
 template <int MAX>
-__global__ void __launch_bounds__(kClipThreads, 2) clip_norm_kernel(
+__global__ void __launch_bounds__(kClipThreads, 5) clip_norm_kernel(
     const __grid_constant__ ClipList<MAX> l, double* sums) {
   __shared__ double red[kClipThreads / 32];
   grid_launch_dependents();
+  const uint32_t total = l.chunk[l.n];
   double acc = 0.0;
-  for (uint32_t c = blockIdx.x; c < l.chunk[l.n]; c += gridDim.x) {
-    const int i = owner(l, c);
-    const int64_t base = static_cast<int64_t>(c - l.chunk[i]) * kChunk;
-    const int64_t left = l.numel[i] - base;
-    const bool wide = (reinterpret_cast<uintptr_t>(l.in[i]) & 15) == 0;
-    float v[32];
-    if (l.bf16[i])
-      load_chunk(static_cast<const __nv_bfloat16*>(l.in[i]) + base, left, wide, v);
+  Chunk c = {};
+  if (blockIdx.x < total) c = find(l, blockIdx.x, 0, l.n);
+  for (uint32_t k = blockIdx.x; k < total; k += gridDim.x) {
+    const Chunk now = c;
+    const auto ahead = [&] {
+      if (k + gridDim.x < total) c = find(l, k + gridDim.x, now.i, l.n);
+    };
+    if (l.bf16[now.i])
+      acc += chunk_squares(static_cast<const __nv_bfloat16*>(l.in[now.i]) + now.base, now.left, ahead);
     else
-      load_chunk(static_cast<const float*>(l.in[i]) + base, left, wide, v);
-    acc += sum_squares(v);
+      acc += chunk_squares(static_cast<const float*>(l.in[now.i]) + now.base, now.left, ahead);
   }
-  acc = cta_sum(acc, red);
-  if (threadIdx.x == 0) sums[blockIdx.x] = acc;
+  acc = warp_sum(acc);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kClipThreads / 32; ++w) acc += red[w];
+    sums[blockIdx.x] = acc;
+  }
 }
 
-template <typename T>
-SPARGE_DEV void scale_chunk(const T* in, T* out, int64_t left, float c) {
-  const bool wide =
-      ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+template <typename T, typename Ahead>
+SPARGE_DEV void scale_chunk(const T* in, T* out, int64_t left, float c, const Ahead& ahead) {
+  if (left >= kChunk &&
+      ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
+    Raw8<T> r[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int at = (k * kClipThreads + threadIdx.x) * 8;
-    if (wide && at + 8 <= left) {
-      Raw8<T> r;
+    for (int k = 0; k < 4; ++k) {
+      const uint4* p = reinterpret_cast<const uint4*>(in + (k * kClipThreads + threadIdx.x) * 8);
 #pragma unroll
-      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-        r.v[i] = reinterpret_cast<const uint4*>(in + at)[i];
+      for (int i = 0; i < pieces8<T>(); ++i) r[k].v[i] = p[i];
+    }
+    ahead();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
       float f[8];
-      unpack8(r, f);
+      unpack8(r[k], f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] *= c;
-      store8(out + at, f);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (at + i < left) out[at + i] = static_cast<T>(static_cast<float>(in[at + i]) * c);
+      store8(out + (k * kClipThreads + threadIdx.x) * 8, f);
     }
+  } else {
+    ahead();
+    const int end = static_cast<int>(left < kChunk ? left : kChunk);
+    for (int at = threadIdx.x; at < end; at += kClipThreads)
+      out[at] = static_cast<T>(static_cast<float>(in[at]) * c);
   }
 }
 
 template <int MAX>
-__global__ void __launch_bounds__(kClipThreads, 2) clip_scale_kernel(
+__global__ void __launch_bounds__(kClipThreads, 5) clip_scale_kernel(
     const __grid_constant__ ClipList<MAX> l, const ClipArgs a) {
-  __shared__ double red[kClipThreads / 32];
-  grid_wait();
-  double v = 0.0;
-  for (int i = threadIdx.x; i < a.n_sums; i += kClipThreads) v += a.sums[i];
-  const double norm = sqrt(cta_sum(v, red));
-  if (a.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = static_cast<float>(norm);
-  if (a.max_norm < 0.f) return;  // the norm alone
-  const double ratio = static_cast<double>(a.max_norm) / (norm + static_cast<double>(a.eps));
-  const float c = ratio > 1.0 ? 1.f : static_cast<float>(ratio);  // NaN stays NaN
-  if (a.in_place && c == 1.f) return;
+  __shared__ float factor;
   const uint32_t total = l.chunk[l.n];
+  const bool writes = a.max_norm >= 0.f;
+  Chunk c = {};
+  if (writes && blockIdx.x < total) c = find(l, total - 1 - blockIdx.x, 0, l.n);
+  grid_wait();
+  if (threadIdx.x < 32) {
+    double v = 0.0;
+    for (int i = threadIdx.x; i < a.n_sums; i += 32) v += a.sums[i];
+    v = warp_sum(v);
+    if (threadIdx.x == 0) {
+      const double norm = sqrt(v);
+      if (a.norm != nullptr && blockIdx.x == 0) *a.norm = static_cast<float>(norm);
+      const double ratio = static_cast<double>(a.max_norm) / (norm + static_cast<double>(a.eps));
+      factor = ratio > 1.0 ? 1.f : static_cast<float>(ratio);  // NaN stays NaN
+    }
+  }
+  if (!writes) return;  // the norm alone
+  __syncthreads();
+  const float f = factor;
+  if (a.in_place && f == 1.f) return;
   for (uint32_t k = blockIdx.x; k < total; k += gridDim.x) {
-    const uint32_t ch = total - 1 - k;
-    const int i = owner(l, ch);
-    const int64_t base = static_cast<int64_t>(ch - l.chunk[i]) * kChunk;
-    const int64_t left = l.numel[i] - base;
-    if (l.bf16[i])
-      scale_chunk(static_cast<const __nv_bfloat16*>(l.in[i]) + base,
-                  static_cast<__nv_bfloat16*>(l.out[i]) + base, left, c);
+    const Chunk now = c;
+    const auto ahead = [&] {
+      if (k + gridDim.x < total) c = find(l, total - 1 - k - gridDim.x, 0, now.i + 1);
+    };
+    if (l.bf16[now.i])
+      scale_chunk(static_cast<const __nv_bfloat16*>(l.in[now.i]) + now.base,
+                  static_cast<__nv_bfloat16*>(l.out[now.i]) + now.base, now.left, f, ahead);
     else
-      scale_chunk(static_cast<const float*>(l.in[i]) + base, static_cast<float*>(l.out[i]) + base,
-                  left, c);
+      scale_chunk(static_cast<const float*>(l.in[now.i]) + now.base,
+                  static_cast<float*>(l.out[now.i]) + now.base, now.left, f, ahead);
   }
 }
 

@@ -36,7 +36,7 @@ struct HeadsPart {
   const void* w;
   void* y;  // head-major bf16: the result, or the gradient that comes back
   void* dx;
-  float* dw_part;  // [slots][H * d]
+  float* dw_part;  // [slots][H * d] or, under a norm over each head, [slots][d]
   int64_t xs[3], ds[3];
   int C, W, plain;
 };
@@ -302,10 +302,11 @@ SPARGE_DEV Pairs load_weight(const HeadsParams& p, const void* w, bool active, i
 
 // A thread's place in the rows of a part: vector v of V covers eight channels
 // of head `head + v * head_step`, from channel c of the head.
-template <bool SPLIT, int D, int V>
+template <bool SPLIT, int D, int V, bool FULL>
 struct Place {
   bool active[V];
   int head, head_step, c;
+  SPARGE_DEV bool here(int v) const { return FULL || active[v]; }
   SPARGE_DEV Place(const Slot& s, int C) {
     constexpr int L = D / 8;  // threads of one head
 #pragma unroll
@@ -316,63 +317,52 @@ struct Place {
   }
 };
 
-// One kernel for each direction, in two forms: JOINT takes Q, K and V (parts
-// 0, 1 and 2, any but one of which may be absent) of a token together, so the
-// angles are computed once for both and one barrier serves both sums; else a
-// part to each blockIdx.y, for parts of different head counts.
-template <bool JOINT>
+// One kernel for each direction, in three forms.  Joint: Q, K and V (parts 0, 1
+// and 2, any but one of which may be absent) of a token together, so the angles
+// are computed once for both and one barrier serves both sums.  Full: the same
+// where all three are there, turned and under a norm over the token, and no
+// thread is without channels, which takes every branch out of the row loop
+// (480p: 100 instead of 104 us forward, 138 instead of 160 us backward).
+// Single: a part to each blockIdx.y, for parts of different head counts.
+enum Form { kSingle, kJoint, kFull };
+template <int FORM>
 constexpr int turned_parts() {
-  return JOINT ? 2 : 1;
+  return FORM == kSingle ? 1 : 2;
 }
-template <bool JOINT>
+template <int FORM>
 constexpr int all_parts() {
-  return JOINT ? 3 : 1;
+  return FORM == kSingle ? 1 : 3;
 }
 
-#ifndef HF_S
-#define HF_S 3
-#endif
-#ifndef HF_T
-#define HF_T 2
-#endif
-#ifndef HF_B
-#define HF_B 2
-#endif
-#ifndef HB_S
-#define HB_S 4
-#endif
-#ifndef HB_B
-#define HB_B 2
-#endif
-// Stages of the ring.
-template <typename TX>
-constexpr int fwd_stages() {
-  return sizeof(TX) == 2 ? HF_S : 2;
-}
-template <typename TX>
-constexpr int bwd_stages() {
-  return sizeof(TX) == 2 ? HB_S : 3;
-}
+// Stages of the ring: one more changes nothing at 480p (109 us both ways,
+// forward), and costs the wide forward its second CTA of an SM.
+constexpr int kFwdStages = 2, kBwdStages = 3;
+// Tokens a slot takes at once.
 template <int V>
 constexpr int fwd_rows() {
-  return HF_T >= V ? HF_T / V : 1;
+  return 2 / V;
 }
+// CTAs of an SM that the registers are budgeted for.  At 480p two: three cost a
+// reload between the two passes over a token (115 us forward against 104).  The
+// wide forward runs best with two as well (720p: 782 us, one 830).
+constexpr int fwd_residents(int tier) { return tier == 2 ? 1 : 2; }
+constexpr int bwd_residents(int tier) { return tier == 0 ? 2 : 1; }
 // Pieces of one stage, and of a thread's whole ring with the weights behind it.
-template <typename TX, bool JOINT, int V>
+template <typename TX, int FORM, int V>
 constexpr int fwd_pieces() {
-  return all_parts<JOINT>() * fwd_rows<V>() * V * pieces8<TX>();
+  return all_parts<FORM>() * fwd_rows<V>() * V * pieces8<TX>();
 }
-template <typename TX, bool JOINT, int V>
+template <typename TX, int FORM, int V>
 constexpr int bwd_pieces() {
-  return all_parts<JOINT>() * V + turned_parts<JOINT>() * V * pieces8<TX>();
+  return all_parts<FORM>() * V + turned_parts<FORM>() * V * pieces8<TX>();
 }
-template <typename TX, bool JOINT, int V>
+template <typename TX, int FORM, int V>
 constexpr int fwd_ring() {
-  return fwd_stages<TX>() * fwd_pieces<TX, JOINT, V>() + turned_parts<JOINT>() * V * 2;
+  return kFwdStages * fwd_pieces<TX, FORM, V>() + turned_parts<FORM>() * V * 2;
 }
-template <typename TX, bool JOINT, int V>
+template <typename TX, int FORM, int V>
 constexpr int bwd_ring() {
-  return bwd_stages<TX>() * bwd_pieces<TX, JOINT, V>() + turned_parts<JOINT>() * V * 2;
+  return kBwdStages * bwd_pieces<TX, FORM, V>() + turned_parts<FORM>() * V * 2;
 }
 constexpr int kAngleBuffers = 2;  // of T tokens (D floats each), for every slot
 
@@ -389,27 +379,30 @@ struct Share {
   }
 };
 
-template <typename TX, bool INTER, int D, int V, bool JOINT>
-__global__ void __launch_bounds__(row_threads(V), V == 1 ? HF_B : 1) heads_fwd_kernel(
+template <typename TX, bool INTER, int D, int TIER, int FORM>
+__global__ void __launch_bounds__(kTiers[TIER].threads, fwd_residents(TIER)) heads_fwd_kernel(
     const __grid_constant__ HeadsParams p) {
-  constexpr int T = fwd_rows<V>(), S = fwd_stages<TX>(), Q8 = pieces8<TX>();
-  constexpr int NT = turned_parts<JOINT>(), NP = all_parts<JOINT>();
-  constexpr int STAGE = fwd_pieces<TX, JOINT, V>(), RING = fwd_ring<TX, JOINT, V>();
+  constexpr int V = kTiers[TIER].vectors;
+  constexpr int T = fwd_rows<V>(), S = kFwdStages, Q8 = pieces8<TX>();
+  constexpr int NT = turned_parts<FORM>(), NP = all_parts<FORM>();
+  constexpr int STAGE = fwd_pieces<TX, FORM, V>(), RING = fwd_ring<TX, FORM, V>();
   constexpr bool SPLIT = split<TX, INTER>();
   extern __shared__ uint4 smem[];
   __shared__ __align__(16) float red[kSlotRedFloats];
   __shared__ Turns turns;
-  const int part0 = JOINT ? 0 : blockIdx.y;
+  constexpr bool FULL = FORM == kFull;
+  const int part0 = FORM == kSingle ? blockIdx.y : 0;
   const HeadsPart& any = p.part[part0];
-  const bool plain = !JOINT && any.plain;
-  const bool rot = p.rotate && !plain;
-  const int norm = plain ? 0 : p.norm;
+  const bool plain = FORM == kSingle && any.plain;
+  const bool rot = FULL || (p.rotate && !plain);
+  const int norm = FULL ? SPARGE_HEADS_NORM_TOKEN : plain ? 0 : p.norm;
   turns.fill(p);
+  clear_red(red);
   __syncthreads();
   const int per_cta = slots_per_cta(any.W);
   Slot s = make_slot(any.W, red);
   if (s.index >= per_cta) return;
-  const Place<SPLIT, D, V> at(s, any.C);
+  const Place<SPLIT, D, V, FULL> at(s, any.C);
   const int H = any.C / D;
   Share mine(p, T, static_cast<int64_t>(blockIdx.x) * per_cta + s.index,
              static_cast<int64_t>(gridDim.x) * per_cta);
@@ -436,12 +429,12 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? HF_B : 1) heads_fwd_k
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const HeadsPart& part = p.part[part0 + i];
-        if (!JOINT || part.x != nullptr) {
+        if (FORM != kJoint || part.x != nullptr) {
 #pragma unroll
           for (int t = 0; t < T; ++t) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-              if (at.active[v] && (t == 0 || second))
+              if (at.here(v) && (t == 0 || second))
                 stage_row<TX, SPLIT, D>(stage + ((i * T + t) * V + v) * Q8,
                                         xp[i] + t * part.xs[1] + v * at.head_step * part.xs[2]);
           }
@@ -470,8 +463,8 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? HF_B : 1) heads_fwd_k
     for (int v = 0; v < V; ++v) {
       const int wc = at.c + (norm == 1 ? (at.head + v * at.head_step) * D : 0);
       keep_weight(weights + (i * V + v) * 2,
-                  load_weight<INTER, SPLIT, D>(p, norm ? p.part[part0 + i].w : nullptr, at.active[v], wc));
-      if (!at.active[v]) {
+                  load_weight<INTER, SPLIT, D>(p, norm ? p.part[part0 + i].w : nullptr, at.here(v), wc));
+      if (!at.here(v)) {
         // Threads behind the last channel add zeros to the sums.
         for (int k = 0; k < S; ++k) {
           for (int t = 0; t < T; ++t) {
@@ -531,7 +524,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? HF_B : 1) heads_fwd_k
       for (int t = 0; t < T; ++t) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const bool ok = at.active[v] && (t == 0 || second) && (!JOINT || part.x != nullptr);
+          const bool ok = at.here(v) && (t == 0 || second) && (FORM != kJoint || part.x != nullptr);
           const int q = (i * T + t) * V + v;
           if (i < NT) {
             Pairs u = x[q];
@@ -570,29 +563,32 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? HF_B : 1) heads_fwd_k
   }
 }
 
-template <typename TX, bool INTER, int D, int V, bool JOINT>
-__global__ void __launch_bounds__(row_threads(V), V == 1 ? HB_B : 1) heads_bwd_kernel(
+template <typename TX, bool INTER, int D, int TIER, int FORM>
+__global__ void __launch_bounds__(kTiers[TIER].threads, bwd_residents(TIER)) heads_bwd_kernel(
     const __grid_constant__ HeadsParams p) {
-  constexpr int S = bwd_stages<TX>(), Q8 = pieces8<TX>();
-  constexpr int NT = turned_parts<JOINT>(), NP = all_parts<JOINT>();
-  constexpr int STAGE = bwd_pieces<TX, JOINT, V>(), RING = bwd_ring<TX, JOINT, V>();
+  constexpr int V = kTiers[TIER].vectors;
+  constexpr int S = kBwdStages, Q8 = pieces8<TX>();
+  constexpr int NT = turned_parts<FORM>(), NP = all_parts<FORM>();
+  constexpr int STAGE = bwd_pieces<TX, FORM, V>(), RING = bwd_ring<TX, FORM, V>();
   constexpr bool SPLIT = split<TX, INTER>();
   constexpr int XAT = NP * V;  // the inputs' rows, behind the gradients' rows
   extern __shared__ uint4 smem[];
   __shared__ __align__(16) float red[kSlotRedFloats];
   __shared__ Turns turns;
   grid_launch_dependents();
-  const int part0 = JOINT ? 0 : blockIdx.y;
+  constexpr bool FULL = FORM == kFull;
+  const int part0 = FORM == kSingle ? blockIdx.y : 0;
   const HeadsPart& any = p.part[part0];
-  const bool plain = !JOINT && any.plain;
-  const bool rot = p.rotate && !plain;
-  const int norm = plain ? 0 : p.norm;
+  const bool plain = FORM == kSingle && any.plain;
+  const bool rot = FULL || (p.rotate && !plain);
+  const int norm = FULL ? SPARGE_HEADS_NORM_TOKEN : plain ? 0 : p.norm;
   turns.fill(p);
+  clear_red(red);
   __syncthreads();
   const int per_cta = slots_per_cta(any.W);
   Slot s = make_slot(any.W, red);
   if (s.index >= per_cta) return;
-  const Place<SPLIT, D, V> at(s, any.C);
+  const Place<SPLIT, D, V, FULL> at(s, any.C);
   const int H = any.C / D;
   const int64_t slot = static_cast<int64_t>(blockIdx.x) * per_cta + s.index;
   Share mine(p, 1, slot, static_cast<int64_t>(gridDim.x) * per_cta);
@@ -620,10 +616,10 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? HB_B : 1) heads_bwd_k
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const HeadsPart& part = p.part[part0 + i];
-        const bool here = !JOINT || part.y != nullptr;
+        const bool here = FORM != kJoint || part.y != nullptr;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          if (here && at.active[v]) {
+          if (here && at.here(v)) {
             stage_row<__nv_bfloat16, SPLIT, D>(
                 stage + i * V + v, static_cast<const __nv_bfloat16*>(part.y) + in + v * far);
             if (i < NT && norm)
@@ -657,9 +653,9 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? HB_B : 1) heads_bwd_k
     for (int v = 0; v < V; ++v) {
       const int wc = at.c + (norm == 1 ? (at.head + v * at.head_step) * D : 0);
       keep_weight(weights + (i * V + v) * 2,
-                  load_weight<INTER, SPLIT, D>(p, norm ? p.part[part0 + i].w : nullptr, at.active[v], wc));
+                  load_weight<INTER, SPLIT, D>(p, norm ? p.part[part0 + i].w : nullptr, at.here(v), wc));
       dw[i * V + v] = {{0, 0}, {0, 0}};
-      if (!at.active[v]) {
+      if (!at.here(v)) {
         for (int k = 0; k < S; ++k) {
           ring[k * STAGE + i * V + v] = make_uint4(0, 0, 0, 0);
           for (int q = 0; q < Q8; ++q)
@@ -722,7 +718,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? HB_B : 1) heads_bwd_k
       const HeadsPart& part = p.part[part0 + i];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const bool ok = at.active[v] && (!JOINT || part.y != nullptr);
+        const bool ok = at.here(v) && (FORM != kJoint || part.y != nullptr);
         TX* out = dx[i] + v * at.head_step * part.ds[2];
         if (i < NT) {
           const int q = i < NT ? i * V + v : 0;
@@ -770,19 +766,51 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? HB_B : 1) heads_bwd_k
   for (int i = 0; i < NT; ++i) {
     float* out = p.part[part0 + i].dw_part;
     if (out == nullptr) continue;
+    if (norm == SPARGE_HEADS_NORM_TOKEN) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (!at.active[v]) continue;
+      for (int v = 0; v < V; ++v) {
+        if (!at.here(v)) continue;
+        float f[8];
+        from_pairs<INTER>(dw[i * V + v], f);
+        store_row<float, SPLIT, D>(out + slot * any.C + (at.head + v * at.head_step) * D + at.c, f);
+      }
+    } else {
+      // One weight for all heads: add the heads of the thread, of the warp, then
+      // warp after warp into the slot's angle buffer.
       float f[8];
-      from_pairs<INTER>(dw[i * V + v], f);
-      store_row<float, SPLIT, D>(out + slot * any.C + (at.head + v * at.head_step) * D + at.c, f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float one[8];
+        from_pairs<INTER>(dw[i * V + v], one);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] += at.here(v) ? one[k] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+#pragma unroll
+        for (int o = D / 8; o < 32; o *= 2) f[k] += __shfl_xor_sync(0xffffffffu, f[k], o);
+      }
+      slot_sync(s);  // the angles, or the part before, have been read
+      for (int w = 0; w < s.W; ++w) {
+        if (w == s.warp && s.lane < D / 8) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float* to = ang + at.c + (!SPLIT || k < 4 ? k : k - 4 + D / 2);
+            *to = w == 0 ? f[k] : *to + f[k];
+            if (w == s.W - 1) out[slot * D + (to - ang)] = *to;
+          }
+        }
+        slot_sync(s);
+      }
     }
   }
 }
 
 struct HeadsPlan {
-  bool joint;
-  int V, ctas, threads, slots;  // slots: of a CTA, at most
+  Form form;
+  int tier, V, ctas, threads, slots;  // slots: of a CTA, at most
   int n;             // parts beside one another in the grid
   int at[3];         // the place of each of the call's parts
   int smem;          // dynamic, of a CTA
@@ -793,15 +821,15 @@ struct HeadsPlan {
 template <typename TX>
 int ring_bytes(const HeadsPlan& pl, bool bwd) {
   if (pl.V == 1) {
-    if (pl.joint) return bwd ? bwd_ring<TX, true, 1>() : fwd_ring<TX, true, 1>();
-    return bwd ? bwd_ring<TX, false, 1>() : fwd_ring<TX, false, 1>();
+    if (pl.form != kSingle) return bwd ? bwd_ring<TX, kJoint, 1>() : fwd_ring<TX, kJoint, 1>();
+    return bwd ? bwd_ring<TX, kSingle, 1>() : fwd_ring<TX, kSingle, 1>();
   }
-  if (pl.joint) return bwd ? bwd_ring<TX, true, 2>() : fwd_ring<TX, true, 2>();
-  return bwd ? bwd_ring<TX, false, 2>() : fwd_ring<TX, false, 2>();
+  if (pl.form != kSingle) return fwd_ring<TX, kJoint, 2>();
+  return bwd ? bwd_ring<TX, kSingle, 2>() : fwd_ring<TX, kSingle, 2>();
 }
 int heads_smem(const HeadsPlan& pl, bool f32, int d, bool bwd) {
   const int ring = f32 ? ring_bytes<float>(pl, bwd) : ring_bytes<__nv_bfloat16>(pl, bwd);
-  const int rows = bwd ? 1 : (HF_T >= pl.V ? HF_T / pl.V : 1);
+  const int rows = bwd ? 1 : 2 / pl.V;
   return 16 * ring * pl.threads + pl.slots * kAngleBuffers * rows * d * static_cast<int>(sizeof(float));
 }
 
@@ -819,25 +847,29 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
   // Together when the rows are alike: angles and barriers are shared, so 480p
   // takes less time than with a part to each blockIdx.y.
   // Wide rows only where a CTA's ring still fits the shared memory.
-  pl.V = row_vectors(widest);
-  pl.joint = a.n_parts > 1 && same && turned <= 2 && plain <= 1 && turned > 0 &&
-             (pl.V == 1 || (!bwd && a.x_type == SPARGE_BF16));
-  pl.n = pl.joint ? 1 : a.n_parts;
+  pl.tier = tier_of(widest);
+  pl.V = kTiers[pl.tier].vectors;
+  const bool joint = a.n_parts > 1 && same && turned <= 2 && plain <= 1 && turned > 0 &&
+                     (pl.V == 1 || (!bwd && a.x_type == SPARGE_BF16));
+  const bool full = joint && a.n_parts == 3 && a.rope != nullptr &&
+                    a.norm == SPARGE_HEADS_NORM_TOKEN && widest % (256 * pl.V) == 0;
+  pl.form = full ? kFull : joint ? kJoint : kSingle;
+  pl.n = joint ? 1 : a.n_parts;
   int slots_min = kMaxSlots;
   for (int i = 0; i < a.n_parts; ++i) {
-    if (!pl.joint) pl.at[i] = i;
+    if (!joint) pl.at[i] = i;
     const int W = slot_warps(a.part[i].H * a.d, pl.V);
     pl.threads = std::max(pl.threads, W * slots_per_cta(W) * 32);
     slots_min = std::min(slots_min, slots_per_cta(W));
     pl.slots = std::max(pl.slots, slots_per_cta(W));
   }
   // A grid that is resident as a whole: every CTA stays for its share of the
-  // rows.  Shared memory limits it, or registers (at most 64 a thread forward,
-  // 128 backward).
+  // rows.  Shared memory limits it, or registers.
   pl.smem = heads_smem(pl, a.x_type == SPARGE_F32, a.d, bwd);
-  const int rows = bwd ? 1 : (HF_T >= pl.V ? HF_T / pl.V : 1);
-  const int per_sm = std::max(1, std::min(65536 / ((bwd ? 65536 / 256 / HB_B / 8 * 8 : 65536 / 256 / HF_B / 8 * 8) * pl.threads),
-                                          kSmemPerSm / (pl.smem + kSmemOfCta)));
+  const int rows = bwd ? 1 : 2 / pl.V;
+  const int per_sm =
+      std::max(1, std::min(bwd ? bwd_residents(pl.tier) : fwd_residents(pl.tier),
+                           std::min(kSmemPerSm / (pl.smem + kSmemOfCta), 2048 / pl.threads)));
   const int64_t units = static_cast<int64_t>(a.B) * ((a.N + rows - 1) / rows);
   const int64_t need = (units + slots_min - 1) / slots_min;
   const int64_t most = (kSMs * per_sm + pl.n - 1) / pl.n;
@@ -846,14 +878,15 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
     if (!bwd || a.norm == 0 || a.part[i].plain || a.part[i].dweight == nullptr) continue;
     const int C = a.part[i].H * a.d;
     pl.dw_off[i] = pl.bytes;
-    pl.bytes += static_cast<size_t>(pl.ctas) * slots_per_cta(slot_warps(C, pl.V)) * C * sizeof(float);
+    pl.bytes += static_cast<size_t>(pl.ctas) * slots_per_cta(slot_warps(C, pl.V)) *
+                (a.norm == SPARGE_HEADS_NORM_TOKEN ? C : a.d) * sizeof(float);
   }
   return pl;
 }
 
 HeadsParams heads_params(const sparge_heads& a, const HeadsPlan& pl) {
   HeadsParams p = {};
-  if (pl.joint) {
+  if (pl.form != kSingle) {
     // An absent part still gives the row its size.
     for (int i = 0; i < 3; ++i) {
       p.part[i].C = a.part[0].H * a.d;
@@ -887,10 +920,10 @@ HeadsParams heads_params(const sparge_heads& a, const HeadsPlan& pl) {
   return p;
 }
 
-template <typename TX, bool INTER, int D, int V, bool JOINT>
-cudaError_t launch_form(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cudaStream_t st) {
-  auto* kernel = bwd ? heads_bwd_kernel<TX, INTER, D, V, JOINT> : heads_fwd_kernel<TX, INTER, D, V, JOINT>;
-  if (pl.smem > 47 * 1024) {
+template <typename Kernel>
+cudaError_t launch_kernel(Kernel* kernel, const HeadsParams& p, const HeadsPlan& pl,
+                          cudaStream_t st) {
+  if (pl.smem > 43 * 1024) {  // 48 KB less what the kernel declares
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
     if (e != cudaSuccess) {
@@ -902,13 +935,29 @@ cudaError_t launch_form(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cud
   return cudaGetLastError();
 }
 
+template <typename TX, bool INTER, int D, int TIER>
+cudaError_t launch_tier(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cudaStream_t st) {
+  if constexpr (TIER == 0) {
+    if (pl.form == kFull)
+      return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, TIER, kFull>, p, pl, st)
+                 : launch_kernel(heads_fwd_kernel<TX, INTER, D, TIER, kFull>, p, pl, st);
+    if (pl.form == kJoint)
+      return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, TIER, kJoint>, p, pl, st)
+                 : launch_kernel(heads_fwd_kernel<TX, INTER, D, TIER, kJoint>, p, pl, st);
+  } else if constexpr (sizeof(TX) == 2) {
+    if (pl.form == kFull) return launch_kernel(heads_fwd_kernel<TX, INTER, D, TIER, kFull>, p, pl, st);
+    if (pl.form == kJoint)
+      return launch_kernel(heads_fwd_kernel<TX, INTER, D, TIER, kJoint>, p, pl, st);
+  }
+  return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, TIER, kSingle>, p, pl, st)
+             : launch_kernel(heads_fwd_kernel<TX, INTER, D, TIER, kSingle>, p, pl, st);
+}
+
 template <typename TX, bool INTER, int D>
 cudaError_t launch_heads(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cudaStream_t st) {
-  if (pl.V == 1)
-    return pl.joint ? launch_form<TX, INTER, D, 1, true>(p, pl, bwd, st)
-                    : launch_form<TX, INTER, D, 1, false>(p, pl, bwd, st);
-  return pl.joint ? launch_form<TX, INTER, D, 2, true>(p, pl, bwd, st)
-                  : launch_form<TX, INTER, D, 2, false>(p, pl, bwd, st);
+  if (pl.tier == 0) return launch_tier<TX, INTER, D, 0>(p, pl, bwd, st);
+  if (pl.tier == 1) return launch_tier<TX, INTER, D, 1>(p, pl, bwd, st);
+  return launch_tier<TX, INTER, D, 2>(p, pl, bwd, st);
 }
 
 cudaError_t dispatch_heads(const sparge_heads& a, const HeadsParams& p, const HeadsPlan& pl,
@@ -986,7 +1035,7 @@ int check_heads(const sparge_heads* a, bool bwd) {
     if (bwd) {
       HEADS_TRY(check_aligned(s.dx, 16));
       HEADS_TRY(check_strides(s.dx_stride, a->x_type));
-      if (normed && s.dweight) HEADS_TRY(check_aligned(s.dweight, 4));
+      if (normed && s.dweight) HEADS_TRY(check_aligned(s.dweight, 16));
     }
   }
   return SPARGE_OK;
@@ -1061,13 +1110,13 @@ int sparge_heads_bwd(const sparge_heads* args, void* workspace, size_t ws_bytes,
     const int C = s.H * args->d;
     float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.dw_off[i]);
     p.part[pl.at[i]].dw_part = part;
-    // One row of C sums a slot; with a norm over each head, H rows of d.
+    // One row of sums a slot, of all channels or of those of a head.
     const bool token = args->norm == SPARGE_HEADS_NORM_TOKEN;
     ReduceJob& j = jobs.job[jobs.n++];
     j.src = part;
     j.C = token ? C : args->d;
     j.ld = j.C;
-    j.nrow = pl.ctas * slots_per_cta(slot_warps(C, pl.V)) * (token ? 1 : s.H);
+    j.nrow = pl.ctas * slots_per_cta(slot_warps(C, pl.V));
     j.nout = 1;
     j.out = s.dweight;
     j.out_bf16 = args->weight_type == SPARGE_BF16;

@@ -153,24 +153,41 @@ SPARGE_DEV F8 load_mod(const float* m, int step) {
   return f8(r);
 }
 
-// One such row as a thread sees it: in registers from row to row where it
-// covers eight channels (V = 1), read again from L1 (which the rows bypass)
-// where it covers sixteen.
-template <int V>
+// One such row as a thread sees it from row to row: in registers where it covers
+// eight channels (V = 1); where it covers sixteen, in shared memory behind the
+// ring (KEEP; read through L1 instead, a third of it comes from L2: 583 instead
+// of 476 us at 720p), or where the backward's ring leaves no room, through L1.
+template <int V, bool KEEP>
 struct Mod {
+  [[maybe_unused]] static constexpr int kPieces = V == 1 || !KEEP ? 0 : 2 * V;
   const float* at;
+  float plus;
   F8 kept;
-  SPARGE_DEV void open(const float* row, float plus, const int (&off)[V][2]) {
+  Ring ring;
+  SPARGE_DEV void open(const float* row, float add_to, const int (&off)[V][2]) {
     at = row;
-    if constexpr (V == 1) kept = add(load_mod(row + off[0][0], off[0][1]), f8(plus));
-  }
-  SPARGE_DEV F8 get(int v, const int (&off)[V][2], float plus) const {
-    if constexpr (V == 1) return kept;
-    return add(load_mod(at + off[v][0], off[v][1]), f8(plus));
+    plus = add_to;
+    if constexpr (V == 1) {
+      kept = add(load_mod(row + off[0][0], off[0][1]), f8(add_to));
+    } else if constexpr (KEEP) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const F8 m = add(load_mod(row + off[v][0], off[v][1]), f8(add_to));
+        reinterpret_cast<ulonglong2&>(ring[2 * v]) = make_ulonglong2(m.v[0], m.v[1]);
+        reinterpret_cast<ulonglong2&>(ring[2 * v + 1]) = make_ulonglong2(m.v[2], m.v[3]);
+      }
+    }
   }
   SPARGE_DEV F8 get(int v, const int (&off)[V][2]) const {
-    if constexpr (V == 1) return kept;
-    return load_mod(at + off[v][0], off[v][1]);
+    if constexpr (V == 1) {
+      return kept;
+    } else if constexpr (KEEP) {
+      const ulonglong2 a = reinterpret_cast<const ulonglong2&>(ring[2 * v]);
+      const ulonglong2 b = reinterpret_cast<const ulonglong2&>(ring[2 * v + 1]);
+      return {{a.x, a.y, b.x, b.y}};
+    } else {
+      return add(load_mod(at + off[v][0], off[v][1]), f8(plus));
+    }
   }
 };
 
@@ -207,80 +224,65 @@ SPARGE_DEV void slot_moments(Slot& s, const F8 (&y)[T * V], const bool (&lo)[V],
     return;
   }
   static_assert(2 * T <= kSlotRed, "reduction buffer");
-  float* red = s.red + s.phase * s.W * kSlotRed;
-  s.phase ^= 1;
+  float* red = slot_half(s);
   if (s.lane % (32 / T) == 0)
     *reinterpret_cast<float2*>(red + s.warp * kSlotRed + 2 * (s.lane / (32 / T))) =
         make_float2(mine, square);
   slot_sync(s);
+  // Lane l joins warps l % 8 and l % 8 + 8 of row l / 8 % T.
+  const int w = s.lane & 7;
+  const float* in = red + w * kSlotRed + 2 * ((s.lane >> 3) % T);
+  const float2 a = *reinterpret_cast<const float2*>(in);
+  const float2 b = *reinterpret_cast<const float2*>(in + 8 * kSlotRed);
+  const float na = counts[w], nb = counts[w + 8];
+  const float m = sum_of_8(fmaf(na, a.x, nb * b.x)) * inv_c;
+  const float da = a.x - m, db = b.x - m;
+  const float q = sum_of_8(fmaf(na * da, da, a.y) + fmaf(nb * db, db, b.y));
 #pragma unroll
-  for (int t = 0; t < T; ++t) mean[t] = m2[t] = 0.f;
-  for (int w = 0; w < s.W; ++w) {
-    const float n = counts[w];
-#pragma unroll
-    for (int t = 0; t < T; ++t) mean[t] = fmaf(n, red[w * kSlotRed + 2 * t], mean[t]);
-  }
-#pragma unroll
-  for (int t = 0; t < T; ++t) mean[t] *= inv_c;
-  for (int w = 0; w < s.W; ++w) {
-    const float n = counts[w];
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const float2 r = *reinterpret_cast<const float2*>(red + w * kSlotRed + 2 * t);
-      const float d = r.x - mean[t];
-      m2[t] += fmaf(n * d, d, r.y);
-    }
+  for (int t = 0; t < T; ++t) {
+    mean[t] = __shfl_sync(0xffffffffu, m, 8 * t);
+    m2[t] = __shfl_sync(0xffffffffu, q, 8 * t);
   }
 }
 
-#ifndef RF_S
-#define RF_S 3
-#endif
-#ifndef RF_T
-#define RF_T 2
-#endif
-#ifndef RF_B
-#define RF_B 2
-#endif
-#ifndef RB_S
-#define RB_S 3
-#endif
-#ifndef RB_T
-#define RB_T 1
-#endif
-#ifndef RB_B
-#define RB_B 2
-#endif
-// Rows a slot takes at once, and pieces of one stage.
+// Rows a slot takes at once (backward with one: 480p 144 instead of 140 us), and
+// pieces of one stage.
 template <int V>
-constexpr int fwd_rows() {
-  return RF_T >= V ? RF_T / V : 1;
+constexpr int rows_at_once() {
+  return 2 / V;
 }
 template <typename TX, typename TB, int V>
 constexpr int fwd_pieces() {
-  return fwd_rows<V>() * V * (pieces8<TX>() + pieces8<TB>());
-}
-template <int V>
-constexpr int bwd_rows() {
-  return V == 1 ? RB_T : 1;
+  return rows_at_once<V>() * V * (pieces8<TX>() + pieces8<TB>());
 }
 template <typename TX, typename TB, int V>
 constexpr int bwd_pieces() {
-  return bwd_rows<V>() * V * 2 * (pieces8<TX>() + pieces8<TB>());
+  return rows_at_once<V>() * V * 2 * (pieces8<TX>() + pieces8<TB>());
 }
+// CTAs of an SM that the registers are budgeted for.  At 480p the backward's two
+// leave 168 a thread, so that every value of two rows is at hand (one modulation
+// a frame, both norms: 125 us against 161 with 128).
+constexpr int fwd_residents(int tier) { return tier == 0 ? 3 : tier == 1 ? 2 : 1; }
+constexpr int bwd_residents(int tier) { return tier == 0 ? 2 : 1; }
 // Stages of the ring; wide rows have as many as a CTA of 512 threads can hold.
-constexpr int kFwdStages = RF_S;
+template <typename TX, typename TB, int V>
+constexpr int fwd_stages() {
+  return V == 1 ? 2 : sizeof(TX) + sizeof(TB) == 8 ? 1 : 2;
+}
 template <typename TX, typename TB, int V>
 constexpr int bwd_stages() {
-  return V == 1 ? RB_S : 24 / bwd_pieces<TX, TB, V>();
+  return V == 1 ? 3 : 24 / bwd_pieces<TX, TB, V>();
 }
 
 // A thread's channels (vector v: fours at c + v * far and F further) and its
 // part of the ring.
-template <int V, int F>
+template <int V, int F, bool FULL>
 struct Lane {
   int c, far;
   bool lo[V], hi[V], all;
+  SPARGE_DEV bool low(int v) const { return FULL || lo[v]; }
+  SPARGE_DEV bool high(int v) const { return FULL || hi[v]; }
+  SPARGE_DEV bool full() const { return FULL || all; }
   int mod[V][2];  // where it reads a row that is kept: inside also behind the end
   Ring ring;
   SPARGE_DEV Lane(const Slot& s, int C, uint4* smem) {
@@ -319,28 +321,32 @@ struct ItemWalk {
   }
 };
 
-template <typename TX, typename TB, int V>
-__global__ void __launch_bounds__(row_threads(V), V == 1 ? RF_B : 1) resnorm_fwd_kernel(
+template <typename TX, typename TB, int TIER>
+__global__ void __launch_bounds__(kTiers[TIER].threads, fwd_residents(TIER)) resnorm_fwd_kernel(
     const __grid_constant__ ResnormParams p) {
-  constexpr int T = fwd_rows<V>(), S = kFwdStages, XQ = pieces8<TX>(), BQ = pieces8<TB>();
+  constexpr int V = kTiers[TIER].vectors;
+  constexpr int T = rows_at_once<V>(), S = fwd_stages<TX, TB, V>(), XQ = pieces8<TX>(), BQ = pieces8<TB>();
   constexpr int PIECES = fwd_pieces<TX, TB, V>(), STAGE = PIECES;
   extern __shared__ uint4 smem[];
   __shared__ __align__(16) float red[kSlotRedFloats];
   __shared__ float counts[16];
   Slot s = make_slot(p.W, red);
   const int per_cta = slots_per_cta(p.W);
-  if (threadIdx.x < p.W) {
+  clear_red(red);
+  if (threadIdx.x < 16) {
+    // Channels of each warp of a slot, none of those it does not have.
     int n = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      n += max(0, min(256, p.C - (v * p.W + static_cast<int>(threadIdx.x)) * 256));
+      if (threadIdx.x < p.W)
+        n += max(0, min(256, p.C - (v * p.W + static_cast<int>(threadIdx.x)) * 256));
     counts[threadIdx.x] = static_cast<float>(n);
   }
   __syncthreads();
   if (s.index >= per_cta) return;
   const float inv_cnt = 1.f / counts[s.warp];
   constexpr int F = four_step<TX>();
-  const Lane<V, F> at(s, p.C, smem);
+  const Lane<V, F, false> at(s, p.C, smem);
   // What is never loaded is zero: threads behind the last channel add zeros.
   if (!at.all) {
     for (int k = 0; k < S * PIECES; ++k) at.ring[k] = make_uint4(0, 0, 0, 0);
@@ -381,7 +387,10 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RF_B : 1) resnorm_fwd
   const float* shift_row = (p.shift != nullptr ? p.shift : g_zeros);
   const float plus = p.unit || p.scale == nullptr ? 1.f : 0.f;
   const float gate_plus = p.gate == nullptr ? 1.f : 0.f;
-  Mod<V> gate, gain, shift;
+  Mod<V, true> gate, gain, shift;
+  gate.ring = at.ring + S * PIECES;
+  gain.ring = gate.ring + gate.kPieces;
+  shift.ring = gain.ring + gain.kPieces;
   int group = -1;
   int k = 0;
   while (now.item < p.items) {
@@ -434,7 +443,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RF_B : 1) resnorm_fwd
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const int i = t * V + v;
-          y[i] = fma(gate.get(v, at.mod, gate_plus), b8[i], f8(rx[i]));
+          y[i] = fma(gate.get(v, at.mod), b8[i], f8(rx[i]));
           if (t < rows) put<F>(static_cast<TX*>(p.y) + o + v * at.far, y[i], at.lo[v], at.hi[v]);
         }
         o += p.C;
@@ -464,7 +473,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RF_B : 1) resnorm_fwd
         const F8 m = f8(-mean[t]), r = f8(rstd[t]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const F8 h = fma(mul(add(y[t * V + v], m), r), gain.get(v, at.mod, plus), shift.get(v, at.mod));
+          const F8 h = fma(mul(add(y[t * V + v], m), r), gain.get(v, at.mod), shift.get(v, at.mod));
           if (t < rows) put<F>(static_cast<TB*>(p.h) + o + v * at.far, h, at.lo[v], at.hi[v]);
         }
         o += p.C;
@@ -484,23 +493,29 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RF_B : 1) resnorm_fwd
   }
 }
 
-template <typename TX, typename TB, int V, bool POST>
-__global__ void __launch_bounds__(row_threads(V), V == 1 ? RB_B : 1) resnorm_bwd_kernel(
+// FULL: every input is there and no thread is without channels, which takes the
+// branches out of the row loop (one modulation a frame, both norms, 480p: 124
+// instead of 155 us).
+template <typename TX, typename TB, int TIER, bool POST, bool FULL>
+__global__ void __launch_bounds__(kTiers[TIER].threads, bwd_residents(TIER)) resnorm_bwd_kernel(
     const __grid_constant__ ResnormParams p) {
-  constexpr int T = bwd_rows<V>(), S = bwd_stages<TX, TB, V>(), XQ = pieces8<TX>(),
+  constexpr int V = kTiers[TIER].vectors;
+  constexpr int T = rows_at_once<V>(), S = bwd_stages<TX, TB, V>(), XQ = pieces8<TX>(),
                 BQ = pieces8<TB>();
   constexpr int PIECES = bwd_pieces<TX, TB, V>(), ROW = 2 * (XQ + BQ), STAGE = PIECES;
   constexpr int SUMS = POST ? 4 : 3;
   extern __shared__ uint4 smem[];
   __shared__ __align__(16) float red[kSlotRedFloats];
   grid_launch_dependents();
+  clear_red(red);
+  __syncthreads();
   Slot s = make_slot(p.W, red);
   const int per_cta = slots_per_cta(p.W);
   if (s.index >= per_cta) return;
   constexpr int F = four_step<TX>();
-  const Lane<V, F> at(s, p.C, smem);
-  const bool normed = p.norm != SPARGE_NORM_NONE, has_b = p.b != nullptr;
-  const bool has_dy = p.dy != nullptr, has_dh = p.dh != nullptr;
+  const Lane<V, F, FULL> at(s, p.C, smem);
+  const bool normed = FULL || p.norm != SPARGE_NORM_NONE, has_b = FULL || p.b != nullptr;
+  const bool has_dy = FULL || p.dy != nullptr, has_dh = FULL || p.dh != nullptr;
   F8 acc[SUMS][V];  // gate, scale, shift, post
 #pragma unroll
   for (int k = 0; k < SUMS; ++k) {
@@ -508,7 +523,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RB_B : 1) resnorm_bwd
     for (int v = 0; v < V; ++v) acc[k][v] = f8(0.f);
   }
   // What is never loaded is zero: absent inputs, threads behind the last channel.
-  if (!(at.all && normed && has_b && has_dy && has_dh)) {
+  if (!(at.full() && normed && has_b && has_dy && has_dh)) {
     for (int k = 0; k < S * PIECES; ++k) at.ring[k] = make_uint4(0, 0, 0, 0);
   }
 
@@ -530,10 +545,10 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RB_B : 1) resnorm_bwd
           for (int v = 0; v < V; ++v) {
             const Ring dst = stage + (t * V + v) * ROW;
             const int64_t ov = o + v * at.far;
-            if (normed) stage_fours<F>(dst, x + ov, at.lo[v], at.hi[v]);
-            if (has_b) stage_fours<F>(dst + XQ, b + ov, at.lo[v], at.hi[v]);
-            if (has_dy) stage_fours<F>(dst + XQ + BQ, dy + ov, at.lo[v], at.hi[v]);
-            if (has_dh) stage_fours<F>(dst + 2 * XQ + BQ, dh + ov, at.lo[v], at.hi[v]);
+            if (normed) stage_fours<F>(dst, x + ov, at.low(v), at.high(v));
+            if (has_b) stage_fours<F>(dst + XQ, b + ov, at.low(v), at.high(v));
+            if (has_dy) stage_fours<F>(dst + XQ + BQ, dy + ov, at.low(v), at.high(v));
+            if (has_dh) stage_fours<F>(dst + 2 * XQ + BQ, dh + ov, at.low(v), at.high(v));
           }
         }
         o += p.C;
@@ -566,7 +581,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RB_B : 1) resnorm_bwd
   const float plus = p.unit || p.scale == nullptr ? 1.f : 0.f;
   const float gate_plus = p.gate == nullptr ? 1.f : 0.f;
   const float one_mean = p.norm == SPARGE_NORM_LAYER ? p.inv_c : 0.f;
-  Mod<V> gate, gain, post;
+  Mod<V, false> gate, gain, post;
   if (POST) post.open(p.post, 0.f, at.mod);
   int group = -1;
   int k = 0;
@@ -600,11 +615,11 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RB_B : 1) resnorm_bwd
           if (has_b) {
             F8 n = unstage<TB>(src + XQ);
             if (POST) n = mul(mul(n, f8(rb[t])), post.get(v, at.mod));
-            y = fma(gate.get(v, at.mod, gate_plus), n, y);
+            y = fma(gate.get(v, at.mod), n, y);
           }
           z[i] = mul(add(y, m), r);
           const F8 h = unstage<TB>(src + 2 * XQ + BQ);
-          d[i] = mul(h, gain.get(v, at.mod, plus));
+          d[i] = mul(h, gain.get(v, at.mod));
           if (t < rows) {
             acc[1][v] = fma(h, z[i], acc[1][v]);
             acc[2][v] = add(acc[2][v], h);
@@ -629,20 +644,20 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RB_B : 1) resnorm_bwd
           const Ring src = stage + i * ROW;
           const F8 g = unstage<TX>(src + XQ + BQ);
           d[i] = normed ? fma(r, fma(z[i], c2, add(d[i], c1)), g) : g;
-          put<F>(static_cast<TX*>(p.dx) + o + v * at.far, d[i], at.lo[v], at.hi[v]);
+          put<F>(static_cast<TX*>(p.dx) + o + v * at.far, d[i], at.low(v), at.high(v));
           if (!has_b) continue;
           const F8 b8 = unstage<TB>(src + XQ);
           if (POST) {
             const F8 bh = mul(b8, f8(rb[t])), w = post.get(v, at.mod);
             acc[0][v] = fma(d[i], mul(bh, w), acc[0][v]);
-            d[i] = mul(d[i], gate.get(v, at.mod, gate_plus));
+            d[i] = mul(d[i], gate.get(v, at.mod));
             acc[SUMS - 1][v] = fma(d[i], bh, acc[SUMS - 1][v]);
             d[i] = mul(d[i], w);
             e[t] += dot(d[i], bh);  // bh is 0 behind the last channel
           } else {
             acc[0][v] = fma(d[i], b8, acc[0][v]);
-            d[i] = mul(d[i], gate.get(v, at.mod, gate_plus));
-            put<F>(static_cast<TB*>(p.db) + o + v * at.far, d[i], at.lo[v], at.hi[v]);
+            d[i] = mul(d[i], gate.get(v, at.mod));
+            put<F>(static_cast<TB*>(p.db) + o + v * at.far, d[i], at.low(v), at.high(v));
           }
         }
       }
@@ -659,8 +674,8 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RB_B : 1) resnorm_bwd
           for (int v = 0; v < V; ++v) {
             const int i = t * V + v;
             const F8 b8 = unstage<TB>(stage + i * ROW + XQ);
-            put<F>(static_cast<TB*>(p.db) + o + v * at.far, mul(fma(b8, c3, d[i]), r), at.lo[v],
-                   at.hi[v]);
+            put<F>(static_cast<TB*>(p.db) + o + v * at.far, mul(fma(b8, c3, d[i]), r), at.low(v),
+                   at.high(v));
           }
         }
         o += p.C;
@@ -676,7 +691,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RB_B : 1) resnorm_bwd
         for (int v = 0; v < V; ++v) {
           if (p.sum[j] != nullptr)
             put<F>(p.sum[j] + static_cast<int64_t>(item) * p.C + at.c + v * at.far, acc[j][v],
-                   at.lo[v], at.hi[v]);
+                   at.low(v), at.high(v));
           acc[j][v] = f8(0.f);
         }
       }
@@ -688,13 +703,13 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? RB_B : 1) resnorm_bwd
     for (int v = 0; v < V; ++v) {
       if (!p.by_group[j] && p.sum[j] != nullptr)
         put<F>(p.sum[j] + static_cast<int64_t>(slot) * p.C + at.c + v * at.far, acc[j][v],
-               at.lo[v], at.hi[v]);
+               at.low(v), at.high(v));
     }
   }
 }
 
 struct ResnormPlan {
-  int V, W, per_cta, threads, ctas, slots, smem;
+  int tier, V, W, per_cta, threads, ctas, slots, smem;
   int groups, R;
   int items, parts;  // items = groups * parts
   // backward: a sum is written per item straight to the output (one part a
@@ -706,7 +721,7 @@ struct ResnormPlan {
 template <typename TX, typename TB, int V>
 int ring_bytes(bool bwd) {
   return 16 * (bwd ? bwd_stages<TX, TB, V>() * bwd_pieces<TX, TB, V>()
-                              : kFwdStages * fwd_pieces<TX, TB, V>());
+                              : fwd_stages<TX, TB, V>() * fwd_pieces<TX, TB, V>() + 3 * Mod<V, true>::kPieces);
 }
 template <typename TX, typename TB>
 int ring_bytes_of(int V, bool bwd) {
@@ -716,7 +731,8 @@ int ring_bytes_of(int V, bool bwd) {
 ResnormPlan resnorm_plan(const sparge_resnorm& a, bool bwd) {
   ResnormPlan pl = {};
   const int64_t M = a.rows;
-  pl.V = row_vectors(a.C);
+  pl.tier = tier_of(a.C);
+  pl.V = kTiers[pl.tier].vectors;
   pl.W = slot_warps(a.C, pl.V);
   pl.per_cta = slots_per_cta(pl.W);
   pl.threads = pl.W * pl.per_cta * 32;
@@ -730,12 +746,17 @@ ResnormPlan resnorm_plan(const sparge_resnorm& a, bool bwd) {
   if (a.shift) groups = std::max(groups, a.shift_groups);
   pl.groups = groups;
   pl.R = static_cast<int>(M / groups);
-  const int T = bwd ? (pl.V == 1 ? RB_T : 1) : (RF_T >= pl.V ? RF_T / pl.V : 1);
-  // A grid that is resident as a whole: shared memory limits it, or registers
-  // (at most 80 a thread forward, 128 backward).
-  const int per_sm = std::max(1, std::min(65536 / ((bwd ? 65536 / 256 / RB_B / 8 * 8 > 128 ? 128 : 65536 / 256 / RB_B / 8 * 8 : 65536 / 256 / RF_B / 8 * 8 > 128 ? 128 : 65536 / 256 / RF_B / 8 * 8) * pl.threads),
-                                          kSmemPerSm / (pl.smem + kSmemOfCta)));
-  const int64_t most = static_cast<int64_t>(kSMs) * per_sm;
+  const int T = 2 / pl.V;
+  // CTAs that are resident at a time: shared memory limits them, or registers.
+  // The backward stays resident for its share of the rows, since every slot
+  // leaves a row of sums; the forward runs several waves, whose CTAs end one by
+  // one instead of all at once with the slowest (480p: one wave 104 us, two 101,
+  // eight 93; 720p: four).
+  const int per_sm =
+      std::max(1, std::min(bwd ? bwd_residents(pl.tier) : fwd_residents(pl.tier),
+                           std::min(kSmemPerSm / (pl.smem + kSmemOfCta), 2048 / pl.threads)));
+  const int waves = bwd ? 1 : pl.V == 1 ? 8 : 4;
+  const int64_t most = static_cast<int64_t>(kSMs) * per_sm * waves;
   const int64_t target = most * pl.per_cta;  // slots that fill the machine
   const int64_t units = (pl.R + T - 1) / T;
   pl.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(units, target / groups)));
@@ -790,12 +811,18 @@ ResnormParams resnorm_params(const sparge_resnorm& a, const ResnormPlan& pl, boo
   return p;
 }
 
-template <typename TX, typename TB, int V>
-cudaError_t launch_form(const ResnormParams& p, const ResnormPlan& pl, bool bwd, cudaStream_t st) {
-  auto* kernel = !bwd                ? resnorm_fwd_kernel<TX, TB, V>
-                 : p.post != nullptr ? resnorm_bwd_kernel<TX, TB, V, true>
-                                     : resnorm_bwd_kernel<TX, TB, V, false>;
-  if (pl.smem > 47 * 1024) {
+template <typename TX, typename TB, int TIER>
+cudaError_t launch_tier(const ResnormParams& p, const ResnormPlan& pl, bool bwd, cudaStream_t st) {
+  const bool post = p.post != nullptr;
+  // (Sixteen channels a thread leave no registers for it.)
+  constexpr bool kFull = TIER == 0;
+  const bool full = kFull && p.C % 256 == 0 && p.norm && p.b && p.dy && p.dh;
+  auto* kernel = !bwd   ? resnorm_fwd_kernel<TX, TB, TIER>
+                 : full ? (post ? resnorm_bwd_kernel<TX, TB, TIER, true, kFull>
+                                : resnorm_bwd_kernel<TX, TB, TIER, false, kFull>)
+                        : (post ? resnorm_bwd_kernel<TX, TB, TIER, true, false>
+                                : resnorm_bwd_kernel<TX, TB, TIER, false, false>);
+  if (pl.smem > 43 * 1024) {  // 48 KB less what the kernel declares
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
     if (e != cudaSuccess) {
@@ -810,7 +837,9 @@ cudaError_t launch_form(const ResnormParams& p, const ResnormPlan& pl, bool bwd,
 template <typename TX, typename TB>
 cudaError_t launch_resnorm(const ResnormParams& p, const ResnormPlan& pl, bool bwd,
                            cudaStream_t st) {
-  return pl.V == 1 ? launch_form<TX, TB, 1>(p, pl, bwd, st) : launch_form<TX, TB, 2>(p, pl, bwd, st);
+  if (pl.tier == 0) return launch_tier<TX, TB, 0>(p, pl, bwd, st);
+  if (pl.tier == 1) return launch_tier<TX, TB, 1>(p, pl, bwd, st);
+  return launch_tier<TX, TB, 2>(p, pl, bwd, st);
 }
 
 cudaError_t dispatch_resnorm(const sparge_resnorm& a, const ResnormParams& p,

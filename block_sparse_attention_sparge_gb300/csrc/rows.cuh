@@ -2,7 +2,7 @@
 // layout kernels and the residual norm kernels).
 //
 // A slot is a group of W warps that owns one row (token) of C channels at a
-// time, V times eight consecutive channels to a thread, so per-channel
+// time, V times eight channels to a thread, so per-channel
 // operands (weights, gates, scales) and per-channel sums stay with the thread
 // from row to row.  A slot takes T rows at once: one barrier serves the sums of
 // all T.  Slots of one CTA are independent of one another: each has its own
@@ -24,30 +24,40 @@ namespace sparge {
 
 constexpr int kSMs = 152;              // of a GB300: sizes grids and workspaces
 constexpr int kSmemPerSm = 228 * 1024;  // shared memory of an SM
-constexpr int kSmemOfCta = 3 * 1024;    // of it a row kernel's CTA takes beside its ring, at most
+constexpr int kSmemOfCta = 6 * 1024;    // of it a row kernel's CTA takes beside its ring, at most
 constexpr int kMaxRowChannels = 8192;
-constexpr int kMaxSlots = 8;           // per CTA; named barriers 1 .. 8
 
-// Channels of a thread, in eights: 1 up to 2048 channels (CTAs of at most 256
-// threads), 2 above (at most 512), so a wide row keeps several CTAs on an SM.
-inline int row_vectors(int C) { return C <= 2048 ? 1 : 2; }
-constexpr int row_threads(int V) { return V == 1 ? 256 : 512; }
-// Warps of one slot, and slots of one CTA: enough to make 8 warps of a CTA
+constexpr int kMaxSlots = 6;            // per CTA; named barriers 1 .. 6
+
+// Kernels are built for three widths of a row.  A thread holds V times eight
+// channels: one up to 1536 channels, two above, so that wide rows too keep
+// CTAs of few warps, several on an SM.
+struct Tier {
+  int vectors, threads;  // V, and the largest CTA
+};
+constexpr Tier kTiers[3] = {{1, 192}, {2, 320}, {2, 512}};
+inline int tier_of(int C) { return C <= 1536 ? 0 : C <= 5120 ? 1 : 2; }
+// Warps of one slot, and slots of one CTA: enough to make 6 warps of a CTA
 // where a row needs fewer.
 __host__ __device__ inline int slot_warps(int C, int V) { return (C + 256 * V - 1) / (256 * V); }
 __host__ __device__ inline int slots_per_cta(int W) { return W >= kMaxSlots ? 1 : kMaxSlots / W; }
+
+// Warps of `regs` registers a thread that an SM holds: each of its four
+// schedulers has 512 registers a lane.
+constexpr int resident_warps(int regs) { return 4 * (512 / regs); }
 
 struct Slot {
   int index;    // in the CTA
   int W, warp;  // warps of the slot; this thread's among them
   int lane, tid;
-  float* red;   // 2 * W * kSlotRed floats of shared memory
+  float* red;   // 2 * kSlotRow floats of shared memory, zeros at the start
   int phase;
 };
 
 // Floats one warp contributes to a slot reduction, at most.
 constexpr int kSlotRed = 4;
-constexpr int kSlotRedFloats = 2 * 16 * kSlotRed;  // of a CTA of at most 16 warps
+constexpr int kSlotRow = 16 * kSlotRed;  // of a slot of at most 16 warps
+constexpr int kSlotRedFloats = kMaxSlots * 2 * kSlotRow;
 
 SPARGE_DEV Slot make_slot(int W, float* red) {
   Slot s;
@@ -59,9 +69,14 @@ SPARGE_DEV Slot make_slot(int W, float* red) {
   s.W = W;
   s.warp = warp - s.index * W;
   s.tid = s.warp * 32 + s.lane;
-  s.red = red + s.index * W * 2 * kSlotRed;
+  s.red = red + s.index * 2 * kSlotRow;
   s.phase = 0;
   return s;
+}
+
+// Before the first reduction, with a barrier behind it.
+SPARGE_DEV void clear_red(float* red) {
+  for (int i = threadIdx.x; i < kSlotRedFloats; i += blockDim.x) red[i] = 0.f;
 }
 
 SPARGE_DEV void slot_sync(const Slot& s) {
@@ -96,44 +111,41 @@ SPARGE_DEV float warp_sums(const float (&in)[K], int lane) {
   return v[0];
 }
 
-// K floats of every warp of the slot, from the lanes that warp_sums leaves them
-// in, to every thread: out[w * kSlotRed + k].  The two halves of `red`
+// Joins the warps of a slot.  Every warp leaves up to four floats in its row of
+// `red`; every warp then reads all of them at once, lane l the float l / 8 of
+// warp l % 8 (and of warp l % 8 + 8: a slot has at most 16), and finishes with
+// three shuffles instead of a loop over the warps.  The two halves of `red`
 // alternate, so one barrier a call is enough: a warp cannot reach the next but
 // one call before every warp has read this one's values.
-template <int K>
-SPARGE_DEV const float* slot_exchange(Slot& s, float mine) {
-  static_assert(K <= kSlotRed, "reduction buffer");
-  float* red = s.red + s.phase * s.W * kSlotRed;
+SPARGE_DEV float* slot_half(Slot& s) {
+  float* red = s.red + s.phase * kSlotRow;
   s.phase ^= 1;
-  if (s.lane % (32 / K) == 0) red[s.warp * kSlotRed + s.lane / (32 / K)] = mine;
-  slot_sync(s);
   return red;
+}
+// Sum over the eight lanes of a group.
+SPARGE_DEV float sum_of_8(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 // Sums v[0..K) over the slot's threads; every thread gets the sums.
 template <int K>
 SPARGE_DEV void slot_sum(Slot& s, float (&v)[K]) {
+  static_assert(K <= kSlotRed, "reduction buffer");
   const float mine = warp_sums(v, s.lane);
   if (s.W == 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, mine, k * (32 / K));
     return;
   }
-  const float* red = slot_exchange<K>(s, mine);
+  float* red = slot_half(s);
+  if (s.lane % (32 / K) == 0) red[s.warp * kSlotRed + s.lane / (32 / K)] = mine;
+  slot_sync(s);
+  const float* in = red + (s.lane & 7) * kSlotRed + (s.lane >> 3) % K;
+  const float sum = sum_of_8(in[0] + in[8 * kSlotRed]);
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = 0.f;
-  for (int w = 0; w < s.W; ++w) {
-    if constexpr (K == 4) {
-      const float4 r = *reinterpret_cast<const float4*>(red + w * kSlotRed);
-      v[0] += r.x, v[1] += r.y, v[2] += r.z, v[3] += r.w;
-    } else if constexpr (K == 2) {
-      const float2 r = *reinterpret_cast<const float2*>(red + w * kSlotRed);
-      v[0] += r.x, v[1] += r.y;
-    } else {
-#pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += red[w * kSlotRed + k];
-    }
-  }
+  for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, sum, 8 * k);
 }
 
 // ------------------------------------------------------ stages of a thread
@@ -253,7 +265,9 @@ SPARGE_DEV Raw8<T> unstage8(Ring src) {
 }
 
 // ------------------------------------------------------- sums of partial rows
-// out[o][c] = sum over r < nrow, in that order, of src[(o * nrow + r) * ld + c].
+// out[o][c] = sum over r < nrow of src[(o * nrow + r) * ld + c], in an order that
+// depends on nrow alone.  C and ld are multiples of 4; 16-byte aligned (out: 8
+// for bf16).
 struct ReduceJob {
   const float* src;
   void* out;
