@@ -344,9 +344,10 @@ constexpr int fwd_rows() {
 }
 // CTAs of an SM that the registers are budgeted for.  At 480p two: three cost a
 // reload between the two passes over a token (115 us forward against 104).  The
-// wide forward runs best with two as well (720p: 782 us, one 830).
-constexpr int fwd_residents(int tier) { return tier == 2 ? 1 : 2; }
-constexpr int bwd_residents(int tier) { return tier == 0 ? 2 : 1; }
+// wide forward too is launched as if two were resident (720p: 777 us, 830 with
+// a grid for one).
+constexpr int fwd_residents(int) { return 2; }
+constexpr int bwd_residents(int V) { return V == 1 ? 2 : 1; }
 // Pieces of one stage, and of a thread's whole ring with the weights behind it.
 template <typename TX, int FORM, int V>
 constexpr int fwd_pieces() {
@@ -379,10 +380,9 @@ struct Share {
   }
 };
 
-template <typename TX, bool INTER, int D, int TIER, int FORM>
-__global__ void __launch_bounds__(kTiers[TIER].threads, fwd_residents(TIER)) heads_fwd_kernel(
+template <typename TX, bool INTER, int D, int V, int FORM>
+__global__ void __launch_bounds__(row_threads(V), V == 1 ? fwd_residents(V) : 0) heads_fwd_kernel(
     const __grid_constant__ HeadsParams p) {
-  constexpr int V = kTiers[TIER].vectors;
   constexpr int T = fwd_rows<V>(), S = kFwdStages, Q8 = pieces8<TX>();
   constexpr int NT = turned_parts<FORM>(), NP = all_parts<FORM>();
   constexpr int STAGE = fwd_pieces<TX, FORM, V>(), RING = fwd_ring<TX, FORM, V>();
@@ -563,10 +563,9 @@ __global__ void __launch_bounds__(kTiers[TIER].threads, fwd_residents(TIER)) hea
   }
 }
 
-template <typename TX, bool INTER, int D, int TIER, int FORM>
-__global__ void __launch_bounds__(kTiers[TIER].threads, bwd_residents(TIER)) heads_bwd_kernel(
+template <typename TX, bool INTER, int D, int V, int FORM>
+__global__ void __launch_bounds__(row_threads(V), V == 1 ? bwd_residents(V) : 0) heads_bwd_kernel(
     const __grid_constant__ HeadsParams p) {
-  constexpr int V = kTiers[TIER].vectors;
   constexpr int S = kBwdStages, Q8 = pieces8<TX>();
   constexpr int NT = turned_parts<FORM>(), NP = all_parts<FORM>();
   constexpr int STAGE = bwd_pieces<TX, FORM, V>(), RING = bwd_ring<TX, FORM, V>();
@@ -810,7 +809,7 @@ __global__ void __launch_bounds__(kTiers[TIER].threads, bwd_residents(TIER)) hea
 
 struct HeadsPlan {
   Form form;
-  int tier, V, ctas, threads, slots;  // slots: of a CTA, at most
+  int V, ctas, threads, slots;  // slots: of a CTA, at most
   int n;             // parts beside one another in the grid
   int at[3];         // the place of each of the call's parts
   int smem;          // dynamic, of a CTA
@@ -847,8 +846,7 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
   // Together when the rows are alike: angles and barriers are shared, so 480p
   // takes less time than with a part to each blockIdx.y.
   // Wide rows only where a CTA's ring still fits the shared memory.
-  pl.tier = tier_of(widest);
-  pl.V = kTiers[pl.tier].vectors;
+  pl.V = row_vectors(widest);
   const bool joint = a.n_parts > 1 && same && turned <= 2 && plain <= 1 && turned > 0 &&
                      (pl.V == 1 || (!bwd && a.x_type == SPARGE_BF16));
   const bool full = joint && a.n_parts == 3 && a.rope != nullptr &&
@@ -868,7 +866,7 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
   pl.smem = heads_smem(pl, a.x_type == SPARGE_F32, a.d, bwd);
   const int rows = bwd ? 1 : 2 / pl.V;
   const int per_sm =
-      std::max(1, std::min(bwd ? bwd_residents(pl.tier) : fwd_residents(pl.tier),
+      std::max(1, std::min(bwd ? bwd_residents(pl.V) : fwd_residents(pl.V),
                            std::min(kSmemPerSm / (pl.smem + kSmemOfCta), 2048 / pl.threads)));
   const int64_t units = static_cast<int64_t>(a.B) * ((a.N + rows - 1) / rows);
   const int64_t need = (units + slots_min - 1) / slots_min;
@@ -935,29 +933,28 @@ cudaError_t launch_kernel(Kernel* kernel, const HeadsParams& p, const HeadsPlan&
   return cudaGetLastError();
 }
 
-template <typename TX, bool INTER, int D, int TIER>
-cudaError_t launch_tier(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cudaStream_t st) {
-  if constexpr (TIER == 0) {
+template <typename TX, bool INTER, int D, int V>
+cudaError_t launch_width(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cudaStream_t st) {
+  if constexpr (V == 1) {
     if (pl.form == kFull)
-      return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, TIER, kFull>, p, pl, st)
-                 : launch_kernel(heads_fwd_kernel<TX, INTER, D, TIER, kFull>, p, pl, st);
+      return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, V, kFull>, p, pl, st)
+                 : launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kFull>, p, pl, st);
     if (pl.form == kJoint)
-      return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, TIER, kJoint>, p, pl, st)
-                 : launch_kernel(heads_fwd_kernel<TX, INTER, D, TIER, kJoint>, p, pl, st);
+      return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, V, kJoint>, p, pl, st)
+                 : launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kJoint>, p, pl, st);
   } else if constexpr (sizeof(TX) == 2) {
-    if (pl.form == kFull) return launch_kernel(heads_fwd_kernel<TX, INTER, D, TIER, kFull>, p, pl, st);
+    if (pl.form == kFull) return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kFull>, p, pl, st);
     if (pl.form == kJoint)
-      return launch_kernel(heads_fwd_kernel<TX, INTER, D, TIER, kJoint>, p, pl, st);
+      return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kJoint>, p, pl, st);
   }
-  return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, TIER, kSingle>, p, pl, st)
-             : launch_kernel(heads_fwd_kernel<TX, INTER, D, TIER, kSingle>, p, pl, st);
+  return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, V, kSingle>, p, pl, st)
+             : launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kSingle>, p, pl, st);
 }
 
 template <typename TX, bool INTER, int D>
 cudaError_t launch_heads(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cudaStream_t st) {
-  if (pl.tier == 0) return launch_tier<TX, INTER, D, 0>(p, pl, bwd, st);
-  if (pl.tier == 1) return launch_tier<TX, INTER, D, 1>(p, pl, bwd, st);
-  return launch_tier<TX, INTER, D, 2>(p, pl, bwd, st);
+  return pl.V == 1 ? launch_width<TX, INTER, D, 1>(p, pl, bwd, st)
+                   : launch_width<TX, INTER, D, 2>(p, pl, bwd, st);
 }
 
 cudaError_t dispatch_heads(const sparge_heads& a, const HeadsParams& p, const HeadsPlan& pl,

@@ -262,8 +262,10 @@ constexpr int bwd_pieces() {
 // CTAs of an SM that the registers are budgeted for.  At 480p the backward's two
 // leave 168 a thread, so that every value of two rows is at hand (one modulation
 // a frame, both norms: 125 us against 161 with 128).
-constexpr int fwd_residents(int tier) { return tier == 0 ? 3 : tier == 1 ? 2 : 1; }
-constexpr int bwd_residents(int tier) { return tier == 0 ? 2 : 1; }
+// For wide rows the bound is left to the compiler: stated as one CTA it makes
+// slower code (720p forward: 565 us against 487).
+constexpr int fwd_residents(int V) { return V == 1 ? 3 : 2; }
+constexpr int bwd_residents(int V) { return V == 1 ? 2 : 1; }
 // Stages of the ring; wide rows have as many as a CTA of 512 threads can hold.
 template <typename TX, typename TB, int V>
 constexpr int fwd_stages() {
@@ -321,10 +323,9 @@ struct ItemWalk {
   }
 };
 
-template <typename TX, typename TB, int TIER>
-__global__ void __launch_bounds__(kTiers[TIER].threads, fwd_residents(TIER)) resnorm_fwd_kernel(
+template <typename TX, typename TB, int V>
+__global__ void __launch_bounds__(row_threads(V), V == 1 ? fwd_residents(V) : 0) resnorm_fwd_kernel(
     const __grid_constant__ ResnormParams p) {
-  constexpr int V = kTiers[TIER].vectors;
   constexpr int T = rows_at_once<V>(), S = fwd_stages<TX, TB, V>(), XQ = pieces8<TX>(), BQ = pieces8<TB>();
   constexpr int PIECES = fwd_pieces<TX, TB, V>(), STAGE = PIECES;
   extern __shared__ uint4 smem[];
@@ -496,10 +497,9 @@ __global__ void __launch_bounds__(kTiers[TIER].threads, fwd_residents(TIER)) res
 // FULL: every input is there and no thread is without channels, which takes the
 // branches out of the row loop (one modulation a frame, both norms, 480p: 124
 // instead of 155 us).
-template <typename TX, typename TB, int TIER, bool POST, bool FULL>
-__global__ void __launch_bounds__(kTiers[TIER].threads, bwd_residents(TIER)) resnorm_bwd_kernel(
+template <typename TX, typename TB, int V, bool POST, bool FULL>
+__global__ void __launch_bounds__(row_threads(V), V == 1 ? bwd_residents(V) : 0) resnorm_bwd_kernel(
     const __grid_constant__ ResnormParams p) {
-  constexpr int V = kTiers[TIER].vectors;
   constexpr int T = rows_at_once<V>(), S = bwd_stages<TX, TB, V>(), XQ = pieces8<TX>(),
                 BQ = pieces8<TB>();
   constexpr int PIECES = bwd_pieces<TX, TB, V>(), ROW = 2 * (XQ + BQ), STAGE = PIECES;
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(kTiers[TIER].threads, bwd_residents(TIER)) res
 }
 
 struct ResnormPlan {
-  int tier, V, W, per_cta, threads, ctas, slots, smem;
+  int V, W, per_cta, threads, ctas, slots, smem;
   int groups, R;
   int items, parts;  // items = groups * parts
   // backward: a sum is written per item straight to the output (one part a
@@ -731,8 +731,7 @@ int ring_bytes_of(int V, bool bwd) {
 ResnormPlan resnorm_plan(const sparge_resnorm& a, bool bwd) {
   ResnormPlan pl = {};
   const int64_t M = a.rows;
-  pl.tier = tier_of(a.C);
-  pl.V = kTiers[pl.tier].vectors;
+  pl.V = row_vectors(a.C);
   pl.W = slot_warps(a.C, pl.V);
   pl.per_cta = slots_per_cta(pl.W);
   pl.threads = pl.W * pl.per_cta * 32;
@@ -753,8 +752,9 @@ ResnormPlan resnorm_plan(const sparge_resnorm& a, bool bwd) {
   // one instead of all at once with the slowest (480p: one wave 104 us, two 101,
   // eight 93; 720p: four).
   const int per_sm =
-      std::max(1, std::min(bwd ? bwd_residents(pl.tier) : fwd_residents(pl.tier),
+      std::max(1, std::min(bwd ? bwd_residents(pl.V) : fwd_residents(pl.V),
                            std::min(kSmemPerSm / (pl.smem + kSmemOfCta), 2048 / pl.threads)));
+  
   const int waves = bwd ? 1 : pl.V == 1 ? 8 : 4;
   const int64_t most = static_cast<int64_t>(kSMs) * per_sm * waves;
   const int64_t target = most * pl.per_cta;  // slots that fill the machine
@@ -811,17 +811,17 @@ ResnormParams resnorm_params(const sparge_resnorm& a, const ResnormPlan& pl, boo
   return p;
 }
 
-template <typename TX, typename TB, int TIER>
-cudaError_t launch_tier(const ResnormParams& p, const ResnormPlan& pl, bool bwd, cudaStream_t st) {
+template <typename TX, typename TB, int V>
+cudaError_t launch_form(const ResnormParams& p, const ResnormPlan& pl, bool bwd, cudaStream_t st) {
   const bool post = p.post != nullptr;
   // (Sixteen channels a thread leave no registers for it.)
-  constexpr bool kFull = TIER == 0;
+  constexpr bool kFull = V == 1;
   const bool full = kFull && p.C % 256 == 0 && p.norm && p.b && p.dy && p.dh;
-  auto* kernel = !bwd   ? resnorm_fwd_kernel<TX, TB, TIER>
-                 : full ? (post ? resnorm_bwd_kernel<TX, TB, TIER, true, kFull>
-                                : resnorm_bwd_kernel<TX, TB, TIER, false, kFull>)
-                        : (post ? resnorm_bwd_kernel<TX, TB, TIER, true, false>
-                                : resnorm_bwd_kernel<TX, TB, TIER, false, false>);
+  auto* kernel = !bwd   ? resnorm_fwd_kernel<TX, TB, V>
+                 : full ? (post ? resnorm_bwd_kernel<TX, TB, V, true, kFull>
+                                : resnorm_bwd_kernel<TX, TB, V, false, kFull>)
+                        : (post ? resnorm_bwd_kernel<TX, TB, V, true, false>
+                                : resnorm_bwd_kernel<TX, TB, V, false, false>);
   if (pl.smem > 43 * 1024) {  // 48 KB less what the kernel declares
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
@@ -837,9 +837,7 @@ cudaError_t launch_tier(const ResnormParams& p, const ResnormPlan& pl, bool bwd,
 template <typename TX, typename TB>
 cudaError_t launch_resnorm(const ResnormParams& p, const ResnormPlan& pl, bool bwd,
                            cudaStream_t st) {
-  if (pl.tier == 0) return launch_tier<TX, TB, 0>(p, pl, bwd, st);
-  if (pl.tier == 1) return launch_tier<TX, TB, 1>(p, pl, bwd, st);
-  return launch_tier<TX, TB, 2>(p, pl, bwd, st);
+  return pl.V == 1 ? launch_form<TX, TB, 1>(p, pl, bwd, st) : launch_form<TX, TB, 2>(p, pl, bwd, st);
 }
 
 cudaError_t dispatch_resnorm(const sparge_resnorm& a, const ResnormParams& p,

@@ -29,14 +29,11 @@ constexpr int kMaxRowChannels = 8192;
 
 constexpr int kMaxSlots = 6;            // per CTA; named barriers 1 .. 6
 
-// Kernels are built for three widths of a row.  A thread holds V times eight
-// channels: one up to 1536 channels, two above, so that wide rows too keep
-// CTAs of few warps, several on an SM.
-struct Tier {
-  int vectors, threads;  // V, and the largest CTA
-};
-constexpr Tier kTiers[3] = {{1, 192}, {2, 320}, {2, 512}};
-inline int tier_of(int C) { return C <= 1536 ? 0 : C <= 5120 ? 1 : 2; }
+// A thread holds V times eight channels: one up to 1536 channels (CTAs of at most
+// 192 threads), two above (512), so that wide rows too keep CTAs of few warps,
+// several on an SM.
+inline int row_vectors(int C) { return C <= 1536 ? 1 : 2; }
+constexpr int row_threads(int V) { return V == 1 ? 192 : 512; }
 // Warps of one slot, and slots of one CTA: enough to make 6 warps of a CTA
 // where a row needs fewer.
 __host__ __device__ inline int slot_warps(int C, int V) { return (C + 256 * V - 1) / (256 * V); }
