@@ -13,6 +13,7 @@ import array
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -126,12 +127,12 @@ _SIGNATURES = {
                          _P, _P], _I),
     "sparge_rope_init": ([ctypes.POINTER(Rope), ctypes.c_int32, ctypes.POINTER(ctypes.c_int32),
                           ctypes.c_double, ctypes.POINTER(ctypes.c_double), ctypes.c_int32], _I),
-    "sparge_heads_fwd": ([ctypes.POINTER(Heads), _P], _I),
-    "sparge_heads_bwd_workspace_bytes": ([ctypes.POINTER(Heads), ctypes.POINTER(_SZ)], _I),
-    "sparge_heads_bwd": ([ctypes.POINTER(Heads), _P, _SZ, _P], _I),
-    "sparge_resnorm_fwd": ([ctypes.POINTER(Resnorm), _P], _I),
-    "sparge_resnorm_bwd_workspace_bytes": ([ctypes.POINTER(Resnorm), ctypes.POINTER(_SZ)], _I),
-    "sparge_resnorm_bwd": ([ctypes.POINTER(Resnorm), _P, _SZ, _P], _I),
+    "sparge_heads_fwd": ([_P, _P], _I),
+    "sparge_heads_bwd_workspace_bytes": ([_P, ctypes.POINTER(_SZ)], _I),
+    "sparge_heads_bwd": ([_P, _P, _SZ, _P], _I),
+    "sparge_resnorm_fwd": ([_P, _P], _I),
+    "sparge_resnorm_bwd_workspace_bytes": ([_P, ctypes.POINTER(_SZ)], _I),
+    "sparge_resnorm_bwd": ([_P, _P, _SZ, _P], _I),
     "sparge_clip_workspace_bytes": ([ctypes.c_int32, ctypes.POINTER(_SZ)], _I),
     "sparge_clip_grads": ([_P, _P, ctypes.c_int32, _F, _F, _P, _P, _SZ, _P], _I),
     "sparge_status_copy_async": ([_P, _P, _P], _I),
@@ -340,6 +341,14 @@ def sparge_attn_bwd(q, k, v, o, lse, dout, row_idx, row_cnt, col_idx, col_cnt,
 
 
 # ------------------------------------------------- around the attention
+#
+# The arguments of these calls are packed into the C structs in one go (the
+# ctypes classes above describe the same layout, field by field): at small sizes
+# a call is as long as the host takes to make it.
+_HEADS = struct.Struct("@6ifi3Pi4x" + "P3q3P3qP2i" * 3)
+_NO_PART = (0,) * 13
+_RESNORM = struct.Struct("@q5if5P3i4x3q12P")
+
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 _HEADS_NORMS = {None: 0, "token": 1, "head": 2}
 _NORMS = {None: 0, "layer": 1, "rms": 2}
@@ -352,34 +361,45 @@ def _type_of(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def _same_device(device, *ts):
-    for t in ts:
-        if t is not None and t.device != device:
-            raise ValueError("expected CUDA tensors on one device")
-    if device.type != "cuda":
+def _cuda_index(first, *others) -> int:
+    """The index of the CUDA device that all of the given tensors are on."""
+    index = first.get_device()
+    if index < 0 or not first.is_cuda:
         raise ValueError("expected CUDA tensors on one device")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError("expected CUDA tensors on one device")
+    return index
 
 
-def _call(fn, where: str, device, *args):
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _call(fn, where: str, index: int, *args):
     """One library call on the device's current stream."""
-    if device.index == torch.cuda.current_device():
-        code = fn(*args, _stream(device))
+    # (torch.cuda.current_stream(index).cuda_stream without building the Stream)
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch.cuda.current_device():
+        code = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            code = fn(*args, _stream(device))
+        with torch.cuda.device(index):
+            code = fn(*args, stream)
     if code != SPARGE_OK:
         raise SpargeError(code, where)
 
 
 def _workspace(fn, where: str, args, device, given):
+    """(pointer, bytes, and the tensor that holds them)"""
     nbytes = _SZ(0)
-    _check(fn(ctypes.byref(args), ctypes.byref(nbytes)), where + "_workspace_bytes")
-    if given is None and nbytes.value:
-        given = torch.empty(nbytes.value, dtype=torch.uint8, device=device)
+    _check(fn(args, ctypes.byref(nbytes)), where + "_workspace_bytes")
     if given is None:
-        return None, 0
-    _same_device(device, given)
-    return given, given.numel() * given.element_size()
+        if nbytes.value == 0:
+            return 0, 0, None
+        given = torch.empty(nbytes.value, dtype=torch.uint8, device=device)
+    elif given.device != device:
+        raise ValueError("expected CUDA tensors on one device")
+    return given.data_ptr(), given.numel() * given.element_size(), given
 
 
 class RopeAxes:
@@ -398,6 +418,7 @@ class RopeAxes:
         self.scale, self.interleaved = scale[:len(pairs)], bool(interleaved)
         pad = 3 - len(pairs)
         self.plan = Rope()
+        self.address = ctypes.addressof(self.plan)
         _check(load_library().sparge_rope_init(
             ctypes.byref(self.plan), self.d, (ctypes.c_int32 * 3)(*pairs, *[0] * pad),
             self.theta, (ctypes.c_double * 3)(*self.scale, *[1.0] * pad), int(self.interleaved)),
@@ -411,38 +432,42 @@ def _token_strides(t, B, N, H):
     return sb if B > 1 else 0, sn if N > 1 else 0, sh if H > 1 else 0
 
 
-def _heads_args(B, N, d, x_type, rope, grid, pos, norm, weights, eps, device):
+def _heads_head(B, N, d, x_type, n_parts, rope, grid, pos, norm, weights, eps, index):
+    """The leading fields of the packed struct, after their checks."""
     if norm not in _HEADS_NORMS:
         raise ValueError("norm must be None, 'token' or 'head'")
-    a = Heads()
-    a.B, a.N, a.d, a.x_type, a.norm, a.eps = B, N, d, x_type, _HEADS_NORMS[norm], eps
+    plan = 0
     if rope is not None:
         if rope.d != d:
             raise ValueError("the rope's head width differs from the tensors'")
-        a.rope = ctypes.addressof(rope.plan)
+        plan = rope.address
     if grid is not None:
-        if grid.dtype != torch.int32 or grid.shape != (B, 3) or not grid.is_contiguous():
-            raise ValueError("grid must be a contiguous int32 [B, 3] tensor")
-        a.grid = grid.data_ptr()
+        if (grid.dtype != torch.int32 or grid.shape != (B, 3) or not grid.is_contiguous()
+                or grid.get_device() != index):
+            raise ValueError("grid must be a contiguous int32 [B, 3] tensor on the same device")
     if pos is not None:
         if (pos.dtype != torch.int32 or pos.dim() != 3 or pos.shape[0] not in (1, B)
-                or pos.shape[1:] != (N, 3) or not pos.is_contiguous()):
-            raise ValueError("pos must be a contiguous int32 [B, N, 3] or [1, N, 3] tensor")
-        a.pos, a.pos_batch = pos.data_ptr(), pos.shape[0]
+                or pos.shape[1:] != (N, 3) or not pos.is_contiguous()
+                or pos.get_device() != index):
+            raise ValueError("pos must be a contiguous int32 [B, N, 3] or [1, N, 3] tensor on the "
+                             "same device")
     if (rope is None) != (grid is None and pos is None) or (grid is not None and pos is not None):
         raise ValueError("a rope needs grid or pos, one of the two")
-    _same_device(device, grid, pos, *weights)
-    given = [w for w in weights if w is not None]
-    if given:
-        a.weight_type = _type_of(given[0], "a norm weight")
-        if norm is None or any(w.dtype != given[0].dtype for w in given):
-            raise ValueError("norm weights need a norm and share one type")
-    return a
+    w_type = None
+    for w in weights:
+        if w is not None:
+            if norm is None or w.get_device() != index or w_type not in (None, w.dtype):
+                raise ValueError("norm weights need a norm, and share one type and the device")
+            w_type = w.dtype
+    if w_type is not None and w_type not in _TYPES:
+        raise ValueError("a norm weight must be bf16 or fp32")
+    return (B, N, d, x_type, _TYPES.get(w_type, 0), _HEADS_NORMS[norm], eps, n_parts, plan,
+            _addr(grid), _addr(pos), 0 if pos is None else pos.shape[0])
 
 
 def _norm_weight(w, norm, H, d):
     if w is None:
-        return None
+        return 0
     if w.shape != ((H * d,) if norm == "token" else (d,)) or not w.is_contiguous():
         raise ValueError("a norm weight is contiguous, [H * d] for 'token' and [d] for 'head'")
     return w.data_ptr()
@@ -458,39 +483,37 @@ def sparge_heads_fwd(q=None, k=None, v=None, rope: RopeAxes | None = None, grid=
     (``"head"``), then ``rope``: with ``grid`` (int32 [B, 3]: frames, height,
     width of each sample; tokens behind them do not turn) or ``pos`` (int32
     [B, N, 3]).  Returns (q, k, v), None for what was not given."""
-    parts = [t for t in (q, k, v) if t is not None]
-    if not parts:
+    first = q if q is not None else k if k is not None else v
+    if first is None:
         raise ValueError("nothing to lay out")
-    first = parts[0]
-    device = first.device
-    _same_device(device, q, k, v)
+    index = _cuda_index(first, q, k, v)
     if first.dim() != 4:
         raise ValueError("expected [B, N, H, d] tensors")
     B, N, _, d = first.shape
-    a = _heads_args(B, N, d, _type_of(first, "q, k and v"), rope, grid, pos, norm,
-                    (q_weight, k_weight), eps, device)
-    res, n = [None, None, None], 0
+    dtype, device = first.dtype, first.device
+    res, parts = [None, None, None], ()
     for i, (t, w) in enumerate(((q, q_weight), (k, k_weight), (v, None))):
         if t is None:
             if w is not None:
                 raise ValueError("a norm weight without its tensor")
             continue
         H = t.shape[2] if t.dim() == 4 else 0
-        if t.shape != (B, N, H, d) or t.dtype != first.dtype:
+        if t.shape != (B, N, H, d) or t.dtype != dtype:
             raise ValueError("q, k and v share their type, batch, length and head width")
-        y = out[i] if out is not None and out[i] is not None else None
+        y = out[i] if out is not None else None
         if y is None:
             y = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=device)
-        else:
-            _same_device(device, y)
-            if y.shape != (B, H, N, d) or y.dtype != torch.bfloat16 or not y.is_contiguous():
-                raise ValueError("out must be contiguous bf16 [B, H, N, d] tensors")
-        p = a.part[n]
-        p.x, p.x_stride = t.data_ptr(), _token_strides(t, B, N, H)
-        p.weight, p.y, p.H, p.plain = _norm_weight(w, norm, H, d), y.data_ptr(), H, i == 2
-        res[i], n = y, n + 1
-    a.n_parts = n
-    _call(load_library().sparge_heads_fwd, "sparge_heads_fwd", device, ctypes.byref(a))
+        elif (y.shape != (B, H, N, d) or y.dtype != torch.bfloat16 or not y.is_contiguous()
+              or y.get_device() != index):
+            raise ValueError("out must be contiguous bf16 [B, H, N, d] tensors on the same device")
+        parts += (t.data_ptr(), *_token_strides(t, B, N, H), _norm_weight(w, norm, H, d),
+                  y.data_ptr(), 0, 0, 0, 0, 0, H, i == 2)
+        res[i] = y
+    n = len(parts) // 13
+    args = _HEADS.pack(*_heads_head(B, N, d, _type_of(first, "q, k and v"), n, rope, grid, pos,
+                                    norm, (q_weight, k_weight), eps, index),
+                       *parts, *_NO_PART * (3 - n))
+    _call(load_library().sparge_heads_fwd, "sparge_heads_fwd", index, args)
     return tuple(res)
 
 
@@ -502,23 +525,20 @@ def sparge_heads_bwd(dq=None, dk=None, dv=None, q=None, k=None, rope: RopeAxes |
     Returns (dq, dk, dv, dq_weight, dk_weight): [B, N, H, d] in the inputs'
     type (``dtype`` where neither q nor k is given), written into ``out`` where
     that is given (slices of one buffer, say), and the weights' gradients."""
-    parts = [t for t in (dq, dk, dv) if t is not None]
-    if not parts:
+    first = dq if dq is not None else dk if dk is not None else dv
+    if first is None:
         raise ValueError("no gradient given")
-    first = parts[0]
-    device = first.device
-    _same_device(device, dq, dk, dv, q, k)
+    index = _cuda_index(first, dq, dk, dv, q, k)
     if first.dim() != 4:
         raise ValueError("expected [B, H, N, d] gradients")
     B, _, N, d = first.shape
+    device = first.device
     outs = out if out is not None else (None, None, None)
-    typed = [t for t in (q, k, *outs) if t is not None]
-    dtype = typed[0].dtype if typed else (dtype or torch.bfloat16)
-    if dtype not in _TYPES or any(t.dtype != dtype for t in typed):
+    typed = [t.dtype for t in (q, k, *outs) if t is not None]
+    dtype = typed[0] if typed else (dtype or torch.bfloat16)
+    if dtype not in _TYPES or any(t != dtype for t in typed):
         raise ValueError("q, k and out share one type, bf16 or fp32")
-    a = _heads_args(B, N, d, _TYPES[dtype], rope, grid, pos, norm, (q_weight, k_weight), eps,
-                    device)
-    res, n = [None] * 5, 0
+    res, parts = [None] * 5, ()
     for i, (g, x, w) in enumerate(((dq, q, q_weight), (dk, k, k_weight), (dv, None, None))):
         if g is None:
             if w is not None:
@@ -527,32 +547,33 @@ def sparge_heads_bwd(dq=None, dk=None, dv=None, q=None, k=None, rope: RopeAxes |
         H = g.shape[1] if g.dim() == 4 else 0
         if g.shape != (B, H, N, d) or g.dtype != torch.bfloat16 or not g.is_contiguous():
             raise ValueError("gradients are contiguous bf16 [B, H, N, d] tensors")
-        p = a.part[n]
-        p.y, p.H, p.plain = g.data_ptr(), H, i == 2
+        xp, xs, wp, dw = 0, (0, 0, 0), 0, 0
         if norm is not None and i < 2:
             if x is None or x.shape != (B, N, H, d):
                 raise ValueError("a norm's gradient needs its input, [B, N, H, d]")
-            p.x, p.x_stride = x.data_ptr(), _token_strides(x, B, N, H)
-            p.weight = _norm_weight(w, norm, H, d)
+            xp, xs = x.data_ptr(), _token_strides(x, B, N, H)
             if w is not None:
+                wp = _norm_weight(w, norm, H, d)
                 res[3 + i] = torch.empty_like(w)
-                p.dweight = res[3 + i].data_ptr()
+                dw = res[3 + i].data_ptr()
         dx = outs[i]
         if dx is None:
             dx = torch.empty((B, N, H, d), dtype=dtype, device=device)
-        else:
-            _same_device(device, dx)
-            if dx.shape != (B, N, H, d):
-                raise ValueError("out must be [B, N, H, d] tensors")
-            if any(st == 0 and n_ > 1 for st, n_ in zip(dx.stride(), dx.shape)):
-                raise ValueError("out must not repeat elements")
-        p.dx, p.dx_stride = dx.data_ptr(), _token_strides(dx, B, N, H)
-        res[i], n = dx, n + 1
-    a.n_parts = n
+        elif dx.shape != (B, N, H, d) or dx.get_device() != index:
+            raise ValueError("out must be [B, N, H, d] tensors on the same device")
+        elif any(st == 0 and n_ > 1 for st, n_ in zip(dx.stride(), dx.shape)):
+            raise ValueError("out must not repeat elements")
+        parts += (xp, *xs, wp, g.data_ptr(), dx.data_ptr(), *_token_strides(dx, B, N, H), dw, H,
+                  i == 2)
+        res[i] = dx
+    n = len(parts) // 13
+    args = _HEADS.pack(*_heads_head(B, N, d, _TYPES[dtype], n, rope, grid, pos, norm,
+                                    (q_weight, k_weight), eps, index),
+                       *parts, *_NO_PART * (3 - n))
     lib = load_library()
-    ws, size = _workspace(lib.sparge_heads_bwd_workspace_bytes, "sparge_heads_bwd", a, device,
-                          workspace)
-    _call(lib.sparge_heads_bwd, "sparge_heads_bwd", device, ctypes.byref(a), _ptr(ws), size)
+    ws, size, _hold = _workspace(lib.sparge_heads_bwd_workspace_bytes, "sparge_heads_bwd", args,
+                                 device, workspace)
+    _call(lib.sparge_heads_bwd, "sparge_heads_bwd", index, args, ws, size)
     return tuple(res)
 
 
@@ -560,7 +581,7 @@ def _modulation(m, what, B, N, C):
     """(pointer, groups, stride) of a gate, scale or shift: [C] for all tokens,
     or [B, F, C] with a row for each run of N / F tokens of a sample."""
     if m is None:
-        return None, 1, 0
+        return 0, 1, 0
     if m.dtype != torch.float32 or m.stride(-1) != 1:
         raise ValueError(f"{what} must be fp32 with contiguous channels")
     if m.shape == (C,):
@@ -579,30 +600,25 @@ def _modulation(m, what, B, N, C):
     return m.data_ptr(), b * f, m.stride(1)
 
 
-def _resnorm_args(x, branch, gate, scale, shift, norm, unit_offset, post_weight, eps, h_type):
+def _resnorm_head(x, branch, gate, scale, shift, norm, unit_offset, post_weight, eps, h_type):
+    """The leading fields of the packed struct, after their checks."""
     if norm not in _NORMS:
         raise ValueError("norm must be None, 'layer' or 'rms'")
     if x.dim() not in (2, 3) or not x.is_contiguous():
         raise ValueError("x must be a contiguous [B, N, C] or [N, C] tensor")
-    _same_device(x.device, branch, gate, scale, shift, post_weight)
-    C = x.shape[-1]
-    B, N = (1, x.shape[0]) if x.dim() == 2 else x.shape[:2]
-    a = Resnorm()
-    a.rows, a.C, a.x_type = B * N, C, _type_of(x, "x")
-    if branch is not None and (branch.shape != x.shape or not branch.is_contiguous()):
+    shape = x.shape
+    C = shape[-1]
+    B, N = (1, shape[0]) if len(shape) == 2 else shape[:2]
+    if branch is not None and (branch.shape != shape or not branch.is_contiguous()):
         raise ValueError("branch must be contiguous, of x's shape")
-    a.branch_type, a.norm, a.unit_offset, a.eps = h_type, _NORMS[norm], bool(unit_offset), eps
-    a.x = x.data_ptr()
-    a.branch = branch.data_ptr() if branch is not None else None
-    a.gate, a.gate_groups, a.gate_stride = _modulation(gate, "gate", B, N, C)
-    a.scale, a.scale_groups, a.scale_stride = _modulation(scale, "scale", B, N, C)
-    a.shift, a.shift_groups, a.shift_stride = _modulation(shift, "shift", B, N, C)
-    if post_weight is not None:
-        if (post_weight.shape != (C,) or post_weight.dtype != torch.float32
-                or not post_weight.is_contiguous()):
-            raise ValueError("post_weight must be contiguous fp32 [C]")
-        a.post_weight = post_weight.data_ptr()
-    return a
+    if post_weight is not None and (post_weight.shape != (C,) or not post_weight.is_contiguous()
+                                    or post_weight.dtype != torch.float32):
+        raise ValueError("post_weight must be contiguous fp32 [C]")
+    gp, gg, gs = _modulation(gate, "gate", B, N, C)
+    cp, cg, cs = _modulation(scale, "scale", B, N, C)
+    sp, sg, ss = _modulation(shift, "shift", B, N, C)
+    return (B * N, C, _type_of(x, "x"), h_type, _NORMS[norm], unit_offset, eps, x.data_ptr(),
+            _addr(branch), gp, cp, sp, gg, cg, sg, gs, cs, ss, _addr(post_weight))
 
 
 def sparge_resnorm_fwd(x, branch=None, gate=None, scale=None, shift=None,
@@ -616,6 +632,7 @@ def sparge_resnorm_fwd(x, branch=None, gate=None, scale=None, shift=None,
     y is x where there is no branch, h (of the branch's type, or ``h_dtype``)
     is None without a norm, stats (fp32 [3, tokens]) is what the backward
     needs."""
+    index = _cuda_index(x, branch, gate, scale, shift, post_weight)
     if branch is not None:
         h_type = _type_of(branch, "branch")
         if h_dtype is not None and h_dtype != branch.dtype:
@@ -626,18 +643,17 @@ def sparge_resnorm_fwd(x, branch=None, gate=None, scale=None, shift=None,
         if h_dtype not in _TYPES:
             raise ValueError("h must be bf16 or fp32")
         h_type = _TYPES[h_dtype]
-    a = _resnorm_args(x, branch, gate, scale, shift, norm, unit_offset, post_weight, eps, h_type)
+    head = _resnorm_head(x, branch, gate, scale, shift, norm, bool(unit_offset), post_weight, eps,
+                         h_type)
     y, h, stats = x, None, None
     if branch is not None:
         y = torch.empty_like(x)
-        a.y = y.data_ptr()
     if norm is not None:
         h = torch.empty_like(x, dtype=h_dtype)
-        a.h = h.data_ptr()
     if want_stats and (norm is not None or post_weight is not None):
-        stats = torch.empty((3, a.rows), dtype=torch.float32, device=x.device)
-        a.stats = stats.data_ptr()
-    _call(load_library().sparge_resnorm_fwd, "sparge_resnorm_fwd", x.device, ctypes.byref(a))
+        stats = torch.empty((3, head[0]), dtype=torch.float32, device=x.device)
+    args = _RESNORM.pack(*head, y.data_ptr(), _addr(h), _addr(stats), 0, 0, 0, 0, 0, 0, 0, 0)
+    _call(load_library().sparge_resnorm_fwd, "sparge_resnorm_fwd", index, args)
     return y, h, stats
 
 
@@ -647,37 +663,28 @@ def sparge_resnorm_bwd(dy, dh, x, branch=None, gate=None, scale=None, shift=None
     """Gradients of ``sparge_resnorm_fwd``: returns (dx, dbranch, dgate, dscale,
     dshift, dpost), None for what was not given.  ``dy`` or ``dh`` may be None
     (zero).  ``want_mods=False`` leaves the four sums out."""
+    index = _cuda_index(x, branch, gate, scale, shift, post_weight, dy, dh, stats)
     like = branch if branch is not None else dh if dh is not None else x
-    a = _resnorm_args(x, branch, gate, scale, shift, norm, unit_offset, post_weight, 0.0,
-                      _type_of(like, "branch and dh"))
-    device = x.device
-    _same_device(device, dy, dh, stats)
+    head = _resnorm_head(x, branch, gate, scale, shift, norm, bool(unit_offset), post_weight, 0.0,
+                         _type_of(like, "branch and dh"))
     for t, ref, what in ((dy, x, "dy"), (dh, like, "dh")):
         if t is not None and (t.shape != x.shape or t.dtype != ref.dtype
                               or not t.is_contiguous()):
             raise ValueError(f"{what} must be contiguous, of x's shape and its own result's type")
-    if stats is not None:
-        if stats.dtype != torch.float32 or stats.numel() != 3 * a.rows or not stats.is_contiguous():
-            raise ValueError("stats must be the forward's fp32 [3, tokens]")
-        a.stats = stats.data_ptr()
-    a.dy, a.dh = (t.data_ptr() if t is not None else None for t in (dy, dh))
+    if stats is not None and (stats.dtype != torch.float32 or stats.numel() != 3 * head[0]
+                              or not stats.is_contiguous()):
+        raise ValueError("stats must be the forward's fp32 [3, tokens]")
+    device = x.device
     dx = torch.empty_like(x)
-    a.dx = dx.data_ptr()
-    dbranch = None
-    if branch is not None:
-        dbranch = torch.empty_like(branch)
-        a.dbranch = dbranch.data_ptr()
-    sums = [None] * 4
-    if want_mods:
-        for i, (m, name) in enumerate(((gate, "dgate"), (scale, "dscale"), (shift, "dshift"),
-                                       (post_weight, "dpost"))):
-            if m is not None:
-                sums[i] = torch.empty(m.shape, dtype=torch.float32, device=device)
-                setattr(a, name, sums[i].data_ptr())
+    dbranch = torch.empty_like(branch) if branch is not None else None
+    sums = [torch.empty(m.shape, dtype=torch.float32, device=device)
+            if want_mods and m is not None else None for m in (gate, scale, shift, post_weight)]
+    args = _RESNORM.pack(*head, 0, 0, _addr(stats), _addr(dy), _addr(dh), dx.data_ptr(),
+                         _addr(dbranch), *(_addr(t) for t in sums))
     lib = load_library()
-    ws, size = _workspace(lib.sparge_resnorm_bwd_workspace_bytes, "sparge_resnorm_bwd", a, device,
-                          workspace)
-    _call(lib.sparge_resnorm_bwd, "sparge_resnorm_bwd", device, ctypes.byref(a), _ptr(ws), size)
+    ws, size, _hold = _workspace(lib.sparge_resnorm_bwd_workspace_bytes, "sparge_resnorm_bwd",
+                                 args, device, workspace)
+    _call(lib.sparge_resnorm_bwd, "sparge_resnorm_bwd", index, args, ws, size)
     return (dx, dbranch, *sums)
 
 
@@ -692,14 +699,16 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
-def _tensor_list(tensors, device, what):
+def _tensor_list(tensors, index, what):
     rows = []
+    types, strided = _TYPES, torch.strided
     for t in tensors:
-        if t.layout is not torch.strided or t.dtype not in _TYPES or t.device != device:
+        if t.layout is not strided or t.dtype not in types or t.get_device() != index:
             raise ValueError(f"{what} must be dense bf16 or fp32 CUDA tensors on one device")
-        if not (t.is_contiguous() or t.numel() == 0 or _dense(t)):
+        n = t.numel()
+        if not (t.is_contiguous() or n == 0 or _dense(t)):
             raise ValueError(f"{what} must have no gaps or repeated elements")
-        rows += (t.data_ptr(), t.numel(), _TYPES[t.dtype])
+        rows += (t.data_ptr(), n, types[t.dtype])
     return array.array("q", rows)  # sparge_tensor: pointer, int64, int32 and padding
 
 
@@ -713,17 +722,15 @@ def sparge_clip_grads(grads, max_norm: float | None, out=None, eps: float = 1e-6
         raise ValueError("expected at least one gradient")
     if max_norm is not None and not (math.isfinite(max_norm) and max_norm >= 0):
         raise ValueError("max_norm must be finite and not negative")
-    device = grads[0].device
-    _same_device(device)
-    table = _tensor_list(grads, device, "gradients")
-    n = len(grads)
+    index = _cuda_index(grads[0])
+    device, n = grads[0].device, len(grads)
+    table = _tensor_list(grads, index, "gradients")
     outs = None
     if out is not None:
         out = list(out)
-        if len(out) != n or any(o.shape != g.shape or o.dtype != g.dtype or o.stride() != g.stride()
-                                for o, g in zip(out, grads)):
-            raise ValueError("out must match the gradients in shape, type and strides")
-        _same_device(device, *out)
+        if len(out) != n or any(o.shape != g.shape or o.dtype != g.dtype or o.get_device() != index
+                                or o.stride() != g.stride() for o, g in zip(out, grads)):
+            raise ValueError("out must match the gradients in shape, type, strides and device")
         outs = array.array("q", [o.data_ptr() for o in out])
     lib = load_library()
     if workspace is None:
@@ -731,9 +738,10 @@ def sparge_clip_grads(grads, max_norm: float | None, out=None, eps: float = 1e-6
         _check(lib.sparge_clip_workspace_bytes(n, ctypes.byref(nbytes)),
                "sparge_clip_workspace_bytes")
         workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=device)
-    _same_device(device, workspace)
+    elif workspace.device != device:
+        raise ValueError("expected CUDA tensors on one device")
     norm = torch.empty((), dtype=torch.float32, device=device)
-    _call(lib.sparge_clip_grads, "sparge_clip_grads", device, table.buffer_info()[0],
+    _call(lib.sparge_clip_grads, "sparge_clip_grads", index, table.buffer_info()[0],
           outs.buffer_info()[0] if outs is not None else None, n,
           -1.0 if max_norm is None else float(max_norm), eps, norm.data_ptr(),
           workspace.data_ptr(), workspace.numel() * workspace.element_size())

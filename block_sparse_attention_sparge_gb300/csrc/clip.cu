@@ -8,13 +8,18 @@
 // get the same bits, and scales its chunks.  The second takes the chunks in
 // reverse: the ones that the first read last are still in L2.
 //
-// A thread squares and adds 32 values in fp32, then adds that to an fp64 sum.
-// Where the fp32 sum left the range in which no square that matters over- or
-// underflows (below 2^-90 or above 2^126), those values are read again and done
-// in fp64, so gradients of any size that fp32 holds give a norm of full
-// precision.  fp64 runs at 1/60 of the fp32 rate here (a warp's addition takes
-// the pipe some 15 cycles): an operation for every value would cap the pass
-// below the memory's rate, and even the last sums are left to single warps.
+// A thread squares and adds 64 values in fp32, four such sums at a time, then
+// adds that to an fp64 sum.  Where a sum left the range in which no square that
+// matters over- or underflows (below 2^-90 or above 2^124), its values are read
+// again and scaled by a power of two first, so gradients of any size that fp32
+// holds give a norm of full precision.  fp64 runs at 1/60 of the fp32 rate here
+// (an addition of a warp takes the pipe some 15 cycles): one for every 32 values
+// kept the pipe busy half of the time, and the last sums are left to single
+// warps (a list of four small tensors: 6 us, 13 with all threads at it).
+//
+// Bound by memory: 680M bf16 values take 203 us for the norm (6.7 TB/s) and 599
+// us in all, which is three passes over 1.36 GB at the rate of a copy; the second
+// read is the price of a factor that only the whole norm gives.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -32,8 +37,12 @@ namespace sparge {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kChunk = kClipThreads * 32;  // values a CTA takes at a time
-constexpr int kClipCtas = kSMs * 6;        // sums of one launch in the workspace
+constexpr int kVectors = 8;  // of eight values, in flight in a thread
+constexpr int kChunk = kClipThreads * 8 * kVectors;  // values a CTA takes at a time
+// The first launch is resident as a whole; the second runs in waves, whose CTAs
+// end one by one instead of all with the slowest (634 us in one, 603 in five,
+// 599 in eleven).
+constexpr int kNormCtas = kSMs * 3, kScaleCtas = kSMs * 32;
 constexpr int kSmallList = 48, kLargeList = 1024;  // tensors of one launch
 
 // A list of tensors as a kernel parameter (27.7 KB of the 32 KB there is for
@@ -84,50 +93,74 @@ SPARGE_DEV void square8(const float (&f)[8], uint64_t& a, uint64_t& b) {
   b = ffma2(s, s, b);
 }
 
-// Eight values of the chunk from place `at`, zeros behind its end.
-template <typename T>
-SPARGE_DEV void load_edge(const T* in, int at, int64_t left, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = at + i < left ? static_cast<float>(in[at + i]) : 0.f;
-}
+// A thread's sum: four chunks' worth in fp32, then on to fp64.
+struct Sum {
+  double total = 0.0;
+  float part = 0.f;
+  int n = 0;
+  SPARGE_DEV void add(float s) {
+    part += s;
+    if (++n == 4) flush();
+  }
+  SPARGE_DEV void flush() {
+    total += part;
+    part = 0.f;
+    n = 0;
+  }
+};
 
-// This thread's 32 values of a chunk: four groups of eight consecutive ones.
-// `ahead` runs while the loads are in flight.
-template <typename T, typename Ahead>
-SPARGE_DEV double chunk_squares(const T* in, int64_t left, const Ahead& ahead) {
+// Sum of the squares of this thread's values of a chunk, scaled by f before they
+// are squared (SCALED).  `ahead` runs while the loads are in flight.
+template <bool SCALED, typename T, typename Ahead>
+SPARGE_DEV float chunk_squares(const T* in, int64_t left, float f, const Ahead& ahead) {
   uint64_t a = 0, b = 0;
   if (left >= kChunk && (reinterpret_cast<uintptr_t>(in) & 15) == 0) {
-    Raw8<T> r[4];
+    Raw8<T> r[kVectors];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = load8(in + (k * kClipThreads + threadIdx.x) * 8);
+    for (int k = 0; k < kVectors; ++k) r[k] = load8(in + (k * kClipThreads + threadIdx.x) * 8);
     ahead();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float f[8];
-      unpack8(r[k], f);
-      square8(f, a, b);
+    for (int k = 0; k < kVectors; ++k) {
+      float v[8];
+      unpack8(r[k], v);
+      if (SCALED) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= f;
+      }
+      square8(v, a, b);
     }
   } else {
     ahead();
-    for (int k = 0; k < 4; ++k) {
-      float f[8];
-      load_edge(in, (k * kClipThreads + threadIdx.x) * 8, left, f);
-      square8(f, a, b);
+    for (int k = 0; k < kVectors; ++k) {
+      const int at = (k * kClipThreads + threadIdx.x) * 8;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = at + i < left ? static_cast<float>(in[at + i]) : 0.f;
+        if (SCALED) v[i] *= f;
+      }
+      square8(v, a, b);
     }
   }
   a = fadd2(a, b);
-  const float s = f32x2_lo(a) + f32x2_hi(a);
-  if (s > 8.0779357e-28f && s < 8.5070592e37f) return s;  // 2^-90, 2^126
-  // All zeros need no second look; squares that vanished do.
-  double d = 0.0;
-  for (int k = 0; k < 4; ++k) {
-    float f[8];
-    load_edge(in, (k * kClipThreads + threadIdx.x) * 8, left, f);
-    for (int i = 0; i < 8; ++i) {
-      if (f[i] != 0.f) d += static_cast<double>(f[i]) * static_cast<double>(f[i]);
-    }
+  return f32x2_lo(a) + f32x2_hi(a);
+}
+
+template <typename T, typename Ahead>
+SPARGE_DEV void add_chunk(const T* in, int64_t left, const Ahead& ahead, Sum& sum) {
+  const float s = chunk_squares<false>(in, left, 1.f, ahead);
+  if (s > 8.0779357e-28f && s < 2.1267648e37f) {  // 2^-90, 2^124
+    sum.add(s);
+    return;
   }
-  return d;
+  // Out of range, or zeros: once more with the values brought into range.  Below,
+  // all of them are under 2^-45, and 2^100 keeps the smallest from vanishing;
+  // above, 2^-70 keeps the largest from overflowing, and what vanishes does not
+  // matter beside it.
+  const bool small = s < 1.f;
+  const float again =
+      chunk_squares<true>(in, left, small ? 1.2676506e30f : 8.4703295e-22f, [] {});
+  sum.total += static_cast<double>(again) * (small ? 0x1p-200 : 0x1p140);
 }
 
 SPARGE_DEV double warp_sum(double v) {
@@ -137,12 +170,12 @@ SPARGE_DEV double warp_sum(double v) {
 }
 
 template <int MAX>
-__global__ void __launch_bounds__(kClipThreads, 5) clip_norm_kernel(
+__global__ void __launch_bounds__(kClipThreads, 3) clip_norm_kernel(
     const __grid_constant__ ClipList<MAX> l, double* sums) {
   __shared__ double red[kClipThreads / 32];
   grid_launch_dependents();
   const uint32_t total = l.chunk[l.n];
-  double acc = 0.0;
+  Sum sum;
   Chunk c = {};
   if (blockIdx.x < total) c = find(l, blockIdx.x, 0, l.n);
   for (uint32_t k = blockIdx.x; k < total; k += gridDim.x) {
@@ -151,11 +184,12 @@ __global__ void __launch_bounds__(kClipThreads, 5) clip_norm_kernel(
       if (k + gridDim.x < total) c = find(l, k + gridDim.x, now.i, l.n);
     };
     if (l.bf16[now.i])
-      acc += chunk_squares(static_cast<const __nv_bfloat16*>(l.in[now.i]) + now.base, now.left, ahead);
+      add_chunk(static_cast<const __nv_bfloat16*>(l.in[now.i]) + now.base, now.left, ahead, sum);
     else
-      acc += chunk_squares(static_cast<const float*>(l.in[now.i]) + now.base, now.left, ahead);
+      add_chunk(static_cast<const float*>(l.in[now.i]) + now.base, now.left, ahead, sum);
   }
-  acc = warp_sum(acc);
+  sum.flush();
+  double acc = warp_sum(sum.total);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -168,16 +202,16 @@ template <typename T, typename Ahead>
 SPARGE_DEV void scale_chunk(const T* in, T* out, int64_t left, float c, const Ahead& ahead) {
   if (left >= kChunk &&
       ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
-    Raw8<T> r[4];
+    Raw8<T> r[kVectors];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kVectors; ++k) {
       const uint4* p = reinterpret_cast<const uint4*>(in + (k * kClipThreads + threadIdx.x) * 8);
 #pragma unroll
       for (int i = 0; i < pieces8<T>(); ++i) r[k].v[i] = p[i];
     }
     ahead();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kVectors; ++k) {
       float f[8];
       unpack8(r[k], f);
 #pragma unroll
@@ -193,7 +227,7 @@ SPARGE_DEV void scale_chunk(const T* in, T* out, int64_t left, float c, const Ah
 }
 
 template <int MAX>
-__global__ void __launch_bounds__(kClipThreads, 5) clip_scale_kernel(
+__global__ void __launch_bounds__(kClipThreads, 3) clip_scale_kernel(
     const __grid_constant__ ClipList<MAX> l, const ClipArgs a) {
   __shared__ float factor;
   const uint32_t total = l.chunk[l.n];
@@ -248,8 +282,8 @@ void fill(ClipList<MAX>& l, const sparge_tensor* t, void* const* out, int count)
   l.n = count;
 }
 
-int list_ctas(uint32_t chunks) {
-  return static_cast<int>(std::max<uint32_t>(1, std::min<uint32_t>(chunks, kClipCtas)));
+int list_ctas(uint32_t chunks, int most) {
+  return static_cast<int>(std::max<uint32_t>(1, std::min<uint32_t>(chunks, most)));
 }
 
 template <int MAX>
@@ -257,7 +291,7 @@ cudaError_t launch_norm(const sparge_tensor* t, int count, double* sums, int* ct
                         cudaStream_t st) {
   ClipList<MAX> l;
   fill(l, t, nullptr, count);
-  *ctas = list_ctas(l.chunk[count]);
+  *ctas = list_ctas(l.chunk[count], kNormCtas);
   clip_norm_kernel<MAX><<<*ctas, kClipThreads, 0, st>>>(l, sums);
   return cudaGetLastError();
 }
@@ -268,7 +302,7 @@ cudaError_t launch_scale(const sparge_tensor* t, void* const* out, int count, co
   ClipList<MAX> l;
   fill(l, t, out, count);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.max_norm < 0.f ? 1 : list_ctas(l.chunk[count]));
+  cfg.gridDim = dim3(a.max_norm < 0.f ? 1 : list_ctas(l.chunk[count], kScaleCtas));
   cfg.blockDim = dim3(kClipThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -358,7 +392,7 @@ extern "C" {
 int sparge_clip_workspace_bytes(int32_t n, size_t* bytes) {
   if (bytes == nullptr || n < 0) return SPARGE_ERR_INVALID_ARG;
   if (n > SPARGE_MAX_TENSORS) return SPARGE_ERR_UNSUPPORTED;
-  *bytes = static_cast<size_t>(lists_of(n)) * kClipCtas * sizeof(double);
+  *bytes = static_cast<size_t>(lists_of(n)) * kNormCtas * sizeof(double);
   return SPARGE_OK;
 }
 
@@ -368,7 +402,7 @@ int sparge_clip_grads(const sparge_tensor* grads, void* const* out, int32_t n, f
   const int rc = check_clip(grads, out, n, max_norm, eps, norm);
   if (rc != SPARGE_OK) return rc;
   const int lists = lists_of(n);
-  if (workspace == nullptr || ws_bytes < static_cast<size_t>(lists) * kClipCtas * sizeof(double))
+  if (workspace == nullptr || ws_bytes < static_cast<size_t>(lists) * kNormCtas * sizeof(double))
     return SPARGE_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return SPARGE_ERR_MISALIGNED;
   ClipArgs a = {};

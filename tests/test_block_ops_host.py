@@ -226,6 +226,7 @@ def test_structs_match_the_header():
     assert ctypes.sizeof(B.HeadsPart) == 96
     assert ctypes.sizeof(B.Heads) == 352
     assert ctypes.sizeof(B.Resnorm) == 208
+    assert (B._HEADS.size, B._RESNORM.size) == (352, 208)
 
 
 def test_cpu_tensors_are_refused():
