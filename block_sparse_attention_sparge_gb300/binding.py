@@ -699,17 +699,28 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
-def _tensor_list(tensors, index, what):
-    rows = []
-    types, strided = _TYPES, torch.strided
-    for t in tensors:
-        if t.layout is not strided or t.dtype not in types or t.get_device() != index:
-            raise ValueError(f"{what} must be dense bf16 or fp32 CUDA tensors on one device")
-        n = t.numel()
-        if not (t.is_contiguous() or n == 0 or _dense(t)):
-            raise ValueError(f"{what} must have no gaps or repeated elements")
-        rows += (t.data_ptr(), n, types[t.dtype])
-    return array.array("q", rows)  # sparge_tensor: pointer, int64, int32 and padding
+def _tensor_lists(grads, outs, index):
+    """The C list of the gradients and the pointers of the outputs (None: in
+    place).  One plain loop: with hundreds of tensors it is most of the call."""
+    rows, ptrs = [], []
+    code = _TYPES.get
+    for t, o in zip(grads, grads if outs is None else outs):
+        dtype, n = t.dtype, t.numel()
+        kind = code(dtype)
+        if kind is None or t.get_device() != index:
+            raise ValueError("gradients must be bf16 or fp32 CUDA tensors on one device")
+        if o is not t and (o.dtype is not dtype or o.numel() != n or o.get_device() != index):
+            raise ValueError("out must match the gradients in type, size and device")
+        if not (t.is_contiguous() and o.is_contiguous()) and n > 0:
+            if not _dense(t):
+                raise ValueError("gradients must have no gaps or repeated elements")
+            if o.shape != t.shape or o.stride() != t.stride():
+                raise ValueError("out must match the gradients in shape and strides")
+        rows += (t.data_ptr(), n, kind)
+        if outs is not None:
+            ptrs.append(o.data_ptr())
+    # sparge_tensor: pointer, int64, int32 and padding
+    return array.array("q", rows), array.array("q", ptrs) if outs is not None else None
 
 
 def sparge_clip_grads(grads, max_norm: float | None, out=None, eps: float = 1e-6, workspace=None):
@@ -724,14 +735,11 @@ def sparge_clip_grads(grads, max_norm: float | None, out=None, eps: float = 1e-6
         raise ValueError("max_norm must be finite and not negative")
     index = _cuda_index(grads[0])
     device, n = grads[0].device, len(grads)
-    table = _tensor_list(grads, index, "gradients")
-    outs = None
     if out is not None:
         out = list(out)
-        if len(out) != n or any(o.shape != g.shape or o.dtype != g.dtype or o.get_device() != index
-                                or o.stride() != g.stride() for o, g in zip(out, grads)):
-            raise ValueError("out must match the gradients in shape, type, strides and device")
-        outs = array.array("q", [o.data_ptr() for o in out])
+        if len(out) != n:
+            raise ValueError("expected one output for each gradient")
+    table, outs = _tensor_lists(grads, out, index)
     lib = load_library()
     if workspace is None:
         nbytes = _SZ(0)

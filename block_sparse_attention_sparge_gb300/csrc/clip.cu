@@ -37,8 +37,11 @@ namespace sparge {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kVectors = 8;  // of eight values, in flight in a thread
-constexpr int kChunk = kClipThreads * 8 * kVectors;  // values a CTA takes at a time
+// Vectors of eight values that a thread takes at a time: eight keep the memory
+// busy; lists that would not give every SM a chunk of that size take one (four
+// tensors of 16384 values: 5 us, 8 with eight).
+constexpr int kFewVectors = 1, kVectors = 8;
+constexpr int chunk_values(int vectors) { return kClipThreads * 8 * vectors; }
 // The first launch is resident as a whole; the second runs in waves, whose CTAs
 // end one by one instead of all with the slowest (634 us in one, 603 in five,
 // 599 in eleven).
@@ -46,7 +49,7 @@ constexpr int kNormCtas = kSMs * 3, kScaleCtas = kSMs * 32;
 constexpr int kSmallList = 48, kLargeList = 1024;  // tensors of one launch
 
 // A list of tensors as a kernel parameter (27.7 KB of the 32 KB there is for
-// the large one; the small one keeps short lists cheap to launch).
+// the large one; a launch copies all of it, so short lists have a small one).
 template <int MAX>
 struct ClipList {
   const void* in[MAX];
@@ -65,23 +68,26 @@ struct ClipArgs {
   int in_place;
 };
 
-// A chunk: values [base, base + left) of tensor i, or the first kChunk of them.
+// A chunk: values [base, base + left) of tensor i, or the first of them.
 struct Chunk {
   int i;
   int64_t base, left;
 };
 
 // Finds chunk c by bisection of the chunk starts, among tensors [lo, hi).
-template <int MAX>
+template <int VEC, int MAX>
 SPARGE_DEV Chunk find(const ClipList<MAX>& l, uint32_t c, int lo, int hi) {
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (l.chunk[mid] <= c) lo = mid;
     else hi = mid;
   }
-  const int64_t base = static_cast<int64_t>(c - l.chunk[lo]) * kChunk;
+  const int64_t base = static_cast<int64_t>(c - l.chunk[lo]) * chunk_values(VEC);
   return {lo, base, l.numel[lo] - base};
 }
+
+// The place in a chunk of this thread's k-th group of eight values.
+SPARGE_DEV int place(int k) { return (k * kClipThreads + static_cast<int>(threadIdx.x)) * 8; }
 
 // Sum of the squares of eight values.
 SPARGE_DEV void square8(const float (&f)[8], uint64_t& a, uint64_t& b) {
@@ -111,16 +117,19 @@ struct Sum {
 
 // Sum of the squares of this thread's values of a chunk, scaled by f before they
 // are squared (SCALED).  `ahead` runs while the loads are in flight.
-template <bool SCALED, typename T, typename Ahead>
+template <int VEC, bool SCALED, typename T, typename Ahead>
 SPARGE_DEV float chunk_squares(const T* in, int64_t left, float f, const Ahead& ahead) {
   uint64_t a = 0, b = 0;
-  if (left >= kChunk && (reinterpret_cast<uintptr_t>(in) & 15) == 0) {
-    Raw8<T> r[kVectors];
+  if ((reinterpret_cast<uintptr_t>(in) & 15) == 0) {
+    Raw8<T> r[VEC];
 #pragma unroll
-    for (int k = 0; k < kVectors; ++k) r[k] = load8(in + (k * kClipThreads + threadIdx.x) * 8);
+    for (int k = 0; k < VEC; ++k) {
+      const int at = place(k);
+      r[k] = at + 8 <= left ? load8(in + at) : zero8<T>();
+    }
     ahead();
 #pragma unroll
-    for (int k = 0; k < kVectors; ++k) {
+    for (int k = 0; k < VEC; ++k) {
       float v[8];
       unpack8(r[k], v);
       if (SCALED) {
@@ -129,26 +138,28 @@ SPARGE_DEV float chunk_squares(const T* in, int64_t left, float f, const Ahead& 
       }
       square8(v, a, b);
     }
+    // The last values of a tensor whose size is no multiple of eight.
+    const int64_t whole = left & ~int64_t(7);
+    if (left < chunk_values(VEC) && threadIdx.x < left - whole) {
+      const float v = SCALED ? static_cast<float>(in[whole + threadIdx.x]) * f
+                             : static_cast<float>(in[whole + threadIdx.x]);
+      a = ffma2(f32x2(v, 0.f), f32x2(v, 0.f), a);
+    }
   } else {
     ahead();
-    for (int k = 0; k < kVectors; ++k) {
-      const int at = (k * kClipThreads + threadIdx.x) * 8;
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = at + i < left ? static_cast<float>(in[at + i]) : 0.f;
-        if (SCALED) v[i] *= f;
-      }
-      square8(v, a, b);
+    const int end = static_cast<int>(left < chunk_values(VEC) ? left : chunk_values(VEC));
+    for (int at = threadIdx.x; at < end; at += kClipThreads) {
+      const float v = SCALED ? static_cast<float>(in[at]) * f : static_cast<float>(in[at]);
+      a = ffma2(f32x2(v, 0.f), f32x2(v, 0.f), a);
     }
   }
   a = fadd2(a, b);
   return f32x2_lo(a) + f32x2_hi(a);
 }
 
-template <typename T, typename Ahead>
+template <int VEC, typename T, typename Ahead>
 SPARGE_DEV void add_chunk(const T* in, int64_t left, const Ahead& ahead, Sum& sum) {
-  const float s = chunk_squares<false>(in, left, 1.f, ahead);
+  const float s = chunk_squares<VEC, false>(in, left, 1.f, ahead);
   if (s > 8.0779357e-28f && s < 2.1267648e37f) {  // 2^-90, 2^124
     sum.add(s);
     return;
@@ -159,7 +170,7 @@ SPARGE_DEV void add_chunk(const T* in, int64_t left, const Ahead& ahead, Sum& su
   // matter beside it.
   const bool small = s < 1.f;
   const float again =
-      chunk_squares<true>(in, left, small ? 1.2676506e30f : 8.4703295e-22f, [] {});
+      chunk_squares<VEC, true>(in, left, small ? 1.2676506e30f : 8.4703295e-22f, [] {});
   sum.total += static_cast<double>(again) * (small ? 0x1p-200 : 0x1p140);
 }
 
@@ -169,7 +180,7 @@ SPARGE_DEV double warp_sum(double v) {
   return v;
 }
 
-template <int MAX>
+template <int MAX, int VEC>
 __global__ void __launch_bounds__(kClipThreads, 3) clip_norm_kernel(
     const __grid_constant__ ClipList<MAX> l, double* sums) {
   __shared__ double red[kClipThreads / 32];
@@ -177,16 +188,16 @@ __global__ void __launch_bounds__(kClipThreads, 3) clip_norm_kernel(
   const uint32_t total = l.chunk[l.n];
   Sum sum;
   Chunk c = {};
-  if (blockIdx.x < total) c = find(l, blockIdx.x, 0, l.n);
+  if (blockIdx.x < total) c = find<VEC>(l, blockIdx.x, 0, l.n);
   for (uint32_t k = blockIdx.x; k < total; k += gridDim.x) {
     const Chunk now = c;
     const auto ahead = [&] {
-      if (k + gridDim.x < total) c = find(l, k + gridDim.x, now.i, l.n);
+      if (k + gridDim.x < total) c = find<VEC>(l, k + gridDim.x, now.i, l.n);
     };
     if (l.bf16[now.i])
-      add_chunk(static_cast<const __nv_bfloat16*>(l.in[now.i]) + now.base, now.left, ahead, sum);
+      add_chunk<VEC>(static_cast<const __nv_bfloat16*>(l.in[now.i]) + now.base, now.left, ahead, sum);
     else
-      add_chunk(static_cast<const float*>(l.in[now.i]) + now.base, now.left, ahead, sum);
+      add_chunk<VEC>(static_cast<const float*>(l.in[now.i]) + now.base, now.left, ahead, sum);
   }
   sum.flush();
   double acc = warp_sum(sum.total);
@@ -198,42 +209,46 @@ __global__ void __launch_bounds__(kClipThreads, 3) clip_norm_kernel(
   }
 }
 
-template <typename T, typename Ahead>
+template <int VEC, typename T, typename Ahead>
 SPARGE_DEV void scale_chunk(const T* in, T* out, int64_t left, float c, const Ahead& ahead) {
-  if (left >= kChunk &&
-      ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
-    Raw8<T> r[kVectors];
+  if (((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
+    Raw8<T> r[VEC];
 #pragma unroll
-    for (int k = 0; k < kVectors; ++k) {
-      const uint4* p = reinterpret_cast<const uint4*>(in + (k * kClipThreads + threadIdx.x) * 8);
+    for (int k = 0; k < VEC; ++k) {
+      const int at = place(k);
+      const uint4* p = reinterpret_cast<const uint4*>(in + at);
 #pragma unroll
-      for (int i = 0; i < pieces8<T>(); ++i) r[k].v[i] = p[i];
+      for (int i = 0; i < pieces8<T>(); ++i)
+        r[k].v[i] = at + 8 <= left ? p[i] : make_uint4(0, 0, 0, 0);
     }
     ahead();
 #pragma unroll
-    for (int k = 0; k < kVectors; ++k) {
+    for (int k = 0; k < VEC; ++k) {
       float f[8];
       unpack8(r[k], f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] *= c;
-      store8(out + (k * kClipThreads + threadIdx.x) * 8, f);
+      if (place(k) + 8 <= left) store8(out + place(k), f);
     }
+    const int64_t whole = left & ~int64_t(7);
+    if (left < chunk_values(VEC) && threadIdx.x < left - whole)
+      out[whole + threadIdx.x] = static_cast<T>(static_cast<float>(in[whole + threadIdx.x]) * c);
   } else {
     ahead();
-    const int end = static_cast<int>(left < kChunk ? left : kChunk);
+    const int end = static_cast<int>(left < chunk_values(VEC) ? left : chunk_values(VEC));
     for (int at = threadIdx.x; at < end; at += kClipThreads)
       out[at] = static_cast<T>(static_cast<float>(in[at]) * c);
   }
 }
 
-template <int MAX>
+template <int MAX, int VEC>
 __global__ void __launch_bounds__(kClipThreads, 3) clip_scale_kernel(
     const __grid_constant__ ClipList<MAX> l, const ClipArgs a) {
   __shared__ float factor;
   const uint32_t total = l.chunk[l.n];
   const bool writes = a.max_norm >= 0.f;
   Chunk c = {};
-  if (writes && blockIdx.x < total) c = find(l, total - 1 - blockIdx.x, 0, l.n);
+  if (writes && blockIdx.x < total) c = find<VEC>(l, total - 1 - blockIdx.x, 0, l.n);
   grid_wait();
   if (threadIdx.x < 32) {
     double v = 0.0;
@@ -253,13 +268,13 @@ __global__ void __launch_bounds__(kClipThreads, 3) clip_scale_kernel(
   for (uint32_t k = blockIdx.x; k < total; k += gridDim.x) {
     const Chunk now = c;
     const auto ahead = [&] {
-      if (k + gridDim.x < total) c = find(l, total - 1 - k - gridDim.x, 0, now.i + 1);
+      if (k + gridDim.x < total) c = find<VEC>(l, total - 1 - k - gridDim.x, 0, now.i + 1);
     };
     if (l.bf16[now.i])
-      scale_chunk(static_cast<const __nv_bfloat16*>(l.in[now.i]) + now.base,
+      scale_chunk<VEC>(static_cast<const __nv_bfloat16*>(l.in[now.i]) + now.base,
                   static_cast<__nv_bfloat16*>(l.out[now.i]) + now.base, now.left, f, ahead);
     else
-      scale_chunk(static_cast<const float*>(l.in[now.i]) + now.base,
+      scale_chunk<VEC>(static_cast<const float*>(l.in[now.i]) + now.base,
                   static_cast<float*>(l.out[now.i]) + now.base, now.left, f, ahead);
   }
 }
@@ -268,39 +283,46 @@ constexpr int64_t kMaxValues = int64_t(1) << 40;  // of one tensor
 
 // Fills a list with tensors [first, first + count).
 template <int MAX>
-void fill(ClipList<MAX>& l, const sparge_tensor* t, void* const* out, int count) {
+void fill(ClipList<MAX>& l, const sparge_tensor* t, void* const* out, int count, int vectors) {
   uint32_t chunks = 0;
+  const int64_t values = chunk_values(vectors);
   for (int i = 0; i < count; ++i) {
     l.in[i] = t[i].data;
     l.out[i] = out != nullptr ? out[i] : t[i].data;
     l.numel[i] = t[i].numel;
     l.bf16[i] = t[i].type == SPARGE_BF16;
     l.chunk[i] = chunks;
-    chunks += static_cast<uint32_t>((t[i].numel + kChunk - 1) / kChunk);
+    chunks += static_cast<uint32_t>((t[i].numel + values - 1) / values);
   }
   l.chunk[count] = chunks;
   l.n = count;
+}
+
+int list_vectors(const sparge_tensor* t, int count) {
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) total += t[i].numel;
+  return total < static_cast<int64_t>(kSMs) * chunk_values(kVectors) ? kFewVectors : kVectors;
 }
 
 int list_ctas(uint32_t chunks, int most) {
   return static_cast<int>(std::max<uint32_t>(1, std::min<uint32_t>(chunks, most)));
 }
 
-template <int MAX>
+template <int MAX, int VEC>
 cudaError_t launch_norm(const sparge_tensor* t, int count, double* sums, int* ctas,
                         cudaStream_t st) {
   ClipList<MAX> l;
-  fill(l, t, nullptr, count);
+  fill(l, t, nullptr, count, VEC);
   *ctas = list_ctas(l.chunk[count], kNormCtas);
-  clip_norm_kernel<MAX><<<*ctas, kClipThreads, 0, st>>>(l, sums);
+  clip_norm_kernel<MAX, VEC><<<*ctas, kClipThreads, 0, st>>>(l, sums);
   return cudaGetLastError();
 }
 
-template <int MAX>
+template <int MAX, int VEC>
 cudaError_t launch_scale(const sparge_tensor* t, void* const* out, int count, const ClipArgs& a,
                          bool first, cudaStream_t st) {
   ClipList<MAX> l;
-  fill(l, t, out, count);
+  fill(l, t, out, count, VEC);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.max_norm < 0.f ? 1 : list_ctas(l.chunk[count], kScaleCtas));
   cfg.blockDim = dim3(kClipThreads);
@@ -310,7 +332,7 @@ cudaError_t launch_scale(const sparge_tensor* t, void* const* out, int count, co
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = first ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, clip_scale_kernel<MAX>, l, a);
+  return cudaLaunchKernelEx(&cfg, clip_scale_kernel<MAX, VEC>, l, a);
 }
 
 // Whether two tensors that are written share memory (or one is listed twice):
@@ -413,10 +435,11 @@ int sparge_clip_grads(const sparge_tensor* grads, void* const* out, int32_t n, f
   for (int k = 0; k < lists; ++k) {
     const int first = k * kLargeList, count = std::min(n - first, kLargeList);
     int ctas = 0;
-    const cudaError_t e =
-        count <= kSmallList
-            ? launch_norm<kSmallList>(grads + first, count, a.sums + a.n_sums, &ctas, stream)
-            : launch_norm<kLargeList>(grads + first, count, a.sums + a.n_sums, &ctas, stream);
+    const bool few = list_vectors(grads + first, count) == kFewVectors;
+    auto* launch = count <= kSmallList
+                       ? (few ? launch_norm<kSmallList, kFewVectors> : launch_norm<kSmallList, kVectors>)
+                       : (few ? launch_norm<kLargeList, kFewVectors> : launch_norm<kLargeList, kVectors>);
+    const cudaError_t e = launch(grads + first, count, a.sums + a.n_sums, &ctas, stream);
     if (e != cudaSuccess) return SPARGE_ERR_CUDA;
     a.n_sums += ctas;
   }
@@ -424,10 +447,12 @@ int sparge_clip_grads(const sparge_tensor* grads, void* const* out, int32_t n, f
     const int first = k * kLargeList, count = std::min(n - first, kLargeList);
     a.norm = k == 0 ? norm : nullptr;
     void* const* o = out != nullptr ? out + first : nullptr;
-    const cudaError_t e =
+    const bool few = list_vectors(grads + first, count) == kFewVectors;
+    auto* launch =
         count <= kSmallList
-            ? launch_scale<kSmallList>(grads + first, o, count, a, k == 0, stream)
-            : launch_scale<kLargeList>(grads + first, o, count, a, k == 0, stream);
+            ? (few ? launch_scale<kSmallList, kFewVectors> : launch_scale<kSmallList, kVectors>)
+            : (few ? launch_scale<kLargeList, kFewVectors> : launch_scale<kLargeList, kVectors>);
+    const cudaError_t e = launch(grads + first, o, count, a, k == 0, stream);
     if (e != cudaSuccess) return SPARGE_ERR_CUDA;
     if (max_norm < 0.f) break;
   }

@@ -36,7 +36,7 @@ struct HeadsPart {
   const void* w;
   void* y;  // head-major bf16: the result, or the gradient that comes back
   void* dx;
-  float* dw_part;  // [slots][H * d] or, under a norm over each head, [slots][d]
+  float* dw_part;  // [CTAs][H * d] or, under a norm over each head, [CTAs][d]
   int64_t xs[3], ds[3];
   int C, W, plain;
 };
@@ -761,21 +761,41 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? bwd_residents(V) : 0)
     }
   }
   if (!norm) return;
+  // One row of weight sums a CTA: its slots, or with one weight for all heads its
+  // warps, add theirs one after the other, in shared memory that the rings no
+  // longer need.
+  const int warps = per_cta * s.W, warp = s.index * s.W + s.warp;
+  const auto cta_sync = [&] { named_barrier_sync(kMaxSlots + 1, warps * 32); };
+  float* row = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     float* out = p.part[part0 + i].dw_part;
     if (out == nullptr) continue;
+    cta_sync();  // the rings, or the row of the part before, have been read
     if (norm == SPARGE_HEADS_NORM_TOKEN) {
+      out += static_cast<int64_t>(blockIdx.x) * any.C;
+      for (int turn = 0; turn < per_cta; ++turn) {
+        if (turn == s.index) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (!at.here(v)) continue;
-        float f[8];
-        from_pairs<INTER>(dw[i * V + v], f);
-        store_row<float, SPLIT, D>(out + slot * any.C + (at.head + v * at.head_step) * D + at.c, f);
+          for (int v = 0; v < V; ++v) {
+            if (!at.here(v)) continue;
+            float f[8];
+            from_pairs<INTER>(dw[i * V + v], f);
+            float* to = row + (at.head + v * at.head_step) * D + at.c;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int o = !SPLIT || k < 4 ? k : k - 4 + D / 2;
+              if (turn > 0) f[k] += to[o];
+              if (turn + 1 < per_cta) to[o] = f[k];
+            }
+            if (turn + 1 == per_cta) store_row<float, SPLIT, D>(out + (to - row), f);
+          }
+        }
+        if (per_cta > 1) cta_sync();
       }
     } else {
-      // One weight for all heads: add the heads of the thread, of the warp, then
-      // warp after warp into the slot's angle buffer.
+      out += static_cast<int64_t>(blockIdx.x) * D;
+      // The heads of the thread, then of the warp.
       float f[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] = 0.f;
@@ -791,17 +811,17 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? bwd_residents(V) : 0)
 #pragma unroll
         for (int o = D / 8; o < 32; o *= 2) f[k] += __shfl_xor_sync(0xffffffffu, f[k], o);
       }
-      slot_sync(s);  // the angles, or the part before, have been read
-      for (int w = 0; w < s.W; ++w) {
-        if (w == s.warp && s.lane < D / 8) {
+      for (int turn = 0; turn < warps; ++turn) {
+        if (turn == warp && s.lane < D / 8) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            float* to = ang + at.c + (!SPLIT || k < 4 ? k : k - 4 + D / 2);
-            *to = w == 0 ? f[k] : *to + f[k];
-            if (w == s.W - 1) out[slot * D + (to - ang)] = *to;
+            const int o = at.c + (!SPLIT || k < 4 ? k : k - 4 + D / 2);
+            if (turn > 0) f[k] += row[o];
+            row[o] = f[k];
           }
+          if (turn + 1 == warps) store_row<float, SPLIT, D>(out + at.c, f);
         }
-        slot_sync(s);
+        cta_sync();
       }
     }
   }
@@ -876,8 +896,8 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
     if (!bwd || a.norm == 0 || a.part[i].plain || a.part[i].dweight == nullptr) continue;
     const int C = a.part[i].H * a.d;
     pl.dw_off[i] = pl.bytes;
-    pl.bytes += static_cast<size_t>(pl.ctas) * slots_per_cta(slot_warps(C, pl.V)) *
-                (a.norm == SPARGE_HEADS_NORM_TOKEN ? C : a.d) * sizeof(float);
+    pl.bytes += static_cast<size_t>(pl.ctas) * (a.norm == SPARGE_HEADS_NORM_TOKEN ? C : a.d) *
+                sizeof(float);
   }
   return pl;
 }
@@ -1107,13 +1127,13 @@ int sparge_heads_bwd(const sparge_heads* args, void* workspace, size_t ws_bytes,
     const int C = s.H * args->d;
     float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.dw_off[i]);
     p.part[pl.at[i]].dw_part = part;
-    // One row of sums a slot, of all channels or of those of a head.
+    // One row of sums a CTA, of all channels or of those of a head.
     const bool token = args->norm == SPARGE_HEADS_NORM_TOKEN;
     ReduceJob& j = jobs.job[jobs.n++];
     j.src = part;
     j.C = token ? C : args->d;
     j.ld = j.C;
-    j.nrow = pl.ctas * slots_per_cta(slot_warps(C, pl.V));
+    j.nrow = pl.ctas;
     j.nout = 1;
     j.out = s.dweight;
     j.out_bf16 = args->weight_type == SPARGE_BF16;

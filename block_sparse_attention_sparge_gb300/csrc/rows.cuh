@@ -192,6 +192,14 @@ SPARGE_DEV Raw8<T> load8(const T* p) {
   return r;
 }
 
+template <typename T>
+SPARGE_DEV Raw8<T> zero8() {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < pieces8<T>(); ++i) r.v[i] = make_uint4(0, 0, 0, 0);
+  return r;
+}
+
 SPARGE_DEV void unpack8(const Raw8<__nv_bfloat16>& r, float (&f)[8]) {
   const uint32_t u[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll

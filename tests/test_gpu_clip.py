@@ -46,6 +46,8 @@ LISTS = [
     [((3, 5), BF), ((1,), BF), ((0,), BF), ((7,), F32), ((0, 4), F32), ((16385,), BF), ((8,), BF)],
     [((1536, 100), BF), ((100,), F32), ((40000,), F32)],
     [((5,), F32)] * 49,
+    [((9,), BF)] * 256,
+    [((2,), BF)] * 257,
     [((3,), BF), ((11,), F32)] * 600,          # more than one list of 1024
     [((2, 3), F32)] * 2050,
     [(((1 << 24) + 3,), BF), ((1 << 22,), F32)],
