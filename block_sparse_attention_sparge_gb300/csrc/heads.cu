@@ -336,7 +336,12 @@ constexpr int all_parts() {
 
 // Stages of the ring: one more changes nothing at 480p (109 us both ways,
 // forward), and costs the wide forward its second CTA of an SM.
-constexpr int kFwdStages = 2, kBwdStages = 3;
+constexpr int kFwdStages = 2;
+// (A joint fp32 row of 640 threads leaves room for two.)
+template <typename TX, int THREADS>
+constexpr int bwd_stages() {
+  return THREADS == 640 && sizeof(TX) == 4 ? 2 : 3;
+}
 // Tokens a slot takes at once.
 template <int V>
 constexpr int fwd_rows() {
@@ -346,8 +351,7 @@ constexpr int fwd_rows() {
 // reload between the two passes over a token (115 us forward against 104).  The
 // wide forward too is launched as if two were resident (720p: 777 us, 830 with
 // a grid for one).
-constexpr int fwd_residents(int) { return 2; }
-constexpr int bwd_residents(int V) { return V == 1 ? 2 : 1; }
+constexpr int kFwdResidents = 2;
 // Pieces of one stage, and of a thread's whole ring with the weights behind it.
 template <typename TX, int FORM, int V>
 constexpr int fwd_pieces() {
@@ -361,9 +365,10 @@ template <typename TX, int FORM, int V>
 constexpr int fwd_ring() {
   return kFwdStages * fwd_pieces<TX, FORM, V>() + turned_parts<FORM>() * V * 2;
 }
-template <typename TX, int FORM, int V>
+template <typename TX, int FORM, int THREADS>
 constexpr int bwd_ring() {
-  return kBwdStages * bwd_pieces<TX, FORM, V>() + turned_parts<FORM>() * V * 2;
+  constexpr int V = bwd_vectors(THREADS);
+  return bwd_stages<TX, THREADS>() * bwd_pieces<TX, FORM, V>() + turned_parts<FORM>() * V * 2;
 }
 constexpr int kAngleBuffers = 2;  // of T tokens (D floats each), for every slot
 
@@ -381,7 +386,7 @@ struct Share {
 };
 
 template <typename TX, bool INTER, int D, int V, int FORM>
-__global__ void __launch_bounds__(row_threads(V), V == 1 ? fwd_residents(V) : 0) heads_fwd_kernel(
+__global__ void __launch_bounds__(row_threads(V), V == 1 ? kFwdResidents : 0) heads_fwd_kernel(
     const __grid_constant__ HeadsParams p) {
   constexpr int T = fwd_rows<V>(), S = kFwdStages, Q8 = pieces8<TX>();
   constexpr int NT = turned_parts<FORM>(), NP = all_parts<FORM>();
@@ -563,10 +568,11 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? fwd_residents(V) : 0)
   }
 }
 
-template <typename TX, bool INTER, int D, int V, int FORM>
-__global__ void __launch_bounds__(row_threads(V), V == 1 ? bwd_residents(V) : 0) heads_bwd_kernel(
+template <typename TX, bool INTER, int D, int THREADS, int FORM>
+__global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_kernel(
     const __grid_constant__ HeadsParams p) {
-  constexpr int S = kBwdStages, Q8 = pieces8<TX>();
+  constexpr int V = bwd_vectors(THREADS);
+  constexpr int S = bwd_stages<TX, THREADS>(), Q8 = pieces8<TX>();
   constexpr int NT = turned_parts<FORM>(), NP = all_parts<FORM>();
   constexpr int STAGE = bwd_pieces<TX, FORM, V>(), RING = bwd_ring<TX, FORM, V>();
   constexpr bool SPLIT = split<TX, INTER>();
@@ -829,6 +835,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? bwd_residents(V) : 0)
 
 struct HeadsPlan {
   Form form;
+  int built;  // the size of CTA that the kernel is built for
   int V, ctas, threads, slots;  // slots: of a CTA, at most
   int n;             // parts beside one another in the grid
   int at[3];         // the place of each of the call's parts
@@ -837,19 +844,22 @@ struct HeadsPlan {
   size_t bytes;
 };
 
+template <typename TX, int FORM>
+int ring_of_form(const HeadsPlan& pl, bool bwd) {
+  if (!bwd) return pl.V == 1 ? fwd_ring<TX, FORM, 1>() : fwd_ring<TX, FORM, 2>();
+  return pl.built == 192   ? bwd_ring<TX, FORM, 192>()
+         : pl.built == 640 ? bwd_ring<TX, FORM, 640>()
+                           : bwd_ring<TX, FORM, 512>();
+}
 template <typename TX>
-int ring_bytes(const HeadsPlan& pl, bool bwd) {
-  if (pl.V == 1) {
-    if (pl.form != kSingle) return bwd ? bwd_ring<TX, kJoint, 1>() : fwd_ring<TX, kJoint, 1>();
-    return bwd ? bwd_ring<TX, kSingle, 1>() : fwd_ring<TX, kSingle, 1>();
-  }
-  if (pl.form != kSingle) return fwd_ring<TX, kJoint, 2>();
-  return bwd ? bwd_ring<TX, kSingle, 2>() : fwd_ring<TX, kSingle, 2>();
+int ring_pieces(const HeadsPlan& pl, bool bwd) {
+  return pl.form == kSingle ? ring_of_form<TX, kSingle>(pl, bwd) : ring_of_form<TX, kJoint>(pl, bwd);
 }
 int heads_smem(const HeadsPlan& pl, bool f32, int d, bool bwd) {
-  const int ring = f32 ? ring_bytes<float>(pl, bwd) : ring_bytes<__nv_bfloat16>(pl, bwd);
+  const int pieces = f32 ? ring_pieces<float>(pl, bwd) : ring_pieces<__nv_bfloat16>(pl, bwd);
   const int rows = bwd ? 1 : 2 / pl.V;
-  return 16 * ring * pl.threads + pl.slots * kAngleBuffers * rows * d * static_cast<int>(sizeof(float));
+  return 16 * pieces * pl.threads +
+         pl.slots * kAngleBuffers * rows * d * static_cast<int>(sizeof(float));
 }
 
 HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
@@ -866,7 +876,8 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
   // Together when the rows are alike: angles and barriers are shared, so 480p
   // takes less time than with a part to each blockIdx.y.
   // Wide rows only where a CTA's ring still fits the shared memory.
-  pl.V = row_vectors(widest);
+  pl.built = bwd ? bwd_threads(widest) : row_threads(row_vectors(widest));
+  pl.V = bwd ? bwd_vectors(pl.built) : row_vectors(widest);
   const bool joint = a.n_parts > 1 && same && turned <= 2 && plain <= 1 && turned > 0 &&
                      (pl.V == 1 || (!bwd && a.x_type == SPARGE_BF16));
   const bool full = joint && a.n_parts == 3 && a.rope != nullptr &&
@@ -885,9 +896,11 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
   // rows.  Shared memory limits it, or registers.
   pl.smem = heads_smem(pl, a.x_type == SPARGE_F32, a.d, bwd);
   const int rows = bwd ? 1 : 2 / pl.V;
-  const int per_sm =
-      std::max(1, std::min(bwd ? bwd_residents(pl.V) : fwd_residents(pl.V),
-                           std::min(kSmemPerSm / (pl.smem + kSmemOfCta), 2048 / pl.threads)));
+  const int warps = pl.threads / 32;
+  const int by_regs = bwd ? resident_warps(bwd_regs(pl.built)) / warps
+                          : kFwdResidents * row_threads(pl.V) / pl.threads;
+  const int per_sm = std::max(1, std::min(std::min(by_regs, 64 / warps),
+                                          kSmemPerSm / (pl.smem + kSmemOfCta)));
   const int64_t units = static_cast<int64_t>(a.B) * ((a.N + rows - 1) / rows);
   const int64_t need = (units + slots_min - 1) / slots_min;
   const int64_t most = (kSMs * per_sm + pl.n - 1) / pl.n;
@@ -941,7 +954,7 @@ HeadsParams heads_params(const sparge_heads& a, const HeadsPlan& pl) {
 template <typename Kernel>
 cudaError_t launch_kernel(Kernel* kernel, const HeadsParams& p, const HeadsPlan& pl,
                           cudaStream_t st) {
-  if (pl.smem > 43 * 1024) {  // 48 KB less what the kernel declares
+  if (pl.smem > 42 * 1024) {  // 48 KB less what the kernel declares
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
     if (e != cudaSuccess) {
@@ -954,27 +967,33 @@ cudaError_t launch_kernel(Kernel* kernel, const HeadsParams& p, const HeadsPlan&
 }
 
 template <typename TX, bool INTER, int D, int V>
-cudaError_t launch_width(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cudaStream_t st) {
-  if constexpr (V == 1) {
-    if (pl.form == kFull)
-      return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, V, kFull>, p, pl, st)
-                 : launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kFull>, p, pl, st);
-    if (pl.form == kJoint)
-      return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, V, kJoint>, p, pl, st)
-                 : launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kJoint>, p, pl, st);
-  } else if constexpr (sizeof(TX) == 2) {
+cudaError_t launch_fwd(const HeadsParams& p, const HeadsPlan& pl, cudaStream_t st) {
+  if constexpr (V == 1 || sizeof(TX) == 2) {
     if (pl.form == kFull) return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kFull>, p, pl, st);
-    if (pl.form == kJoint)
-      return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kJoint>, p, pl, st);
+    if (pl.form == kJoint) return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kJoint>, p, pl, st);
   }
-  return bwd ? launch_kernel(heads_bwd_kernel<TX, INTER, D, V, kSingle>, p, pl, st)
-             : launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kSingle>, p, pl, st);
+  return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kSingle>, p, pl, st);
+}
+
+template <typename TX, bool INTER, int D, int THREADS>
+cudaError_t launch_bwd(const HeadsParams& p, const HeadsPlan& pl, cudaStream_t st) {
+  if constexpr (bwd_vectors(THREADS) == 1) {
+    if (pl.form == kFull)
+      return launch_kernel(heads_bwd_kernel<TX, INTER, D, THREADS, kFull>, p, pl, st);
+    if (pl.form == kJoint)
+      return launch_kernel(heads_bwd_kernel<TX, INTER, D, THREADS, kJoint>, p, pl, st);
+  }
+  return launch_kernel(heads_bwd_kernel<TX, INTER, D, THREADS, kSingle>, p, pl, st);
 }
 
 template <typename TX, bool INTER, int D>
 cudaError_t launch_heads(const HeadsParams& p, const HeadsPlan& pl, bool bwd, cudaStream_t st) {
-  return pl.V == 1 ? launch_width<TX, INTER, D, 1>(p, pl, bwd, st)
-                   : launch_width<TX, INTER, D, 2>(p, pl, bwd, st);
+  if (bwd) {
+    if (pl.built == 192) return launch_bwd<TX, INTER, D, 192>(p, pl, st);
+    if (pl.built == 640) return launch_bwd<TX, INTER, D, 640>(p, pl, st);
+    return launch_bwd<TX, INTER, D, 512>(p, pl, st);
+  }
+  return pl.V == 1 ? launch_fwd<TX, INTER, D, 1>(p, pl, st) : launch_fwd<TX, INTER, D, 2>(p, pl, st);
 }
 
 cudaError_t dispatch_heads(const sparge_heads& a, const HeadsParams& p, const HeadsPlan& pl,

@@ -153,13 +153,13 @@ SPARGE_DEV F8 load_mod(const float* m, int step) {
   return f8(r);
 }
 
-// One such row as a thread sees it from row to row: in registers where it covers
-// eight channels (V = 1); where it covers sixteen, in shared memory behind the
-// ring (KEEP; read through L1 instead, a third of it comes from L2: 583 instead
-// of 476 us at 720p), or where the backward's ring leaves no room, through L1.
-template <int V, bool KEEP>
+// One such row as a thread sees it from row to row: in registers where it has
+// them to spare; else in shared memory behind the ring (read through L1 instead,
+// a third of it comes from L2: 583 instead of 476 us at 720p); where the ring
+// leaves no room, through L1.
+enum Where { kRegisters, kShared, kCached };
+template <int V, Where WHERE>
 struct Mod {
-  [[maybe_unused]] static constexpr int kPieces = V == 1 || !KEEP ? 0 : 2 * V;
   const float* at;
   float plus;
   F8 kept;
@@ -167,9 +167,10 @@ struct Mod {
   SPARGE_DEV void open(const float* row, float add_to, const int (&off)[V][2]) {
     at = row;
     plus = add_to;
-    if constexpr (V == 1) {
+    if constexpr (WHERE == kRegisters) {
+      static_assert(V == 1, "eight channels");
       kept = add(load_mod(row + off[0][0], off[0][1]), f8(add_to));
-    } else if constexpr (KEEP) {
+    } else if constexpr (WHERE == kShared) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const F8 m = add(load_mod(row + off[v][0], off[v][1]), f8(add_to));
@@ -179,9 +180,9 @@ struct Mod {
     }
   }
   SPARGE_DEV F8 get(int v, const int (&off)[V][2]) const {
-    if constexpr (V == 1) {
+    if constexpr (WHERE == kRegisters) {
       return kept;
-    } else if constexpr (KEEP) {
+    } else if constexpr (WHERE == kShared) {
       const ulonglong2 a = reinterpret_cast<const ulonglong2&>(ring[2 * v]);
       const ulonglong2 b = reinterpret_cast<const ulonglong2&>(ring[2 * v + 1]);
       return {{a.x, a.y, b.x, b.y}};
@@ -190,6 +191,10 @@ struct Mod {
     }
   }
 };
+template <int V, Where WHERE>
+constexpr int mod_pieces() {
+  return WHERE == kShared ? 2 * V : 0;
+}
 
 // Mean and sum of squares about it of each of T rows over the slot.  `cnt`:
 // channels of this warp, `full` of every warp but the last, `last` of that.
@@ -233,7 +238,7 @@ SPARGE_DEV void slot_moments(Slot& s, const F8 (&y)[T * V], const bool (&lo)[V],
   const int w = s.lane & 7;
   const float* in = red + w * kSlotRed + 2 * ((s.lane >> 3) % T);
   const float2 a = *reinterpret_cast<const float2*>(in);
-  const float2 b = *reinterpret_cast<const float2*>(in + 8 * kSlotRed);
+  const float2 b = *reinterpret_cast<const float2*>(in + 8 * kSlotRed);  // (16 warps at most)
   const float na = counts[w], nb = counts[w + 8];
   const float m = sum_of_8(fmaf(na, a.x, nb * b.x)) * inv_c;
   const float da = a.x - m, db = b.x - m;
@@ -245,35 +250,45 @@ SPARGE_DEV void slot_moments(Slot& s, const F8 (&y)[T * V], const bool (&lo)[V],
   }
 }
 
-// Rows a slot takes at once (backward with one: 480p 144 instead of 140 us), and
+// Rows a slot takes at once (480p backward with one: 144 instead of 140 us), and
 // pieces of one stage.
 template <int V>
-constexpr int rows_at_once() {
+constexpr int fwd_rows() {
   return 2 / V;
+}
+template <int THREADS>
+constexpr int bwd_rows() {
+  return THREADS == 192 ? 2 : 1;
 }
 template <typename TX, typename TB, int V>
 constexpr int fwd_pieces() {
-  return rows_at_once<V>() * V * (pieces8<TX>() + pieces8<TB>());
+  return fwd_rows<V>() * V * (pieces8<TX>() + pieces8<TB>());
 }
-template <typename TX, typename TB, int V>
+template <typename TX, typename TB, int THREADS>
 constexpr int bwd_pieces() {
-  return rows_at_once<V>() * V * 2 * (pieces8<TX>() + pieces8<TB>());
+  return bwd_rows<THREADS>() * bwd_vectors(THREADS) * 2 * (pieces8<TX>() + pieces8<TB>());
 }
-// CTAs of an SM that the registers are budgeted for.  At 480p the backward's two
-// leave 168 a thread, so that every value of two rows is at hand (one modulation
-// a frame, both norms: 125 us against 161 with 128).
-// For wide rows the bound is left to the compiler: stated as one CTA it makes
-// slower code (720p forward: 565 us against 487).
+template <int V>
+constexpr Where fwd_where() {
+  return V == 1 ? kRegisters : kShared;
+}
+template <int THREADS>
+constexpr Where bwd_where() {
+  return THREADS == 192 ? kRegisters : THREADS == 640 ? kShared : kCached;
+}
+// CTAs of an SM that the forward's registers are budgeted for.  For wide rows the
+// bound is left to the compiler: stated as one CTA it makes slower code (720p:
+// 565 us against 487).
 constexpr int fwd_residents(int V) { return V == 1 ? 3 : 2; }
-constexpr int bwd_residents(int V) { return V == 1 ? 2 : 1; }
-// Stages of the ring; wide rows have as many as a CTA of 512 threads can hold.
+// Stages of the ring; wide rows have as many as a CTA can hold.
 template <typename TX, typename TB, int V>
 constexpr int fwd_stages() {
   return V == 1 ? 2 : sizeof(TX) + sizeof(TB) == 8 ? 1 : 2;
 }
-template <typename TX, typename TB, int V>
+template <typename TX, typename TB, int THREADS>
 constexpr int bwd_stages() {
-  return V == 1 ? 3 : 24 / bwd_pieces<TX, TB, V>();
+  constexpr int pieces = bwd_pieces<TX, TB, THREADS>();
+  return THREADS == 192 ? 3 : THREADS == 640 ? (16 / pieces < 3 ? 16 / pieces : 3) : 24 / pieces;
 }
 
 // A thread's channels (vector v: fours at c + v * far and F further) and its
@@ -326,11 +341,11 @@ struct ItemWalk {
 template <typename TX, typename TB, int V>
 __global__ void __launch_bounds__(row_threads(V), V == 1 ? fwd_residents(V) : 0) resnorm_fwd_kernel(
     const __grid_constant__ ResnormParams p) {
-  constexpr int T = rows_at_once<V>(), S = fwd_stages<TX, TB, V>(), XQ = pieces8<TX>(), BQ = pieces8<TB>();
+  constexpr int T = fwd_rows<V>(), S = fwd_stages<TX, TB, V>(), XQ = pieces8<TX>(), BQ = pieces8<TB>();
   constexpr int PIECES = fwd_pieces<TX, TB, V>(), STAGE = PIECES;
   extern __shared__ uint4 smem[];
   __shared__ __align__(16) float red[kSlotRedFloats];
-  __shared__ float counts[16];
+  __shared__ float counts[16];  // a slot of the forward has at most 16 warps
   Slot s = make_slot(p.W, red);
   const int per_cta = slots_per_cta(p.W);
   clear_red(red);
@@ -388,10 +403,12 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? fwd_residents(V) : 0)
   const float* shift_row = (p.shift != nullptr ? p.shift : g_zeros);
   const float plus = p.unit || p.scale == nullptr ? 1.f : 0.f;
   const float gate_plus = p.gate == nullptr ? 1.f : 0.f;
-  Mod<V, true> gate, gain, shift;
+  constexpr Where WHERE = fwd_where<V>();
+  constexpr int KEPT = mod_pieces<V, WHERE>();
+  Mod<V, WHERE> gate, gain, shift;
   gate.ring = at.ring + S * PIECES;
-  gain.ring = gate.ring + gate.kPieces;
-  shift.ring = gain.ring + gain.kPieces;
+  gain.ring = gate.ring + KEPT;
+  shift.ring = gain.ring + KEPT;
   int group = -1;
   int k = 0;
   while (now.item < p.items) {
@@ -497,12 +514,12 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? fwd_residents(V) : 0)
 // FULL: every input is there and no thread is without channels, which takes the
 // branches out of the row loop (one modulation a frame, both norms, 480p: 124
 // instead of 155 us).
-template <typename TX, typename TB, int V, bool POST, bool FULL>
-__global__ void __launch_bounds__(row_threads(V), V == 1 ? bwd_residents(V) : 0) resnorm_bwd_kernel(
+template <typename TX, typename TB, int THREADS, bool POST, bool FULL>
+__global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) resnorm_bwd_kernel(
     const __grid_constant__ ResnormParams p) {
-  constexpr int T = rows_at_once<V>(), S = bwd_stages<TX, TB, V>(), XQ = pieces8<TX>(),
-                BQ = pieces8<TB>();
-  constexpr int PIECES = bwd_pieces<TX, TB, V>(), ROW = 2 * (XQ + BQ), STAGE = PIECES;
+  constexpr int V = bwd_vectors(THREADS), T = bwd_rows<THREADS>(),
+                S = bwd_stages<TX, TB, THREADS>(), XQ = pieces8<TX>(), BQ = pieces8<TB>();
+  constexpr int PIECES = bwd_pieces<TX, TB, THREADS>(), ROW = 2 * (XQ + BQ), STAGE = PIECES;
   constexpr int SUMS = POST ? 4 : 3;
   extern __shared__ uint4 smem[];
   __shared__ __align__(16) float red[kSlotRedFloats];
@@ -581,7 +598,12 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? bwd_residents(V) : 0)
   const float plus = p.unit || p.scale == nullptr ? 1.f : 0.f;
   const float gate_plus = p.gate == nullptr ? 1.f : 0.f;
   const float one_mean = p.norm == SPARGE_NORM_LAYER ? p.inv_c : 0.f;
-  Mod<V, false> gate, gain, post;
+  constexpr Where WHERE = bwd_where<THREADS>();
+  constexpr int KEPT = mod_pieces<V, WHERE>();
+  Mod<V, WHERE> gate, gain, post;
+  gate.ring = at.ring + S * PIECES;
+  gain.ring = gate.ring + KEPT;
+  post.ring = gain.ring + KEPT;
   if (POST) post.open(p.post, 0.f, at.mod);
   int group = -1;
   int k = 0;
@@ -710,6 +732,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? bwd_residents(V) : 0)
 
 struct ResnormPlan {
   int V, W, per_cta, threads, ctas, slots, smem;
+  int built;  // the size of CTA that the backward kernel is built for
   int groups, R;
   int items, parts;  // items = groups * parts
   // backward: a sum is written per item straight to the output (one part a
@@ -719,42 +742,53 @@ struct ResnormPlan {
 };
 
 template <typename TX, typename TB, int V>
-int ring_bytes(bool bwd) {
-  return 16 * (bwd ? bwd_stages<TX, TB, V>() * bwd_pieces<TX, TB, V>()
-                              : fwd_stages<TX, TB, V>() * fwd_pieces<TX, TB, V>() + 3 * Mod<V, true>::kPieces);
+int fwd_ring() {
+  return fwd_stages<TX, TB, V>() * fwd_pieces<TX, TB, V>() + 3 * mod_pieces<V, fwd_where<V>()>();
 }
+template <typename TX, typename TB, int THREADS>
+int bwd_ring() {
+  return bwd_stages<TX, TB, THREADS>() * bwd_pieces<TX, TB, THREADS>() +
+         3 * mod_pieces<bwd_vectors(THREADS), bwd_where<THREADS>()>();
+}
+// Pieces of a thread's ring, with the rows that it keeps.
 template <typename TX, typename TB>
-int ring_bytes_of(int V, bool bwd) {
-  return V == 1 ? ring_bytes<TX, TB, 1>(bwd) : ring_bytes<TX, TB, 2>(bwd);
+int ring_pieces(int V, int threads, bool bwd) {
+  if (!bwd) return V == 1 ? fwd_ring<TX, TB, 1>() : fwd_ring<TX, TB, 2>();
+  return threads == 192   ? bwd_ring<TX, TB, 192>()
+         : threads == 640 ? bwd_ring<TX, TB, 640>()
+                          : bwd_ring<TX, TB, 512>();
 }
 
 ResnormPlan resnorm_plan(const sparge_resnorm& a, bool bwd) {
   ResnormPlan pl = {};
   const int64_t M = a.rows;
-  pl.V = row_vectors(a.C);
+  pl.built = bwd ? bwd_threads(a.C) : 0;
+  pl.V = bwd ? bwd_vectors(pl.built) : row_vectors(a.C);
   pl.W = slot_warps(a.C, pl.V);
   pl.per_cta = slots_per_cta(pl.W);
   pl.threads = pl.W * pl.per_cta * 32;
-  const int ring = a.x_type == SPARGE_BF16 ? ring_bytes_of<__nv_bfloat16, __nv_bfloat16>(pl.V, bwd)
-                   : a.branch_type == SPARGE_BF16 ? ring_bytes_of<float, __nv_bfloat16>(pl.V, bwd)
-                                                  : ring_bytes_of<float, float>(pl.V, bwd);
-  pl.smem = ring * pl.threads;
+  const int ring =
+      a.x_type == SPARGE_BF16 ? ring_pieces<__nv_bfloat16, __nv_bfloat16>(pl.V, pl.built, bwd)
+      : a.branch_type == SPARGE_BF16 ? ring_pieces<float, __nv_bfloat16>(pl.V, pl.built, bwd)
+                                     : ring_pieces<float, float>(pl.V, pl.built, bwd);
+  pl.smem = ring * pl.threads * 16;
   int groups = 1;
   if (a.gate) groups = std::max(groups, a.gate_groups);
   if (a.scale) groups = std::max(groups, a.scale_groups);
   if (a.shift) groups = std::max(groups, a.shift_groups);
   pl.groups = groups;
   pl.R = static_cast<int>(M / groups);
-  const int T = 2 / pl.V;
+  const int T = bwd ? (pl.built == 192 ? 2 : 1) : 2 / pl.V;
   // CTAs that are resident at a time: shared memory limits them, or registers.
   // The backward stays resident for its share of the rows, since every slot
   // leaves a row of sums; the forward runs several waves, whose CTAs end one by
   // one instead of all at once with the slowest (480p: one wave 104 us, two 101,
   // eight 93; 720p: four).
-  const int per_sm =
-      std::max(1, std::min(bwd ? bwd_residents(pl.V) : fwd_residents(pl.V),
-                           std::min(kSmemPerSm / (pl.smem + kSmemOfCta), 2048 / pl.threads)));
-  
+  const int warps = pl.threads / 32;
+  const int by_regs = bwd ? resident_warps(bwd_regs(pl.built)) / warps
+                          : fwd_residents(pl.V) * row_threads(pl.V) / pl.threads;
+  const int per_sm = std::max(1, std::min(std::min(by_regs, 64 / warps),
+                                          kSmemPerSm / (pl.smem + kSmemOfCta)));
   const int waves = bwd ? 1 : pl.V == 1 ? 8 : 4;
   const int64_t most = static_cast<int64_t>(kSMs) * per_sm * waves;
   const int64_t target = most * pl.per_cta;  // slots that fill the machine
@@ -811,18 +845,10 @@ ResnormParams resnorm_params(const sparge_resnorm& a, const ResnormPlan& pl, boo
   return p;
 }
 
-template <typename TX, typename TB, int V>
-cudaError_t launch_form(const ResnormParams& p, const ResnormPlan& pl, bool bwd, cudaStream_t st) {
-  const bool post = p.post != nullptr;
-  // (Sixteen channels a thread leave no registers for it.)
-  constexpr bool kFull = V == 1;
-  const bool full = kFull && p.C % 256 == 0 && p.norm && p.b && p.dy && p.dh;
-  auto* kernel = !bwd   ? resnorm_fwd_kernel<TX, TB, V>
-                 : full ? (post ? resnorm_bwd_kernel<TX, TB, V, true, kFull>
-                                : resnorm_bwd_kernel<TX, TB, V, false, kFull>)
-                        : (post ? resnorm_bwd_kernel<TX, TB, V, true, false>
-                                : resnorm_bwd_kernel<TX, TB, V, false, false>);
-  if (pl.smem > 43 * 1024) {  // 48 KB less what the kernel declares
+template <typename Kernel>
+cudaError_t launch_kernel(Kernel* kernel, const ResnormParams& p, const ResnormPlan& pl,
+                          cudaStream_t st) {
+  if (pl.smem > 42 * 1024) {  // 48 KB less what the kernel declares
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
     if (e != cudaSuccess) {
@@ -834,10 +860,29 @@ cudaError_t launch_form(const ResnormParams& p, const ResnormPlan& pl, bool bwd,
   return cudaGetLastError();
 }
 
+template <typename TX, typename TB, int THREADS>
+cudaError_t launch_bwd(const ResnormParams& p, const ResnormPlan& pl, cudaStream_t st) {
+  // (Sixteen channels a thread leave no registers for the full form.)
+  constexpr bool kFull = bwd_vectors(THREADS) == 1;
+  const bool post = p.post != nullptr;
+  const bool full = kFull && p.C % 256 == 0 && p.norm && p.b && p.dy && p.dh;
+  auto* kernel = full ? (post ? resnorm_bwd_kernel<TX, TB, THREADS, true, kFull>
+                              : resnorm_bwd_kernel<TX, TB, THREADS, false, kFull>)
+                      : (post ? resnorm_bwd_kernel<TX, TB, THREADS, true, false>
+                              : resnorm_bwd_kernel<TX, TB, THREADS, false, false>);
+  return launch_kernel(kernel, p, pl, st);
+}
+
 template <typename TX, typename TB>
 cudaError_t launch_resnorm(const ResnormParams& p, const ResnormPlan& pl, bool bwd,
                            cudaStream_t st) {
-  return pl.V == 1 ? launch_form<TX, TB, 1>(p, pl, bwd, st) : launch_form<TX, TB, 2>(p, pl, bwd, st);
+  if (bwd) {
+    if (pl.built == 192) return launch_bwd<TX, TB, 192>(p, pl, st);
+    if (pl.built == 640) return launch_bwd<TX, TB, 640>(p, pl, st);
+    return launch_bwd<TX, TB, 512>(p, pl, st);
+  }
+  return pl.V == 1 ? launch_kernel(resnorm_fwd_kernel<TX, TB, 1>, p, pl, st)
+                   : launch_kernel(resnorm_fwd_kernel<TX, TB, 2>, p, pl, st);
 }
 
 cudaError_t dispatch_resnorm(const sparge_resnorm& a, const ResnormParams& p,

@@ -24,7 +24,7 @@ namespace sparge {
 
 constexpr int kSMs = 152;              // of a GB300: sizes grids and workspaces
 constexpr int kSmemPerSm = 228 * 1024;  // shared memory of an SM
-constexpr int kSmemOfCta = 6 * 1024;    // of it a row kernel's CTA takes beside its ring, at most
+constexpr int kSmemOfCta = 7 * 1024;    // of it a row kernel's CTA takes beside its ring, at most
 constexpr int kMaxRowChannels = 8192;
 
 constexpr int kMaxSlots = 6;            // per CTA; named barriers 1 .. 6
@@ -34,6 +34,13 @@ constexpr int kMaxSlots = 6;            // per CTA; named barriers 1 .. 6
 // several on an SM.
 inline int row_vectors(int C) { return C <= 1536 ? 1 : 2; }
 constexpr int row_threads(int V) { return V == 1 ? 192 : 512; }
+// The backward, whose sums stay in registers, has no room for sixteen channels
+// up to 5120 of them: there it takes eight and CTAs of up to 640 threads.
+inline int bwd_threads(int C) { return C <= 1536 ? 192 : C <= 5120 ? 640 : 512; }
+constexpr int bwd_vectors(int threads) { return threads == 512 ? 2 : 1; }
+// Registers of a thread that its CTAs leave: two of six warps an SM, one of
+// twenty, one of sixteen.
+constexpr int bwd_regs(int threads) { return threads == 192 ? 168 : threads == 640 ? 96 : 128; }
 // Warps of one slot, and slots of one CTA: enough to make 6 warps of a CTA
 // where a row needs fewer.
 __host__ __device__ inline int slot_warps(int C, int V) { return (C + 256 * V - 1) / (256 * V); }
@@ -53,7 +60,8 @@ struct Slot {
 
 // Floats one warp contributes to a slot reduction, at most.
 constexpr int kSlotRed = 4;
-constexpr int kSlotRow = 16 * kSlotRed;  // of a slot of at most 16 warps
+constexpr int kMaxWarps = 24;            // of a slot
+constexpr int kSlotRow = kMaxWarps * kSlotRed;
 constexpr int kSlotRedFloats = kMaxSlots * 2 * kSlotRow;
 
 SPARGE_DEV Slot make_slot(int W, float* red) {
@@ -110,8 +118,8 @@ SPARGE_DEV float warp_sums(const float (&in)[K], int lane) {
 
 // Joins the warps of a slot.  Every warp leaves up to four floats in its row of
 // `red`; every warp then reads all of them at once, lane l the float l / 8 of
-// warp l % 8 (and of warp l % 8 + 8: a slot has at most 16), and finishes with
-// three shuffles instead of a loop over the warps.  The two halves of `red`
+// warps l % 8, l % 8 + 8 and so on, and finishes with three shuffles instead of
+// a loop over the warps.  The two halves of `red`
 // alternate, so one barrier a call is enough: a warp cannot reach the next but
 // one call before every warp has read this one's values.
 SPARGE_DEV float* slot_half(Slot& s) {
@@ -140,7 +148,10 @@ SPARGE_DEV void slot_sum(Slot& s, float (&v)[K]) {
   if (s.lane % (32 / K) == 0) red[s.warp * kSlotRed + s.lane / (32 / K)] = mine;
   slot_sync(s);
   const float* in = red + (s.lane & 7) * kSlotRed + (s.lane >> 3) % K;
-  const float sum = sum_of_8(in[0] + in[8 * kSlotRed]);
+  float sum = in[0];
+  if (s.W > 8) sum += in[8 * kSlotRed];
+  if (s.W > 16) sum += in[16 * kSlotRed];
+  sum = sum_of_8(sum);
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, sum, 8 * k);
 }
