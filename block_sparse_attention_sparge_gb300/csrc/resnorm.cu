@@ -250,15 +250,15 @@ SPARGE_DEV void slot_moments(Slot& s, const F8 (&y)[T * V], const bool (&lo)[V],
   }
 }
 
-// Rows a slot takes at once (480p backward with one: 144 instead of 140 us), and
-// pieces of one stage.
+// Rows a slot takes at once (backward with one: 144 instead of 140 us at 480p, 1017
+// instead of 738 us at 720p in bf16), and pieces of one stage.
 template <int V>
 constexpr int fwd_rows() {
   return 2 / V;
 }
 template <int THREADS>
 constexpr int bwd_rows() {
-  return THREADS == 192 ? 2 : 1;
+  return 2 / bwd_vectors(THREADS);
 }
 template <typename TX, typename TB, int V>
 constexpr int fwd_pieces() {
@@ -778,7 +778,7 @@ ResnormPlan resnorm_plan(const sparge_resnorm& a, bool bwd) {
   if (a.shift) groups = std::max(groups, a.shift_groups);
   pl.groups = groups;
   pl.R = static_cast<int>(M / groups);
-  const int T = bwd ? (pl.built == 192 ? 2 : 1) : 2 / pl.V;
+  const int T = 2 / pl.V;
   // CTAs that are resident at a time: shared memory limits them, or registers.
   // The backward stays resident for its share of the rows, since every slot
   // leaves a row of sums; the forward runs several waves, whose CTAs end one by
