@@ -418,11 +418,14 @@ class RopeAxes:
         self.scale, self.interleaved = scale[:len(pairs)], bool(interleaved)
         pad = 3 - len(pairs)
         self.plan = Rope()
-        self.address = ctypes.addressof(self.plan)
         _check(load_library().sparge_rope_init(
             ctypes.byref(self.plan), self.d, (ctypes.c_int32 * 3)(*pairs, *[0] * pad),
             self.theta, (ctypes.c_double * 3)(*self.scale, *[1.0] * pad), int(self.interleaved)),
             "sparge_rope_init")
+
+    @property
+    def address(self) -> int:
+        return ctypes.addressof(self.plan)
 
 
 def _token_strides(t, B, N, H):
@@ -463,6 +466,12 @@ def _heads_head(B, N, d, x_type, n_parts, rope, grid, pos, norm, weights, eps, i
         raise ValueError("a norm weight must be bf16 or fp32")
     return (B, N, d, x_type, _TYPES.get(w_type, 0), _HEADS_NORMS[norm], eps, n_parts, plan,
             _addr(grid), _addr(pos), 0 if pos is None else pos.shape[0])
+
+
+def _apart(outs):
+    starts = [t.data_ptr() for t in outs if t is not None]
+    if len(set(starts)) != len(starts):
+        raise ValueError("the outputs must not overlap")
 
 
 def _norm_weight(w, norm, H, d):
@@ -509,6 +518,8 @@ def sparge_heads_fwd(q=None, k=None, v=None, rope: RopeAxes | None = None, grid=
         parts += (t.data_ptr(), *_token_strides(t, B, N, H), _norm_weight(w, norm, H, d),
                   y.data_ptr(), 0, 0, 0, 0, 0, H, i == 2)
         res[i] = y
+    if out is not None:
+        _apart(res)
     n = len(parts) // 13
     args = _HEADS.pack(*_heads_head(B, N, d, _type_of(first, "q, k and v"), n, rope, grid, pos,
                                     norm, (q_weight, k_weight), eps, index),
@@ -566,6 +577,8 @@ def sparge_heads_bwd(dq=None, dk=None, dv=None, q=None, k=None, rope: RopeAxes |
         parts += (xp, *xs, wp, g.data_ptr(), dx.data_ptr(), *_token_strides(dx, B, N, H), dw, H,
                   i == 2)
         res[i] = dx
+    if out is not None:
+        _apart(res[:3])
     n = len(parts) // 13
     args = _HEADS.pack(*_heads_head(B, N, d, _TYPES[dtype], n, rope, grid, pos, norm,
                                     (q_weight, k_weight), eps, index),

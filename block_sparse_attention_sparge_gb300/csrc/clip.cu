@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kClipThreads, 3) clip_scale_kernel(
     if (threadIdx.x == 0) {
       const double norm = sqrt(v);
       if (a.norm != nullptr && blockIdx.x == 0) *a.norm = static_cast<float>(norm);
-      const double ratio = static_cast<double>(a.max_norm) / (norm + static_cast<double>(a.eps));
+      const double over = norm + static_cast<double>(a.eps);
+      const double ratio = over == 0.0 ? 1.0 : static_cast<double>(a.max_norm) / over;
       factor = ratio > 1.0 ? 1.f : static_cast<float>(ratio);  // NaN stays NaN
     }
   }

@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? kFwdResidents : 0) he
 #pragma unroll
         for (int v = 1; v < V; ++v) ts[i] += sums[i * V + v];
       }
-      slot_sum(s, ts);  // its barrier also publishes the angles
+      slot_sum<warp_eights(row_threads(V))>(s, ts);  // its barrier also publishes the angles
 #pragma unroll
       for (int i = 0; i < NT * T * V; ++i) sums[i] = ts[i / V];
       if (s.W == 1) slot_sync(s);
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
 #pragma unroll
         for (int v = 1; v < V; ++v) ts[i] += sums[((i / 2) * V + v) * 2 + i % 2];
       }
-      slot_sum(s, ts);
+      slot_sum<warp_eights(THREADS)>(s, ts);
 #pragma unroll
       for (int i = 0; i < 2 * NT * V; ++i) sums[i] = ts[(i / (2 * V)) * 2 + i % 2];
       if (s.W == 1) slot_sync(s);
@@ -862,6 +862,8 @@ int heads_smem(const HeadsPlan& pl, bool f32, int d, bool bwd) {
          pl.slots * kAngleBuffers * rows * d * static_cast<int>(sizeof(float));
 }
 
+constexpr int kDeclared = 5184;  // shared memory that a kernel declares, at most
+
 HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
   HeadsPlan pl = {};
   int turned = 0, plain = 0, widest = 0;
@@ -900,7 +902,7 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
   const int by_regs = bwd ? resident_warps(bwd_regs(pl.built)) / warps
                           : kFwdResidents * row_threads(pl.V) / pl.threads;
   const int per_sm = std::max(1, std::min(std::min(by_regs, 64 / warps),
-                                          kSmemPerSm / (pl.smem + kSmemOfCta)));
+                                          kSmemPerSm / (pl.smem + kSmemOfCta + kDeclared)));
   const int64_t units = static_cast<int64_t>(a.B) * ((a.N + rows - 1) / rows);
   const int64_t need = (units + slots_min - 1) / slots_min;
   const int64_t most = (kSMs * per_sm + pl.n - 1) / pl.n;
@@ -1037,7 +1039,7 @@ int check_strides(const int64_t (&s)[3], int x_type) {
 int check_heads(const sparge_heads* a, bool bwd) {
   if (a == nullptr) return SPARGE_ERR_INVALID_ARG;
   if (a->B < 1 || a->N < 1 || a->n_parts < 1 || a->n_parts > 3) return SPARGE_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(a->B) * a->N > INT32_MAX) return SPARGE_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(a->B) * a->N > INT32_MAX / 2) return SPARGE_ERR_UNSUPPORTED;
   if (a->d != 64 && a->d != 128) return SPARGE_ERR_UNSUPPORTED;
   if (a->x_type != SPARGE_BF16 && a->x_type != SPARGE_F32) return SPARGE_ERR_UNSUPPORTED;
   if (a->weight_type != SPARGE_BF16 && a->weight_type != SPARGE_F32) return SPARGE_ERR_UNSUPPORTED;

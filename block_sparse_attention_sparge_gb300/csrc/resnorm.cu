@@ -234,15 +234,23 @@ SPARGE_DEV void slot_moments(Slot& s, const F8 (&y)[T * V], const bool (&lo)[V],
     *reinterpret_cast<float2*>(red + s.warp * kSlotRed + 2 * (s.lane / (32 / T))) =
         make_float2(mine, square);
   slot_sync(s);
-  // Lane l joins warps l % 8 and l % 8 + 8 of row l / 8 % T.
+  // Lane l joins warps l % 8 (and l % 8 + 8) of row l / 8 % T.
   const int w = s.lane & 7;
   const float* in = red + w * kSlotRed + 2 * ((s.lane >> 3) % T);
   const float2 a = *reinterpret_cast<const float2*>(in);
-  const float2 b = *reinterpret_cast<const float2*>(in + 8 * kSlotRed);  // (16 warps at most)
-  const float na = counts[w], nb = counts[w + 8];
-  const float m = sum_of_8(fmaf(na, a.x, nb * b.x)) * inv_c;
-  const float da = a.x - m, db = b.x - m;
-  const float q = sum_of_8(fmaf(na * da, da, a.y) + fmaf(nb * db, db, b.y));
+  const float na = counts[w];
+  float m, q;
+  if constexpr (V == 1) {
+    m = sum_of_8(na * a.x) * inv_c;
+    const float da = a.x - m;
+    q = sum_of_8(fmaf(na * da, da, a.y));
+  } else {
+    const float2 b = *reinterpret_cast<const float2*>(in + 8 * kSlotRed);
+    const float nb = counts[w + 8];
+    m = sum_of_8(fmaf(na, a.x, nb * b.x)) * inv_c;
+    const float da = a.x - m, db = b.x - m;
+    q = sum_of_8(fmaf(na * da, da, a.y) + fmaf(nb * db, db, b.y));
+  }
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     mean[t] = __shfl_sync(0xffffffffu, m, 8 * t);
@@ -446,7 +454,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? fwd_residents(V) : 0)
 #pragma unroll
           for (int v = 1; v < V; ++v) rbs[t] += dot(b8[t * V + v], b8[t * V + v]);
         }
-        slot_sum(s, rbs);
+        slot_sum<warp_eights(row_threads(V))>(s, rbs);
 #pragma unroll
         for (int t = 0; t < T; ++t) {
           rbs[t] = rsqrtf(rbs[t] * p.inv_c + p.eps);
@@ -482,7 +490,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? fwd_residents(V) : 0)
 #pragma unroll
           for (int v = 1; v < V; ++v) rstd[t] += dot(y[t * V + v], y[t * V + v]);
         }
-        slot_sum(s, rstd);
+        slot_sum<warp_eights(row_threads(V))>(s, rstd);
       }
       int64_t o = static_cast<int64_t>(row) * p.C + at.c;
 #pragma unroll
@@ -650,7 +658,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) resnorm_bwd_k
           sums[2 * t + 1] += dot(d[i], z[i]);
         }
       }
-      slot_sum(s, sums);
+      slot_sum<warp_eights(THREADS)>(s, sums);
     }
     float e[T];
     int64_t o = static_cast<int64_t>(row) * p.C + at.c;
@@ -686,7 +694,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) resnorm_bwd_k
       o += p.C;
     }
     if (POST) {
-      slot_sum(s, e);
+      slot_sum<warp_eights(THREADS)>(s, e);
       o = static_cast<int64_t>(row) * p.C + at.c;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
@@ -759,6 +767,8 @@ int ring_pieces(int V, int threads, bool bwd) {
                           : bwd_ring<TX, TB, 512>();
 }
 
+constexpr int kDeclared = 4672;  // shared memory that a kernel declares, at most
+
 ResnormPlan resnorm_plan(const sparge_resnorm& a, bool bwd) {
   ResnormPlan pl = {};
   const int64_t M = a.rows;
@@ -788,7 +798,7 @@ ResnormPlan resnorm_plan(const sparge_resnorm& a, bool bwd) {
   const int by_regs = bwd ? resident_warps(bwd_regs(pl.built)) / warps
                           : fwd_residents(pl.V) * row_threads(pl.V) / pl.threads;
   const int per_sm = std::max(1, std::min(std::min(by_regs, 64 / warps),
-                                          kSmemPerSm / (pl.smem + kSmemOfCta)));
+                                          kSmemPerSm / (pl.smem + kSmemOfCta + kDeclared)));
   const int waves = bwd ? 1 : pl.V == 1 ? 8 : 4;
   const int64_t most = static_cast<int64_t>(kSMs) * per_sm * waves;
   const int64_t target = most * pl.per_cta;  // slots that fill the machine

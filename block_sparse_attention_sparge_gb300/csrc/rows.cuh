@@ -24,7 +24,7 @@ namespace sparge {
 
 constexpr int kSMs = 152;              // of a GB300: sizes grids and workspaces
 constexpr int kSmemPerSm = 228 * 1024;  // shared memory of an SM
-constexpr int kSmemOfCta = 7 * 1024;    // of it a row kernel's CTA takes beside its ring, at most
+constexpr int kSmemOfCta = 1024;      // of it reserved for each CTA
 constexpr int kMaxRowChannels = 8192;
 
 constexpr int kMaxSlots = 6;            // per CTA; named barriers 1 .. 6
@@ -38,6 +38,8 @@ constexpr int row_threads(int V) { return V == 1 ? 192 : 512; }
 // up to 5120 of them: there it takes eight and CTAs of up to 640 threads.
 inline int bwd_threads(int C) { return C <= 1536 ? 192 : C <= 5120 ? 640 : 512; }
 constexpr int bwd_vectors(int threads) { return threads == 512 ? 2 : 1; }
+// Eights of warps of a slot, of a kernel built for CTAs of so many threads.
+constexpr int warp_eights(int threads) { return (threads / 32 + 7) / 8; }
 // Registers of a thread that its CTAs leave: two of six warps an SM, one of
 // twenty, one of sixteen.
 constexpr int bwd_regs(int threads) { return threads == 192 ? 168 : threads == 640 ? 96 : 128; }
@@ -134,8 +136,9 @@ SPARGE_DEV float sum_of_8(float v) {
   return v;
 }
 
-// Sums v[0..K) over the slot's threads; every thread gets the sums.
-template <int K>
+// Sums v[0..K) over the slot's threads; every thread gets the sums.  A slot of
+// the kernel has at most 8 * EIGHTS warps.
+template <int EIGHTS, int K>
 SPARGE_DEV void slot_sum(Slot& s, float (&v)[K]) {
   static_assert(K <= kSlotRed, "reduction buffer");
   const float mine = warp_sums(v, s.lane);
@@ -149,8 +152,8 @@ SPARGE_DEV void slot_sum(Slot& s, float (&v)[K]) {
   slot_sync(s);
   const float* in = red + (s.lane & 7) * kSlotRed + (s.lane >> 3) % K;
   float sum = in[0];
-  if (s.W > 8) sum += in[8 * kSlotRed];
-  if (s.W > 16) sum += in[16 * kSlotRed];
+#pragma unroll
+  for (int e = 1; e < EIGHTS; ++e) sum += in[8 * e * kSlotRed];
   sum = sum_of_8(sum);
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, sum, 8 * k);

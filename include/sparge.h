@@ -286,13 +286,13 @@ typedef struct sparge_heads_part {
   void* dx;              /* sparge_heads_bwd: gradient of x, of x_type (out) */
   int64_t dx_stride[3];
   void* dweight;         /* sparge_heads_bwd: gradient of weight, of weight_type
-                            (out); NULL: not wanted */
+                            (out, 16-byte aligned); NULL: not wanted */
   int32_t H;             /* heads; H * d <= 8192 */
   int32_t plain;         /* nonzero: neither norm nor rotation (V) */
 } sparge_heads_part;
 
 typedef struct sparge_heads {
-  int32_t B, N, d;       /* d in {64, 128}; B * N < 2^31 */
+  int32_t B, N, d;       /* d in {64, 128}; B * N < 2^30 */
   int32_t x_type, weight_type;
   int32_t norm;          /* enum sparge_heads_norm */
   float eps;
@@ -345,7 +345,7 @@ enum sparge_norm { SPARGE_NORM_NONE = 0, SPARGE_NORM_LAYER = 1, SPARGE_NORM_RMS 
  * on.  NULL gate or scale = 1 (gain 1), NULL shift = 0.
  */
 typedef struct sparge_resnorm {
-  int64_t rows;          /* tokens of all samples */
+  int64_t rows;          /* tokens of all samples; < 2^30 */
   int32_t C;             /* channels: a multiple of 8, at most 8192 */
   int32_t x_type;        /* x, y, dy, dx */
   int32_t branch_type;   /* branch, h, dbranch, dh; with a bf16 x: bf16 */
@@ -410,7 +410,7 @@ int sparge_clip_workspace_bytes(int32_t n, size_t* bytes);
  *           must not overlap, with one another or with another input (a tensor
  *           listed twice included): SPARGE_ERR_INVALID_ARG.
  *   max_norm : finite; below 0: the norm alone, nothing is written to a tensor.
- *   norm  : fp32 [1] out (device).
+ *   norm  : fp32 [1] out (device).  A norm of 0 with an eps of 0: factor 1.
  * A gradient that holds NaN makes the norm and every result NaN; one that
  * holds an infinity makes the norm infinite and the factor 0.
  */

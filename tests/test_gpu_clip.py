@@ -1,8 +1,8 @@
 """Gradient norm and clipping (sparge_clip_grads) against 64 bits.
 
-Bounds: 32 squares are summed in fp32 (a product and at most 16 additions
-behind one another: 17 * 2^-24 of the sum, half of it after the root), the rest
-in fp64; with the rounding of the norm itself 2^-20 in all.  The factor adds its
+Bounds: sums of squares are fp32 over 64 values and then over four such sums (at
+most 16 fused additions, 3 more and 4: 23 * 2^-24 of the sum, half of it after
+the root), the rest is fp64; with the rounding of the norm itself 2^-20 in all.  The factor adds its
 rounding and a scaled value its own."""
 
 import math
@@ -147,6 +147,8 @@ def test_zeros_infinities_and_nan():
     b = torch.ones(100, device=DEV, dtype=BF)
     assert math.isnan(float(B.sparge_clip_grads([a, b], 1.0)))
     assert b.isnan().all() and a.isnan().all()
+    z = torch.zeros(9, device=DEV)
+    assert float(B.sparge_clip_grads([z], 0.0, eps=0.0)) == 0.0 and (z == 0).all()
     e = torch.empty(0, device=DEV)
     assert float(B.sparge_clip_grads([e], 1.0)) == 0.0
 

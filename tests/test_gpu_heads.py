@@ -365,6 +365,11 @@ def test_refusals_on_the_device():
                 dict(norm="token", q=q[:, :4])):
         with pytest.raises(ValueError):
             B.sparge_heads_bwd(dq, **bad)
+    same = torch.zeros(1, 8, 2, 64, dtype=BF, device=DEV)
+    with pytest.raises(ValueError):
+        B.sparge_heads_bwd(dq, dq, out=(same, same, None))
+    with pytest.raises(ValueError):
+        B.sparge_heads_fwd(q, q, out=(dq, dq, None))
     with pytest.raises(B.SpargeError) as e:
         B.sparge_heads_bwd(dq, q=q, norm="head", q_weight=torch.ones(64, device=DEV),
                            workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
