@@ -337,10 +337,10 @@ constexpr int all_parts() {
 // Stages of the ring: one more changes nothing at 480p (109 us both ways,
 // forward), and costs the wide forward its second CTA of an SM.
 constexpr int kFwdStages = 2;
-// (A joint fp32 row of 640 threads leaves room for two.)
+// (Two tokens at once, or a joint fp32 row of 640 threads, leave room for two.)
 template <typename TX, int THREADS>
 constexpr int bwd_stages() {
-  return THREADS == 640 && sizeof(TX) == 4 ? 2 : 3;
+  return THREADS == 192 || (THREADS == 640 && sizeof(TX) == 4) ? 2 : 3;
 }
 // Tokens a slot takes at once.
 template <int V>
@@ -357,9 +357,16 @@ template <typename TX, int FORM, int V>
 constexpr int fwd_pieces() {
   return all_parts<FORM>() * fwd_rows<V>() * V * pieces8<TX>();
 }
-template <typename TX, int FORM, int V>
+// (One at a time: 480p 141 instead of 135 us, in fp32 240 instead of 205.  CTAs
+// of 640 threads have no registers for two.)
+template <int THREADS>
+constexpr int bwd_rows() {
+  return THREADS == 192 ? 2 : 1;
+}
+template <typename TX, int FORM, int THREADS>
 constexpr int bwd_pieces() {
-  return all_parts<FORM>() * V + turned_parts<FORM>() * V * pieces8<TX>();
+  return bwd_rows<THREADS>() * bwd_vectors(THREADS) *
+         (all_parts<FORM>() + turned_parts<FORM>() * pieces8<TX>());
 }
 template <typename TX, int FORM, int V>
 constexpr int fwd_ring() {
@@ -368,7 +375,7 @@ constexpr int fwd_ring() {
 template <typename TX, int FORM, int THREADS>
 constexpr int bwd_ring() {
   constexpr int V = bwd_vectors(THREADS);
-  return bwd_stages<TX, THREADS>() * bwd_pieces<TX, FORM, V>() + turned_parts<FORM>() * V * 2;
+  return bwd_stages<TX, THREADS>() * bwd_pieces<TX, FORM, THREADS>() + turned_parts<FORM>() * V * 2;
 }
 constexpr int kAngleBuffers = 2;  // of T tokens (D floats each), for every slot
 
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? kFwdResidents : 0) he
   constexpr int STAGE = fwd_pieces<TX, FORM, V>(), RING = fwd_ring<TX, FORM, V>();
   constexpr bool SPLIT = split<TX, INTER>();
   extern __shared__ uint4 smem[];
-  __shared__ __align__(16) float red[kSlotRedFloats];
+  __shared__ __align__(16) float red[red_floats(row_threads(V))];
   __shared__ Turns turns;
   constexpr bool FULL = FORM == kFull;
   const int part0 = FORM == kSingle ? blockIdx.y : 0;
@@ -402,10 +409,9 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? kFwdResidents : 0) he
   const bool rot = FULL || (p.rotate && !plain);
   const int norm = FULL ? SPARGE_HEADS_NORM_TOKEN : plain ? 0 : p.norm;
   turns.fill(p);
-  clear_red(red);
+  Slot s = make_slot(any.W, red, red_half(row_threads(V)));
   __syncthreads();
   const int per_cta = slots_per_cta(any.W);
-  Slot s = make_slot(any.W, red);
   if (s.index >= per_cta) return;
   const Place<SPLIT, D, V, FULL> at(s, any.C);
   const int H = any.C / D;
@@ -572,13 +578,14 @@ template <typename TX, bool INTER, int D, int THREADS, int FORM>
 __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_kernel(
     const __grid_constant__ HeadsParams p) {
   constexpr int V = bwd_vectors(THREADS);
-  constexpr int S = bwd_stages<TX, THREADS>(), Q8 = pieces8<TX>();
+  constexpr int T = bwd_rows<THREADS>(), S = bwd_stages<TX, THREADS>(), Q8 = pieces8<TX>();
   constexpr int NT = turned_parts<FORM>(), NP = all_parts<FORM>();
-  constexpr int STAGE = bwd_pieces<TX, FORM, V>(), RING = bwd_ring<TX, FORM, V>();
+  constexpr int STAGE = bwd_pieces<TX, FORM, THREADS>(), RING = bwd_ring<TX, FORM, THREADS>();
   constexpr bool SPLIT = split<TX, INTER>();
-  constexpr int XAT = NP * V;  // the inputs' rows, behind the gradients' rows
+  constexpr int XAT = NP * T * V;  // the inputs' rows, behind the gradients' rows
   extern __shared__ uint4 smem[];
-  __shared__ __align__(16) float red[kSlotRedFloats];
+  constexpr int RED = 2 * NT * T > kSlotRed ? 2 * NT * T : kSlotRed;
+  __shared__ __align__(16) float red[red_floats(THREADS, RED)];
   __shared__ Turns turns;
   grid_launch_dependents();
   constexpr bool FULL = FORM == kFull;
@@ -588,19 +595,18 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
   const bool rot = FULL || (p.rotate && !plain);
   const int norm = FULL ? SPARGE_HEADS_NORM_TOKEN : plain ? 0 : p.norm;
   turns.fill(p);
-  clear_red(red);
+  Slot s = make_slot(any.W, red, red_half(THREADS, RED));
   __syncthreads();
   const int per_cta = slots_per_cta(any.W);
-  Slot s = make_slot(any.W, red);
   if (s.index >= per_cta) return;
   const Place<SPLIT, D, V, FULL> at(s, any.C);
   const int H = any.C / D;
   const int64_t slot = static_cast<int64_t>(blockIdx.x) * per_cta + s.index;
-  Share mine(p, 1, slot, static_cast<int64_t>(gridDim.x) * per_cta);
+  Share mine(p, T, slot, static_cast<int64_t>(gridDim.x) * per_cta);
 
   const Ring ring = {smem + threadIdx.x, static_cast<int>(blockDim.x)};
   const Ring weights = ring + S * STAGE;
-  float* ang = reinterpret_cast<float*>(smem + blockDim.x * RING) + s.index * kAngleBuffers * D;
+  float* ang = reinterpret_cast<float*>(smem + blockDim.x * RING) + s.index * kAngleBuffers * T * D;
   const int64_t far = static_cast<int64_t>(at.head_step) * p.N * D;
   int64_t in = ((static_cast<int64_t>(mine.b) * H + at.head) * p.N + mine.n) * D + at.c;
   const TX* xp[NT];
@@ -618,27 +624,33 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
   const auto issue = [&](Ring stage) {
     if (ahead_left > 0) {
       --ahead_left;
+      const bool second = T == 1 || ahead_n + 1 < p.N;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const HeadsPart& part = p.part[part0 + i];
         const bool here = FORM != kJoint || part.y != nullptr;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          if (here && at.here(v)) {
+        for (int t = 0; t < T; ++t) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            if (!(here && at.here(v) && (t == 0 || second))) continue;
+            const int q = (i * T + t) * V + v;
             stage_row<__nv_bfloat16, SPLIT, D>(
-                stage + i * V + v, static_cast<const __nv_bfloat16*>(part.y) + in + v * far);
+                stage + q, static_cast<const __nv_bfloat16*>(part.y) + in + t * D + v * far);
             if (i < NT && norm)
-              stage_row<TX, SPLIT, D>(stage + XAT + (i * V + v) * Q8,
-                                      xp[i < NT ? i : 0] + v * at.head_step * part.xs[2]);
+              stage_row<TX, SPLIT, D>(
+                  stage + XAT + q * Q8,
+                  xp[i < NT ? i : 0] + t * part.xs[1] + v * at.head_step * part.xs[2]);
           }
         }
-        if (i < NT) xp[i < NT ? i : 0] += part.xs[1];
+        if (i < NT) xp[i < NT ? i : 0] += T * part.xs[1];
       }
-      in += D;
-      if (++ahead_n == p.N) {
+      in += T * D;
+      ahead_n += T;
+      if (ahead_n >= p.N) {
         ahead_n = 0;
         ++ahead_b;
-        in += static_cast<int64_t>(H - 1) * p.N * D;
+        in = (static_cast<int64_t>(ahead_b) * H + at.head) * p.N * D + at.c;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           const HeadsPart& part = p.part[part0 + i];
@@ -662,16 +674,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
       dw[i * V + v] = {{0, 0}, {0, 0}};
       if (!at.here(v)) {
         for (int k = 0; k < S; ++k) {
-          ring[k * STAGE + i * V + v] = make_uint4(0, 0, 0, 0);
-          for (int q = 0; q < Q8; ++q)
-            ring[k * STAGE + XAT + (i * V + v) * Q8 + q] = make_uint4(0, 0, 0, 0);
+          for (int t = 0; t < T; ++t) {
+            const int at_row = (i * T + t) * V + v;
+            ring[k * STAGE + at_row] = make_uint4(0, 0, 0, 0);
+            for (int q = 0; q < Q8; ++q)
+              ring[k * STAGE + XAT + at_row * Q8 + q] = make_uint4(0, 0, 0, 0);
+          }
         }
       }
     }
   }
 
   const float inv = 1.f / (norm == 1 ? any.C : D);
-  Angles<1, D> angles;
+  Angles<T, D> angles;
   int b = mine.b, n = mine.n, buf = 0;
   if (rot && mine.left > 0) {
     angles.start(p, b, n);
@@ -682,17 +697,17 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
   for (; mine.left > 0; --mine.left) {
     cp_async_wait<S - 1>();
     const Ring stage = ring + k * STAGE;
-    const float* cs = ang + buf * D;
-    Pairs g[NT * V];
-    float sums[2 * NT * V];
+    const float* cs = ang + buf * T * D;
+    Pairs g[NT * T * V];
+    float sums[2 * NT * T * V];
 #pragma unroll
-    for (int i = 0; i < NT * V; ++i) {
+    for (int i = 0; i < NT * T * V; ++i) {
       g[i] = unstage_pairs<__nv_bfloat16, INTER>(stage + i);
-      if (rot) g[i] = rotate<true, INTER, SPLIT, D>(g[i], cs, at.c);
+      if (rot) g[i] = rotate<true, INTER, SPLIT, D>(g[i], cs + i / V % T * D, at.c);
       if (norm) {
         const Pairs x = unstage_pairs<TX, INTER>(stage + XAT + i * Q8);
         sums[2 * i] = dot(x, x);
-        sums[2 * i + 1] = dot(x, mul(g[i], unstage_weight(weights + i * 2)));
+        sums[2 * i + 1] = dot(x, mul(g[i], unstage_weight(weights + (i / (T * V) * V + i % V) * 2)));
       }
     }
     // The next token's angles, into the buffer that every warp has read before
@@ -700,63 +715,71 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
     buf ^= 1;
     if (rot) {
       angles.next(p);
-      angles.fill(p, s, turns, ang + buf * D);
+      angles.fill(p, s, turns, ang + buf * T * D);
     }
     if (norm == 1) {
-      float ts[2 * NT];
+      float ts[2 * NT * T];
 #pragma unroll
-      for (int i = 0; i < 2 * NT; ++i) {
+      for (int i = 0; i < 2 * NT * T; ++i) {
         ts[i] = sums[(i / 2) * 2 * V + i % 2];
 #pragma unroll
         for (int v = 1; v < V; ++v) ts[i] += sums[((i / 2) * V + v) * 2 + i % 2];
       }
       slot_sum<warp_eights(THREADS)>(s, ts);
 #pragma unroll
-      for (int i = 0; i < 2 * NT * V; ++i) sums[i] = ts[(i / (2 * V)) * 2 + i % 2];
+      for (int i = 0; i < 2 * NT * T * V; ++i) sums[i] = ts[(i / (2 * V)) * 2 + i % 2];
       if (s.W == 1) slot_sync(s);
     } else {
       if (norm == 2) head_sum<D>(sums);
       if (rot) slot_sync(s);
     }
+    const bool second = T == 1 || n + 1 < p.N;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const HeadsPart& part = p.part[part0 + i];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const bool ok = at.here(v) && (FORM != kJoint || part.y != nullptr);
-        TX* out = dx[i] + v * at.head_step * part.ds[2];
-        if (i < NT) {
-          const int q = i < NT ? i * V + v : 0;
-          Pairs o = g[q];
-          if (norm) {
-            const Pairs xh = mul(unstage_pairs<TX, INTER>(stage + XAT + q * Q8),
-                                 rsqrtf(sums[2 * q] * inv + p.eps));
-            const float r = rsqrtf(sums[2 * q] * inv + p.eps);
-            dw[q] = fma(o, xh, dw[q]);
-            // r (g w - xh mean(g w xh))
-            o = mul(fma(xh, -(sums[2 * q + 1] * inv * r), mul(o, unstage_weight(weights + q * 2))), r);
-          }
-          float f[8];
-          from_pairs<INTER>(o, f);
-          if (ok) store_row<TX, SPLIT, D>(out, f);
-        } else {
-          const Raw8<__nv_bfloat16> r = unstage8<__nv_bfloat16>(stage + i * V + v);
-          if (ok) {
-            if constexpr (sizeof(TX) == 2) {
-              store_row_raw<SPLIT, D>(out, r);
-            } else {
-              float f[8];
-              unpack8(r, f);
-              store_row<TX, SPLIT, D>(out, f);
+      for (int t = 0; t < T; ++t) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const bool ok = at.here(v) && (t == 0 || second) && (FORM != kJoint || part.y != nullptr);
+          TX* out = dx[i] + t * part.ds[1] + v * at.head_step * part.ds[2];
+          const int row = (i * T + t) * V + v;
+          if (i < NT) {
+            const int q = i < NT ? row : 0;
+            Pairs o = g[q];
+            if (norm) {
+              const float r = rsqrtf(sums[2 * q] * inv + p.eps);
+              const Pairs xh = mul(unstage_pairs<TX, INTER>(stage + XAT + q * Q8), r);
+              Pairs& to = dw[i < NT ? i * V + v : 0];
+              // (A second token behind the sample's end has left-over values.)
+              if (t == 0 || second) to = fma(o, xh, to);
+              // r (g w - xh mean(g w xh))
+              const Pairs w = unstage_weight(weights + (i * V + v) * 2);
+              o = mul(fma(xh, -(sums[2 * q + 1] * inv * r), mul(o, w)), r);
+            }
+            float f[8];
+            from_pairs<INTER>(o, f);
+            if (ok) store_row<TX, SPLIT, D>(out, f);
+          } else {
+            const Raw8<__nv_bfloat16> r = unstage8<__nv_bfloat16>(stage + row);
+            if (ok) {
+              if constexpr (sizeof(TX) == 2) {
+                store_row_raw<SPLIT, D>(out, r);
+              } else {
+                float f[8];
+                unpack8(r, f);
+                store_row<TX, SPLIT, D>(out, f);
+              }
             }
           }
         }
       }
-      dx[i] += part.ds[1];
+      dx[i] += T * part.ds[1];
     }
     issue(stage);
     k = k + 1 == S ? 0 : k + 1;
-    if (++n == p.N) {
+    n += T;
+    if (n >= p.N) {
       n = 0;
       ++b;
 #pragma unroll
@@ -857,7 +880,7 @@ int ring_pieces(const HeadsPlan& pl, bool bwd) {
 }
 int heads_smem(const HeadsPlan& pl, bool f32, int d, bool bwd) {
   const int pieces = f32 ? ring_pieces<float>(pl, bwd) : ring_pieces<__nv_bfloat16>(pl, bwd);
-  const int rows = bwd ? 1 : 2 / pl.V;
+  const int rows = bwd ? (pl.built == 192 ? 2 : 1) : 2 / pl.V;
   return 16 * pieces * pl.threads +
          pl.slots * kAngleBuffers * rows * d * static_cast<int>(sizeof(float));
 }
@@ -897,7 +920,7 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
   // A grid that is resident as a whole: every CTA stays for its share of the
   // rows.  Shared memory limits it, or registers.
   pl.smem = heads_smem(pl, a.x_type == SPARGE_F32, a.d, bwd);
-  const int rows = bwd ? 1 : 2 / pl.V;
+  const int rows = bwd ? (pl.built == 192 ? 2 : 1) : 2 / pl.V;
   const int warps = pl.threads / 32;
   const int by_regs = bwd ? resident_warps(bwd_regs(pl.built)) / warps
                           : kFwdResidents * row_threads(pl.V) / pl.threads;

@@ -352,11 +352,10 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? fwd_residents(V) : 0)
   constexpr int T = fwd_rows<V>(), S = fwd_stages<TX, TB, V>(), XQ = pieces8<TX>(), BQ = pieces8<TB>();
   constexpr int PIECES = fwd_pieces<TX, TB, V>(), STAGE = PIECES;
   extern __shared__ uint4 smem[];
-  __shared__ __align__(16) float red[kSlotRedFloats];
+  __shared__ __align__(16) float red[red_floats(row_threads(V))];
   __shared__ float counts[16];  // a slot of the forward has at most 16 warps
-  Slot s = make_slot(p.W, red);
+  Slot s = make_slot(p.W, red, red_half(row_threads(V)));
   const int per_cta = slots_per_cta(p.W);
-  clear_red(red);
   if (threadIdx.x < 16) {
     // Channels of each warp of a slot, none of those it does not have.
     int n = 0;
@@ -530,11 +529,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) resnorm_bwd_k
   constexpr int PIECES = bwd_pieces<TX, TB, THREADS>(), ROW = 2 * (XQ + BQ), STAGE = PIECES;
   constexpr int SUMS = POST ? 4 : 3;
   extern __shared__ uint4 smem[];
-  __shared__ __align__(16) float red[kSlotRedFloats];
+  __shared__ __align__(16) float red[red_floats(THREADS)];
   grid_launch_dependents();
-  clear_red(red);
+  Slot s = make_slot(p.W, red, red_half(THREADS));
   __syncthreads();
-  Slot s = make_slot(p.W, red);
   const int per_cta = slots_per_cta(p.W);
   if (s.index >= per_cta) return;
   constexpr int F = four_step<TX>();

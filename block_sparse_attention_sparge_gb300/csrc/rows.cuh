@@ -56,17 +56,24 @@ struct Slot {
   int index;    // in the CTA
   int W, warp;  // warps of the slot; this thread's among them
   int lane, tid;
-  float* red;   // 2 * kSlotRow floats of shared memory, zeros at the start
+  float* red;   // two halves of `half` floats of shared memory, zeros at the start
+  int half;
   int phase;
 };
 
-// Floats one warp contributes to a slot reduction, at most.
+// Floats a warp contributes to a slot's reduction, at most, in most kernels; of
+// one half of a slot's buffer, in a kernel built for so many threads; and of the
+// buffers of a CTA.
 constexpr int kSlotRed = 4;
-constexpr int kMaxWarps = 24;            // of a slot
-constexpr int kSlotRow = kMaxWarps * kSlotRed;
-constexpr int kSlotRedFloats = kMaxSlots * 2 * kSlotRow;
+constexpr int red_half(int threads, int per_warp = kSlotRed) {
+  return warp_eights(threads) * 8 * per_warp;
+}
+constexpr int red_floats(int threads, int per_warp = kSlotRed) {
+  return kMaxSlots * 2 * red_half(threads, per_warp);
+}
 
-SPARGE_DEV Slot make_slot(int W, float* red) {
+// Clears `red` (the CTA's buffers); a barrier of the CTA has to follow.
+SPARGE_DEV Slot make_slot(int W, float* red, int half) {
   Slot s;
   // The shuffle tells the compiler that the warp's index is the same in all
   // lanes, so what follows from it is computed once for the warp.
@@ -76,14 +83,11 @@ SPARGE_DEV Slot make_slot(int W, float* red) {
   s.W = W;
   s.warp = warp - s.index * W;
   s.tid = s.warp * 32 + s.lane;
-  s.red = red + s.index * 2 * kSlotRow;
+  s.red = red + s.index * 2 * half;
+  s.half = half;
+  for (int i = threadIdx.x; i < kMaxSlots * 2 * half; i += blockDim.x) red[i] = 0.f;
   s.phase = 0;
   return s;
-}
-
-// Before the first reduction, with a barrier behind it.
-SPARGE_DEV void clear_red(float* red) {
-  for (int i = threadIdx.x; i < kSlotRedFloats; i += blockDim.x) red[i] = 0.f;
 }
 
 SPARGE_DEV void slot_sync(const Slot& s) {
@@ -125,7 +129,7 @@ SPARGE_DEV float warp_sums(const float (&in)[K], int lane) {
 // alternate, so one barrier a call is enough: a warp cannot reach the next but
 // one call before every warp has read this one's values.
 SPARGE_DEV float* slot_half(Slot& s) {
-  float* red = s.red + s.phase * kSlotRow;
+  float* red = s.red + s.phase * s.half;
   s.phase ^= 1;
   return red;
 }
@@ -140,23 +144,41 @@ SPARGE_DEV float sum_of_8(float v) {
 // the kernel has at most 8 * EIGHTS warps.
 template <int EIGHTS, int K>
 SPARGE_DEV void slot_sum(Slot& s, float (&v)[K]) {
-  static_assert(K <= kSlotRed, "reduction buffer");
   const float mine = warp_sums(v, s.lane);
   if (s.W == 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, mine, k * (32 / K));
     return;
   }
+  constexpr int R = K > kSlotRed ? K : kSlotRed;  // floats of a warp
   float* red = slot_half(s);
-  if (s.lane % (32 / K) == 0) red[s.warp * kSlotRed + s.lane / (32 / K)] = mine;
+  if (s.lane % (32 / K) == 0) red[s.warp * R + s.lane / (32 / K)] = mine;
   slot_sync(s);
-  const float* in = red + (s.lane & 7) * kSlotRed + (s.lane >> 3) % K;
-  float sum = in[0];
+  if constexpr (K <= 4) {
+    const float* in = red + (s.lane & 7) * R + (s.lane >> 3) % K;
+    float sum = in[0];
 #pragma unroll
-  for (int e = 1; e < EIGHTS; ++e) sum += in[8 * e * kSlotRed];
-  sum = sum_of_8(sum);
+    for (int e = 1; e < EIGHTS; ++e) sum += in[8 * e * R];
+    sum = sum_of_8(sum);
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, sum, 8 * k);
+    for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, sum, 8 * k);
+  } else {
+    static_assert(K == 8, "two floats of a warp to a lane");
+    const float2* in = reinterpret_cast<const float2*>(red + (s.lane & 7) * R) + (s.lane >> 3);
+    float2 sum = in[0];
+#pragma unroll
+    for (int e = 1; e < EIGHTS; ++e) {
+      const float2 more = in[8 * e * R / 2];
+      sum.x += more.x, sum.y += more.y;
+    }
+    sum.x = sum_of_8(sum.x);
+    sum.y = sum_of_8(sum.y);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __shfl_sync(0xffffffffu, sum.x, 8 * k);
+      v[2 * k + 1] = __shfl_sync(0xffffffffu, sum.y, 8 * k);
+    }
+  }
 }
 
 // ------------------------------------------------------ stages of a thread
