@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -736,6 +737,14 @@ def _tensor_lists(grads, outs, index):
     return array.array("q", rows), array.array("q", ptrs) if outs is not None else None
 
 
+@functools.lru_cache(maxsize=64)
+def _clip_workspace_bytes(n: int) -> int:
+    nbytes = _SZ(0)
+    _check(load_library().sparge_clip_workspace_bytes(n, ctypes.byref(nbytes)),
+           "sparge_clip_workspace_bytes")
+    return nbytes.value
+
+
 def sparge_clip_grads(grads, max_norm: float | None, out=None, eps: float = 1e-6, workspace=None):
     """Global 2-norm of a list of gradients (fp32 scalar tensor, returned
     without waiting for the GPU), and g * min(1, max_norm / (norm + eps)) in
@@ -755,10 +764,7 @@ def sparge_clip_grads(grads, max_norm: float | None, out=None, eps: float = 1e-6
     table, outs = _tensor_lists(grads, out, index)
     lib = load_library()
     if workspace is None:
-        nbytes = _SZ(0)
-        _check(lib.sparge_clip_workspace_bytes(n, ctypes.byref(nbytes)),
-               "sparge_clip_workspace_bytes")
-        workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=device)
+        workspace = torch.empty(_clip_workspace_bytes(n), dtype=torch.uint8, device=device)
     elif workspace.device != device:
         raise ValueError("expected CUDA tensors on one device")
     norm = torch.empty((), dtype=torch.float32, device=device)
