@@ -573,7 +573,8 @@ def sparge_heads_bwd(dq=None, dk=None, dv=None, q=None, k=None, rope: RopeAxes |
             dx = torch.empty((B, N, H, d), dtype=dtype, device=device)
         elif dx.shape != (B, N, H, d) or dx.get_device() != index:
             raise ValueError("out must be [B, N, H, d] tensors on the same device")
-        elif any(st == 0 and n_ > 1 for st, n_ in zip(dx.stride(), dx.shape)):
+        elif 0 in dx.stride() and any(st == 0 and n_ > 1
+                                      for st, n_ in zip(dx.stride(), dx.shape)):
             raise ValueError("out must not repeat elements")
         parts += (xp, *xs, wp, g.data_ptr(), dx.data_ptr(), *_token_strides(dx, B, N, H), dw, H,
                   i == 2)

@@ -17,7 +17,7 @@
 // kept the pipe busy half of the time, and the last sums are left to single
 // warps (a list of four small tensors: 6 us, 13 with all threads at it).
 //
-// Bound by memory: 680M bf16 values take 203 us for the norm (6.7 TB/s) and 599
+// Bound by memory: 680M bf16 values take 203 us for the norm (6.7 TB/s) and 593
 // us in all, which is three passes over 1.36 GB at the rate of a copy; the second
 // read is the price of a factor that only the whole norm gives.
 #include <cuda_bf16.h>
@@ -437,9 +437,9 @@ int sparge_clip_grads(const sparge_tensor* grads, void* const* out, int32_t n, f
     const int first = k * kLargeList, count = std::min(n - first, kLargeList);
     int ctas = 0;
     const bool few = list_vectors(grads + first, count) == kFewVectors;
-    auto* launch = count <= kSmallList
-                       ? (few ? launch_norm<kSmallList, kFewVectors> : launch_norm<kSmallList, kVectors>)
-                       : (few ? launch_norm<kLargeList, kFewVectors> : launch_norm<kLargeList, kVectors>);
+    const bool small = count <= kSmallList;
+    auto* launch = few ? launch_norm<kSmallList, kFewVectors> : launch_norm<kSmallList, kVectors>;
+    if (!small) launch = few ? launch_norm<kLargeList, kFewVectors> : launch_norm<kLargeList, kVectors>;
     const cudaError_t e = launch(grads + first, count, a.sums + a.n_sums, &ctas, stream);
     if (e != cudaSuccess) return SPARGE_ERR_CUDA;
     a.n_sums += ctas;

@@ -16,6 +16,16 @@
 // A frequency is held as a 64-bit fraction of a turn (f / 2 pi * 2^64), so
 // pos * f is reduced to one turn by the wrap of an integer product, exactly for
 // every 32-bit position; sincospif then sees an argument in [-1, 1).
+//
+// Bound by memory: forward reads and writes every value once, backward reads the
+// gradient and the input and writes once (no normed row is kept for it; r comes
+// from the input again).  A row's statistics need all of its channels, so a slot
+// of warps holds a whole token and both tensors share its angles, computed once
+// for all heads.  Measured, bf16, norm over the token: 32760 tokens of 12 x 128,
+// Q, K and V: forward 99 us for 604 MB (6.1 TB/s), backward 137 us for 805 MB
+// (5.9 TB/s); 75600 tokens of 40 x 128: 777 us for 4.64 GB (6.0 TB/s) and 1072
+// us for 6.2 GB (5.8 TB/s).  What is missing to a copy's 6.8 TB/s is latency: 12
+// warps an SM, whose registers hold two tokens' channels, and a barrier a unit.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -24,8 +34,8 @@
 #include <algorithm>
 
 #include "common.cuh"
-#include "kernels.h"
 #include "rows.cuh"
+#include "sparge.h"
 
 namespace sparge {
 
@@ -334,8 +344,8 @@ constexpr int all_parts() {
   return FORM == kSingle ? 1 : 3;
 }
 
-// Stages of the ring: one more changes nothing at 480p (109 us both ways,
-// forward), and costs the wide forward its second CTA of an SM.
+// Stages of the ring: one more changes nothing in the forward of 12 heads (the
+// same time within 1 %), and costs the wide forward its second CTA of an SM.
 constexpr int kFwdStages = 2;
 // (Two tokens at once, or a joint fp32 row of 640 threads, leave room for two.)
 template <typename TX, int THREADS>

@@ -17,6 +17,16 @@
 // The variance is the sum of squares about each warp's own mean, joined by the
 // exact rule for two groups, so a row whose mean is far above its spread keeps
 // its digits.
+//
+// Bound by memory: the forward reads x and b and writes y and h, the backward
+// reads x, b, dy and dh and writes dx and db, each value once; the statistics
+// and the column sums stay in registers.  A slot of warps holds whole rows,
+// because both norms need all of a row before its first value can be written.
+// Measured: 32760 rows of 1536 (fp32 x, bf16 b): forward 93 us for 604 MB (6.5
+// TB/s), backward 140 us for 906 MB (6.5 TB/s); bf16 with a norm before and after
+// and one modulation a frame, backward: 106 us for 605 MB (5.7 TB/s, held back by
+// instruction issue); 75600 rows of 5120, forward 472 us for 3.10 GB (6.6 TB/s),
+// backward with fp32 x 1060 us for 7.0 GB (6.6 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -25,8 +35,8 @@
 #include <algorithm>
 
 #include "common.cuh"
-#include "kernels.h"
 #include "rows.cuh"
+#include "sparge.h"
 
 namespace sparge {
 
@@ -199,8 +209,9 @@ constexpr int mod_pieces() {
 // Mean and sum of squares about it of each of T rows over the slot.  `cnt`:
 // channels of this warp, `full` of every warp but the last, `last` of that.
 template <int T, int V>
-SPARGE_DEV void slot_moments(Slot& s, const F8 (&y)[T * V], const bool (&lo)[V], const bool (&hi)[V], float inv_cnt,
-                             const float* counts, float inv_c, float (&mean)[T], float (&m2)[T]) {
+SPARGE_DEV void slot_moments(Slot& s, const F8 (&y)[T * V], const bool (&lo)[V],
+                             const bool (&hi)[V], float inv_cnt, const float* counts, float inv_c,
+                             float (&mean)[T], float (&m2)[T]) {
   float part[T];
 #pragma unroll
   for (int t = 0; t < T; ++t) {
@@ -459,7 +470,8 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? fwd_residents(V) : 0)
           rbs[t] = rsqrtf(rbs[t] * p.inv_c + p.eps);
 #pragma unroll
           for (int v = 0; v < V; ++v)
-            b8[t * V + v] = mul(mul(b8[t * V + v], f8(rbs[t])), load_mod(p.post + at.mod[v][0], at.mod[v][1]));
+            b8[t * V + v] = mul(mul(b8[t * V + v], f8(rbs[t])),
+                                load_mod(p.post + at.mod[v][0], at.mod[v][1]));
         }
       }
       int64_t o = static_cast<int64_t>(row) * p.C + at.c;
