@@ -22,10 +22,10 @@
 // from the input again).  A row's statistics need all of its channels, so a slot
 // of warps holds a whole token and both tensors share its angles, computed once
 // for all heads.  Measured, bf16, norm over the token: 32760 tokens of 12 x 128,
-// Q, K and V: forward 99 us for 604 MB (6.1 TB/s), backward 137 us for 805 MB
-// (5.9 TB/s); 75600 tokens of 40 x 128: 777 us for 4.64 GB (6.0 TB/s) and 1072
+// Q, K and V: forward 96 us for 604 MB (6.3 TB/s), backward 131 us for 805 MB
+// (6.1 TB/s); 75600 tokens of 40 x 128: 780 us for 4.64 GB (5.9 TB/s) and 1075
 // us for 6.2 GB (5.8 TB/s).  What is missing to a copy's 6.8 TB/s is latency: 12
-// warps an SM, whose registers hold two tokens' channels, and a barrier a unit.
+// warps an SM (20 in the wide backward), and a barrier a unit.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -48,6 +48,10 @@ struct HeadsPart {
   void* dx;
   float* dw_part;  // [CTAs][H * d] or, under a norm over each head, [CTAs][d]
   int64_t xs[3], ds[3];
+  // From a slot's unit to its next: samples and tokens, the same in elements of
+  // x, y and dx, and what to add where the token would lie behind the sample.
+  int db, dn;
+  int64_t x_step, y_step, d_step, x_wrap, y_wrap, d_wrap;
   int C, W, plain;
 };
 
@@ -57,6 +61,7 @@ struct HeadsParams {
   const int32_t* pos;
   int64_t pos_ld;  // elements between samples of pos
   int M, N;        // rows in all, rows of one sample
+  int span;        // N rounded up to whole units
   int norm, rotate, w_bf16;
   float eps;
   uint64_t turn[64];
@@ -79,19 +84,22 @@ struct Turns {
 // The cosines and sines of a slot's tokens, T at a time, each computed once for
 // all heads of its parts: [T][cos | sin][D / 2] floats of shared memory.
 // Thread i of the slot owns pair i % (D / 2) of token i / (D / 2) (and more of
-// them where the slot is narrow).  Coordinates are counted on from token to
-// token, so the divisions are done once a sample; a thread whose coordinate did
-// not change keeps its values, which for time and height is nearly always.
+// them where the slot is narrow).  Coordinates are counted on from unit to
+// unit, so the divisions are done once a sample; a thread whose coordinate did
+// not change keeps its values.
 template <int T, int D>
 struct Angles {
   static constexpr int P = D / 2;
   int n, b;        // the next token
   int it, ih, iw;  // its coordinates on the grid
   int t, h, w;     // the sample's grid; t = 0: nothing turns
+  int dt, dh, dw;  // a step between units, as coordinates
+  int held;        // a given position (of the thread's first pair), read a unit
+                   // ahead: read when it is needed, 480p takes 122 us, not 97
   int last;        // position behind cs, sn
   float cs, sn;
 
-  SPARGE_DEV void open(const HeadsParams& p, int sample, int token) {
+  SPARGE_DEV void open(const HeadsParams& p, int sample, int token, int dn) {
     b = sample;
     n = token;
     it = ih = iw = t = 0;
@@ -101,11 +109,15 @@ struct Angles {
       t = 0;
       return;
     }
+    place(n, it, ih, iw);
+    place(dn, dt, dh, dw);
+  }
+  SPARGE_DEV void place(int token, int& ct, int& ch, int& cw) const {
     const int64_t hw = static_cast<int64_t>(h) * w;
-    it = hw > n ? 0 : n / static_cast<int>(hw);
-    const int rest = n - static_cast<int>(it * hw);
-    ih = rest / w;
-    iw = rest - ih * w;
+    ct = hw > token ? 0 : token / static_cast<int>(hw);
+    const int rest = token - static_cast<int>(ct * hw);
+    ch = rest / w;
+    cw = rest - ch * w;
   }
   // The position of the token `on` (0 or 1) tokens on along axis a.
   SPARGE_DEV int position(const HeadsParams& p, int on, int a) const {
@@ -124,11 +136,14 @@ struct Angles {
       if (++ch == h) ch = 0, ++ct;
     }
   }
+  SPARGE_DEV void hold(const HeadsParams& p, const Slot& s, const Turns& turns) {
+    if (p.pos != nullptr && s.tid < T * P) held = position(p, s.tid / P, turns.axis[s.tid % P]);
+  }
   SPARGE_DEV void fill(const HeadsParams& p, const Slot& s, const Turns& turns, float* out) {
     for (int i = s.tid; i < T * P; i += s.W * 32) {
       const int j = i % P;
-      const int pos = position(p, i / P, turns.axis[j]);
       const bool first = i == s.tid;
+      const int pos = p.pos != nullptr && first ? held : position(p, i / P, turns.axis[j]);
       float c = cs, q = sn;
       if (!(first && pos == last)) {
         const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns.turn[j];
@@ -140,18 +155,26 @@ struct Angles {
       out[(i / P) * D + P + j] = q;
     }
   }
-  // On to the next unit of at most T tokens of a sample.
-  SPARGE_DEV void next(const HeadsParams& p) {
-    n += T;
-    if (n >= p.N) {
-      open(p, b + 1, 0);
+  // On to the slot's next unit.
+  SPARGE_DEV void next(const HeadsParams& p, const HeadsPart& part, const Slot& s,
+                       const Turns& turns) {
+    n += part.dn;
+    if (part.db > 0 || n >= p.span) {
+      const bool wrap = n >= p.span;
+      open(p, b + part.db + wrap, wrap ? n - p.span : n, part.dn);
     } else if (t > 0) {
-#pragma unroll
-      for (int k = 0; k < T; ++k) step(it, ih, iw);
+      iw += dw;
+      ih += dh;
+      it += dt;
+      if (iw >= w) iw -= w, ++ih;
+      if (ih >= h) ih -= h, ++it;
     }
+    hold(p, s, turns);
   }
-  SPARGE_DEV void start(const HeadsParams& p, int sample, int token) {
-    open(p, sample, token);
+  SPARGE_DEV void start(const HeadsParams& p, const HeadsPart& part, const Slot& s,
+                        const Turns& turns, int sample, int token) {
+    open(p, sample, token, part.dn);
+    hold(p, s, turns);
     last = 0, cs = 1.f, sn = 0.f;  // position 0 turns nothing
   }
 };
@@ -332,7 +355,8 @@ struct Place {
 // are computed once for both and one barrier serves both sums.  Full: the same
 // where all three are there, turned and under a norm over the token, and no
 // thread is without channels, which takes every branch out of the row loop
-// (480p: 100 instead of 104 us forward, 138 instead of 160 us backward).
+// (when it was added, 480p: 100 instead of 104 us forward, 138 instead of 160 us
+// backward).
 // Single: a part to each blockIdx.y, for parts of different head counts.
 enum Form { kSingle, kJoint, kFull };
 template <int FORM>
@@ -344,8 +368,8 @@ constexpr int all_parts() {
   return FORM == kSingle ? 1 : 3;
 }
 
-// Stages of the ring: one more changes nothing in the forward of 12 heads (the
-// same time within 1 %), and costs the wide forward its second CTA of an SM.
+// Stages of the ring: with one more the forward of 12 heads takes 109 us instead
+// of 96, and that of 40 heads 774 instead of 782.
 constexpr int kFwdStages = 2;
 // (Two tokens at once, or a joint fp32 row of 640 threads, leave room for two.)
 template <typename TX, int THREADS>
@@ -357,17 +381,17 @@ template <int V>
 constexpr int fwd_rows() {
   return 2 / V;
 }
-// CTAs of an SM that the registers are budgeted for.  At 480p two: three cost a
-// reload between the two passes over a token (115 us forward against 104).  The
-// wide forward too is launched as if two were resident (720p: 777 us, 830 with
-// a grid for one).
+// CTAs of an SM that the registers are budgeted for.  At 480p two: with three the
+// forward takes 111 us instead of 96, with one token at a time and three 98, and
+// four 108.  The wide forward too is launched as if two were resident (720p: 782
+// us, 830 with a grid for one).
 constexpr int kFwdResidents = 2;
 // Pieces of one stage, and of a thread's whole ring with the weights behind it.
 template <typename TX, int FORM, int V>
 constexpr int fwd_pieces() {
   return all_parts<FORM>() * fwd_rows<V>() * V * pieces8<TX>();
 }
-// (One at a time: 480p 141 instead of 135 us, in fp32 240 instead of 205.  CTAs
+// (One at a time: 480p 141 instead of 137 us, in fp32 240 instead of 205.  CTAs
 // of 640 threads have no registers for two.)
 template <int THREADS>
 constexpr int bwd_rows() {
@@ -389,16 +413,18 @@ constexpr int bwd_ring() {
 }
 constexpr int kAngleBuffers = 2;  // of T tokens (D floats each), for every slot
 
-// A slot's share of the units (at most T tokens of one sample), in a row.
+// A slot's share of the units (at most T tokens of one sample): one of every
+// `nslots`, so that the machine is at neighbouring tokens at any time and each
+// head's rows are written side by side (480p: 96 and 131 us; with a run of tokens
+// to each slot 100 and 137).
 struct Share {
   int left, b, n;  // units, and the first one's sample and token
-  SPARGE_DEV Share(const HeadsParams& p, int T, int64_t slot, int64_t nslots) {
-    const int per_sample = (p.N + T - 1) / T;
-    const int64_t units = static_cast<int64_t>(p.M / p.N) * per_sample;
-    const int begin = static_cast<int>(units * slot / nslots);
-    left = static_cast<int>(units * (slot + 1) / nslots) - begin;
-    b = begin / per_sample;
-    n = (begin - b * per_sample) * T;
+  SPARGE_DEV Share(const HeadsParams& p, int T, int slot, int nslots) {
+    const int per_sample = p.span / T;
+    const int units = p.M / p.N * per_sample;
+    left = slot < units ? (units - slot - 1) / nslots + 1 : 0;
+    b = slot / per_sample;
+    n = (slot - b * per_sample) * T;
   }
 };
 
@@ -425,8 +451,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? kFwdResidents : 0) he
   if (s.index >= per_cta) return;
   const Place<SPLIT, D, V, FULL> at(s, any.C);
   const int H = any.C / D;
-  Share mine(p, T, static_cast<int64_t>(blockIdx.x) * per_cta + s.index,
-             static_cast<int64_t>(gridDim.x) * per_cta);
+  Share mine(p, T, blockIdx.x * per_cta + s.index, gridDim.x * per_cta);
   if (mine.left == 0) return;
 
   // Shared memory: the threads' rings, then the slots' angles.
@@ -434,15 +459,13 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? kFwdResidents : 0) he
   const Ring weights = ring + S * STAGE;
   float* ang = reinterpret_cast<float*>(smem + blockDim.x * RING) + s.index * kAngleBuffers * T * D;
   const TX* xp[NP];
-  int64_t xs[NP];  // elements from one unit to the next
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const HeadsPart& part = p.part[part0 + i];
     xp[i] = static_cast<const TX*>(part.x) + at.head * part.xs[2] + at.c + mine.b * part.xs[0] +
             mine.n * part.xs[1];
-    xs[i] = T * part.xs[1];
   }
-  int ahead_b = mine.b, ahead_n = mine.n, ahead_left = mine.left;
+  int ahead_n = mine.n, ahead_left = mine.left;
   const auto issue = [&](Ring stage) {
     if (ahead_left > 0) {
       --ahead_left;
@@ -460,17 +483,13 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? kFwdResidents : 0) he
                                         xp[i] + t * part.xs[1] + v * at.head_step * part.xs[2]);
           }
         }
-        xp[i] += xs[i];
+        xp[i] += part.x_step;
       }
-      ahead_n += T;
-      if (ahead_n >= p.N) {
-        ahead_n = 0;
-        ++ahead_b;
+      ahead_n += any.dn;
+      if (ahead_n >= p.span) {
+        ahead_n -= p.span;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const HeadsPart& part = p.part[part0 + i];
-          xp[i] = static_cast<const TX*>(part.x) + at.head * part.xs[2] + at.c + ahead_b * part.xs[0];
-        }
+        for (int i = 0; i < NP; ++i) xp[i] += p.part[part0 + i].x_wrap;
       }
     }
     cp_async_commit();
@@ -499,7 +518,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? kFwdResidents : 0) he
 
   const float inv = 1.f / (norm == 1 ? any.C : D);
   Angles<T, D> angles;
-  angles.start(p, mine.b, mine.n);
+  angles.start(p, any, s, turns, mine.b, mine.n);
   int n = mine.n;
   int64_t out = ((static_cast<int64_t>(mine.b) * H + at.head) * p.N + n) * D + at.c;
   const int64_t far = static_cast<int64_t>(at.head_step) * p.N * D;
@@ -509,7 +528,7 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? kFwdResidents : 0) he
     buf ^= 1;
     if (rot) {
       angles.fill(p, s, turns, cs);
-      angles.next(p);
+      angles.next(p, any, s, turns);
     }
     cp_async_wait<S - 1>();
     const Ring stage = ring + k * STAGE;
@@ -574,12 +593,11 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? kFwdResidents : 0) he
     }
     issue(stage);
     k = k + 1 == S ? 0 : k + 1;
-    n += T;
-    out += T * D;
-    if (n >= p.N) {
-      // Token 0 of the next sample.
-      out += (static_cast<int64_t>(H) * p.N - n) * D;
-      n = 0;
+    n += any.dn;
+    out += any.y_step;
+    if (n >= p.span) {
+      n -= p.span;
+      out += any.y_wrap;
     }
   }
 }
@@ -611,8 +629,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
   if (s.index >= per_cta) return;
   const Place<SPLIT, D, V, FULL> at(s, any.C);
   const int H = any.C / D;
-  const int64_t slot = static_cast<int64_t>(blockIdx.x) * per_cta + s.index;
-  Share mine(p, T, slot, static_cast<int64_t>(gridDim.x) * per_cta);
+  Share mine(p, T, blockIdx.x * per_cta + s.index, gridDim.x * per_cta);
 
   const Ring ring = {smem + threadIdx.x, static_cast<int>(blockDim.x)};
   const Ring weights = ring + S * STAGE;
@@ -630,7 +647,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
     dx[i] = static_cast<TX*>(part.dx) + at.head * part.ds[2] + at.c + mine.b * part.ds[0] +
             mine.n * part.ds[1];
   }
-  int ahead_b = mine.b, ahead_n = mine.n, ahead_left = mine.left;
+  int ahead_n = mine.n, ahead_left = mine.left;
   const auto issue = [&](Ring stage) {
     if (ahead_left > 0) {
       --ahead_left;
@@ -653,19 +670,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
                   xp[i < NT ? i : 0] + t * part.xs[1] + v * at.head_step * part.xs[2]);
           }
         }
-        if (i < NT) xp[i < NT ? i : 0] += T * part.xs[1];
+        if (i < NT) xp[i < NT ? i : 0] += part.x_step;
       }
-      in += T * D;
-      ahead_n += T;
-      if (ahead_n >= p.N) {
-        ahead_n = 0;
-        ++ahead_b;
-        in = (static_cast<int64_t>(ahead_b) * H + at.head) * p.N * D + at.c;
+      in += any.y_step;
+      ahead_n += any.dn;
+      if (ahead_n >= p.span) {
+        ahead_n -= p.span;
+        in += any.y_wrap;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const HeadsPart& part = p.part[part0 + i];
-          xp[i] = static_cast<const TX*>(part.x) + at.head * part.xs[2] + at.c + ahead_b * part.xs[0];
-        }
+        for (int i = 0; i < NT; ++i) xp[i] += p.part[part0 + i].x_wrap;
       }
     }
     cp_async_commit();
@@ -697,10 +710,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
 
   const float inv = 1.f / (norm == 1 ? any.C : D);
   Angles<T, D> angles;
-  int b = mine.b, n = mine.n, buf = 0;
+  int n = mine.n, buf = 0;
   if (rot && mine.left > 0) {
-    angles.start(p, b, n);
+    angles.start(p, any, s, turns, mine.b, n);
     angles.fill(p, s, turns, ang);
+    angles.next(p, any, s, turns);
     slot_sync(s);
   }
   int k = 0;
@@ -724,8 +738,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
     // the barrier of the token before; this token's barrier publishes them.
     buf ^= 1;
     if (rot) {
-      angles.next(p);
       angles.fill(p, s, turns, ang + buf * T * D);
+      angles.next(p, any, s, turns);
     }
     if (norm == 1) {
       float ts[2 * NT * T];
@@ -784,19 +798,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
           }
         }
       }
-      dx[i] += T * part.ds[1];
+      dx[i] += part.d_step;
     }
     issue(stage);
     k = k + 1 == S ? 0 : k + 1;
-    n += T;
-    if (n >= p.N) {
-      n = 0;
-      ++b;
+    n += any.dn;
+    if (n >= p.span) {
+      n -= p.span;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const HeadsPart& part = p.part[part0 + i];
-        dx[i] = static_cast<TX*>(part.dx) + at.head * part.ds[2] + at.c + b * part.ds[0];
-      }
+      for (int i = 0; i < NP; ++i) dx[i] += p.part[part0 + i].d_wrap;
     }
   }
   if (!norm) return;
@@ -870,6 +880,7 @@ struct HeadsPlan {
   Form form;
   int built;  // the size of CTA that the kernel is built for
   int V, ctas, threads, slots;  // slots: of a CTA, at most
+  int rows;          // tokens that a slot takes at once
   int n;             // parts beside one another in the grid
   int at[3];         // the place of each of the call's parts
   int smem;          // dynamic, of a CTA
@@ -890,9 +901,8 @@ int ring_pieces(const HeadsPlan& pl, bool bwd) {
 }
 int heads_smem(const HeadsPlan& pl, bool f32, int d, bool bwd) {
   const int pieces = f32 ? ring_pieces<float>(pl, bwd) : ring_pieces<__nv_bfloat16>(pl, bwd);
-  const int rows = bwd ? (pl.built == 192 ? 2 : 1) : 2 / pl.V;
   return 16 * pieces * pl.threads +
-         pl.slots * kAngleBuffers * rows * d * static_cast<int>(sizeof(float));
+         pl.slots * kAngleBuffers * pl.rows * d * static_cast<int>(sizeof(float));
 }
 
 constexpr int kDeclared = 5184;  // shared memory that a kernel declares, at most
@@ -929,14 +939,14 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
   }
   // A grid that is resident as a whole: every CTA stays for its share of the
   // rows.  Shared memory limits it, or registers.
+  pl.rows = bwd ? (pl.built == 192 ? 2 : 1) : 2 / pl.V;
   pl.smem = heads_smem(pl, a.x_type == SPARGE_F32, a.d, bwd);
-  const int rows = bwd ? (pl.built == 192 ? 2 : 1) : 2 / pl.V;
   const int warps = pl.threads / 32;
   const int by_regs = bwd ? resident_warps(bwd_regs(pl.built)) / warps
                           : kFwdResidents * row_threads(pl.V) / pl.threads;
   const int per_sm = std::max(1, std::min(std::min(by_regs, 64 / warps),
                                           kSmemPerSm / (pl.smem + kSmemOfCta + kDeclared)));
-  const int64_t units = static_cast<int64_t>(a.B) * ((a.N + rows - 1) / rows);
+  const int64_t units = static_cast<int64_t>(a.B) * ((a.N + pl.rows - 1) / pl.rows);
   const int64_t need = (units + slots_min - 1) / slots_min;
   const int64_t most = (kSMs * per_sm + pl.n - 1) / pl.n;
   pl.ctas = static_cast<int>(std::max<int64_t>(1, std::min(need, most)));
@@ -952,13 +962,19 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
 
 HeadsParams heads_params(const sparge_heads& a, const HeadsPlan& pl) {
   HeadsParams p = {};
-  if (pl.form != kSingle) {
-    // An absent part still gives the row its size.
-    for (int i = 0; i < 3; ++i) {
-      p.part[i].C = a.part[0].H * a.d;
-      p.part[i].W = slot_warps(p.part[i].C, pl.V);
-    }
-  }
+  const int per_sample = (a.N + pl.rows - 1) / pl.rows;
+  p.span = per_sample * pl.rows;
+  const auto shape = [&](HeadsPart& o, int H) {
+    o.C = H * a.d;
+    o.W = slot_warps(o.C, pl.V);
+    const int slots = pl.ctas * slots_per_cta(o.W);
+    o.db = slots / per_sample;
+    o.dn = slots % per_sample * pl.rows;
+    o.y_step = (static_cast<int64_t>(o.db) * H * a.N + o.dn) * a.d;
+    o.y_wrap = (static_cast<int64_t>(H) * a.N - p.span) * a.d;
+  };
+  // An absent part still gives the row its size.
+  for (int i = 0; i < 3 && pl.form != kSingle; ++i) shape(p.part[i], a.part[0].H);
   for (int i = 0; i < a.n_parts; ++i) {
     const sparge_heads_part& s = a.part[i];
     HeadsPart& o = p.part[pl.at[i]];
@@ -966,9 +982,12 @@ HeadsParams heads_params(const sparge_heads& a, const HeadsPlan& pl) {
     o.w = s.weight;
     o.y = s.y;
     o.dx = s.dx;
-    for (int k = 0; k < 3; ++k) o.xs[k] = s.x_stride[k], o.ds[k] = s.dx_stride[k];
-    o.C = s.H * a.d;
-    o.W = slot_warps(o.C, pl.V);
+    for (int k = a.B == 1; k < 3; ++k) o.xs[k] = s.x_stride[k], o.ds[k] = s.dx_stride[k];
+    shape(o, s.H);
+    o.x_step = o.db * o.xs[0] + o.dn * o.xs[1];
+    o.d_step = o.db * o.ds[0] + o.dn * o.ds[1];
+    o.x_wrap = o.xs[0] - p.span * o.xs[1];
+    o.d_wrap = o.ds[0] - p.span * o.ds[1];
     o.plain = s.plain;
   }
   p.grid = a.grid;
