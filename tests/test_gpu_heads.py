@@ -91,6 +91,41 @@ def test_forward_and_backward(case):
         assert x is None or torch.equal(x, y)
 
 
+@pytest.mark.parametrize("given", [False, True], ids=["grid", "pos"])
+@pytest.mark.parametrize("case", [(6000, 1, 2, 64, BF, "head"), (700, 5, 12, 128, BF, "token"),
+                                  (900, 4, 3, 64, F32, "token"), (350, 3, 20, 128, F32, "token")],
+                         ids=lambda c: "-".join(str(x) for x in c[:4]))
+def test_steps_over_several_samples(case, given):
+    """More short samples than the machine has slots: a slot's next token lies
+    samples further on."""
+    b, n, h, d, dtype, norm = case
+    q, k, v, wq, wk = _make(b, n, h, d, dtype, norm, seed=3)
+    g = _gen(6)
+    rope = B.RopeAxes(d, _pairs(d))
+    how = dict(rope=rope, norm=norm)
+    how["q_weight"], how["k_weight"] = _dev(wq, wk)
+    if given:
+        pos = torch.randint(-9, 2000, (b, n, 3), generator=g, dtype=torch.int32)
+        how["pos"] = pos.to(DEV)
+        at = pos.double()
+    else:
+        grid = torch.randint(1, 4, (b, 3), generator=g, dtype=torch.int32)
+        how["grid"] = grid.to(DEV)
+        at = R.positions(b, n, grid)
+    cs = R.angles(at, _pairs(d), d)
+    got = B.sparge_heads_fwd(*_dev(q, k, v), **how)
+    _check_fwd(got[0], q, wq, norm, cs, True)
+    _check_fwd(got[1], k, wk, norm, cs, True)
+    assert torch.equal(got[2].cpu(), v.to(BF).transpose(1, 2))
+    dq, dk, dv = (_rand(g, b, h, n, d) for _ in range(3))
+    grads = B.sparge_heads_bwd(*_dev(dq, dk, dv, q, k), **how)
+    for i, dy, x, w in ((0, dq, q, wq), (1, dk, k, wk)):
+        dx, bound, dw, dwb = R.heads_bwd(R.f64(dy), R.f64(x), R.f64(w), norm, cs, True)
+        R.check(grads[i], dx, bound)
+        R.check(grads[3 + i], dw, dwb)
+    assert torch.equal(grads[2].cpu(), dv.to(dtype).transpose(1, 2))
+
+
 @pytest.mark.parametrize("norm", ["token", "head"])
 def test_norm_weight_type_apart_from_the_input_type_and_no_weight(norm):
     q, k, v, wq, _ = _make(1, 19, 3, 64, BF, norm, w_dtype=F32)
