@@ -350,15 +350,17 @@ struct Place {
   }
 };
 
-// One kernel for each direction, in three forms.  Joint: Q, K and V (parts 0, 1
+// One kernel for each direction, in four forms.  Joint: Q, K and V (parts 0, 1
 // and 2, any but one of which may be absent) of a token together, so the angles
 // are computed once for both and one barrier serves both sums.  Full: the same
 // where all three are there, turned and under a norm over the token, and no
 // thread is without channels, which takes every branch out of the row loop
 // (when it was added, 480p: 100 instead of 104 us forward, 138 instead of 160 us
-// backward).
+// backward).  FullHead: the same under a norm over each head of 128 channels (480p:
+// 98 instead of 107 us, 131 instead of 144; heads of 64 stay with Joint: 100 and
+// 139 us against 102 and 144).
 // Single: a part to each blockIdx.y, for parts of different head counts.
-enum Form { kSingle, kJoint, kFull };
+enum Form { kSingle, kJoint, kFull, kFullHead };
 template <int FORM>
 constexpr int turned_parts() {
   return FORM == kSingle ? 1 : 2;
@@ -438,12 +440,15 @@ __global__ void __launch_bounds__(row_threads(V), V == 1 ? kFwdResidents : 0) he
   extern __shared__ uint4 smem[];
   __shared__ __align__(16) float red[red_floats(row_threads(V))];
   __shared__ Turns turns;
-  constexpr bool FULL = FORM == kFull;
+  constexpr bool FULL = FORM >= kFull;
   const int part0 = FORM == kSingle ? blockIdx.y : 0;
   const HeadsPart& any = p.part[part0];
   const bool plain = FORM == kSingle && any.plain;
   const bool rot = FULL || (p.rotate && !plain);
-  const int norm = FULL ? SPARGE_HEADS_NORM_TOKEN : plain ? 0 : p.norm;
+  const int norm = FORM == kFull       ? SPARGE_HEADS_NORM_TOKEN
+                   : FORM == kFullHead ? SPARGE_HEADS_NORM_HEAD
+                   : plain             ? 0
+                                       : p.norm;
   turns.fill(p);
   Slot s = make_slot(any.W, red, red_half(row_threads(V)));
   __syncthreads();
@@ -616,12 +621,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
   __shared__ __align__(16) float red[red_floats(THREADS, RED)];
   __shared__ Turns turns;
   grid_launch_dependents();
-  constexpr bool FULL = FORM == kFull;
+  constexpr bool FULL = FORM >= kFull;
   const int part0 = FORM == kSingle ? blockIdx.y : 0;
   const HeadsPart& any = p.part[part0];
   const bool plain = FORM == kSingle && any.plain;
   const bool rot = FULL || (p.rotate && !plain);
-  const int norm = FULL ? SPARGE_HEADS_NORM_TOKEN : plain ? 0 : p.norm;
+  const int norm = FORM == kFull       ? SPARGE_HEADS_NORM_TOKEN
+                   : FORM == kFullHead ? SPARGE_HEADS_NORM_HEAD
+                   : plain             ? 0
+                                       : p.norm;
   turns.fill(p);
   Slot s = make_slot(any.W, red, red_half(THREADS, RED));
   __syncthreads();
@@ -926,8 +934,12 @@ HeadsPlan heads_plan(const sparge_heads& a, bool bwd) {
   const bool joint = a.n_parts > 1 && same && turned <= 2 && plain <= 1 && turned > 0 &&
                      (pl.V == 1 || (!bwd && a.x_type == SPARGE_BF16));
   const bool full = joint && a.n_parts == 3 && a.rope != nullptr &&
-                    a.norm == SPARGE_HEADS_NORM_TOKEN && widest % (256 * pl.V) == 0;
-  pl.form = full ? kFull : joint ? kJoint : kSingle;
+                    (a.norm == SPARGE_HEADS_NORM_TOKEN ||
+                     (a.norm == SPARGE_HEADS_NORM_HEAD && a.d == 128)) &&
+                    widest % (256 * pl.V) == 0;
+  pl.form = !full ? (joint ? kJoint : kSingle)
+            : a.norm == SPARGE_HEADS_NORM_TOKEN ? kFull
+                                                : kFullHead;
   pl.n = joint ? 1 : a.n_parts;
   int slots_min = kMaxSlots;
   for (int i = 0; i < a.n_parts; ++i) {
@@ -1024,6 +1036,10 @@ template <typename TX, bool INTER, int D, int V>
 cudaError_t launch_fwd(const HeadsParams& p, const HeadsPlan& pl, cudaStream_t st) {
   if constexpr (V == 1 || sizeof(TX) == 2) {
     if (pl.form == kFull) return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kFull>, p, pl, st);
+    if constexpr (D == 128) {
+      if (pl.form == kFullHead)
+        return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kFullHead>, p, pl, st);
+    }
     if (pl.form == kJoint) return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kJoint>, p, pl, st);
   }
   return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kSingle>, p, pl, st);
@@ -1034,6 +1050,10 @@ cudaError_t launch_bwd(const HeadsParams& p, const HeadsPlan& pl, cudaStream_t s
   if constexpr (bwd_vectors(THREADS) == 1) {
     if (pl.form == kFull)
       return launch_kernel(heads_bwd_kernel<TX, INTER, D, THREADS, kFull>, p, pl, st);
+    if constexpr (D == 128) {
+      if (pl.form == kFullHead)
+        return launch_kernel(heads_bwd_kernel<TX, INTER, D, THREADS, kFullHead>, p, pl, st);
+    }
     if (pl.form == kJoint)
       return launch_kernel(heads_bwd_kernel<TX, INTER, D, THREADS, kJoint>, p, pl, st);
   }

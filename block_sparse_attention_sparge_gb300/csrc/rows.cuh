@@ -308,8 +308,7 @@ SPARGE_DEV Raw8<T> unstage8(Ring src) {
 // ------------------------------------------------------- sums of partial rows
 // out[o][c] = sum over r < nrow of src[(o * nrow + r) * ld + c], in an order that
 // depends on nrow alone.  C and ld are multiples of 4, nout * C is below 2^31;
-// 16-byte aligned (out: 8
-// for bf16).
+// 16-byte aligned (out: 8 for bf16).
 struct ReduceJob {
   const float* src;
   void* out;

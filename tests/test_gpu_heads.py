@@ -56,6 +56,15 @@ CASES = [
     (1, 9, 63, 128, BF, "token", False, (3, 3, 1)),
     (1, 6000, 1, 64, BF, "head", False, (15, 20, 20)),  # many rows a slot
     (2, 3001, 9, 128, BF, "token", True, (6, 25, 20)),
+    # a norm over each head of full rows
+    (2, 301, 4, 128, BF, "head", True, (6, 7, 7)),
+    (1, 2, 2, 128, F32, "head", False, (1, 1, 2)),
+    (3, 1501, 12, 128, BF, "head", False, (15, 10, 10)),
+    (1, 77, 12, 128, F32, "head", True, (7, 11, 1)),
+    (2, 301, 40, 128, BF, "head", True, (6, 7, 7)),
+    (1, 333, 40, 128, BF, "head", False, (3, 10, 11)),
+    (1, 45, 40, 128, F32, "head", False, (3, 3, 5)),
+    (1, 9, 64, 128, BF, "head", True, (3, 3, 1)),
 ]
 
 
