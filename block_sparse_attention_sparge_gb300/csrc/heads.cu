@@ -22,8 +22,8 @@
 // from the input again).  A row's statistics need all of its channels, so a slot
 // of warps holds a whole token and both tensors share its angles, computed once
 // for all heads.  Measured, bf16, norm over the token: 32760 tokens of 12 x 128,
-// Q, K and V: forward 96 us for 604 MB (6.3 TB/s), backward 131 us for 805 MB
-// (6.1 TB/s); 75600 tokens of 40 x 128: 780 us for 4.64 GB (5.9 TB/s) and 1075
+// Q, K and V: forward 96 us for 604 MB (6.3 TB/s), backward 129 us for 805 MB
+// (6.2 TB/s); 75600 tokens of 40 x 128: 780 us for 4.64 GB (5.9 TB/s) and 1075
 // us for 6.2 GB (5.8 TB/s).  What is missing to a copy's 6.8 TB/s is latency: 12
 // warps an SM (20 in the wide backward), and a barrier a unit.
 #include <cuda_bf16.h>
@@ -53,7 +53,16 @@ struct HeadsPart {
   int db, dn;
   int64_t x_step, y_step, d_step, x_wrap, y_wrap, d_wrap;
   int C, W, plain;
+  SPARGE_DEV void advance(int span, int& b, int& n) const {
+    b += db;
+    n += dn;
+    if (n >= span) n -= span, ++b;
+  }
 };
+// The element of a part at which a thread's channels of a token begin.
+SPARGE_DEV int64_t part_at(const int64_t (&stride)[3], int b, int n, int head, int c) {
+  return b * stride[0] + n * stride[1] + head * stride[2] + c;
+}
 
 struct HeadsParams {
   HeadsPart part[3];
@@ -85,8 +94,7 @@ struct Turns {
 // all heads of its parts: [T][cos | sin][D / 2] floats of shared memory.
 // Thread i of the slot owns pair i % (D / 2) of token i / (D / 2) (and more of
 // them where the slot is narrow).  Coordinates are counted on from unit to
-// unit, so the divisions are done once a sample; a thread whose coordinate did
-// not change keeps its values.
+// unit, so the divisions are done once a sample.
 template <int T, int D>
 struct Angles {
   static constexpr int P = D / 2;
@@ -96,8 +104,6 @@ struct Angles {
   int dt, dh, dw;  // a step between units, as coordinates
   int held;        // a given position (of the thread's first pair), read a unit
                    // ahead: read when it is needed, 480p takes 122 us, not 97
-  int last;        // position behind cs, sn
-  float cs, sn;
 
   SPARGE_DEV void open(const HeadsParams& p, int sample, int token, int dn) {
     b = sample;
@@ -142,15 +148,12 @@ struct Angles {
   SPARGE_DEV void fill(const HeadsParams& p, const Slot& s, const Turns& turns, float* out) {
     for (int i = s.tid; i < T * P; i += s.W * 32) {
       const int j = i % P;
-      const bool first = i == s.tid;
-      const int pos = p.pos != nullptr && first ? held : position(p, i / P, turns.axis[j]);
-      float c = cs, q = sn;
-      if (!(first && pos == last)) {
-        const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns.turn[j];
-        sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f,
-                  &q, &c);  // 2^-31: half turns
-      }
-      if (first) last = pos, cs = c, sn = q;
+      const int pos =
+          p.pos != nullptr && i == s.tid ? held : position(p, i / P, turns.axis[j]);
+      const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns.turn[j];
+      float c, q;
+      sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &q,
+                &c);  // 2^-31: half turns
       out[(i / P) * D + j] = c;
       out[(i / P) * D + P + j] = q;
     }
@@ -158,10 +161,10 @@ struct Angles {
   // On to the slot's next unit.
   SPARGE_DEV void next(const HeadsParams& p, const HeadsPart& part, const Slot& s,
                        const Turns& turns) {
-    n += part.dn;
-    if (part.db > 0 || n >= p.span) {
-      const bool wrap = n >= p.span;
-      open(p, b + part.db + wrap, wrap ? n - p.span : n, part.dn);
+    const int before = b;
+    part.advance(p.span, b, n);
+    if (b != before) {
+      open(p, b, n, part.dn);
     } else if (t > 0) {
       iw += dw;
       ih += dh;
@@ -175,7 +178,6 @@ struct Angles {
                         const Turns& turns, int sample, int token) {
     open(p, sample, token, part.dn);
     hold(p, s, turns);
-    last = 0, cs = 1.f, sn = 0.f;  // position 0 turns nothing
   }
 };
 
@@ -357,8 +359,8 @@ struct Place {
 // thread is without channels, which takes every branch out of the row loop
 // (when it was added, 480p: 100 instead of 104 us forward, 138 instead of 160 us
 // backward).  FullHead: the same under a norm over each head of 128 channels (480p:
-// 98 instead of 107 us, 131 instead of 144; heads of 64 stay with Joint: 100 and
-// 139 us against 102 and 144).
+// 98 instead of 107 us, 131 instead of 144; heads of 64, which stay with Joint, gain
+// nothing from it).
 // Single: a part to each blockIdx.y, for parts of different head counts.
 enum Form { kSingle, kJoint, kFull, kFullHead };
 template <int FORM>
@@ -417,7 +419,7 @@ constexpr int kAngleBuffers = 2;  // of T tokens (D floats each), for every slot
 
 // A slot's share of the units (at most T tokens of one sample): one of every
 // `nslots`, so that the machine is at neighbouring tokens at any time and each
-// head's rows are written side by side (480p: 96 and 131 us; with a run of tokens
+// head's rows are written side by side (480p: 96 and 130 us; with a run of tokens
 // to each slot 100 and 137).
 struct Share {
   int left, b, n;  // units, and the first one's sample and token
@@ -643,26 +645,26 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
   const Ring weights = ring + S * STAGE;
   float* ang = reinterpret_cast<float*>(smem + blockDim.x * RING) + s.index * kAngleBuffers * T * D;
   const int64_t far = static_cast<int64_t>(at.head_step) * p.N * D;
-  int64_t in = ((static_cast<int64_t>(mine.b) * H + at.head) * p.N + mine.n) * D + at.c;
-  const TX* xp[NT];
+  // The places of what is read are computed for each unit: kept like those of the
+  // results, their registers spill in the wide kernels (720p, norm per head: 1042
+  // us, 1413 with all kept; norm over the token 1078, 1122 with none).
   TX* dx[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const HeadsPart& part = p.part[part0 + i];
-    if (i < NT)
-      xp[i] = static_cast<const TX*>(part.x) + at.head * part.xs[2] + at.c + mine.b * part.xs[0] +
-              mine.n * part.xs[1];
-    dx[i] = static_cast<TX*>(part.dx) + at.head * part.ds[2] + at.c + mine.b * part.ds[0] +
-            mine.n * part.ds[1];
+    dx[i] = static_cast<TX*>(part.dx) + part_at(part.ds, mine.b, mine.n, at.head, at.c);
   }
-  int ahead_n = mine.n, ahead_left = mine.left;
+  int ahead_b = mine.b, ahead_n = mine.n, ahead_left = mine.left;
   const auto issue = [&](Ring stage) {
     if (ahead_left > 0) {
       --ahead_left;
       const bool second = T == 1 || ahead_n + 1 < p.N;
+      const int64_t in = ((static_cast<int64_t>(ahead_b) * H + at.head) * p.N + ahead_n) * D + at.c;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const HeadsPart& part = p.part[part0 + i];
+        const TX* x = static_cast<const TX*>(part.x);
+        if (i < NT && norm) x += part_at(part.xs, ahead_b, ahead_n, at.head, at.c);
         const bool here = FORM != kJoint || part.y != nullptr;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
@@ -675,19 +677,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == 192 ? 2 : 0) heads_bwd_ker
             if (i < NT && norm)
               stage_row<TX, SPLIT, D>(
                   stage + XAT + q * Q8,
-                  xp[i < NT ? i : 0] + t * part.xs[1] + v * at.head_step * part.xs[2]);
+                  x + t * part.xs[1] + v * at.head_step * part.xs[2]);
           }
         }
-        if (i < NT) xp[i < NT ? i : 0] += part.x_step;
       }
-      in += any.y_step;
-      ahead_n += any.dn;
-      if (ahead_n >= p.span) {
-        ahead_n -= p.span;
-        in += any.y_wrap;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) xp[i] += p.part[part0 + i].x_wrap;
-      }
+      any.advance(p.span, ahead_b, ahead_n);
     }
     cp_async_commit();
   };
