@@ -23,8 +23,8 @@
 // and the column sums stay in registers.  A slot of warps holds whole rows,
 // because both norms need all of a row before its first value can be written.
 // Measured: 32760 rows of 1536 (fp32 x, bf16 b): forward 93 us for 604 MB (6.5
-// TB/s), backward 140 us for 906 MB (6.5 TB/s); bf16 with a norm before and after
-// and one modulation a frame, backward: 106 us for 605 MB (5.7 TB/s, held back by
+// TB/s), backward 139 us for 906 MB (6.5 TB/s); bf16 with a norm before and after
+// and one modulation a frame, backward: 104 us for 605 MB (5.8 TB/s, held back by
 // instruction issue); 75600 rows of 5120, forward 472 us for 3.10 GB (6.6 TB/s),
 // backward with fp32 x 1060 us for 7.0 GB (6.6 TB/s).
 #include <cuda_bf16.h>
