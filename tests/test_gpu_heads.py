@@ -136,6 +136,27 @@ def test_steps_over_several_samples(case, given):
 
 
 @pytest.mark.parametrize("norm", ["token", "head"])
+def test_steps_over_several_samples_with_few_key_heads(norm):
+    b, n, d = 900, 5, 64
+    g = _gen(8)
+    q, k, v = (_rand(g, b, n, h, d) for h in (12, 3, 5))
+    grid = torch.randint(1, 4, (b, 3), generator=g, dtype=torch.int32)
+    rope = B.RopeAxes(d, _pairs(d), interleaved=False)
+    cs = R.angles(R.positions(b, n, grid), _pairs(d), d)
+    how = dict(rope=rope, grid=grid.to(DEV), norm=norm)
+    got = B.sparge_heads_fwd(*_dev(q, k, v), **how)
+    _check_fwd(got[0], q, None, norm, cs, False)
+    _check_fwd(got[1], k, None, norm, cs, False)
+    assert torch.equal(got[2].cpu(), v.transpose(1, 2))
+    dq, dk, dv = (_rand(g, b, h, n, d) for h in (12, 3, 5))
+    grads = B.sparge_heads_bwd(*_dev(dq, dk, dv, q, k), **how)
+    for i, dy, x in ((0, dq, q), (1, dk, k)):
+        dx, bound, _, _ = R.heads_bwd(R.f64(dy), R.f64(x), None, norm, cs, False)
+        R.check(grads[i], dx, bound)
+    assert torch.equal(grads[2].cpu(), dv.transpose(1, 2))
+
+
+@pytest.mark.parametrize("norm", ["token", "head"])
 def test_norm_weight_type_apart_from_the_input_type_and_no_weight(norm):
     q, k, v, wq, _ = _make(1, 19, 3, 64, BF, norm, w_dtype=F32)
     qd, kd, wd = _dev(q, k, wq)
