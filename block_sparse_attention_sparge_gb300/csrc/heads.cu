@@ -1011,47 +1011,52 @@ HeadsParams heads_params(const sparge_heads& a, const HeadsPlan& pl) {
   return p;
 }
 
-template <typename Kernel>
-cudaError_t launch_kernel(Kernel* kernel, const HeadsParams& p, const HeadsPlan& pl,
-                          cudaStream_t st) {
-  if (pl.smem > 42 * 1024) {  // 48 KB less what the kernel declares
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
-    if (e != cudaSuccess) {
-      cudaGetLastError();  // the next launch must not report it
-      return e;
-    }
-  }
-  kernel<<<dim3(pl.ctas, pl.n), pl.threads, pl.smem, st>>>(p);
-  return cudaGetLastError();
+// Shared memory of a kernel built for CTAs of THREADS whose slots take T tokens,
+// at most: the rings of all its threads and the angles of as many slots as there
+// can be.
+template <int PIECES, int THREADS, int T, int D>
+constexpr int most_smem() {
+  constexpr int most = 16 * PIECES * THREADS + kMaxSlots * kAngleBuffers * T * D * 4;
+  static_assert(most + kDeclared <= kSmemPerCta, "shared memory of a CTA");
+  return most;
+}
+
+template <typename TX, bool INTER, int D, int V, int FORM>
+cudaError_t launch_fwd_form(const HeadsParams& p, const HeadsPlan& pl, cudaStream_t st) {
+  return launch_row_kernel(heads_fwd_kernel<TX, INTER, D, V, FORM>, p, dim3(pl.ctas, pl.n),
+                           pl.threads, pl.smem,
+                           most_smem<fwd_ring<TX, FORM, V>(), row_threads(V), fwd_rows<V>(), D>(), st);
 }
 
 template <typename TX, bool INTER, int D, int V>
 cudaError_t launch_fwd(const HeadsParams& p, const HeadsPlan& pl, cudaStream_t st) {
   if constexpr (V == 1 || sizeof(TX) == 2) {
-    if (pl.form == kFull) return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kFull>, p, pl, st);
+    if (pl.form == kFull) return launch_fwd_form<TX, INTER, D, V, kFull>(p, pl, st);
     if constexpr (D == 128) {
-      if (pl.form == kFullHead)
-        return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kFullHead>, p, pl, st);
+      if (pl.form == kFullHead) return launch_fwd_form<TX, INTER, D, V, kFullHead>(p, pl, st);
     }
-    if (pl.form == kJoint) return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kJoint>, p, pl, st);
+    if (pl.form == kJoint) return launch_fwd_form<TX, INTER, D, V, kJoint>(p, pl, st);
   }
-  return launch_kernel(heads_fwd_kernel<TX, INTER, D, V, kSingle>, p, pl, st);
+  return launch_fwd_form<TX, INTER, D, V, kSingle>(p, pl, st);
+}
+
+template <typename TX, bool INTER, int D, int THREADS, int FORM>
+cudaError_t launch_bwd_form(const HeadsParams& p, const HeadsPlan& pl, cudaStream_t st) {
+  return launch_row_kernel(
+      heads_bwd_kernel<TX, INTER, D, THREADS, FORM>, p, dim3(pl.ctas, pl.n), pl.threads, pl.smem,
+      most_smem<bwd_ring<TX, FORM, THREADS>(), THREADS, bwd_rows<THREADS>(), D>(), st);
 }
 
 template <typename TX, bool INTER, int D, int THREADS>
 cudaError_t launch_bwd(const HeadsParams& p, const HeadsPlan& pl, cudaStream_t st) {
   if constexpr (bwd_vectors(THREADS) == 1) {
-    if (pl.form == kFull)
-      return launch_kernel(heads_bwd_kernel<TX, INTER, D, THREADS, kFull>, p, pl, st);
+    if (pl.form == kFull) return launch_bwd_form<TX, INTER, D, THREADS, kFull>(p, pl, st);
     if constexpr (D == 128) {
-      if (pl.form == kFullHead)
-        return launch_kernel(heads_bwd_kernel<TX, INTER, D, THREADS, kFullHead>, p, pl, st);
+      if (pl.form == kFullHead) return launch_bwd_form<TX, INTER, D, THREADS, kFullHead>(p, pl, st);
     }
-    if (pl.form == kJoint)
-      return launch_kernel(heads_bwd_kernel<TX, INTER, D, THREADS, kJoint>, p, pl, st);
+    if (pl.form == kJoint) return launch_bwd_form<TX, INTER, D, THREADS, kJoint>(p, pl, st);
   }
-  return launch_kernel(heads_bwd_kernel<TX, INTER, D, THREADS, kSingle>, p, pl, st);
+  return launch_bwd_form<TX, INTER, D, THREADS, kSingle>(p, pl, st);
 }
 
 template <typename TX, bool INTER, int D>

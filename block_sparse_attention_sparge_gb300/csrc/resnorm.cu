@@ -760,11 +760,11 @@ struct ResnormPlan {
 };
 
 template <typename TX, typename TB, int V>
-int fwd_ring() {
+constexpr int fwd_ring() {
   return fwd_stages<TX, TB, V>() * fwd_pieces<TX, TB, V>() + 3 * mod_pieces<V, fwd_where<V>()>();
 }
 template <typename TX, typename TB, int THREADS>
-int bwd_ring() {
+constexpr int bwd_ring() {
   return bwd_stages<TX, TB, THREADS>() * bwd_pieces<TX, TB, THREADS>() +
          3 * mod_pieces<bwd_vectors(THREADS), bwd_where<THREADS>()>();
 }
@@ -865,19 +865,18 @@ ResnormParams resnorm_params(const sparge_resnorm& a, const ResnormPlan& pl, boo
   return p;
 }
 
-template <typename Kernel>
+template <int PIECES, int THREADS, typename Kernel>
 cudaError_t launch_kernel(Kernel* kernel, const ResnormParams& p, const ResnormPlan& pl,
                           cudaStream_t st) {
-  if (pl.smem > 42 * 1024) {  // 48 KB less what the kernel declares
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
-    if (e != cudaSuccess) {
-      cudaGetLastError();  // the next launch must not report it
-      return e;
-    }
-  }
-  kernel<<<pl.ctas, pl.threads, pl.smem, st>>>(p);
-  return cudaGetLastError();
+  constexpr int most = 16 * PIECES * THREADS;  // the rings of all the threads it is built for
+  static_assert(most + kDeclared <= kSmemPerCta, "shared memory of a CTA");
+  return launch_row_kernel(kernel, p, dim3(pl.ctas), pl.threads, pl.smem, most, st);
+}
+
+template <typename TX, typename TB, int V>
+cudaError_t launch_fwd(const ResnormParams& p, const ResnormPlan& pl, cudaStream_t st) {
+  return launch_kernel<fwd_ring<TX, TB, V>(), row_threads(V)>(resnorm_fwd_kernel<TX, TB, V>, p, pl,
+                                                              st);
 }
 
 template <typename TX, typename TB, int THREADS>
@@ -890,7 +889,7 @@ cudaError_t launch_bwd(const ResnormParams& p, const ResnormPlan& pl, cudaStream
                               : resnorm_bwd_kernel<TX, TB, THREADS, false, kFull>)
                       : (post ? resnorm_bwd_kernel<TX, TB, THREADS, true, false>
                               : resnorm_bwd_kernel<TX, TB, THREADS, false, false>);
-  return launch_kernel(kernel, p, pl, st);
+  return launch_kernel<bwd_ring<TX, TB, THREADS>(), THREADS>(kernel, p, pl, st);
 }
 
 template <typename TX, typename TB>
@@ -901,8 +900,7 @@ cudaError_t launch_resnorm(const ResnormParams& p, const ResnormPlan& pl, bool b
     if (pl.built == 640) return launch_bwd<TX, TB, 640>(p, pl, st);
     return launch_bwd<TX, TB, 512>(p, pl, st);
   }
-  return pl.V == 1 ? launch_kernel(resnorm_fwd_kernel<TX, TB, 1>, p, pl, st)
-                   : launch_kernel(resnorm_fwd_kernel<TX, TB, 2>, p, pl, st);
+  return pl.V == 1 ? launch_fwd<TX, TB, 1>(p, pl, st) : launch_fwd<TX, TB, 2>(p, pl, st);
 }
 
 cudaError_t dispatch_resnorm(const sparge_resnorm& a, const ResnormParams& p,

@@ -25,6 +25,7 @@ namespace sparge {
 constexpr int kSMs = 152;              // of a GB300: sizes grids and workspaces
 constexpr int kSmemPerSm = 228 * 1024;  // shared memory of an SM
 constexpr int kSmemOfCta = 1024;      // of it reserved for each CTA
+constexpr int kSmemPerCta = 227 * 1024;  // that one CTA can ask for
 constexpr int kMaxRowChannels = 8192;
 
 constexpr int kMaxSlots = 6;            // per CTA; named barriers 1 .. 6
@@ -205,6 +206,25 @@ struct Ring {
 template <typename T>
 constexpr int pieces8() {  // pieces of eight values
   return static_cast<int>(sizeof(T)) / 2;
+}
+
+// Launches a kernel with `smem` bytes of dynamic shared memory.  `most` is what
+// any call of this kernel can ask for: the limit belongs to the kernel on its
+// device, not to the call, so set to a call's own size it could be lowered by
+// another host thread between the setting and the launch, which then fails.
+template <typename Kernel, typename Params>
+cudaError_t launch_row_kernel(Kernel* kernel, const Params& p, dim3 grid, int threads, int smem,
+                              int most, cudaStream_t st) {
+  if (most > 42 * 1024) {  // 48 KB less what the kernels declare
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) {
+      cudaGetLastError();  // the next launch must not report it
+      return e;
+    }
+  }
+  kernel<<<grid, threads, smem, st>>>(p);
+  return cudaGetLastError();
 }
 
 // ------------------------------------------------- eight values of a thread
