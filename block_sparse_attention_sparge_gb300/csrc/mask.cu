@@ -48,6 +48,7 @@ namespace {
 constexpr int kSelThreads = 512;               // 16 warps, one row each
 constexpr int kSelMaxRows = kSelThreads / 32;  // rows per CTA upper bound
 constexpr int kSelLogitFloats = 20480;         // 80 KB of logits per CTA
+constexpr int kMaxMk = 8192;                   // kv-blocks at the largest N
 constexpr unsigned kFull = 0xffffffffu;
 
 // ---------------------------------------------------------------- pooling
@@ -948,9 +949,12 @@ cudaError_t launch_select_from_prob(const Geom& g, const float* prob, int ktop, 
   const int R = select_rows_per_cta(g.Mk);
   const int nrb = (g.Mq + R - 1) / R;
   const size_t smem = sizeof(SelSmem) + (size_t)R * g.Mk * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(select_from_prob_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  // The limit belongs to the kernel, not to the call: the same for every length,
+  // or another host thread could lower it before this launch.
+  static_assert(kSelLogitFloats >= kMaxMk, "one row at least");
+  cudaError_t e = cudaFuncSetAttribute(
+      select_from_prob_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      static_cast<int>(sizeof(SelSmem) + kSelLogitFloats * sizeof(float)));
   if (e != cudaSuccess) return e;
   select_from_prob_kernel<<<static_cast<unsigned>((long long)g.BH * nrb), kSelThreads, smem, st>>>(
       prob, g.Mq, g.Mk, g.Mkw, R, ktop, p, bitmask, row_idx, row_cnt);
@@ -1019,9 +1023,11 @@ cudaError_t launch_mask_pipeline_impl(const Geom& g, const void* q, const void* 
     R = R < 1 ? 1 : (R > kSelkRows ? kSelkRows : R);
     const int nrb = (g.Mq + R - 1) / R;
     const size_t smem = sizeof(SelkSmem) + (size_t)R * g.Mk * sizeof(float);
-    if ((e = cudaFuncSetAttribute(select_logits_kernel,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(smem))) != cudaSuccess)
+    static_assert(kSelkLogitFloats >= kMaxMk, "one row at least");
+    if ((e = cudaFuncSetAttribute(  // the same for every length (see above)
+             select_logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+             static_cast<int>(sizeof(SelkSmem) + kSelkLogitFloats * sizeof(float)))) !=
+        cudaSuccess)
       return e;
     if ((e = launch_pdl(select_logits_kernel, static_cast<unsigned>((long long)g.BH * nrb),
                         kSelkThreads, smem, st, static_cast<const float*>(logits), g.Mq, g.Mk,

@@ -65,6 +65,30 @@ def _resnorm_bwd(c):
     return fn, out[:2], (x, b, dy, dh, stats)
 
 
+def _mask(n):
+    """Above 512 kv-blocks: the selection that keeps its rows in shared memory."""
+    q, k = _rand(1, 1, 1, n, 64), _rand(2, 1, 1, n, 64)
+    shp, size = B._shape(q), ctypes.c_size_t(0)
+    lib = B.load_library()
+    assert lib.sparge_mask_workspace_bytes(ctypes.byref(shp), ctypes.byref(size)) == 0
+    ws = torch.empty(size.value, dtype=torch.uint8, device=DEV)
+    res = B.sparge_mask(q, k, 0.05, 0.5, want_csc=False, workspace=ws)
+    args = [ctypes.byref(shp), B._ptr(q), B._ptr(k), 0.05, 0.5, 0.0, B._ptr(res["bitmask"]),
+            B._ptr(res["row_idx"]), B._ptr(res["row_cnt"]), None, None, None, None, B._ptr(ws),
+            ws.numel(), None]
+    return (lambda st: lib.sparge_mask(*args, st)), [res["bitmask"]], (q, k, ws, res, shp)
+
+
+def _mask_from_prob(n):
+    mq, mk = B.num_blocks(n, 128), B.num_blocks(n, 64)
+    prob = torch.softmax(_rand(1, 1, 1, mq, mk, dtype=F32), -1)
+    res = B.sparge_mask_from_prob(prob, 0.05, 0.5, n, 64, want_csc=False)
+    lib, shp = B.load_library(), B.Shape(1, 1, n, 64, 128, 64)
+    args = [ctypes.byref(shp), B._ptr(prob), 0.05, 0.5, B._ptr(res["bitmask"]),
+            B._ptr(res["row_idx"]), B._ptr(res["row_cnt"]), None, None]
+    return (lambda st: lib.sparge_mask_from_prob(*args, st)), [res["bitmask"]], (prob, res, shp)
+
+
 def _run(*made):
     torch.cuda.synchronize()
     want = [[t.clone() for t in out] for _, out, _ in made]
@@ -98,3 +122,9 @@ def _run(*made):
 @pytest.mark.parametrize("narrow,wide", [(1024, 1536), (2560, 5120)])
 def test_two_widths_at_once(make, narrow, wide):
     _run(make(narrow), make(wide))
+
+
+@pytest.mark.parametrize("make", [_mask, _mask_from_prob], ids=lambda f: f.__name__)
+def test_two_lengths_of_the_mask_at_once(make):
+    """528 and 1024 kv-blocks: rows of different size beside one another."""
+    _run(make(33792), make(65536))
