@@ -153,7 +153,7 @@ SPARGE_DEV void put(T* p, const F8& a, bool lo, bool hi) {
 
 // What stands for an absent gate, scale or shift: read like one, it keeps
 // null checks out of the row loops (an absent gate or gain is 0 + 1).
-__device__ float g_zeros[kMaxRowChannels];
+__device__ __align__(16) float g_zeros[kMaxRowChannels];  // read as uint4
 
 // Eight channels of a gate, scale, shift or weight; `step` between the fours.
 SPARGE_DEV F8 load_mod(const float* m, int step) {
