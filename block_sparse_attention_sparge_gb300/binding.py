@@ -475,6 +475,12 @@ def _apart(outs):
         raise ValueError("the outputs must not overlap")
 
 
+def _written(outs, given):
+    """Tells autograd that the call has written the outputs that it was given."""
+    torch.autograd.graph.increment_version(
+        [o for t, o in zip(outs, given) if t is not None and o is not None])
+
+
 def _norm_weight(w, norm, H, d):
     if w is None:
         return 0
@@ -526,6 +532,8 @@ def sparge_heads_fwd(q=None, k=None, v=None, rope: RopeAxes | None = None, grid=
                                     norm, (q_weight, k_weight), eps, index),
                        *parts, *_NO_PART * (3 - n))
     _call(load_library().sparge_heads_fwd, "sparge_heads_fwd", index, args)
+    if out is not None:
+        _written(res, out)
     return tuple(res)
 
 
@@ -589,6 +597,8 @@ def sparge_heads_bwd(dq=None, dk=None, dv=None, q=None, k=None, rope: RopeAxes |
     ws, size, _hold = _workspace(lib.sparge_heads_bwd_workspace_bytes, "sparge_heads_bwd", args,
                                  device, workspace)
     _call(lib.sparge_heads_bwd, "sparge_heads_bwd", index, args, ws, size)
+    if out is not None:
+        _written(res, out)
     return tuple(res)
 
 
