@@ -493,12 +493,14 @@ def sparge_heads_fwd(q=None, k=None, v=None, rope: RopeAxes | None = None, grid=
                      norm: str | None = None, q_weight=None, k_weight=None, eps: float = 1e-6,
                      out=None):
     """Projections to the attention's layout: each of q, k and v is bf16 or
-    fp32 [B, N, H, d] of any batch, token and head stride (slices of a fused
-    projection need no copy) and comes back as bf16 [B, H, N, d].  Q and K pass
+    fp32 [B, N, H, d] of any batch, token and head stride (multiples of 16
+    bytes: slices of a fused projection need no copy) and comes back as bf16
+    [B, H, N, d].  Q and K pass
     an RMS norm over the token's H * d channels (``"token"``) or over each head
     (``"head"``), then ``rope``: with ``grid`` (int32 [B, 3]: frames, height,
     width of each sample; tokens behind them do not turn) or ``pos`` (int32
-    [B, N, 3]).  Returns (q, k, v), None for what was not given."""
+    [B, N, 3]).  Returns (q, k, v), None for what was not given; ``out``, where
+    they are written, must not share memory with one another or an input."""
     first = q if q is not None else k if k is not None else v
     if first is None:
         raise ValueError("nothing to lay out")
@@ -544,7 +546,8 @@ def sparge_heads_bwd(dq=None, dk=None, dv=None, q=None, k=None, rope: RopeAxes |
     [B, H, N, d]); q and k are the forward's inputs, needed under a norm.
     Returns (dq, dk, dv, dq_weight, dk_weight): [B, N, H, d] in the inputs'
     type (``dtype`` where neither q nor k is given), written into ``out`` where
-    that is given (slices of one buffer, say), and the weights' gradients."""
+    that is given (slices of one buffer, say; no shared memory with one another
+    or an input, q and k themselves apart), and the weights' gradients."""
     first = dq if dq is not None else dk if dk is not None else dv
     if first is None:
         raise ValueError("no gradient given")

@@ -1150,6 +1150,142 @@ int check_heads(const sparge_heads* a, bool bwd) {
   return SPARGE_OK;
 }
 
+// Where a tensor's bytes lie: runs of `run` bytes, one of each head of each token.
+struct Layout {
+  int64_t at, n[3], step[3], run;
+  int64_t span;  // from the first byte to the last; -1: more than there can be
+};
+constexpr int64_t kMaxSpan = int64_t(1) << 56;
+Layout layout_of(const void* p, const int64_t (&stride)[3], const sparge_heads& a, int H,
+                 int64_t size) {
+  Layout l = {static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)), {a.B, a.N, H}, {}, a.d * size, 0};
+  l.span = l.run;
+  for (int k = 0; k < 3; ++k) {
+    if (l.n[k] == 1) continue;
+    if (l.span < 0 || stride[k] > kMaxSpan / size / l.n[k]) {
+      l.span = -1;
+      continue;
+    }
+    l.step[k] = stride[k] * size;
+    l.span += l.step[k] * (l.n[k] - 1);
+  }
+  return l;
+}
+Layout head_major(const void* p, const sparge_heads& a, int H) {
+  const int64_t head = static_cast<int64_t>(a.N) * a.d;
+  return layout_of(p, {H * head, a.d, head}, a, H, 2);
+}
+
+// Whether two runs, `delta` bytes apart and further by any of the dimensions'
+// multiples of their steps, can share a byte: -before < delta + sum < after.  The
+// largest step comes first, so where dimensions nest, which they do in views of
+// a tensor, a few multiples of each are in question.  `other` is false as long as
+// the two are the same run of one tensor.  More than `left` trials: taken as yes.
+struct Dimension {
+  int64_t step, lo, hi;  // multiples from lo to hi, 0 among them
+};
+bool runs_meet(const Dimension* d, int n, int64_t delta, int64_t before, int64_t after, bool other,
+               int& left) {
+  if (--left < 0) return true;
+  if (n == 0) return other && delta > -before && delta < after;
+  if (d->step == 0)  // a run that repeats meets itself
+    return runs_meet(d + 1, n - 1, delta, before, after, other || d->hi > 0, left);
+  int64_t lo = 0, hi = 0;  // what the smaller steps can add
+  for (int j = 1; j < n; ++j) lo += d[j].step * d[j].lo, hi += d[j].step * d[j].hi;
+  // (Division rounds towards 0: one multiple to spare.  Of a tensor and itself one
+  // order of each pair is enough.)
+  const int64_t first = std::max(other ? d->lo : 0, (-before - delta - hi) / d->step - 1);
+  const int64_t last = std::min(d->hi, (after - delta - lo) / d->step + 1);
+  for (int64_t c = first; c <= last; ++c)
+    if (runs_meet(d + 1, n - 1, delta + c * d->step, before, after, other || c != 0, left))
+      return true;
+  return false;
+}
+constexpr int kTrials = 1 << 16;
+bool larger_step(const Dimension& a, const Dimension& b) { return a.step > b.step; }
+
+bool meets_itself(const Layout& a) {
+  if (a.span < 0) return true;
+  Dimension d[3];
+  for (int k = 0; k < 3; ++k) d[k] = {a.step[k], 1 - a.n[k], a.n[k] - 1};
+  std::sort(d, d + 3, larger_step);
+  // Each step clears all that the smaller ones reach: the usual case.
+  int64_t reach = a.run;
+  bool nested = true;
+  for (int k = 2; k >= 0; --k) {
+    if (d[k].hi > 0) nested = nested && d[k].step >= reach;
+    reach += d[k].step * d[k].hi;
+  }
+  int left = kTrials;
+  return !nested && runs_meet(d, 3, 0, a.run, a.run, false, left);
+}
+
+bool meet(const Layout& a, const Layout& b) {
+  if (a.span < 0 || b.span < 0) return true;
+  const int64_t delta = b.at - a.at;
+  if (delta >= a.span || -delta >= b.span) return false;
+  Dimension d[6];
+  int n = 0;
+  for (int k = 0; k < 3; ++k)
+    if (a.n[k] > 1) d[n++] = {a.step[k], 1 - a.n[k], 0};
+  for (int k = 0; k < 3; ++k) {
+    if (b.n[k] == 1) continue;
+    Dimension* same = std::find_if(d, d + n, [&](const Dimension& o) {
+      return o.step == b.step[k] && o.hi == 0;
+    });
+    if (same == d + n) d[n++] = {b.step[k], 0, 0};
+    same->hi = b.n[k] - 1;
+  }
+  std::sort(d, d + n, larger_step);
+  int left = kTrials;
+  return runs_meet(d, n, delta, b.run, a.run, true, left);
+}
+
+// Written where it is read, by the thread that read it.
+bool same_place(const Layout& a, const Layout& b) {
+  bool same = a.at == b.at && a.run == b.run;
+  for (int k = 0; k < 3; ++k) same = same && a.n[k] == b.n[k] && a.step[k] == b.step[k];
+  return same;
+}
+
+// Places of a call's tensors: outputs, and what is read beside them.
+struct Places {
+  int n;
+  Layout x[3], y[3], dx[3];
+  bool has_x[3];
+  Places(const sparge_heads& a, bool bwd) : n(a.n_parts) {
+    const int64_t size = a.x_type == SPARGE_F32 ? 4 : 2;
+    for (int i = 0; i < n; ++i) {
+      const sparge_heads_part& s = a.part[i];
+      has_x[i] = !bwd || (a.norm != SPARGE_HEADS_NORM_NONE && !s.plain);
+      x[i] = layout_of(s.x, s.x_stride, a, s.H, size);
+      y[i] = head_major(s.y, a, s.H);
+      dx[i] = layout_of(s.dx, s.dx_stride, a, s.H, size);
+    }
+  }
+  int outputs_apart(bool bwd) const {
+    const Layout* out = bwd ? dx : y;
+    for (int i = 0; i < n; ++i) {
+      if (meets_itself(out[i])) return SPARGE_ERR_INVALID_ARG;
+      for (int j = 0; j < i; ++j)
+        if (meet(out[i], out[j])) return SPARGE_ERR_INVALID_ARG;
+    }
+    return SPARGE_OK;
+  }
+  int inputs_apart(bool bwd) const {
+    const Layout* out = bwd ? dx : y;
+    for (int i = 0; i < n; ++i) {
+      for (int j = 0; j < n; ++j) {
+        if (has_x[j] && !(i == j && same_place(out[i], x[j])) && meet(out[i], x[j]))
+          return SPARGE_ERR_INVALID_ARG;
+        if (bwd && !(i == j && same_place(out[i], y[j])) && meet(out[i], y[j]))
+          return SPARGE_ERR_INVALID_ARG;
+      }
+    }
+    return SPARGE_OK;
+  }
+};
+
 int status_of(cudaError_t e) { return e == cudaSuccess ? SPARGE_OK : SPARGE_ERR_CUDA; }
 
 }  // namespace
@@ -1192,6 +1328,9 @@ int sparge_rope_init(sparge_rope* rope, int32_t d, const int32_t* pairs, double 
 
 int sparge_heads_fwd(const sparge_heads* args, sparge_stream_t stream) {
   HEADS_TRY(check_heads(args, false));
+  const Places places(*args, false);
+  HEADS_TRY(places.outputs_apart(false));
+  HEADS_TRY(places.inputs_apart(false));
   const HeadsPlan pl = heads_plan(*args, false);
   return status_of(dispatch_heads(*args, heads_params(*args, pl), pl, false, stream));
 }
@@ -1206,11 +1345,14 @@ int sparge_heads_bwd_workspace_bytes(const sparge_heads* args, size_t* bytes) {
 int sparge_heads_bwd(const sparge_heads* args, void* workspace, size_t ws_bytes,
                      sparge_stream_t stream) {
   HEADS_TRY(check_heads(args, true));
+  const Places places(*args, true);
+  HEADS_TRY(places.outputs_apart(true));
   const HeadsPlan pl = heads_plan(*args, true);
   if (pl.bytes > 0) {
     if (workspace == nullptr || ws_bytes < pl.bytes) return SPARGE_ERR_WORKSPACE;
     HEADS_TRY(check_aligned(workspace, 16));
   }
+  HEADS_TRY(places.inputs_apart(true));
   HeadsParams p = heads_params(*args, pl);
   ReduceJobs jobs = {};
   for (int i = 0; i < args->n_parts; ++i) {

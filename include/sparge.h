@@ -315,6 +315,9 @@ typedef struct sparge_heads {
  * of channels turned by its position's angle, rounded to bf16 and written
  * head-major.  Pointers and strides are multiples of 16 bytes; channels of a
  * head are contiguous.  A slice of a fused projection needs no copy.
+ * Outputs (y; dx in the backward) that share memory with themselves, with one
+ * another or with an input are refused (SPARGE_ERR_INVALID_ARG); one may lie
+ * exactly on its own part's input of the same element type and strides.
  */
 int sparge_heads_fwd(const sparge_heads* args, sparge_stream_t stream);
 
