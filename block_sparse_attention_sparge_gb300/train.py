@@ -41,6 +41,14 @@ from torch.autograd.function import once_differentiable
 from . import binding as B
 
 
+def _gradient(g, dtype):
+    """A gradient as the library reads it: dense, of the given type, on a 16-byte
+    boundary. Autograd hands over views that begin anywhere (the pieces of a
+    concatenation's gradient), which are contiguous already."""
+    g = g.to(dtype).contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class SparseAttentionFunction(torch.autograd.Function):
     """O = block-sparse attention(Q, K, V) under a fixed block mask.
 
@@ -58,7 +66,7 @@ class SparseAttentionFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         q, k, v, o, lse, row_idx, row_cnt, col_idx, col_cnt = ctx.saved_tensors
-        dout = dout.to(torch.bfloat16).contiguous()
+        dout = _gradient(dout, torch.bfloat16)
         dq, dk, dv = B.sparge_attn_bwd(q, k, v, o, lse, dout, row_idx, row_cnt, col_idx,
                                        col_cnt, ctx.softmax_scale)
         return dq, dk, dv, None, None, None, None, None
@@ -96,7 +104,7 @@ class HeadsFunction(torch.autograd.Function):
         q, k, wq, wk, grid, pos = ctx.saved_tensors
         need = ctx.needs_input_grad
         wanted = (need[0] or need[3], need[1] or need[4], need[2])
-        dq, dk, dv = (g.to(torch.bfloat16).contiguous() if g is not None and w else None
+        dq, dk, dv = (_gradient(g, torch.bfloat16) if g is not None and w else None
                       for g, w in zip((dq, dk, dv), wanted))
         if dq is None and dk is None and dv is None:
             return (None,) * 10
@@ -137,8 +145,8 @@ class ResidualNormFunction(torch.autograd.Function):
         need = ctx.needs_input_grad
         if dy is None and dh is None:
             return (None,) * 10
-        dy = dy.to(x.dtype).contiguous() if dy is not None else None
-        dh = dh.to(ctx.h_dtype).contiguous() if dh is not None else None
+        dy = _gradient(dy, x.dtype) if dy is not None else None
+        dh = _gradient(dh, ctx.h_dtype) if dh is not None else None
         grads = B.sparge_resnorm_bwd(dy, dh, x, branch, gate, scale, shift, stats,
                                      post_weight=post_weight, want_mods=any(need[2:6]), **ctx.how)
         return (*(g if w else None for g, w in zip(grads, need)), *(None,) * 4)
