@@ -48,7 +48,7 @@ constexpr int chunk_values(int vectors) { return kClipThreads * 8 * vectors; }
 constexpr int kNormCtas = kSMs * 3, kScaleCtas = kSMs * 32;
 constexpr int kSmallList = 48, kLargeList = 1024;  // tensors of one launch
 
-// A list of tensors as a kernel parameter (27.7 KB of the 32 KB there is for
+// A list of tensors as a kernel parameter (29704 of the 32764 bytes there are for
 // the large one; a launch copies all of it, so short lists have a small one).
 template <int MAX>
 struct ClipList {
@@ -67,6 +67,8 @@ struct ClipArgs {
   float max_norm, eps;
   int in_place;
 };
+
+static_assert(sizeof(ClipList<kLargeList>) + sizeof(ClipArgs) <= 32764, "kernel parameters");
 
 // A chunk: values [base, base + left) of tensor i, or the first of them.
 struct Chunk {

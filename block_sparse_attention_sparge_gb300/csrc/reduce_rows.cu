@@ -1,5 +1,6 @@
 // Sums of the partial rows that the row kernels leave (one row of per-channel
-// sums a slot), in a fixed order: repeated calls give the same bits.
+// sums a CTA of the head layout, a slot or a share of a group of the residual
+// norm), in a fixed order: repeated calls give the same bits.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -206,8 +206,8 @@ constexpr int mod_pieces() {
   return WHERE == kShared ? 2 * V : 0;
 }
 
-// Mean and sum of squares about it of each of T rows over the slot.  `cnt`:
-// channels of this warp, `full` of every warp but the last, `last` of that.
+// Mean and sum of squares about it of each of T rows over the slot.  `inv_cnt`: 1 /
+// channels of this warp; `counts`: those of each warp of the slot.
 template <int T, int V>
 SPARGE_DEV void slot_moments(Slot& s, const F8 (&y)[T * V], const bool (&lo)[V],
                              const bool (&hi)[V], float inv_cnt, const float* counts, float inv_c,

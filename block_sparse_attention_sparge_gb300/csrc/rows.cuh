@@ -123,10 +123,11 @@ SPARGE_DEV float warp_sums(const float (&in)[K], int lane) {
   return v[0];
 }
 
-// Joins the warps of a slot.  Every warp leaves up to four floats in its row of
-// `red`; every warp then reads all of them at once, lane l the float l / 8 of
-// warps l % 8, l % 8 + 8 and so on, and finishes with three shuffles instead of
-// a loop over the warps.  The two halves of `red`
+// Joins the warps of a slot.  Every warp leaves up to four floats (eight in the
+// head layout's backward of two tokens) in its row of `red`; every warp then reads
+// all of them at once, lane l the float l / 8 (or the two from l / 8 * 2) of warps
+// l % 8, l % 8 + 8 and so on, and finishes with three shuffles instead of a loop
+// over the warps.  The two halves of `red`
 // alternate, so one barrier a call is enough: a warp cannot reach the next but
 // one call before every warp has read this one's values.
 SPARGE_DEV float* slot_half(Slot& s) {
