@@ -110,7 +110,8 @@ struct Angles {
     n = token;
     it = ih = iw = t = 0;
     if (p.grid == nullptr || b * static_cast<int64_t>(p.N) >= p.M) return;
-    t = p.grid[3 * b], h = p.grid[3 * b + 1], w = p.grid[3 * b + 2];
+    const int32_t* size = p.grid + 3 * static_cast<int64_t>(b);  // (past 2^31 with N = 1)
+    t = size[0], h = size[1], w = size[2];
     if (t < 1 || h < 1 || w < 1) {
       t = 0;
       return;

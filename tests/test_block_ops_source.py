@@ -22,3 +22,14 @@ def test_device_arrays_state_an_alignment():
                               int(align.group(1)) if align else 0))
     assert len(found) >= 2  # the zeros of resnorm.cu, the scratch of mask_noalloc.cu
     assert not [f for f in found if f[2] < 16]
+
+
+def test_sample_offsets_into_the_grid_are_64_bits():
+    """B * N goes to 2^30 - 1, so with one token a sample 3 * b passes 2^31 (where
+    a 32-bit product would read in front of the grid): nothing that a run on
+    tensors of ordinary size shows."""
+    text = open(os.path.join(CSRC, "heads.cu")).read()
+    reads = re.findall(r"p\.grid\s*[\[+][^;]*;", text)
+    assert reads
+    for r in reads:
+        assert "int64_t" in r, r
