@@ -94,7 +94,7 @@ class HeadsFunction(torch.autograd.Function):
         ctx.save_for_backward(q if keep else None, k if keep else None, q_weight, k_weight, grid,
                               pos)
         ctx.how = dict(rope=rope, norm=norm, eps=eps)
-        ctx.dtype = next(t.dtype for t in (q, k, v) if t is not None)
+        ctx.dtype = next((t.dtype for t in (q, k, v) if t is not None), None)
         return B.sparge_heads_fwd(q, k, v, rope=rope, grid=grid, pos=pos, norm=norm,
                                   q_weight=q_weight, k_weight=k_weight, eps=eps)
 
