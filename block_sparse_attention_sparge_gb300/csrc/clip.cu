@@ -148,6 +148,8 @@ SPARGE_DEV float chunk_squares(const T* in, int64_t left, float f, const Ahead& 
       a = ffma2(f32x2(v, 0.f), f32x2(v, 0.f), a);
     }
   } else {
+    // Off a 16-byte boundary a value at a time (170M bf16 values in 340 tensors, with
+    // their scaling: 826 us, 154 on one).
     ahead();
     const int end = static_cast<int>(left < chunk_values(VEC) ? left : chunk_values(VEC));
     for (int at = threadIdx.x; at < end; at += kClipThreads) {
