@@ -100,3 +100,19 @@ def test_one_head_in_place_and_orders_that_lie_apart():
     for out in (sliced, outer, (both[:, ::2], both[:, 1::2, :1], both[:, 1::2, 1:3])):
         for got, ref in zip(B.sparge_heads_bwd(*g, out=out), want):
             assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("n,h", [(77, 1), (1, 5), (1, 40)])
+def test_gradients_in_place_of_the_gradients_they_come_from(n, h, interleaved):
+    """One head, or one token a sample: both layouts are the same."""
+    b, d = 203, 128
+    g = [_rand(i, b, h, n, d) for i in range(3)]
+    q, k = _rand(5, b, n, h, d), _rand(6, b, n, h, d)
+    pos = torch.randint(0, 99, (b, n, 3), generator=torch.Generator().manual_seed(7))
+    how = dict(norm="head", pos=pos.to(DEV, torch.int32),
+               rope=B.RopeAxes(d, (22, 21, 21), interleaved=interleaved))
+    want = B.sparge_heads_bwd(*g, q, k, **how)[:3]
+    got = B.sparge_heads_bwd(*g, q, k, out=[t.view(b, n, h, d) for t in g], **how)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
