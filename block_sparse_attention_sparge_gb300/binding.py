@@ -469,16 +469,10 @@ def _heads_head(B, N, d, x_type, n_parts, rope, grid, pos, norm, weights, eps, i
             _addr(grid), _addr(pos), 0 if pos is None else pos.shape[0])
 
 
-def _apart(outs):
-    starts = [t.data_ptr() for t in outs if t is not None]
+def _apart(starts):
+    """(The library compares the whole places; this is the plainest mistake.)"""
     if len(set(starts)) != len(starts):
         raise ValueError("the outputs must not overlap")
-
-
-def _written(outs, given):
-    """Tells autograd that the call has written the outputs that it was given."""
-    torch.autograd.graph.increment_version(
-        [o for t, o in zip(outs, given) if t is not None and o is not None])
 
 
 def _norm_weight(w, norm, H, d):
@@ -509,7 +503,7 @@ def sparge_heads_fwd(q=None, k=None, v=None, rope: RopeAxes | None = None, grid=
         raise ValueError("expected [B, N, H, d] tensors")
     B, N, _, d = first.shape
     dtype, device = first.dtype, first.device
-    res, parts = [None, None, None], ()
+    res, parts, starts, given = [None, None, None], (), [], []
     for i, (t, w) in enumerate(((q, q_weight), (k, k_weight), (v, None))):
         if t is None:
             if w is not None:
@@ -524,18 +518,22 @@ def sparge_heads_fwd(q=None, k=None, v=None, rope: RopeAxes | None = None, grid=
         elif (y.shape != (B, H, N, d) or y.dtype != torch.bfloat16 or not y.is_contiguous()
               or y.get_device() != index):
             raise ValueError("out must be contiguous bf16 [B, H, N, d] tensors on the same device")
+        else:
+            given.append(y)
+        at = y.data_ptr()
         parts += (t.data_ptr(), *_token_strides(t, B, N, H), _norm_weight(w, norm, H, d),
-                  y.data_ptr(), 0, 0, 0, 0, 0, H, i == 2)
+                  at, 0, 0, 0, 0, 0, H, i == 2)
+        starts.append(at)
         res[i] = y
-    if out is not None:
-        _apart(res)
+    if given:
+        _apart(starts)
     n = len(parts) // 13
     args = _HEADS.pack(*_heads_head(B, N, d, _type_of(first, "q, k and v"), n, rope, grid, pos,
                                     norm, (q_weight, k_weight), eps, index),
                        *parts, *_NO_PART * (3 - n))
     _call(load_library().sparge_heads_fwd, "sparge_heads_fwd", index, args)
-    if out is not None:
-        _written(res, out)
+    if given:
+        torch.autograd.graph.increment_version(given)
     return tuple(res)
 
 
@@ -561,7 +559,7 @@ def sparge_heads_bwd(dq=None, dk=None, dv=None, q=None, k=None, rope: RopeAxes |
     dtype = typed[0] if typed else (dtype or torch.bfloat16)
     if dtype not in _TYPES or any(t != dtype for t in typed):
         raise ValueError("q, k and out share one type, bf16 or fp32")
-    res, parts = [None] * 5, ()
+    res, parts, starts, given = [None] * 5, (), [], []
     for i, (g, x, w) in enumerate(((dq, q, q_weight), (dk, k, k_weight), (dv, None, None))):
         if g is None:
             if w is not None:
@@ -587,11 +585,14 @@ def sparge_heads_bwd(dq=None, dk=None, dv=None, q=None, k=None, rope: RopeAxes |
         elif 0 in dx.stride() and any(st == 0 and n_ > 1
                                       for st, n_ in zip(dx.stride(), dx.shape)):
             raise ValueError("out must not repeat elements")
-        parts += (xp, *xs, wp, g.data_ptr(), dx.data_ptr(), *_token_strides(dx, B, N, H), dw, H,
-                  i == 2)
+        else:
+            given.append(dx)
+        at = dx.data_ptr()
+        parts += (xp, *xs, wp, g.data_ptr(), at, *_token_strides(dx, B, N, H), dw, H, i == 2)
+        starts.append(at)
         res[i] = dx
-    if out is not None:
-        _apart(res[:3])
+    if given:
+        _apart(starts)
     n = len(parts) // 13
     args = _HEADS.pack(*_heads_head(B, N, d, _TYPES[dtype], n, rope, grid, pos, norm,
                                     (q_weight, k_weight), eps, index),
@@ -600,8 +601,8 @@ def sparge_heads_bwd(dq=None, dk=None, dv=None, q=None, k=None, rope: RopeAxes |
     ws, size, _hold = _workspace(lib.sparge_heads_bwd_workspace_bytes, "sparge_heads_bwd", args,
                                  device, workspace)
     _call(lib.sparge_heads_bwd, "sparge_heads_bwd", index, args, ws, size)
-    if out is not None:
-        _written(res, out)
+    if given:
+        torch.autograd.graph.increment_version(given)
     return tuple(res)
 
 
