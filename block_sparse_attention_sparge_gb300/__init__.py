@@ -15,6 +15,8 @@ from .binding import (  # noqa: F401
     sparge_attn_bwd,
     sparge_attn_fwd,
     sparge_clip_grads,
+    sparge_cross_bwd,
+    sparge_cross_fwd,
     sparge_debug_wait_probe,
     sparge_heads_bwd,
     sparge_heads_fwd,
@@ -39,5 +41,7 @@ __all__ = [
     "sparge_resnorm_fwd",
     "sparge_resnorm_bwd",
     "sparge_clip_grads",
+    "sparge_cross_fwd",
+    "sparge_cross_bwd",
     "sparge_debug_wait_probe",
 ]

@@ -37,6 +37,8 @@ __all__ = [
     "sparge_resnorm_fwd",
     "sparge_resnorm_bwd",
     "sparge_clip_grads",
+    "sparge_cross_fwd",
+    "sparge_cross_bwd",
     "sparge_debug_wait_probe",
     "num_blocks",
     "SPARGE_OK",
@@ -108,6 +110,22 @@ class Resnorm(ctypes.Structure):
                 ("dpost", ctypes.c_void_p)]
 
 
+_HEADS_TENSOR = (ctypes.c_void_p, ctypes.c_int64 * 3)
+
+
+class Cross(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Bk", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("N", ctypes.c_int32), ("M", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("kv_len", ctypes.c_void_p),
+                *((n + s, t) for n in ("q", "k", "v", "o")
+                  for s, t in zip(("", "_stride"), _HEADS_TENSOR)),
+                ("lse", ctypes.c_void_p),
+                *((n + s, t) for n in ("dout", "dq", "dk", "dv")
+                  for s, t in zip(("", "_stride"), _HEADS_TENSOR)),
+                ("status", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
@@ -136,6 +154,10 @@ _SIGNATURES = {
     "sparge_resnorm_bwd": ([_P, _P, _SZ, _P], _I),
     "sparge_clip_workspace_bytes": ([ctypes.c_int32, ctypes.POINTER(_SZ)], _I),
     "sparge_clip_grads": ([_P, _P, ctypes.c_int32, _F, _F, _P, _P, _SZ, _P], _I),
+    "sparge_cross_fwd_workspace_bytes": ([_P, ctypes.POINTER(_SZ)], _I),
+    "sparge_cross_fwd": ([_P, _P, _SZ, _P], _I),
+    "sparge_cross_bwd_workspace_bytes": ([_P, ctypes.POINTER(_SZ)], _I),
+    "sparge_cross_bwd": ([_P, _P, _SZ, _P], _I),
     "sparge_status_copy_async": ([_P, _P, _P], _I),
     "sparge_read_status": ([_P, _P, ctypes.POINTER(ctypes.c_int32)], _I),
     "sparge_debug_wait_probe": ([_P, ctypes.c_uint64, _P], _I),
@@ -349,6 +371,7 @@ def sparge_attn_bwd(q, k, v, o, lse, dout, row_idx, row_cnt, col_idx, col_cnt,
 _HEADS = struct.Struct("@6ifi3Pi4x" + "P3q3P3qP2i" * 3)
 _NO_PART = (0,) * 13
 _RESNORM = struct.Struct("@q5if5P3i4x3q12P")
+_CROSS = struct.Struct("@7ifP" + "P3q" * 4 + "P" + "P3q" * 4 + "P")
 
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 _HEADS_NORMS = {None: 0, "token": 1, "head": 2}
@@ -790,6 +813,113 @@ def sparge_clip_grads(grads, max_norm: float | None, out=None, eps: float = 1e-6
     if max_norm is not None:
         torch.autograd.graph.increment_version(grads if out is None else out)
     return norm
+
+
+# ------------------------------------------------ attention over a context
+_NO_TENSOR = (0, 0, 0, 0)
+
+
+def _heads_tensor(t, what, shape, index):
+    """(pointer, batch stride, head stride, token stride) of a bf16 tensor
+    [batch, heads, tokens, d] in any order of the first three."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape:
+        raise ValueError(f"{what} must be a bf16 {list(shape)} tensor on the same device")
+    sb, sh, sn, sc = t.stride()
+    if sc != 1:
+        raise ValueError(f"the channels of {what} must be contiguous")
+    return t.data_ptr(), sb, sh, sn
+
+
+def _cross_head(q, k, v, kv_len, softmax_scale, index):
+    """The leading fields of the packed struct, after their checks."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("expected [batch, heads, tokens, d] tensors")
+    B, H, N, d = q.shape
+    Bk, Hk, M, _ = k.shape
+    if kv_len is not None and (kv_len.dtype is not torch.int32 or kv_len.shape != (B,)
+                               or kv_len.get_device() != index or not kv_len.is_contiguous()):
+        raise ValueError("kv_len must be a contiguous int32 [B] tensor on the same device")
+    keys = torch.Size((Bk, Hk, M, d))
+    return (B, Bk, H, Hk, N, M, d, softmax_scale, _addr(kv_len),
+            *_heads_tensor(q, "q", q.shape, index), *_heads_tensor(k, "k", keys, index),
+            *_heads_tensor(v, "v", keys, index))
+
+
+def _cross_lse(lse, q, index):
+    if (lse.dtype is not torch.float32 or lse.shape != q.shape[:3] or lse.get_device() != index
+            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [B, H, N] tensor on the same device")
+    return lse.data_ptr()
+
+
+def _cross_status(status, check_status, device):
+    if status is None and check_status:
+        status = torch.zeros(1, dtype=torch.int32, device=device)
+    return status
+
+
+def sparge_cross_fwd(q, k, v, kv_len=None, softmax_scale: float = 0.0, check_status=False,
+                     out=None, lse=None, status=None, workspace=None):
+    """Attention over a context: softmax(scale q k^T) v with bf16 q [B, H, N, d],
+    k and v [Bk, Hk, M, d]; Hk divides H (query head h reads key head
+    h // (H // Hk)), Bk is B, or 1 for one context of all samples.  The first
+    three dimensions may lie in any order (strides of multiples of 16 bytes): a
+    transposed view of projections [B, N, H, d] needs no copy.  ``kv_len`` (int32
+    [B]): the valid context tokens of each sample, all without it; what lies
+    behind them is not used, and a sample of length 0 gets O = 0, LSE = -inf.
+    Returns (O, of q's shape and, unless ``out`` is given, dense; LSE fp32
+    [B, H, N])."""
+    index = _cuda_index(q, k, v)
+    device = q.device
+    head = _cross_head(q, k, v, kv_len, softmax_scale, index)
+    o = out if out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=device)
+    given = [t for t in (out, lse) if t is not None]
+    if lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=device)
+    status = _cross_status(status, check_status, device)
+    args = _CROSS.pack(*head, *_heads_tensor(o, "out", q.shape, index),
+                       _cross_lse(lse, q, index), *_NO_TENSOR * 4, _addr(status))
+    lib = load_library()
+    ws, size, _hold = _workspace(lib.sparge_cross_fwd_workspace_bytes, "sparge_cross_fwd", args,
+                                 device, workspace)
+    _call(lib.sparge_cross_fwd, "sparge_cross_fwd", index, args, ws, size)
+    if given:
+        torch.autograd.graph.increment_version(given)
+    if check_status:
+        _finish(status, True, "sparge_cross_fwd")
+    return o, lse
+
+
+def sparge_cross_bwd(q, k, v, o, lse, dout, kv_len=None, softmax_scale: float = 0.0,
+                     check_status=False, workspace=None, out=None, status=None):
+    """Gradients (dQ, dK, dV) of ``sparge_cross_fwd``: o and lse as it returned
+    them, dout of o's shape.  dK and dV are summed over the heads of a group and,
+    with one context, over the samples; they are 0 behind the samples' lengths.
+    ``out``: three tensors to write them into, of any order of the first three
+    dimensions (slices of one buffer, say)."""
+    index = _cuda_index(q, k, v, o, lse, dout)
+    device = q.device
+    head = _cross_head(q, k, v, kv_len, softmax_scale, index)
+    if out is None:
+        outs = [torch.empty(t.shape, dtype=torch.bfloat16, device=device) for t in (q, k, v)]
+    else:
+        outs = list(out)
+        if len(outs) != 3:
+            raise ValueError("out must be three tensors")
+    status = _cross_status(status, check_status, device)
+    args = _CROSS.pack(*head, *_heads_tensor(o, "o", q.shape, index), _cross_lse(lse, q, index),
+                       *_heads_tensor(dout, "dout", q.shape, index),
+                       *(x for t, like, what in zip(outs, (q, k, v), ("dq", "dk", "dv"))
+                         for x in _heads_tensor(t, what, like.shape, index)), _addr(status))
+    lib = load_library()
+    ws, size, _hold = _workspace(lib.sparge_cross_bwd_workspace_bytes, "sparge_cross_bwd", args,
+                                 device, workspace)
+    _call(lib.sparge_cross_bwd, "sparge_cross_bwd", index, args, ws, size)
+    if out is not None:
+        torch.autograd.graph.increment_version(outs)
+    if check_status:
+        _finish(status, True, "sparge_cross_bwd")
+    return tuple(outs)
 
 
 def sparge_debug_wait_probe(timeout_ns: int = 10_000_000, device="cuda") -> int:

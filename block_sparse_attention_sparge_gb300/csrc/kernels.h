@@ -83,5 +83,8 @@ int validate_mask_args(const sparge_shape* shape, const void* q, const void* k, 
 
 // tma.cu: 3-D bf16 tensor map over [BH, N, d] with a (64 x box_rows) 128-byte-swizzled box.
 int make_tmap_bf16(void* tmap_out, const void* base, int BH, int N, int d, int box_rows);
+// The same over [batch, heads, len, d] with strides in elements (batch, head, token).
+int make_tmap_bf16_4d(void* tmap_out, const void* base, int batch, int heads, int len, int d,
+                      const int64_t (&stride)[3], int box_rows);
 
 }  // namespace sparge

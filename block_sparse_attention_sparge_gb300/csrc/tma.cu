@@ -50,4 +50,26 @@ int make_tmap_bf16(void* tmap_out, const void* base, int BH, int N, int d, int b
   return r == CUDA_SUCCESS ? 0 : -1;
 }
 
+// [batch, heads, len, d] bf16 with strides (in elements) between samples, heads
+// and tokens; dims {d, len, heads, batch}.  Box = 64 elements by box_rows tokens of
+// one head.  Rows past len read as zeros.  The stride of a dimension of size 1 is
+// not used and may hold anything.
+int make_tmap_bf16_4d(void* tmap_out, const void* base, int batch, int heads, int len, int d,
+                      const int64_t (&stride)[3], int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return -1;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(len),
+                        static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(batch)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(len > 1 ? stride[2] : d) * 2,
+                           static_cast<cuuint64_t>(heads > 1 ? stride[1] : d) * 2,
+                           static_cast<cuuint64_t>(batch > 1 ? stride[0] : d) * 2};
+  cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_rows), 1u, 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  CUresult r = fn(static_cast<CUtensorMap*>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -1;
+}
+
 }  // namespace sparge

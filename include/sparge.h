@@ -421,6 +421,66 @@ int sparge_clip_grads(const sparge_tensor* grads, void* const* out, int32_t n, f
                       float eps, float* norm, void* workspace, size_t ws_bytes,
                       sparge_stream_t stream);
 
+/*
+ * Attention over a context
+ * ------------------------
+ * Queries of video tokens over the tokens of a context (a text prompt, image
+ * tokens; or a few queries over many video tokens):
+ *   S = scale * Q K^T over the sample's first kv_len keys,
+ *   LSE = log sum exp S,  O = exp(S - LSE) V.
+ * All tensors are bf16 [batch, heads, tokens, d], d contiguous, with strides of
+ * their own: as the attention lays them out or as projections do ([batch, tokens,
+ * heads, d]).  Query head h reads key head h / (H / Hk).
+ */
+typedef struct sparge_cross {
+  int32_t B, Bk;           /* samples of Q; contexts: B, or 1 for all samples */
+  int32_t H, Hk;           /* heads of Q; of K and V, a divisor of H */
+  int32_t N, M, d;         /* query tokens, context tokens (each 1 .. 524288); 64 or 128 */
+  float softmax_scale;     /* 0 = 1/sqrt(d) */
+  const int32_t* kv_len;   /* [B] (device): valid context tokens of each sample, taken
+                              into [0, M]; NULL: all.  K and V behind them are not
+                              used, whatever they hold.  0: O = 0, LSE = -inf */
+  /* Strides: elements between samples, heads and tokens, positive multiples of 8
+   * (one of a dimension of size 1 may hold anything); pointers 16-byte aligned. */
+  const void* q;  int64_t q_stride[3];   /* [B, H, N, d] */
+  const void* k;  int64_t k_stride[3];   /* [Bk, Hk, M, d] */
+  const void* v;  int64_t v_stride[3];
+  void* o;        int64_t o_stride[3];   /* [B, H, N, d]; out of the forward */
+  float* lse;                            /* [B, H, N] dense; out of the forward (NULL:
+                                            not wanted), read by the backward */
+  /* sparge_cross_bwd only */
+  const void* dout; int64_t dout_stride[3];
+  void* dq;       int64_t dq_stride[3];
+  void* dk;       int64_t dk_stride[3];
+  void* dv;       int64_t dv_stride[3];
+  int32_t* status;                       /* nullable; records SPARGE_ERR_TIMEOUT if a
+                                            bounded wait runs out */
+} sparge_cross;
+
+/* Workspace of sparge_cross_fwd: partial results where few queries read many keys
+ * (else 0).  Sizes alone decide: pointers are not looked at. */
+int sparge_cross_fwd_workspace_bytes(const sparge_cross* args, size_t* bytes);
+
+/*
+ * One launch; a second joins partial results where there are some.  The output may
+ * not share memory with an input (SPARGE_ERR_INVALID_ARG).
+ */
+int sparge_cross_fwd(const sparge_cross* args, void* workspace, size_t ws_bytes,
+                     sparge_stream_t stream);
+
+int sparge_cross_bwd_workspace_bytes(const sparge_cross* args, size_t* bytes);
+
+/*
+ * sparge_cross_bwd -- gradients of sparge_cross_fwd; the probabilities are computed
+ * again from LSE:  P = exp(S - LSE), D = rowsum(dO * O), dS = P * (dO V^T - D),
+ *   dQ = scale * dS K,  dK = scale * dS^T Q,  dV = P^T dO,
+ * dK and dV summed over the query heads that read the key head and, with one
+ * context for all, over the samples; 0 where no query reads a token.  Sums are
+ * taken in a fixed order: repeated calls give the same bits.
+ */
+int sparge_cross_bwd(const sparge_cross* args, void* workspace, size_t ws_bytes,
+                     sparge_stream_t stream);
+
 /* Enqueues on `stream` a copy of the device status word into *host_status
  * (caller-owned, page-locked host memory for the copy to be asynchronous) and
  * returns without waiting; the value is valid once the stream has reached the
