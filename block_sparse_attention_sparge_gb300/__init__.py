@@ -22,6 +22,8 @@ from .binding import (  # noqa: F401
     sparge_heads_fwd,
     sparge_mask,
     sparge_mask_from_prob,
+    sparge_muon_step,
+    sparge_orthogonalize,
     sparge_pool,
     sparge_resnorm_bwd,
     sparge_resnorm_fwd,
@@ -43,5 +45,7 @@ __all__ = [
     "sparge_clip_grads",
     "sparge_cross_fwd",
     "sparge_cross_bwd",
+    "sparge_orthogonalize",
+    "sparge_muon_step",
     "sparge_debug_wait_probe",
 ]

@@ -39,6 +39,8 @@ __all__ = [
     "sparge_clip_grads",
     "sparge_cross_fwd",
     "sparge_cross_bwd",
+    "sparge_orthogonalize",
+    "sparge_muon_step",
     "sparge_debug_wait_probe",
     "num_blocks",
     "SPARGE_OK",
@@ -126,6 +128,21 @@ class Cross(ctypes.Structure):
                 ("status", ctypes.c_void_p)]
 
 
+class Matrix(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("grad_type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32), ("grad", ctypes.c_void_p),
+                ("grad_stride", ctypes.c_int64), ("momentum", ctypes.c_void_p),
+                ("momentum_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("keep", ctypes.c_float), ("step", ctypes.c_float)]
+
+
+class Ortho(ctypes.Structure):
+    _fields_ = [("mats", ctypes.c_void_p), ("n", ctypes.c_int32), ("steps", ctypes.c_int32),
+                ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+                ("eps", ctypes.c_float), ("mu", ctypes.c_float), ("nesterov", ctypes.c_int32),
+                ("update", ctypes.c_int32), ("half", ctypes.c_int32), ("status", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
@@ -158,6 +175,8 @@ _SIGNATURES = {
     "sparge_cross_fwd": ([_P, _P, _SZ, _P], _I),
     "sparge_cross_bwd_workspace_bytes": ([_P, ctypes.POINTER(_SZ)], _I),
     "sparge_cross_bwd": ([_P, _P, _SZ, _P], _I),
+    "sparge_orthogonalize_workspace_bytes": ([_P, ctypes.POINTER(_SZ)], _I),
+    "sparge_orthogonalize": ([_P, _P, _SZ, _P], _I),
     "sparge_status_copy_async": ([_P, _P, _P], _I),
     "sparge_read_status": ([_P, _P, ctypes.POINTER(ctypes.c_int32)], _I),
     "sparge_debug_wait_probe": ([_P, ctypes.c_uint64, _P], _I),
@@ -371,6 +390,8 @@ def sparge_attn_bwd(q, k, v, o, lse, dout, row_idx, row_cnt, col_idx, col_cnt,
 _HEADS = struct.Struct("@6ifi3Pi4x" + "P3q3P3qP2i" * 3)
 _NO_PART = (0,) * 13
 _RESNORM = struct.Struct("@q5if5P3i4x3q12P")
+_MATRIX = struct.Struct("@4i" + "Pq" * 3 + "2f")
+_ORTHO = struct.Struct("@P2i5f3iP")
 _CROSS = struct.Struct("@7ifP" + "P3q" * 4 + "P" + "P3q" * 4 + "P")
 
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -920,6 +941,122 @@ def sparge_cross_bwd(q, k, v, o, lse, dout, kv_len=None, softmax_scale: float = 
     if check_status:
         _finish(status, True, "sparge_cross_bwd")
     return tuple(outs)
+
+
+# ------------------------------------------------ orthogonalised updates
+_NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def _matrix(t, what, shape, flipped, index):
+    """(pointer, elements between rows) of a matrix, or with ``flipped`` of its
+    transposed form."""
+    if t.shape != shape or t.get_device() != index or t.dtype not in _TYPES:
+        raise ValueError(f"{what} must be bf16 or fp32 matrices of their gradient's shape and device")
+    (sr, sc), (r, c) = t.stride(), shape
+    if flipped:
+        sr, sc, r, c = sc, sr, c, r
+    if sc != 1 and c > 1:
+        raise ValueError(f"{what}: the values of a matrix's rows (or, for all of its tensors, of "
+                         "its columns) must be contiguous")
+    return t.data_ptr(), sr if r > 1 else c
+
+
+def _is_flipped(t) -> bool:
+    """Whether t's columns lie contiguous and its rows do not."""
+    return t.stride(1) != 1 and t.shape[1] > 1 and (t.stride(0) == 1 or t.shape[0] == 1)
+
+
+def _orthogonalize(grads, outs, momenta, factors, steps, coefficients, eps, mu, nesterov, half,
+                   workspace, status, check_status, where):
+    index = _cuda_index(grads[0])
+    device = grads[0].device
+    a, b, c = coefficients
+    rows = {False: [], True: []}
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if g.dim() != 2:
+            raise ValueError("expected matrices")
+        shape, flipped = g.shape, _is_flipped(g)
+        n, m = reversed(shape) if flipped else shape
+        mom = momenta[i] if momenta is not None else None
+        if mom is not None and mom.dtype is not torch.float32:
+            raise ValueError("momenta must be fp32")
+        keep, step = factors[i] if factors is not None else (0.0, 0.0)
+        packed = _MATRIX.pack(
+            n, m, _TYPES.get(g.dtype, -1), _TYPES.get(o.dtype, -1),
+            *_matrix(g, "gradients", shape, flipped, index),
+            *(_matrix(mom, "momenta", shape, flipped, index) if mom is not None else (0, 0)),
+            *_matrix(o, "results", shape, flipped, index), keep, step)
+        rows[o.dtype is torch.bfloat16 if half is None else bool(half)].append(packed)
+    lib = load_library()
+    status = _cross_status(status, check_status, device)
+    for fast, part in rows.items():
+        if not part:
+            continue
+        table = ctypes.create_string_buffer(b"".join(part))
+        args = _ORTHO.pack(ctypes.addressof(table), len(part), steps, a, b, c, eps, mu,
+                           bool(nesterov), factors is not None, fast, _addr(status))
+        ws, size, _hold = _workspace(lib.sparge_orthogonalize_workspace_bytes,
+                                     "sparge_orthogonalize", args, device, workspace)
+        _call(lib.sparge_orthogonalize, where, index, args, ws, size)
+    if check_status:
+        _finish(status, True, where)
+
+
+def sparge_orthogonalize(mats, out=None, steps: int = 5, coefficients=_NEWTON_SCHULZ,
+                         eps: float = 1e-7, half: bool | None = None, workspace=None,
+                         status=None, check_status=False):
+    """Matrices to nearly orthogonal ones of the same singular vectors: X = G / (|G|
+    + eps), then ``steps`` times X <- a X + (b A + c A A) X with A = X X^T (the
+    transposed form for tall ones).  ``mats``: a list of bf16 or fp32 matrices of any
+    sizes up to 65536, of any row stride (or, transposed, column stride); results of
+    the same types, or written to ``out`` (a matrix may be its own).  ``half``: the
+    products take fp16 values (results off by some 2^-9 of their size) or pairs of
+    them (some 2^-20, three times the work); None: as the results are bf16 or
+    fp32."""
+    mats = list(mats)
+    if not mats:
+        raise ValueError("expected at least one matrix")
+    if out is None:
+        outs = [torch.empty(m.shape[::-1], dtype=m.dtype, device=m.device).t()
+                if m.dim() == 2 and _is_flipped(m) else
+                torch.empty(m.shape, dtype=m.dtype, device=m.device) for m in mats]
+    else:
+        outs = list(out)
+        if len(outs) != len(mats):
+            raise ValueError("expected one result for each matrix")
+    _orthogonalize(mats, outs, None, None, steps, coefficients, eps, 0.0, False, half, workspace,
+                   status, check_status, "sparge_orthogonalize")
+    if out is not None:
+        torch.autograd.graph.increment_version(outs)
+    return outs
+
+
+def sparge_muon_step(weights, grads, momenta, lr: float, momentum: float = 0.95,
+                     nesterov: bool = True, weight_decay: float = 0.0, rms: float | None = None,
+                     steps: int = 5, coefficients=_NEWTON_SCHULZ, eps: float = 1e-7,
+                     half: bool | None = None, workspace=None, status=None, check_status=False):
+    """One optimiser step on matrices, in place: m <- momentum * m + g; U = g +
+    momentum * m (``nesterov``) or m; w <- (1 - lr * weight_decay) * w - lr * gain *
+    O, O the orthogonalised U (``sparge_orthogonalize``).  gain is sqrt(max(1, rows /
+    columns)), or with ``rms`` what gives the update about that root mean square:
+    rms * sqrt(max(rows, columns)).  Weights and gradients are bf16 or fp32, momenta
+    fp32 (``momenta`` None: U = g).  ``half`` None: as the weights are bf16 or fp32."""
+    weights, grads = list(weights), list(grads)
+    momenta = list(momenta) if momenta is not None else None
+    if not weights:
+        raise ValueError("expected at least one matrix")
+    if len(grads) != len(weights) or (momenta is not None and len(momenta) != len(weights)):
+        raise ValueError("expected one gradient and one momentum for each weight")
+    factors = []
+    for w in weights:
+        if w.dim() != 2 or 0 in w.shape:
+            raise ValueError("expected matrices")
+        r, c = w.shape
+        gain = math.sqrt(max(1.0, r / c)) if rms is None else rms * math.sqrt(max(r, c))
+        factors.append((1.0 - lr * weight_decay, lr * gain))
+    _orthogonalize(grads, weights, momenta, factors, steps, coefficients, eps, momentum, nesterov,
+                   half, workspace, status, check_status, "sparge_muon_step")
+    torch.autograd.graph.increment_version(weights if momenta is None else weights + momenta)
 
 
 def sparge_debug_wait_probe(timeout_ns: int = 10_000_000, device="cuda") -> int:

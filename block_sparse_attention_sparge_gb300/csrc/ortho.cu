@@ -1,0 +1,956 @@
+// Orthogonalised updates on sm_103a: the Newton-Schulz iteration
+//   X = U / (|U| + eps),  X <- a X + B X,  B = b A + c A A,  A = X X^T
+// over a list of matrices, X the short side by the long one (tall matrices are
+// worked on transposed).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "common.cuh"
+#include "places.h"
+#include "rows.cuh"
+#include "sparge.h"
+
+namespace sparge {
+
+namespace {
+
+// ------------------------------------------------------------------- layout
+// X, A and B lie in the workspace as tiles of 128 rows x 64 columns of fp16, 16 KB
+// each, rows of 128 bytes with the 16-byte pieces swizzled as the tensor cores read
+// them: every operand tile is one contiguous copy, as it stands.  Rows and columns
+// are padded with zeros to multiples of 128, which stay zeros through the products.
+// A tile of fp32 values (X of the exact form) is 32 KB, its rows 256 bytes.
+constexpr int kTR = 128, kTC = 64;
+constexpr uint32_t kTile = kTR * kTC * 2;
+
+// Scales (powers of two) that keep the fp16 values away from fp16's subnormals: the
+// values of A and B, whose sizes are some units at most; those of X by the root of
+// its columns, so that they are near one when the rows have norm one.
+constexpr float kScaleA = 256.f;
+inline int x_exponent(int n) { return static_cast<int>(lround(log2(static_cast<double>(n)) / 2)); }
+
+constexpr int kMaxBatch = 64;
+constexpr int64_t kMaxValues = int64_t(1) << 27;  // of a batch
+constexpr int kNormParts = 256;                   // partial sums of a matrix
+
+// A matrix as the products see it.  Offsets are in tiles of 16 KB from the base.
+struct Shape {
+  int mb, nb;        // blocks of 128 rows and columns of X
+  int end_a, end_x;  // running count of output tiles: of A and B, of X
+  uint32_t x[2], a, b;
+  int kx;            // exponent of X's scale
+};
+struct ShapeBatch {
+  int n;
+  Shape s[kMaxBatch];
+};
+
+// A matrix as the first and last kernels see it.
+struct Matrix {
+  const void* grad;
+  float* mom;
+  void* out;
+  int64_t gs, ms, os;
+  int rows, cols;
+  float keep, step;
+  int grad_f32, out_f32, tall;
+  int nb;             // blocks of 128 columns of X
+  int end_p, end_t;   // running counts: CTAs of the norm, tiles of X
+  uint32_t x0, xn;    // X at the start and at the end
+  int parts, part0;   // partial sums of the norm
+  int kx;
+};
+struct MatrixBatch {
+  int n;
+  uint8_t* base;
+  double* partial;
+  float mu, eps;
+  int nesterov, update;
+  Matrix m[kMaxBatch];
+};
+
+// Tiles of a value's form: hi (fp16), then lo (fp16), then, in the exact form, fp32.
+// Each plane of X holds mb * 2 nb tiles.
+template <bool EXACT>
+__host__ __device__ constexpr int x_planes() { return EXACT ? 4 : 2; }  // in tiles of 16 KB
+template <bool EXACT>
+__host__ __device__ constexpr int a_planes() { return EXACT ? 2 : 1; }
+
+// Byte offset of the 16-byte piece ch (eight values) of row r in a tile.
+SPARGE_DEV uint32_t piece(int r, int ch) { return r * 128 + ((ch ^ (r & 7)) << 4); }
+
+SPARGE_DEV uint32_t pack_half2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+SPARGE_DEV void unpack_half8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    f[2 * i] = v.x, f[2 * i + 1] = v.y;
+  }
+}
+// f to fp16 pairs: hi = fp16(f), lo = fp16(f - hi); hi + lo is off by 2^-22 of f at
+// most (while lo is no subnormal).
+SPARGE_DEV void split_half8(const float (&f)[8], uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = pack_half2(f[2 * i], f[2 * i + 1]);
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    l[i] = pack_half2(f[2 * i] - v.x, f[2 * i + 1] - v.y);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Eight values of X (a piece of a tile) out of and into its planes, `plane` bytes apart.
+template <bool EXACT>
+SPARGE_DEV void load_x(const uint8_t* tiles, int64_t tile, int64_t plane, int r, int ch,
+                       float (&f)[8]) {
+  if constexpr (EXACT) {
+    const float4* p = reinterpret_cast<const float4*>(tiles + 2 * plane + tile * 2 * kTile +
+                                                      r * 256 + ch * 32);
+    const float4 u = __ldcg(p), v = __ldcg(p + 1);
+    f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
+    f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
+  } else {
+    const uint8_t* p = tiles + tile * kTile + piece(r, ch);
+    float lo[8];
+    unpack_half8(__ldcg(reinterpret_cast<const uint4*>(p)), f);
+    unpack_half8(__ldcg(reinterpret_cast<const uint4*>(p + plane)), lo);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] += lo[i];
+  }
+}
+template <bool EXACT>
+SPARGE_DEV void store_x(uint8_t* tiles, int64_t tile, int64_t plane, int r, int ch,
+                        const float (&f)[8]) {
+  uint4 hi, lo;
+  split_half8(f, hi, lo);
+  uint8_t* p = tiles + tile * kTile + piece(r, ch);
+  *reinterpret_cast<uint4*>(p) = hi;
+  *reinterpret_cast<uint4*>(p + plane) = lo;
+  if constexpr (EXACT) {
+    float4* q = reinterpret_cast<float4*>(tiles + 2 * plane + tile * 2 * kTile + r * 256 + ch * 32);
+    q[0] = make_float4(f[0], f[1], f[2], f[3]);
+    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+}
+
+// --------------------------------------------------- the matrices themselves
+// Eight values of a row from column c on (0 behind the last); 16-byte loads where
+// the place allows them.
+template <typename T>
+SPARGE_DEV void read8(const T* row, int c, int cols, float (&f)[8]) {
+  if (c + 8 <= cols && reinterpret_cast<uintptr_t>(row + c) % 16 == 0) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < pieces8<T>(); ++i) r.v[i] = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
+    unpack8(r, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? static_cast<float>(row[c + i]) : 0.f;
+  }
+}
+template <typename T>
+SPARGE_DEV void write8(T* row, int c, int cols, const float (&f)[8]) {
+  if (c + 8 <= cols && reinterpret_cast<uintptr_t>(row + c) % 16 == 0) {
+    store8(row + c, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < cols) row[c + i] = static_cast<T>(f[i]);
+  }
+}
+SPARGE_DEV void read_any(const void* base, int f32, int64_t at, int c, int cols, float (&f)[8]) {
+  if (f32)
+    read8(static_cast<const float*>(base) + at, c, cols, f);
+  else
+    read8(static_cast<const __nv_bfloat16*>(base) + at, c, cols, f);
+}
+SPARGE_DEV void write_any(void* base, int f32, int64_t at, int c, int cols, const float (&f)[8]) {
+  if (f32)
+    write8(static_cast<float*>(base) + at, c, cols, f);
+  else
+    write8(static_cast<__nv_bfloat16*>(base) + at, c, cols, f);
+}
+
+// U at a row: the gradient, or with a momentum what the momentum (as stored) makes of it.
+SPARGE_DEV void read_u(const MatrixBatch& p, const Matrix& m, int r, int c, float (&u)[8]) {
+  read_any(m.grad, m.grad_f32, r * m.gs, c, m.cols, u);
+  if (m.mom == nullptr) return;
+  float v[8];
+  read8(m.mom + r * m.ms, c, m.cols, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = p.nesterov ? fmaf(p.mu, v[i], u[i]) : v[i];
+}
+
+template <typename End>
+SPARGE_DEV int find(int n, int at, End end) {  // the first i with at < end(i)
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (at < end(mid)) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Squares of any size: those of values near one as they are, the others scaled.
+struct Squares {
+  float big = 0.f, mid = 0.f, small = 0.f;
+  SPARGE_DEV void add(float x) {
+    const float a = fabsf(x);
+    if (a > 0x1p40f) {
+      big = fmaf(x * 0x1p-70f, x * 0x1p-70f, big);
+    } else if (a < 0x1p-40f) {
+      small = fmaf(x * 0x1p100f, x * 0x1p100f, small);
+    } else {
+      mid = fmaf(x, x, mid);  // NaN too
+    }
+  }
+  SPARGE_DEV double total() const {
+    return static_cast<double>(big) * 0x1p140 + mid + static_cast<double>(small) * 0x1p-200;
+  }
+};
+
+// Sum over the 256 threads of a CTA, in a fixed order; all of them get it.
+SPARGE_DEV double cta_sum(double v) {
+  __shared__ double part[8];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += part[i];
+  return s;
+}
+
+// The momentum's step and the partial sums of U^2.  A CTA takes every parts-th
+// piece of 16 rows x 128 columns.
+__global__ void __launch_bounds__(256) ortho_norm_kernel(const __grid_constant__ MatrixBatch p) {
+  grid_launch_dependents();
+  grid_wait();
+  const int i = find(p.n, blockIdx.x, [&](int k) { return p.m[k].end_p; });
+  const Matrix& m = p.m[i];
+  const int part = blockIdx.x - (m.end_p - m.parts);
+  const int across = (m.cols + 127) / 128;
+  const int pieces = (m.rows + 15) / 16 * across;
+  double sum = 0.0;
+  for (int q = part; q < pieces; q += m.parts) {
+    const int r = q / across * 16 + threadIdx.x / 16, c = q % across * 128 + threadIdx.x % 16 * 8;
+    if (r >= m.rows || c >= m.cols) continue;
+    float u[8];
+    read_any(m.grad, m.grad_f32, r * m.gs, c, m.cols, u);
+    if (m.mom != nullptr) {
+      float v[8];
+      read8(m.mom + r * m.ms, c, m.cols, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = fmaf(p.mu, v[k], u[k]);
+        u[k] = p.nesterov ? fmaf(p.mu, v[k], u[k]) : v[k];
+      }
+      write8(m.mom + r * m.ms, c, m.cols, v);
+    }
+    Squares s;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s.add(u[k]);
+    sum += s.total();
+  }
+  sum = cta_sum(sum);
+  if (threadIdx.x == 0) p.partial[m.part0 + part] = sum;
+}
+
+constexpr int kPitch = kTC + 1;  // floats of a row of a transposed tile in shared memory
+
+// X of the start: U / (|U| + eps) in its tiles.  One CTA to a tile.
+template <bool EXACT>
+__global__ void __launch_bounds__(256) ortho_start_kernel(const __grid_constant__ MatrixBatch p) {
+  __shared__ float t[kTR * kPitch];
+  grid_launch_dependents();
+  grid_wait();
+  const int i = find(p.n, blockIdx.x, [&](int k) { return p.m[k].end_t; });
+  const Matrix& m = p.m[i];
+  double sum = 0.0;
+  for (int k = threadIdx.x; k < m.parts; k += 256) sum += __ldcg(p.partial + m.part0 + k);
+  sum = cta_sum(sum);
+  // 2^kx / (|U| + eps) as two factors, neither of which leaves fp32's range.
+  const double inv = scalbn(1.0, m.kx) / (sqrt(sum) + static_cast<double>(p.eps));
+  int e = 0;
+  const double frac = frexp(inv, &e);
+  const bool fine = inv > 0.0 && inv < 1e300;
+  const float f1 = fine ? scalbnf(1.f, e / 2) : 1.f;
+  const float f2 = fine ? scalbnf(static_cast<float>(frac), e - e / 2) : static_cast<float>(inv);
+  const int tiles = m.end_t - (i > 0 ? p.m[i - 1].end_t : 0);
+  const int tile = blockIdx.x - (m.end_t - tiles);
+  const int64_t plane = static_cast<int64_t>(tiles) * kTile;
+  const int r0 = tile / (2 * m.nb) * kTR, c0 = tile % (2 * m.nb) * kTC;
+  uint8_t* x = p.base + static_cast<int64_t>(m.x0) * kTile;
+  if (m.tall) {
+    // Rows of the tile are columns of the matrix: 64 rows of it, 128 columns.
+    for (int k = threadIdx.x; k < kTC * 16; k += 256) {
+      const int r = c0 + k / 16, c = r0 + k % 16 * 8;
+      float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (r < m.rows && c < m.cols) read_u(p, m, r, c, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[(k % 16 * 8 + j) * kPitch + k / 16] = u[j];
+    }
+    __syncthreads();
+  }
+  for (int k = threadIdx.x; k < kTR * 8; k += 256) {
+    const int r = k / 8, ch = k % 8;
+    float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (m.tall) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = t[r * kPitch + ch * 8 + j];
+    } else if (r0 + r < m.rows && c0 + ch * 8 < m.cols) {
+      read_u(p, m, r0 + r, c0 + ch * 8, u);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = u[j] * f1 * f2;
+    store_x<EXACT>(x, tile, plane, r, ch, u);
+  }
+}
+
+// The result out of the last X's tiles: X itself, or the weight's step.
+template <bool EXACT>
+__global__ void __launch_bounds__(256) ortho_finish_kernel(const __grid_constant__ MatrixBatch p) {
+  __shared__ float t[kTR * kPitch];
+  grid_wait();
+  const int i = find(p.n, blockIdx.x, [&](int k) { return p.m[k].end_t; });
+  const Matrix& m = p.m[i];
+  const int tiles = m.end_t - (i > 0 ? p.m[i - 1].end_t : 0);
+  const int tile = blockIdx.x - (m.end_t - tiles);
+  const int64_t plane = static_cast<int64_t>(tiles) * kTile;
+  const int r0 = tile / (2 * m.nb) * kTR, c0 = tile % (2 * m.nb) * kTC;
+  const uint8_t* x = p.base + static_cast<int64_t>(m.xn) * kTile;
+  const float back = scalbnf(1.f, -m.kx);
+  auto put = [&](int r, int c, float (&f)[8]) {
+    if (p.update) {
+      float w[8];
+      read_any(m.out, m.out_f32, r * m.os, c, m.cols, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = fmaf(-m.step, f[j], m.keep * w[j]);
+    }
+    write_any(m.out, m.out_f32, r * m.os, c, m.cols, f);
+  };
+  for (int k = threadIdx.x; k < kTR * 8; k += 256) {
+    const int r = k / 8, ch = k % 8;
+    if (!m.tall && (r0 + r >= m.rows || c0 + ch * 8 >= m.cols)) continue;
+    float f[8];
+    load_x<EXACT>(x, tile, plane, r, ch, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= back;
+    if (m.tall) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[r * kPitch + ch * 8 + j] = f[j];
+    } else {
+      put(r0 + r, c0 + ch * 8, f);
+    }
+  }
+  if (!m.tall) return;
+  __syncthreads();
+  for (int k = threadIdx.x; k < kTC * 16; k += 256) {
+    const int r = c0 + k / 16, c = r0 + k % 16 * 8;
+    if (r >= m.rows || c >= m.cols) continue;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = t[(k % 16 * 8 + j) * kPitch + k / 16];
+    put(r, c, f);
+  }
+}
+
+// ----------------------------------------------------------------- products
+enum Product { kGram, kSquare, kApply };  // A = X X^T;  B = b A + c A A;  X = a X + B X
+
+// A CTA's output tile is 128 rows x BN columns; the contraction runs in steps of 64.
+// Eight epilogue warps read one accumulator while the products fill the other.
+template <int BN, bool EXACT>
+struct GemmCfg {
+  static constexpr int kWarps = 8;  // epilogue
+  static constexpr int kThreads = (kWarps + 2) * 32;
+  static constexpr int kPlanes = EXACT ? 2 : 1;  // operands: hi, or hi and lo
+  static constexpr uint32_t kA = kTile;
+  static constexpr uint32_t kB = BN * 128;
+  static constexpr uint32_t kStage = kPlanes * (kA + kB);
+  static constexpr int NST = static_cast<int>(192 * 1024 / kStage);
+  static constexpr uint32_t off_bar = NST * kStage;
+  static constexpr int B_F = 0;             // NST: a stage's tiles landed
+  static constexpr int B_E = NST;           // NST: its products done
+  static constexpr int B_AF = 2 * NST;      // 2: an accumulator complete
+  static constexpr int B_AE = B_AF + 2;     // 2, all epilogue threads: it was read
+  static constexpr int B_DONE = B_AE + 2;
+  static constexpr int NBAR = B_DONE + 1;
+  static constexpr uint32_t off_slot = off_bar + NBAR * 8;
+  static constexpr uint32_t bytes = off_slot + 16;
+  // The tensor cores round a sum towards zero at each addition, so a long one drifts:
+  // with 32 additions in a row the result was off by 1e-5.  The exact form therefore
+  // reads its accumulators out every kChunk steps (8 additions) and adds those in
+  // registers; the products with a lo, 2^-11 of the others, have an accumulator of
+  // their own for the whole tile.
+  static constexpr int kAcc = EXACT ? 2 : 1;
+  static constexpr int kChunk = EXACT ? 2 : INT_MAX;
+  static constexpr uint32_t tmem_cols = 2 * kAcc * BN;
+};
+
+struct GemmParams {
+  uint8_t* base;
+  int tiles;
+  int from;          // which of a matrix's two X is read; the other is written
+  float a, b, c;
+  int32_t* status;
+};
+
+struct GemmTile {
+  const Shape* s;
+  int rb, cb;   // block of rows, first 64-column tile
+  int steps;    // of the contraction
+};
+template <int BN, Product KIND>
+SPARGE_DEV GemmTile gemm_tile(const ShapeBatch& sb, int t) {
+  const int i = find(sb.n, t, [&](int k) { return KIND == kApply ? sb.s[k].end_x : sb.s[k].end_a; });
+  const Shape& s = sb.s[i];
+  const int before = i == 0 ? 0 : KIND == kApply ? sb.s[i - 1].end_x : sb.s[i - 1].end_a;
+  const int across = ((KIND == kApply ? s.nb : s.mb) * 128 + BN - 1) / BN;
+  GemmTile g;
+  g.s = &s;
+  g.rb = (t - before) / across;
+  g.cb = (t - before) % across * (BN / 64);
+  g.steps = 2 * (KIND == kGram ? s.nb : s.mb);
+  return g;
+}
+
+template <int BN, bool EXACT, Product KIND>
+__global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
+    ortho_gemm_kernel(const __grid_constant__ ShapeBatch sb, const __grid_constant__ GemmParams p) {
+  using C = GemmCfg<BN, EXACT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t s0 = smem_u32(smem_raw);
+  if ((s0 & 1023u) != 0u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) report_error(p.status, SPARGE_ERR_CUDA);
+    return;
+  }
+  auto bar = [&](int i) -> uint32_t { return s0 + C::off_bar + 8u * i; };
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem_raw + C::off_slot);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kProducer = C::kWarps, kIssuer = C::kWarps + 1;
+  grid_launch_dependents();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NBAR; ++i)
+      mbar_init(bar(i), i == C::B_AE || i == C::B_AE + 1 ? 32 * C::kWarps : 1);
+    fence_barrier_init();
+  }
+  if (warp == kIssuer) {
+    tmem_alloc(smem_u32(slot), C::tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  grid_wait();  // the operands are the previous kernel's
+
+  const uint32_t x_in = p.from, x_out = p.from ^ 1;
+  if (warp == kProducer) {
+    if (lane == 0) {
+      bool ok = true;
+      int g = 0;
+      for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
+        const GemmTile w = gemm_tile<BN, KIND>(sb, t);
+        const Shape& s = *w.s;
+        const int mb = s.mb, xt = 2 * s.nb, at = 2 * mb;  // tiles of a row of X; of A
+        const int64_t x_plane = static_cast<int64_t>(mb) * xt * kTile;
+        const int64_t a_plane = static_cast<int64_t>(mb) * at * kTile;
+        const uint8_t* X = p.base + static_cast<int64_t>(s.x[x_in]) * kTile;
+        const uint8_t* A = p.base + static_cast<int64_t>(KIND == kSquare ? s.a : s.b) * kTile;
+        const int blocks = min(BN / 128, (KIND == kApply ? s.nb : mb) - w.cb / 2);
+        for (int k = 0; k < w.steps; ++k, ++g) {
+          const int st = g % C::NST;
+          if (g >= C::NST && !mbar_wait(bar(C::B_E + st), ((g / C::NST) - 1) & 1, kWaitTimeoutNs)) {
+            ok = false;
+            break;
+          }
+          const uint32_t b_bytes = blocks * kTile;
+          mbar_arrive_expect_tx(bar(C::B_F + st), C::kPlanes * (C::kA + b_bytes));
+          for (int pl = 0; pl < C::kPlanes; ++pl) {
+            const uint32_t da = s0 + st * C::kStage + pl * C::kA;
+            const uint32_t db = s0 + st * C::kStage + C::kPlanes * C::kA + pl * C::kB;
+            if constexpr (KIND == kGram) {
+              bulk_load(da, X + pl * x_plane + static_cast<int64_t>(w.rb * xt + k) * kTile, kTile,
+                        bar(C::B_F + st));
+              for (int j = 0; j < blocks; ++j)
+                bulk_load(db + j * kTile,
+                          X + pl * x_plane + static_cast<int64_t>((w.cb / 2 + j) * xt + k) * kTile,
+                          kTile, bar(C::B_F + st));
+            } else {
+              bulk_load(da, A + pl * a_plane + static_cast<int64_t>(w.rb * at + k) * kTile, kTile,
+                        bar(C::B_F + st));
+              if constexpr (KIND == kSquare) {
+                for (int j = 0; j < blocks; ++j)
+                  bulk_load(db + j * kTile,
+                            A + pl * a_plane + static_cast<int64_t>((w.cb / 2 + j) * at + k) * kTile,
+                            kTile, bar(C::B_F + st));
+              } else {
+                // 64 rows of X: half of each column's tile.
+                for (int j = 0; j < 2 * blocks; ++j)
+                  bulk_load(db + j * (kTile / 2),
+                            X + pl * x_plane + static_cast<int64_t>((k >> 1) * xt + w.cb + j) * kTile +
+                                (k & 1) * (kTile / 2),
+                            kTile / 2, bar(C::B_F + st));
+              }
+            }
+          }
+        }
+      }
+      if (!ok) report_error(p.status, SPARGE_ERR_TIMEOUT);
+      // Let the last copies land before the CTA can exit.
+      for (int i = max(0, g - C::NST); i < g; ++i)
+        mbar_wait(bar(C::B_F + i % C::NST), (i / C::NST) & 1, kWaitTimeoutNs);
+    }
+  } else if (warp == kIssuer) {
+    // The whole warp runs the loop; one elected lane issues each MMA.  B's rows are
+    // the contraction's in kApply (MN-major), its columns in the others (K-major).
+    constexpr uint32_t id = idesc_fp16(kTR, BN, false, KIND == kApply);
+    bool ok = true;
+    int g = 0, q = 0, odd = 0;
+    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, odd ^= 1) {
+      const GemmTile w = gemm_tile<BN, KIND>(sb, t);
+      const uint32_t cross = tmem + (2 + odd) * BN;
+      for (int k0 = 0; ok && k0 < w.steps; k0 += min(C::kChunk, w.steps - k0), ++q) {
+        const int buf = q & 1;
+        if (q >= 2 && !warp_wait(bar(C::B_AE + buf), ((q >> 1) - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + buf * BN;
+        const int n = min(C::kChunk, w.steps - k0);
+        for (int k = 0; k < n; ++k, ++g) {
+          const int st = g % C::NST;
+          if (!warp_wait(bar(C::B_F + st), (g / C::NST) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = s0 + st * C::kStage, sbb = sa + C::kPlanes * C::kA;
+          // hi hi; hi lo and lo hi (lo lo is below what fp32 keeps).
+#pragma unroll
+          for (int pr = 0; pr < (EXACT ? 3 : 1); ++pr) {
+            const uint64_t da = sdesc_sw128(sa + (pr == 2 ? C::kA : 0), 16, 1024);
+            const uint64_t db = sdesc_sw128(sbb + (pr == 1 ? C::kB : 0),
+                                            KIND == kApply ? kTile / 2 : 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              warp_mma_bf16(pr > 0 ? cross : d, sdesc_add(da, kk * 32),
+                            sdesc_add(db, KIND == kApply ? kk * 2048 : kk * 32), id,
+                            (k > 0 || pr > 1 || kk > 0 || (pr == 1 && k0 > 0)) ? 1u : 0u);
+          }
+          warp_commit(bar(C::B_E + st));
+        }
+        if (ok) warp_commit(bar(C::B_AF + buf));
+      }
+    }
+    if (!ok && lane == 0) report_error(p.status, SPARGE_ERR_TIMEOUT);
+    warp_commit(bar(C::B_DONE));
+    warp_wait(bar(C::B_DONE), 0);
+  } else {
+    // Thread = row r (TMEM lane); the two warps of a quarter take every other
+    // 64-column tile.
+    const int quarter = warp & 3, half = warp >> 2;
+    const int r = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    bool ok = true;
+    int q = 0, odd = 0;
+    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, odd ^= 1) {
+      const GemmTile w = gemm_tile<BN, KIND>(sb, t);
+      const Shape& s = *w.s;
+      const int mb = s.mb, xt = 2 * s.nb, at = 2 * mb;
+      const int64_t x_plane = static_cast<int64_t>(mb) * xt * kTile;
+      const int64_t a_plane = static_cast<int64_t>(mb) * at * kTile;
+      const uint8_t* A = p.base + static_cast<int64_t>(s.a) * kTile;
+      uint8_t* G = p.base + static_cast<int64_t>(KIND == kGram ? s.a : s.b) * kTile;
+      const uint8_t* X = p.base + static_cast<int64_t>(s.x[x_in]) * kTile;
+      uint8_t* Y = p.base + static_cast<int64_t>(s.x[x_out]) * kTile;
+      const int cols = min(BN / 64, (KIND == kApply ? xt : at) - w.cb);
+      // A = X X^T comes scaled by 4^kx, A A by kScaleA^2, B X by kScaleA.
+      const float f = KIND == kGram     ? scalbnf(kScaleA, -2 * s.kx)
+                      : KIND == kSquare ? p.c / kScaleA
+                                        : 1.f / kScaleA;
+      // Eight products' sums (piece ch of the thread's row in a tile) to their place.
+      auto put = [&](int64_t tile, int ch, float (&y)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= f;
+        if constexpr (KIND == kApply) {
+          float x[8];
+          load_x<EXACT>(X, tile, x_plane, r, ch, x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = fmaf(p.a, x[i], y[i]);
+          store_x<EXACT>(Y, tile, x_plane, r, ch, y);
+        } else {
+          const int64_t at_byte = tile * kTile + piece(r, ch);
+          if constexpr (KIND == kSquare) {
+            float x[8];
+            unpack_half8(__ldcg(reinterpret_cast<const uint4*>(A + at_byte)), x);
+            if constexpr (EXACT) {
+              float lo[8];
+              unpack_half8(__ldcg(reinterpret_cast<const uint4*>(A + a_plane + at_byte)), lo);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] += lo[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = fmaf(p.b, x[i], y[i]);
+          }
+          uint4 hi, lo;
+          split_half8(y, hi, lo);
+          *reinterpret_cast<uint4*>(G + at_byte) = hi;
+          if constexpr (EXACT) *reinterpret_cast<uint4*>(G + a_plane + at_byte) = lo;
+        }
+      };
+      const int64_t first = static_cast<int64_t>(w.rb) * (KIND == kApply ? xt : at) + w.cb;
+      if constexpr (EXACT) {
+        static_assert(BN == 128, "a thread's sums are those of one tile");
+        float acc[64];
+        for (int k0 = 0; k0 < w.steps; k0 += C::kChunk, ++q) {
+          const int buf = q & 1;
+          if (!warp_wait(bar(C::B_AF + buf), (q >> 1) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const bool last = k0 + C::kChunk >= w.steps;
+#pragma unroll
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            float v[32];
+            tmem_ld32(lanes + buf * BN + half * 64 + c0, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c0 + i] = k0 == 0 ? v[i] : acc[c0 + i] + v[i];
+            if (last) {
+              tmem_ld32(lanes + (2 + odd) * BN + half * 64 + c0, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[c0 + i] += v[i];
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(bar(C::B_AE + buf));
+        }
+        if (ok && half < cols) {
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = acc[8 * ch + i];
+            put(first + half, ch, y);
+          }
+        }
+      } else {
+        const int buf = q & 1;
+        if (!warp_wait(bar(C::B_AF + buf), (q >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int j = half; j < cols; j += 2) {
+#pragma unroll
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            float v[32];
+            tmem_ld32(lanes + buf * BN + j * 64 + c0, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = v[8 * e + i];
+              put(first + j, c0 / 8 + e, y);
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(bar(C::B_AE + buf));
+        ++q;
+      }
+    }
+    if (!ok) report_error(p.status, SPARGE_ERR_TIMEOUT);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssuer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::tmem_cols);
+  }
+}
+
+// -------------------------------------------------------------------- host
+// A launch that may start while the kernel before it on the stream ends
+// (programmatic dependent launch); every kernel here waits before it reads.
+template <typename... Params>
+cudaError_t launch_chained(void (*kernel)(Params...), int grid, int threads, uint32_t smem,
+                           cudaStream_t st, const Params&... params) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, params...);
+}
+
+int blocks_of(int n) { return (n + 127) / 128; }
+
+// The matrices [at, end) of a list as one batch, and its workspace.
+struct Batch {
+  int end;
+  ShapeBatch shapes;
+  MatrixBatch mats;
+  size_t bytes;        // tiles, then the partial sums
+  int norm_ctas, tiles, tiles_a, tiles_x;
+};
+
+Batch make_batch(const sparge_ortho& a, int at, int BN) {
+  Batch b = {};
+  const bool exact = !a.half;
+  int64_t values = 0;
+  uint32_t used = 0;  // tiles of 16 KB
+  int partials = 0, i = at;
+  for (; i < a.n && i - at < kMaxBatch; ++i) {
+    const sparge_matrix& s = a.mats[i];
+    const int rb = blocks_of(s.rows), cb = blocks_of(s.cols);
+    const int64_t size = static_cast<int64_t>(rb) * cb * 128 * 128;
+    if (i > at && values + size > kMaxValues) break;
+    values += size;
+    const int k = i - at;
+    Shape& h = b.shapes.s[k];
+    Matrix& m = b.mats.m[k];
+    m.tall = s.rows > s.cols;
+    h.mb = std::min(rb, cb);
+    h.nb = std::max(rb, cb);
+    h.kx = x_exponent(std::max(s.rows, s.cols));
+    const uint32_t xt = static_cast<uint32_t>(h.mb) * 2 * h.nb, at_ = static_cast<uint32_t>(h.mb) * 2 * h.mb;
+    for (int j = 0; j < 2; ++j) {
+      h.x[j] = used;
+      used += xt * (exact ? x_planes<true>() : x_planes<false>());
+    }
+    h.a = used;
+    used += at_ * (exact ? a_planes<true>() : a_planes<false>());
+    h.b = used;
+    used += at_ * (exact ? a_planes<true>() : a_planes<false>());
+    b.tiles_a += h.mb * ((h.mb * 128 + BN - 1) / BN);
+    b.tiles_x += h.mb * ((h.nb * 128 + BN - 1) / BN);
+    h.end_a = b.tiles_a;
+    h.end_x = b.tiles_x;
+    m.grad = s.grad;
+    m.mom = s.momentum;
+    m.out = s.out;
+    m.gs = s.grad_stride;
+    m.ms = s.momentum_stride;
+    m.os = s.out_stride;
+    m.rows = s.rows;
+    m.cols = s.cols;
+    m.keep = s.keep;
+    m.step = s.step;
+    m.grad_f32 = s.grad_type == SPARGE_F32;
+    m.out_f32 = s.out_type == SPARGE_F32;
+    m.nb = h.nb;
+    m.kx = h.kx;
+    m.parts = std::min(kNormParts, (s.rows + 15) / 16 * cb);
+    m.part0 = partials;
+    partials += m.parts;
+    b.norm_ctas += m.parts;
+    m.end_p = b.norm_ctas;
+    b.tiles += static_cast<int>(xt);
+    m.end_t = b.tiles;
+    m.x0 = h.x[0];
+    m.xn = h.x[a.steps & 1];
+  }
+  b.end = i;
+  b.shapes.n = b.mats.n = i - at;
+  b.mats.mu = a.mu;
+  b.mats.eps = a.eps;
+  b.mats.nesterov = a.nesterov;
+  b.mats.update = a.update;
+  const size_t tiles = static_cast<size_t>(used) * kTile;
+  b.mats.partial = reinterpret_cast<double*>(tiles);  // an offset until the base is known
+  b.bytes = tiles + static_cast<size_t>(partials) * sizeof(double);
+  return b;
+}
+
+constexpr int kBN = 128;
+
+template <bool EXACT>
+cudaError_t run_batch(const sparge_ortho& a, Batch& b, uint8_t* ws, cudaStream_t st) {
+  using C = GemmCfg<kBN, EXACT>;
+  b.mats.base = ws;
+  b.mats.partial = reinterpret_cast<double*>(ws + reinterpret_cast<uintptr_t>(b.mats.partial));
+#define ORTHO_RUN(...)                      \
+  do {                                      \
+    const cudaError_t e_ = (__VA_ARGS__);   \
+    if (e_ != cudaSuccess) return e_;       \
+  } while (0)
+  ORTHO_RUN(launch_chained(ortho_norm_kernel, b.norm_ctas, 256, 0, st, b.mats));
+  ORTHO_RUN(launch_chained(ortho_start_kernel<EXACT>, b.tiles, 256, 0, st, b.mats));
+  GemmParams p = {ws, 0, 0, a.a, a.b, a.c, a.status};
+  for (int i = 0; i < a.steps; ++i) {
+    p.from = i & 1;
+    p.tiles = b.tiles_a;
+    const int grid_a = std::min(b.tiles_a, kSMs), grid_x = std::min(b.tiles_x, kSMs);
+    ORTHO_RUN(launch_chained(ortho_gemm_kernel<kBN, EXACT, kGram>, grid_a, C::kThreads, C::bytes, st,
+                             b.shapes, p));
+    ORTHO_RUN(launch_chained(ortho_gemm_kernel<kBN, EXACT, kSquare>, grid_a, C::kThreads, C::bytes,
+                             st, b.shapes, p));
+    p.tiles = b.tiles_x;
+    ORTHO_RUN(launch_chained(ortho_gemm_kernel<kBN, EXACT, kApply>, grid_x, C::kThreads, C::bytes,
+                             st, b.shapes, p));
+  }
+  ORTHO_RUN(launch_chained(ortho_finish_kernel<EXACT>, b.tiles, 256, 0, st, b.mats));
+#undef ORTHO_RUN
+  return cudaSuccess;
+}
+
+#define ORTHO_TRY(expr)               \
+  do {                                \
+    const int rc_ = (expr);           \
+    if (rc_ != SPARGE_OK) return rc_; \
+  } while (0)
+
+constexpr int kMaxSide = 65536, kMaxSteps = 64;
+
+int check_sizes(const sparge_ortho* a) {
+  if (a == nullptr || a->n < 1 || a->mats == nullptr) return SPARGE_ERR_INVALID_ARG;
+  if (a->n > SPARGE_MAX_TENSORS) return SPARGE_ERR_UNSUPPORTED;
+  for (int i = 0; i < a->n; ++i) {
+    const sparge_matrix& m = a->mats[i];
+    if (m.rows < 1 || m.cols < 1) return SPARGE_ERR_INVALID_ARG;
+    if (m.rows > kMaxSide || m.cols > kMaxSide) return SPARGE_ERR_UNSUPPORTED;
+  }
+  return SPARGE_OK;
+}
+
+int check_place(const void* p, int64_t stride, int type, const sparge_matrix& m) {
+  if (p == nullptr) return SPARGE_ERR_INVALID_ARG;
+  if (type != SPARGE_BF16 && type != SPARGE_F32) return SPARGE_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(p) % (type == SPARGE_F32 ? 4 : 2) != 0) return SPARGE_ERR_MISALIGNED;
+  if (m.rows > 1 && (stride < 1 || stride > int64_t(1) << 40)) return SPARGE_ERR_INVALID_ARG;
+  return SPARGE_OK;
+}
+
+// A tensor of the list and what is done with it.
+struct Place {
+  Layout at;
+  int mat;
+  bool written, momentum;
+};
+
+int check_ortho(const sparge_ortho* a) {
+  ORTHO_TRY(check_sizes(a));
+  if (a->steps < 0 || a->steps > kMaxSteps) return SPARGE_ERR_INVALID_ARG;
+  for (float f : {a->a, a->b, a->c})
+    if (!(fabsf(f) <= 16.f)) return SPARGE_ERR_INVALID_ARG;
+  if (!isfinite(a->eps) || a->eps < 0.f || !isfinite(a->mu)) return SPARGE_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(a->status) % 4 != 0) return SPARGE_ERR_MISALIGNED;
+  std::vector<Place> places;
+  places.reserve(3 * static_cast<size_t>(a->n));
+  for (int i = 0; i < a->n; ++i) {
+    const sparge_matrix& m = a->mats[i];
+    ORTHO_TRY(check_place(m.grad, m.grad_stride, m.grad_type, m));
+    ORTHO_TRY(check_place(m.out, m.out_stride, m.out_type, m));
+    if (!isfinite(m.keep) || !isfinite(m.step)) return SPARGE_ERR_INVALID_ARG;
+    auto put = [&](const void* p, int64_t stride, int type, bool written, bool momentum) {
+      const int64_t size = type == SPARGE_F32 ? 4 : 2;
+      places.push_back({layout_of(p, {m.rows, 1, 1}, {stride, 0, 0}, m.cols * size, size), i, written,
+                        momentum});
+    };
+    put(m.grad, m.grad_stride, m.grad_type, false, false);
+    put(m.out, m.out_stride, m.out_type, true, false);
+    if (m.momentum != nullptr) {
+      ORTHO_TRY(check_place(m.momentum, m.momentum_stride, SPARGE_F32, m));
+      put(m.momentum, m.momentum_stride, SPARGE_F32, true, true);
+    }
+  }
+  // In the order of their first bytes, each is compared with those before it that
+  // reach so far.
+  std::sort(places.begin(), places.end(),
+            [](const Place& x, const Place& y) { return x.at.at < y.at.at; });
+  std::vector<int> open;
+  for (size_t i = 0; i < places.size(); ++i) {
+    const Place& x = places[i];
+    if (x.written && meets_itself(x.at)) return SPARGE_ERR_INVALID_ARG;
+    size_t kept = 0;
+    for (size_t k = 0; k < open.size(); ++k) {
+      const Place& y = places[open[k]];
+      if (y.at.span >= 0 && y.at.at + y.at.span <= x.at.at) continue;
+      open[kept++] = open[k];
+      if (!x.written && !y.written) continue;
+      // (a result in its own gradient's place)
+      if (x.mat == y.mat && x.written != y.written && !x.momentum && !y.momentum &&
+          same_place(x.at, y.at) && !a->update)
+        continue;
+      if (meet(x.at, y.at)) return SPARGE_ERR_INVALID_ARG;
+    }
+    open.resize(kept);
+    open.push_back(static_cast<int>(i));
+  }
+  return SPARGE_OK;
+}
+
+size_t workspace_of(const sparge_ortho& a) {
+  size_t most = 0;
+  for (int at = 0; at < a.n;) {
+    const Batch b = make_batch(a, at, kBN);
+    most = std::max(most, b.bytes);
+    at = b.end;
+  }
+  return most;
+}
+
+}  // namespace
+
+}  // namespace sparge
+
+using namespace sparge;
+
+extern "C" {
+
+int sparge_orthogonalize_workspace_bytes(const sparge_ortho* args, size_t* bytes) {
+  if (bytes == nullptr) return SPARGE_ERR_INVALID_ARG;
+  ORTHO_TRY(check_sizes(args));
+  *bytes = workspace_of(*args);
+  return SPARGE_OK;
+}
+
+int sparge_orthogonalize(const sparge_ortho* args, void* workspace, size_t ws_bytes,
+                         sparge_stream_t stream) try {
+  ORTHO_TRY(check_ortho(args));
+  if (workspace == nullptr || ws_bytes < workspace_of(*args)) return SPARGE_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return SPARGE_ERR_MISALIGNED;
+  for (int at = 0; at < args->n;) {
+    Batch b = make_batch(*args, at, kBN);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const cudaError_t e = args->half ? run_batch<false>(*args, b, ws, stream)
+                                     : run_batch<true>(*args, b, ws, stream);
+    if (e != cudaSuccess) return SPARGE_ERR_CUDA;
+    at = b.end;
+  }
+  return SPARGE_OK;
+} catch (...) {  // no memory for the list on the host
+  return SPARGE_ERR_INVALID_ARG;
+}
+
+}  // extern "C"

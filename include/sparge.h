@@ -481,6 +481,61 @@ int sparge_cross_bwd_workspace_bytes(const sparge_cross* args, size_t* bytes);
 int sparge_cross_bwd(const sparge_cross* args, void* workspace, size_t ws_bytes,
                      sparge_stream_t stream);
 
+/*
+ * Orthogonalised updates
+ * ----------------------
+ * A matrix (the gradient of a projection) to a nearly orthogonal one of the same
+ * singular vectors, by products alone (the Newton-Schulz iteration of the Muon
+ * optimiser):
+ *   X = U / (|U| + eps),   `steps` times  X <- a X + (b A + c A A) X,  A = X X^T
+ * (X^T X for tall matrices), |U| the 2-norm of all values.
+ */
+typedef struct sparge_matrix {
+  int32_t rows, cols;      /* each 1 .. 65536 */
+  int32_t grad_type;       /* enum sparge_type */
+  int32_t out_type;
+  const void* grad;        /* [rows, cols]; rows `grad_stride` elements apart */
+  int64_t grad_stride;
+  float* momentum;         /* fp32; NULL: U = grad.  Else momentum <- mu * momentum +
+                              grad, and U = grad + mu * momentum (nesterov), or U =
+                              momentum */
+  int64_t momentum_stride;
+  void* out;               /* X, or with `update` a weight: out <- keep * out - step * X */
+  int64_t out_stride;
+  float keep, step;        /* with `update` */
+} sparge_matrix;
+
+typedef struct sparge_ortho {
+  const sparge_matrix* mats; /* host array; copied by the call */
+  int32_t n;               /* at most SPARGE_MAX_TENSORS */
+  int32_t steps;           /* 0 .. 64 */
+  float a, b, c;           /* finite, at most 16 in size */
+  float eps;
+  float mu;                /* with a momentum */
+  int32_t nesterov;
+  int32_t update;
+  int32_t half;            /* nonzero: products of fp16 values (X itself is kept in 22
+                              bits, so X is off by some 2^-9 of its size); 0: of fp16
+                              pairs, three products for each (some 2^-20) */
+  int32_t* status;         /* nullable; records SPARGE_ERR_TIMEOUT if a bounded wait
+                              runs out */
+} sparge_ortho;
+
+/* Workspace: X, A and B of as many matrices as are worked on at once.  Sizes alone
+ * decide. */
+int sparge_orthogonalize_workspace_bytes(const sparge_ortho* args, size_t* bytes);
+
+/*
+ * sparge_orthogonalize -- all matrices of a list at once: 3 + 3 * steps launches
+ * for up to 64 matrices (of up to 2^27 values).  Matrices of which one is written
+ * (out, momentum) must not share memory with another tensor of the list
+ * (SPARGE_ERR_INVALID_ARG), but out may lie exactly on its own grad.  Repeated
+ * calls give the same bits.  A matrix with NaN or infinities becomes NaN; zeros
+ * stay zeros (with an eps above 0).
+ */
+int sparge_orthogonalize(const sparge_ortho* args, void* workspace, size_t ws_bytes,
+                         sparge_stream_t stream);
+
 /* Enqueues on `stream` a copy of the device status word into *host_status
  * (caller-owned, page-locked host memory for the copy to be asynchronous) and
  * returns without waiting; the value is valid once the stream has reached the
