@@ -31,6 +31,11 @@ positions over time, height and width, and the attention's layout),
 and ``clip_grad_norm_``. ``AttentionBlock`` uses the first two when it is given
 a rope or a norm, ``BlockStack`` joins each block's residual with the next
 block's norm, and ``distillation_step`` clips when it is given a bound.
+
+Between the self-attention and the next block stands the attention over a text or
+image context: ``cross_attention`` with autograd, ``CrossAttentionBlock`` around it,
+which ``BlockStack`` takes like any other block. ``Muon`` is an optimiser for the
+blocks' matrices whose whole step runs in the library.
 """
 
 from __future__ import annotations
@@ -47,6 +52,17 @@ def _gradient(g, dtype):
     concatenation's gradient), which are contiguous already."""
     g = g.to(dtype).contiguous()
     return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
+def _strided(t):
+    """[batch, heads, tokens, d] in bf16 as the library reads it: any strides of
+    multiples of 16 bytes, so views of projections [batch, tokens, heads, d] stay
+    where they are; copied else (an expanded gradient, a view at an odd place)."""
+    t = t.to(torch.bfloat16)
+    *outer, last = t.stride()
+    fits = (last == 1 and t.data_ptr() % 16 == 0
+            and all(s > 0 and s % 8 == 0 for s, n in zip(outer, t.shape) if n > 1))
+    return t if fits else t.clone(memory_format=torch.contiguous_format)
 
 
 class SparseAttentionFunction(torch.autograd.Function):
@@ -174,6 +190,34 @@ def clip_grad_norm_(parameters, max_norm: float, eps: float = 1e-6) -> torch.Ten
     return B.sparge_clip_grads(grads, max_norm, eps=eps)
 
 
+class CrossAttentionFunction(torch.autograd.Function):
+    """``sparge_cross_fwd`` with the gradients of ``sparge_cross_bwd``; the output
+    and the gradients lie as their inputs do."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, kv_len, softmax_scale):
+        ctx.dtypes = [t.dtype for t in (q, k, v)]
+        q, k, v = (_strided(t) for t in (q, k, v))
+        o, lse = B.sparge_cross_fwd(q, k, v, kv_len, softmax_scale, out=torch.empty_like(q))
+        ctx.save_for_backward(q, k, v, o, lse, kv_len)
+        ctx.softmax_scale = softmax_scale
+        return o
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        q, k, v, o, lse, kv_len = ctx.saved_tensors
+        grads = B.sparge_cross_bwd(q, k, v, o, lse, _strided(dout), kv_len, ctx.softmax_scale,
+                                   out=[torch.empty_like(t) for t in (q, k, v)])
+        return (*(g.to(t) for g, t in zip(grads, ctx.dtypes)), None, None)
+
+
+def cross_attention(q, k, v, kv_len=None, softmax_scale: float = 0.0):
+    """Attention of q [B, H, N, d] over the context k, v [Bk, Hk, M, d], with
+    autograd: see ``sparge_cross_fwd``. Gradients flow to q, k and v."""
+    return CrossAttentionFunction.apply(q, k, v, kv_len, softmax_scale)
+
+
 class AttentionBlock(torch.nn.Module):
     """Multi-head attention block on tokens x [B, N, C]: Q, K, V projections
     to H heads of width d, attention, output projection back to C. Weights are
@@ -212,11 +256,13 @@ class AttentionBlock(torch.nn.Module):
             self.norm_q, self.norm_k = (torch.nn.Parameter(torch.ones(width, device=device))
                                         for _ in range(2))
 
+    modulated = True  # takes a row of run_blocks' modulation
+
     def _heads(self, t, b, n):
         return (t.reshape(b, n, self.heads, self.head_dim).permute(0, 2, 1, 3)
                 .to(torch.bfloat16).contiguous())
 
-    def attend(self, x, grid=None):
+    def attend(self, x, grid=None, context=None, kv_len=None):
         """The attention of tokens x, without the residual and its norm."""
         b, n, _ = x.shape
         if self.rope is None and self.qk_norm is None:
@@ -243,16 +289,78 @@ class AttentionBlock(torch.nn.Module):
                           modulation[:, :, None] if modulation is not None else None)
 
 
-def run_blocks(blocks, x, grid=None, modulation=None):
+class CrossAttentionBlock(torch.nn.Module):
+    """Attention of tokens x [B, N, C] over a context [B or 1, M, context_channels]:
+    H query heads, ``kv_heads`` key heads (a divisor of H), projections in fp32, the
+    attention in bf16 through the library. ``qk_norm`` ("token" or "head") is the RMS
+    norm of Q and K, with learned weights. With ``norm`` ("layer" or "rms") the block
+    is residual: x + attention(norm(x)). ``kv_len`` (int32 [B]) counts the valid
+    context tokens of each sample."""
+
+    modulated = False
+
+    def __init__(self, channels: int, heads: int, head_dim: int, context_channels: int,
+                 kv_heads: int | None = None, generator: torch.Generator | None = None,
+                 device="cuda", qk_norm: str | None = None, norm: str | None = None):
+        super().__init__()
+        self.heads, self.head_dim, self.kv_heads = heads, head_dim, kv_heads or heads
+        self.qk_norm, self.norm = qk_norm, norm
+        inner, key_inner = heads * head_dim, self.kv_heads * head_dim
+
+        def weight(rows, cols):
+            w = torch.randn((rows, cols), generator=generator) * rows ** -0.5
+            return torch.nn.Parameter(w.to(device))
+
+        self.wq = weight(channels, inner)
+        self.wk = weight(context_channels, key_inner)
+        self.wv = weight(context_channels, key_inner)
+        self.wo = weight(inner, channels)
+        if qk_norm is not None:
+            widths = (inner, key_inner) if qk_norm == "token" else (head_dim, head_dim)
+            self.norm_q, self.norm_k = (torch.nn.Parameter(torch.ones(w, device=device))
+                                        for w in widths)
+
+    def _heads(self, t, heads):
+        return t.unflatten(-1, (heads, self.head_dim))
+
+    def attend(self, x, grid=None, context=None, kv_len=None):
+        """The attention of tokens x, without the residual and its norm."""
+        if context is None:
+            raise ValueError("a cross attention block needs a context")
+        q = self._heads(x @ self.wq, self.heads)
+        k, v = (self._heads(context @ w, self.kv_heads) for w in (self.wk, self.wv))
+        if self.qk_norm is None:
+            q, k, v = (t.to(torch.bfloat16).transpose(1, 2) for t in (q, k, v))
+        else:
+            q, _, _ = qkv_heads(q, norm=self.qk_norm, q_weight=self.norm_q)
+            _, k, v = qkv_heads(None, k, v, norm=self.qk_norm, k_weight=self.norm_k)
+        o = cross_attention(q, k, v, kv_len)
+        return o.transpose(1, 2).flatten(2).float() @ self.wo
+
+    def forward(self, x, context, kv_len=None):
+        if self.norm is None:
+            return self.attend(x, None, context, kv_len)
+        return run_blocks([self], x, context=context, kv_len=kv_len)
+
+
+def run_blocks(blocks, x, grid=None, modulation=None, context=None, kv_len=None):
     """Residual blocks one after another, each block's join in one pass with the
     next block's norm. ``modulation`` is fp32 [B, F, blocks, 3, C]: shift, scale
-    and gate of each block, or None."""
+    and gate of each block that takes one (attention over a context does not), or
+    None. ``context`` and ``kv_len`` go to the blocks that attend to one."""
+    rows, count = [], 0
+    for block in blocks:
+        rows.append(count if block.modulated else None)
+        count += block.modulated
+
     def mod(i, k):
-        return modulation[:, :, i, k] if modulation is not None else None
+        if modulation is None or rows[i] is None:
+            return None
+        return modulation[:, :, rows[i], k]
 
     _, h = residual_norm(x, None, None, mod(0, 1), mod(0, 0), blocks[0].norm)
     for i, block in enumerate(blocks):
-        o = block.attend(h, grid)
+        o = block.attend(h, grid, context, kv_len)
         if i + 1 < len(blocks):
             x, h = residual_norm(x, o, mod(i, 2), mod(i + 1, 1), mod(i + 1, 0),
                                  blocks[i + 1].norm)
@@ -262,7 +370,7 @@ def run_blocks(blocks, x, grid=None, modulation=None):
 
 
 class BlockStack(torch.nn.Module):
-    """Residual attention blocks in a row (``run_blocks``)."""
+    """Residual blocks of self- and cross attention in a row (``run_blocks``)."""
 
     def __init__(self, blocks):
         super().__init__()
@@ -270,8 +378,59 @@ class BlockStack(torch.nn.Module):
         if len(self.blocks) == 0 or any(b.norm is None for b in self.blocks):
             raise ValueError("expected blocks with a norm")
 
-    def forward(self, x, grid=None, modulation=None):
-        return run_blocks(self.blocks, x, grid, modulation)
+    def forward(self, x, grid=None, modulation=None, context=None, kv_len=None):
+        return run_blocks(self.blocks, x, grid, modulation, context, kv_len)
+
+
+class Muon(torch.optim.Optimizer):
+    """Optimiser of matrices by orthogonalised momenta: ``sparge_muon_step`` over all
+    parameters of a group at once. Momenta are fp32 whatever the parameters' type.
+    ``half`` (the default) takes the products in fp16, which leaves the update off by
+    some 2^-9 of its size; None goes by the parameters' type."""
+
+    def __init__(self, params, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,
+                 weight_decay: float = 0.0, rms: float | None = None, steps: int = 5,
+                 half: bool | None = True):
+        super().__init__(params, dict(lr=lr, momentum=momentum, nesterov=nesterov,
+                                      weight_decay=weight_decay, rms=rms, steps=steps, half=half))
+        for group in self.param_groups:
+            if any(p.dim() != 2 for p in group["params"]):
+                raise ValueError("Muon takes matrices; give other parameters to another optimiser")
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            places = {}
+            for p in group["params"]:
+                if p.grad is None or p.numel() == 0:
+                    continue
+                state = self.state[p]
+                if "momentum" not in state:
+                    state["momentum"] = torch.zeros_like(p, dtype=torch.float32)
+                g = p.grad
+                if g.stride() != p.stride():  # in the weight's order
+                    g = torch.empty_like(p, dtype=g.dtype).copy_(g)
+                for at, t in zip(places.setdefault(p.device, ([], [], [])),
+                                 (p, g, state["momentum"])):
+                    at.append(t)
+            how = {k: v for k, v in group.items() if k != "params"}
+            for weights, grads, momenta in places.values():
+                B.sparge_muon_step(weights, grads, momenta, **how)
+        return loss
+
+    def load_state_dict(self, state_dict):
+        super().load_state_dict(state_dict)
+        # (which casts a state to its parameter's type)
+        mine = [p for group in self.param_groups for p in group["params"]]
+        theirs = [i for group in state_dict["param_groups"] for i in group["params"]]
+        for p, i in zip(mine, theirs):
+            m = state_dict["state"].get(i, {}).get("momentum")
+            if m is not None:
+                self.state[p]["momentum"] = torch.empty_like(p, dtype=torch.float32).copy_(m)
 
 
 def distillation_step(student, teacher, x: torch.Tensor, optimizer: torch.optim.Optimizer,
