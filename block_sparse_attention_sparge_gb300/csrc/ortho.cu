@@ -45,6 +45,7 @@ struct Shape {
   int mb, nb;        // blocks of 128 rows and columns of X
   int end_a, end_x;  // running count of output tiles: of A and B, of X
   uint32_t x[2], a, b;
+  uint32_t v;        // fp32 vectors: see below
   int kx;            // exponent of X's scale
 };
 struct ShapeBatch {
@@ -64,6 +65,7 @@ struct Matrix {
   int nb;             // blocks of 128 columns of X
   int end_p, end_t;   // running counts: CTAs of the norm, tiles of X
   uint32_t x0, xn;    // X at the start and at the end
+  uint32_t v;
   int parts, part0;   // partial sums of the norm
   int kx;
 };
@@ -75,6 +77,21 @@ struct MatrixBatch {
   int nesterov, update;
   Matrix m[kMaxBatch];
 };
+
+// Diagonals.  A and B are near multiples of the identity once X's rows have norm one,
+// and what rounding takes from those (fp16's, and the tensor cores', which round
+// sums towards zero at each addition) is what the result is off by.  So the
+// diagonals are kept apart, in fp32, and the tiles of A and B hold zeros there:
+// with A = D + E,
+//   d_i = sum of row i's squares of X,
+//   B_ij = E_ij (b + c (d_i + d_j)) + c (E E)_ij,   B_ii = b d_i + c (d_i^2 + (E E)_ii),
+//   X_i <- (a + B_ii) X_i + sum over k != i of B_ik X_k.
+// The squares come from whoever writes X, a sum for each row of each tile.
+// Vectors of a matrix, from v on: [2 nb] of the sums of squares of X as stored
+// (scaled by 4^kx), then d, then B_ii, each of 128 mb values.
+SPARGE_DEV float* vectors(uint8_t* base, uint32_t v) {
+  return reinterpret_cast<float*>(base + static_cast<int64_t>(v) * kTile);
+}
 
 // Tiles of a value's form: hi (fp16), then lo (fp16), then, in the exact form, fp32.
 // Each plane of X holds mb * 2 nb tiles.
@@ -318,6 +335,13 @@ __global__ void __launch_bounds__(256) ortho_start_kernel(const __grid_constant_
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[j] = u[j] * f1 * f2;
     store_x<EXACT>(x, tile, plane, r, ch, u);
+    float squares = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) squares = fmaf(u[j], u[j], squares);
+    squares = sum_of_8(squares);  // the eight threads of a row
+    if (ch == 0)
+      vectors(p.base, m.v)[static_cast<int64_t>(tile % (2 * m.nb)) * (tiles / (2 * m.nb) * kTR) + r0 + r] =
+          squares;
   }
 }
 
@@ -392,13 +416,12 @@ struct GemmCfg {
   static constexpr int NBAR = B_DONE + 1;
   static constexpr uint32_t off_slot = off_bar + NBAR * 8;
   static constexpr uint32_t bytes = off_slot + 16;
-  // The tensor cores round a sum towards zero at each addition, so a long one drifts:
-  // with 32 additions in a row the result was off by 1e-5.  The exact form therefore
-  // reads its accumulators out every kChunk steps (8 additions) and adds those in
-  // registers; the products with a lo, 2^-11 of the others, have an accumulator of
-  // their own for the whole tile.
+  // The tensor cores round a sum towards zero at each addition, so a long one drifts.
+  // The exact form therefore reads its accumulators out every kChunk steps and adds
+  // those in registers; the products with a lo, 2^-11 of the others, have an
+  // accumulator of their own for the whole tile.
   static constexpr int kAcc = EXACT ? 2 : 1;
-  static constexpr int kChunk = EXACT ? 2 : INT_MAX;
+  static constexpr int kChunk = EXACT ? 8 : INT_MAX;
   static constexpr uint32_t tmem_cols = 2 * kAcc * BN;
 };
 
@@ -586,37 +609,69 @@ __global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
       const float f = KIND == kGram     ? scalbnf(kScaleA, -2 * s.kx)
                       : KIND == kSquare ? p.c / kScaleA
                                         : 1.f / kScaleA;
-      // Eight products' sums (piece ch of the thread's row in a tile) to their place.
-      auto put = [&](int64_t tile, int ch, float (&y)[8]) {
+      float* vec = vectors(p.base, s.v);
+      const int64_t rows = static_cast<int64_t>(mb) * kTR;
+      float* dA = vec + static_cast<int64_t>(xt) * rows;
+      float* dB = dA + rows;
+      const int row = w.rb * kTR + r;
+      const float d_row = KIND == kSquare ? __ldcg(dA + row) : 0.f;
+      const float a_row = KIND == kApply ? p.a + __ldcg(dB + row) : 0.f;
+      // Eight products' sums (piece ch of the thread's row in the j-th tile) to their
+      // place; returns the sum of X's squares.
+      const int64_t first = static_cast<int64_t>(w.rb) * (KIND == kApply ? xt : at) + w.cb;
+      auto put = [&](int j, int ch, float (&y)[8]) -> float {
+        const int64_t tile = first + j;
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] *= f;
         if constexpr (KIND == kApply) {
-          float x[8];
+          float x[8], squares = 0.f;
           load_x<EXACT>(X, tile, x_plane, r, ch, x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = fmaf(p.a, x[i], y[i]);
+          for (int i = 0; i < 8; ++i) {
+            y[i] = fmaf(a_row, x[i], y[i]);
+            squares = fmaf(y[i], y[i], squares);
+          }
           store_x<EXACT>(Y, tile, x_plane, r, ch, y);
+          return squares;
         } else {
           const int64_t at_byte = tile * kTile + piece(r, ch);
+          const int col = (w.cb + j) * kTC + ch * 8;
           if constexpr (KIND == kSquare) {
-            float x[8];
-            unpack_half8(__ldcg(reinterpret_cast<const uint4*>(A + at_byte)), x);
+            float e[8];
+            unpack_half8(__ldcg(reinterpret_cast<const uint4*>(A + at_byte)), e);
             if constexpr (EXACT) {
               float lo[8];
               unpack_half8(__ldcg(reinterpret_cast<const uint4*>(A + a_plane + at_byte)), lo);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] += lo[i];
+              for (int i = 0; i < 8; ++i) e[i] += lo[i];
+            }
+            const float4 d0 = __ldcg(reinterpret_cast<const float4*>(dA + col));
+            const float4 d1 = __ldcg(reinterpret_cast<const float4*>(dA + col) + 1);
+            const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = fmaf(e[i], fmaf(p.c, d_row + d[i], p.b), y[i]);
+          }
+          if (row >= col && row < col + 8) {  // the diagonal
+            if constexpr (KIND == kGram) {
+              float sum = 0.f;
+              for (int i = 0; i < xt; ++i) sum += __ldcg(vec + i * rows + row);
+              dA[row] = scalbnf(sum, -2 * s.kx);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = fmaf(p.b, x[i], y[i]);
+            for (int i = 0; i < 8; ++i) {
+              if (col + i != row) continue;
+              if constexpr (KIND == kSquare)
+                dB[row] = fmaf(d_row, fmaf(p.c, d_row, p.b), y[i] / kScaleA);
+              y[i] = 0.f;
+            }
           }
           uint4 hi, lo;
           split_half8(y, hi, lo);
           *reinterpret_cast<uint4*>(G + at_byte) = hi;
           if constexpr (EXACT) *reinterpret_cast<uint4*>(G + a_plane + at_byte) = lo;
+          return 0.f;
         }
       };
-      const int64_t first = static_cast<int64_t>(w.rb) * (KIND == kApply ? xt : at) + w.cb;
       if constexpr (EXACT) {
         static_assert(BN == 128, "a thread's sums are those of one tile");
         float acc[64];
@@ -644,13 +699,15 @@ __global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
           mbar_arrive(bar(C::B_AE + buf));
         }
         if (ok && half < cols) {
+          float squares = 0.f;
 #pragma unroll
           for (int ch = 0; ch < 8; ++ch) {
             float y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = acc[8 * ch + i];
-            put(first + half, ch, y);
+            squares += put(half, ch, y);
           }
+          if (KIND == kApply) vec[(w.cb + half) * rows + row] = squares;
         }
       } else {
         const int buf = q & 1;
@@ -660,6 +717,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
         }
         tc_fence_after();
         for (int j = half; j < cols; j += 2) {
+          float squares = 0.f;
 #pragma unroll
           for (int c0 = 0; c0 < 64; c0 += 32) {
             float v[32];
@@ -669,9 +727,10 @@ __global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
               float y[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) y[i] = v[8 * e + i];
-              put(first + j, c0 / 8 + e, y);
+              squares += put(j, c0 / 8 + e, y);
             }
           }
+          if (KIND == kApply) vec[(w.cb + j) * rows + row] = squares;
         }
         tc_fence_before();
         mbar_arrive(bar(C::B_AE + buf));
@@ -752,6 +811,9 @@ Batch make_batch(const sparge_ortho& a, int at, int BN) {
     used += at_ * (exact ? a_planes<true>() : a_planes<false>());
     h.b = used;
     used += at_ * (exact ? a_planes<true>() : a_planes<false>());
+    h.v = used;
+    used += (static_cast<uint32_t>(h.mb) * (2 * h.nb + 2) * kTR * sizeof(float) + kTile - 1) / kTile;
+    m.v = h.v;
     b.tiles_a += h.mb * ((h.mb * 128 + BN - 1) / BN);
     b.tiles_x += h.mb * ((h.nb * 128 + BN - 1) / BN);
     h.end_a = b.tiles_a;

@@ -79,11 +79,11 @@ def test_workspace(lib):
     assert f(None, ctypes.byref(n)) == INV
     assert lib.sparge_orthogonalize(None, None, 0, None) == INV
     assert f(ctypes.byref(_args(half=1)), ctypes.byref(n)) == 0
-    # X twice in two planes, A and B, of 128 x 128 fp16 values
-    one = 6 * 32768
+    # X twice in two planes, A and B, of 128 x 128 fp16 values, and fp32 vectors
+    one = 6 * 32768 + 16384
     assert one < n.value <= one + 256 * 8
     assert f(ctypes.byref(_args()), ctypes.byref(n)) == 0
-    assert 12 * 32768 < n.value <= 12 * 32768 + 256 * 8
+    assert 12 * 32768 + 16384 < n.value <= 12 * 32768 + 16384 + 256 * 8
     a = _args(half=1)
     assert f(ctypes.byref(a), ctypes.byref(n)) == 0
     assert lib.sparge_orthogonalize(ctypes.byref(a), FAKE, n.value - 1, None) == WS
