@@ -86,5 +86,7 @@ int make_tmap_bf16(void* tmap_out, const void* base, int BH, int N, int d, int b
 // The same over [batch, heads, len, d] with strides in elements (batch, head, token).
 int make_tmap_bf16_4d(void* tmap_out, const void* base, int batch, int heads, int len, int d,
                       const int64_t (&stride)[3], int box_rows);
+// 2-D map over rows of 128 bytes (fp16), unswizzled: boxes of box_rows rows.
+int make_tmap_rows(void* tmap_out, const void* base, int64_t bytes, int box_rows);
 
 }  // namespace sparge

@@ -2,6 +2,7 @@
 //   X = U / (|U| + eps),  X <- a X + B X,  B = b A + c A A,  A = X X^T
 // over a list of matrices, X the short side by the long one (tall matrices are
 // worked on transposed).
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -13,6 +14,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "kernels.h"
 #include "places.h"
 #include "rows.cuh"
 #include "sparge.h"
@@ -103,6 +105,9 @@ __host__ __device__ constexpr int a_planes() { return EXACT ? 2 : 1; }
 // Byte offset of the 16-byte piece ch (eight values) of row r in a tile.
 SPARGE_DEV uint32_t piece(int r, int ch) { return r * 128 + ((ch ^ (r & 7)) << 4); }
 
+// The same in a tile of fp32 values (four to a piece).
+SPARGE_DEV uint32_t piece32(int r, int ch) { return r * 256 + ((ch ^ (r & 7)) << 4); }
+
 SPARGE_DEV uint32_t pack_half2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -134,9 +139,9 @@ template <bool EXACT>
 SPARGE_DEV void load_x(const uint8_t* tiles, int64_t tile, int64_t plane, int r, int ch,
                        float (&f)[8]) {
   if constexpr (EXACT) {
-    const float4* p = reinterpret_cast<const float4*>(tiles + 2 * plane + tile * 2 * kTile +
-                                                      r * 256 + ch * 32);
-    const float4 u = __ldcg(p), v = __ldcg(p + 1);
+    const uint8_t* p = tiles + 2 * plane + tile * 2 * kTile;
+    const float4 u = __ldcg(reinterpret_cast<const float4*>(p + piece32(r, 2 * ch)));
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(p + piece32(r, 2 * ch + 1)));
     f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
     f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
   } else {
@@ -157,9 +162,9 @@ SPARGE_DEV void store_x(uint8_t* tiles, int64_t tile, int64_t plane, int r, int 
   *reinterpret_cast<uint4*>(p) = hi;
   *reinterpret_cast<uint4*>(p + plane) = lo;
   if constexpr (EXACT) {
-    float4* q = reinterpret_cast<float4*>(tiles + 2 * plane + tile * 2 * kTile + r * 256 + ch * 32);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+    uint8_t* q = tiles + 2 * plane + tile * 2 * kTile;
+    *reinterpret_cast<float4*>(q + piece32(r, 2 * ch)) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(q + piece32(r, 2 * ch + 1)) = make_float4(f[4], f[5], f[6], f[7]);
   }
 }
 
@@ -396,23 +401,32 @@ __global__ void __launch_bounds__(256) ortho_finish_kernel(const __grid_constant
 // ----------------------------------------------------------------- products
 enum Product { kGram, kSquare, kApply };  // A = X X^T;  B = b A + c A A;  X = a X + B X
 
-// A CTA's output tile is 128 rows x BN columns; the contraction runs in steps of 64.
+// An output tile is 128 rows x 128 columns of one CTA (CG 1), or 256 rows of a pair
+// of CTAs (CG 2) x 256 columns (128 in the exact form), where each loads its rows of
+// A and half of B's columns: half the bytes for as many products.  The contraction
+// runs in steps of 64.  A and B are symmetric: tiles below the diagonal's blocks are
+// not computed, the others are written twice, as they are and transposed.
 // Eight epilogue warps read one accumulator while the products fill the other.
-template <int BN, bool EXACT>
+template <int CG, bool EXACT>
 struct GemmCfg {
+  static constexpr int BN = CG == 2 && !EXACT ? 256 : 128;
   static constexpr int kWarps = 8;  // epilogue
   static constexpr int kThreads = (kWarps + 2) * 32;
   static constexpr int kPlanes = EXACT ? 2 : 1;  // operands: hi, or hi and lo
   static constexpr uint32_t kA = kTile;
-  static constexpr uint32_t kB = BN * 128;
+  static constexpr uint32_t kB = BN / CG * 128;
   static constexpr uint32_t kStage = kPlanes * (kA + kB);
-  static constexpr int NST = static_cast<int>(192 * 1024 / kStage);
-  static constexpr uint32_t off_bar = NST * kStage;
-  static constexpr int B_F = 0;             // NST: a stage's tiles landed
+  // An epilogue warp's own: 32 rows of a tile, in two planes of fp16 or one of fp32.
+  static constexpr uint32_t kHold = 8192;
+  static constexpr int NST = static_cast<int>((226 * 1024 - kWarps * kHold) / kStage);
+  static constexpr uint32_t off_hold = NST * kStage;
+  static constexpr uint32_t off_bar = off_hold + kWarps * kHold;
+  static constexpr int B_F = 0;             // NST: a stage's tiles landed (of both CTAs)
   static constexpr int B_E = NST;           // NST: its products done
   static constexpr int B_AF = 2 * NST;      // 2: an accumulator complete
-  static constexpr int B_AE = B_AF + 2;     // 2, all epilogue threads: it was read
-  static constexpr int B_DONE = B_AE + 2;
+  static constexpr int B_AE = B_AF + 2;     // 2, all epilogue warps (of both CTAs): it was read
+  static constexpr int B_H = B_AE + 2;      // kWarps: what the warp holds landed
+  static constexpr int B_DONE = B_H + kWarps;
   static constexpr int NBAR = B_DONE + 1;
   static constexpr uint32_t off_slot = off_bar + NBAR * 8;
   static constexpr uint32_t bytes = off_slot + 16;
@@ -420,9 +434,8 @@ struct GemmCfg {
   // The exact form therefore reads its accumulators out every kChunk steps and adds
   // those in registers; the products with a lo, 2^-11 of the others, have an
   // accumulator of their own for the whole tile.
-  static constexpr int kAcc = EXACT ? 2 : 1;
-  static constexpr int kChunk = EXACT ? 8 : INT_MAX;
-  static constexpr uint32_t tmem_cols = 2 * kAcc * BN;
+  static constexpr int kChunk = EXACT ? 4 : INT_MAX;
+  static constexpr uint32_t tmem_cols = (EXACT ? 4 : 2) * BN;
 };
 
 struct GemmParams {
@@ -435,50 +448,80 @@ struct GemmParams {
 
 struct GemmTile {
   const Shape* s;
-  int rb, cb;   // block of rows, first 64-column tile
+  int rb, cb;   // first block of 128 rows, of 128 columns
   int steps;    // of the contraction
 };
-template <int BN, Product KIND>
+// Output tiles of a matrix: all of X's, those of A that reach the diagonal or above.
+template <int CG, bool EXACT>
+__host__ __device__ inline int row_tiles(int mb) { return (mb + CG - 1) / CG; }
+template <int CG, bool EXACT>
+__host__ __device__ inline int col_tiles(int nb) {
+  constexpr int CU = GemmCfg<CG, EXACT>::BN / 128;
+  return (nb + CU - 1) / CU;
+}
+template <int CG, bool EXACT>
+__host__ __device__ inline int first_col(int i) {  // of row i of A's tiles
+  return i * CG / (GemmCfg<CG, EXACT>::BN / 128);
+}
+template <int CG, bool EXACT, Product KIND>
 SPARGE_DEV GemmTile gemm_tile(const ShapeBatch& sb, int t) {
+  constexpr int CU = GemmCfg<CG, EXACT>::BN / 128;
   const int i = find(sb.n, t, [&](int k) { return KIND == kApply ? sb.s[k].end_x : sb.s[k].end_a; });
   const Shape& s = sb.s[i];
-  const int before = i == 0 ? 0 : KIND == kApply ? sb.s[i - 1].end_x : sb.s[i - 1].end_a;
-  const int across = ((KIND == kApply ? s.nb : s.mb) * 128 + BN - 1) / BN;
+  t -= i == 0 ? 0 : KIND == kApply ? sb.s[i - 1].end_x : sb.s[i - 1].end_a;
   GemmTile g;
   g.s = &s;
-  g.rb = (t - before) / across;
-  g.cb = (t - before) % across * (BN / 64);
   g.steps = 2 * (KIND == kGram ? s.nb : s.mb);
+  const int across = col_tiles<CG, EXACT>(KIND == kApply ? s.nb : s.mb);
+  int row = 0;
+  if (KIND == kApply) {
+    row = t / across;
+    t -= row * across;
+  } else {
+    for (int n; t >= (n = across - first_col<CG, EXACT>(row)); ++row) t -= n;
+    t += first_col<CG, EXACT>(row);
+  }
+  g.rb = row * CG;
+  g.cb = t * CU;
   return g;
 }
 
-template <int BN, bool EXACT, Product KIND>
-__global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
-    ortho_gemm_kernel(const __grid_constant__ ShapeBatch sb, const __grid_constant__ GemmParams p) {
-  using C = GemmCfg<BN, EXACT>;
+template <int CG, bool EXACT, Product KIND>
+__global__ void __launch_bounds__(GemmCfg<CG, EXACT>::kThreads, 1)
+    ortho_gemm_kernel(const __grid_constant__ CUtensorMap tm128,
+                      const __grid_constant__ CUtensorMap tm64,
+                      const __grid_constant__ ShapeBatch sb, const __grid_constant__ GemmParams p) {
+  using C = GemmCfg<CG, EXACT>;
+  constexpr int BN = C::BN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t s0 = smem_u32(smem_raw);
-  if ((s0 & 1023u) != 0u) {  // the swizzled tiles need 1024-byte alignment
-    if (threadIdx.x == 0) report_error(p.status, SPARGE_ERR_CUDA);
-    return;
-  }
   auto bar = [&](int i) -> uint32_t { return s0 + C::off_bar + 8u * i; };
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem_raw + C::off_slot);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
+  const int first_tile = blockIdx.x / CG, stride = gridDim.x / CG;
   constexpr int kProducer = C::kWarps, kIssuer = C::kWarps + 1;
   grid_launch_dependents();
 
   if (threadIdx.x == 0) {
+    // (The swizzled tiles need 1024-byte alignment.)
+    if ((s0 & 1023u) != 0u) report_error(p.status, SPARGE_ERR_CUDA);
     for (int i = 0; i < C::NBAR; ++i)
-      mbar_init(bar(i), i == C::B_AE || i == C::B_AE + 1 ? 32 * C::kWarps : 1);
+      mbar_init(bar(i), i == C::B_AE || i == C::B_AE + 1 ? C::kWarps * CG : 1);
     fence_barrier_init();
   }
   if (warp == kIssuer) {
-    tmem_alloc(smem_u32(slot), C::tmem_cols);
-    tmem_relinquish();
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(smem_u32(slot), C::tmem_cols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(slot), C::tmem_cols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // the other CTA's barriers are ready
   tc_fence_after();
   const uint32_t tmem = *slot;
   grid_wait();  // the operands are the previous kernel's
@@ -488,48 +531,58 @@ __global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
     if (lane == 0) {
       bool ok = true;
       int g = 0;
-      for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
-        const GemmTile w = gemm_tile<BN, KIND>(sb, t);
+      for (int t = first_tile; ok && t < p.tiles; t += stride) {
+        const GemmTile w = gemm_tile<CG, EXACT, KIND>(sb, t);
         const Shape& s = *w.s;
         const int mb = s.mb, xt = 2 * s.nb, at = 2 * mb;  // tiles of a row of X; of A
-        const int64_t x_plane = static_cast<int64_t>(mb) * xt * kTile;
-        const int64_t a_plane = static_cast<int64_t>(mb) * at * kTile;
-        const uint8_t* X = p.base + static_cast<int64_t>(s.x[x_in]) * kTile;
-        const uint8_t* A = p.base + static_cast<int64_t>(KIND == kSquare ? s.a : s.b) * kTile;
-        const int blocks = min(BN / 128, (KIND == kApply ? s.nb : mb) - w.cb / 2);
+        const int nb = KIND == kApply ? s.nb : mb;         // blocks of columns of the output
+        // Rows of 128 bytes from the base: X, and A or B.
+        const int64_t X = static_cast<int64_t>(s.x[x_in]) * kTR;
+        const int64_t A = static_cast<int64_t>(KIND == kSquare ? s.a : s.b) * kTR;
+        const int64_t x_plane = static_cast<int64_t>(mb) * xt * kTR;
+        const int64_t a_plane = static_cast<int64_t>(mb) * at * kTR;
+        const int rb = w.rb + rank;
+        const int both = min(CG, mb - w.rb);                   // CTAs with rows
+        const int wide = min(BN / 128, nb - w.cb);             // blocks with columns
+        const uint32_t bytes = C::kPlanes * (both * kTile + wide * kTile);
         for (int k = 0; k < w.steps; ++k, ++g) {
           const int st = g % C::NST;
           if (g >= C::NST && !mbar_wait(bar(C::B_E + st), ((g / C::NST) - 1) & 1, kWaitTimeoutNs)) {
             ok = false;
             break;
           }
-          const uint32_t b_bytes = blocks * kTile;
-          mbar_arrive_expect_tx(bar(C::B_F + st), C::kPlanes * (C::kA + b_bytes));
+          if (rank == 0) mbar_arrive_expect_tx(bar(C::B_F + st), bytes);
+          const uint32_t full = CG == 2 ? cluster_addr(bar(C::B_F + st), 0) : bar(C::B_F + st);
+          auto load = [&](uint32_t dst, int64_t row, int rows) {
+            if constexpr (CG == 2)
+              tma_load_2d_pair(dst, rows == kTR ? &tm128 : &tm64, full, 0, static_cast<int>(row));
+            else
+              bulk_load(dst, p.base + row * 128, rows * 128, full);
+          };
           for (int pl = 0; pl < C::kPlanes; ++pl) {
             const uint32_t da = s0 + st * C::kStage + pl * C::kA;
             const uint32_t db = s0 + st * C::kStage + C::kPlanes * C::kA + pl * C::kB;
-            if constexpr (KIND == kGram) {
-              bulk_load(da, X + pl * x_plane + static_cast<int64_t>(w.rb * xt + k) * kTile, kTile,
-                        bar(C::B_F + st));
-              for (int j = 0; j < blocks; ++j)
-                bulk_load(db + j * kTile,
-                          X + pl * x_plane + static_cast<int64_t>((w.cb / 2 + j) * xt + k) * kTile,
-                          kTile, bar(C::B_F + st));
+            const int64_t xp = X + pl * x_plane, ap = A + pl * a_plane;
+            if (rb < mb)
+              load(da, KIND == kGram ? xp + static_cast<int64_t>(rb * xt + k) * kTR
+                                     : ap + static_cast<int64_t>(rb * at + k) * kTR, kTR);
+            if constexpr (KIND == kApply) {
+              // 64 rows of X: half of each column's tile.
+              constexpr int kCols = BN / CG / 64;
+              for (int j = 0; j < kCols; ++j) {
+                const int col = 2 * w.cb + rank * kCols + j;
+                if (col < xt)
+                  load(db + j * (kTile / 2),
+                       xp + static_cast<int64_t>((k >> 1) * xt + col) * kTR + (k & 1) * 64, 64);
+              }
             } else {
-              bulk_load(da, A + pl * a_plane + static_cast<int64_t>(w.rb * at + k) * kTile, kTile,
-                        bar(C::B_F + st));
-              if constexpr (KIND == kSquare) {
-                for (int j = 0; j < blocks; ++j)
-                  bulk_load(db + j * kTile,
-                            A + pl * a_plane + static_cast<int64_t>((w.cb / 2 + j) * at + k) * kTile,
-                            kTile, bar(C::B_F + st));
-              } else {
-                // 64 rows of X: half of each column's tile.
-                for (int j = 0; j < 2 * blocks; ++j)
-                  bulk_load(db + j * (kTile / 2),
-                            X + pl * x_plane + static_cast<int64_t>((k >> 1) * xt + w.cb + j) * kTile +
-                                (k & 1) * (kTile / 2),
-                            kTile / 2, bar(C::B_F + st));
+              // Rows of the other side: a block, or half of one.
+              const int64_t from = KIND == kGram ? xp : ap;
+              const int across = KIND == kGram ? xt : at;
+              if constexpr (CG == 2 && BN == 128) {
+                load(db, from + static_cast<int64_t>(w.cb * across + k) * kTR + rank * 64, 64);
+              } else if (w.cb + rank < nb) {
+                load(db, from + static_cast<int64_t>((w.cb + rank) * across + k) * kTR, kTR);
               }
             }
           }
@@ -537,21 +590,27 @@ __global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
       }
       if (!ok) report_error(p.status, SPARGE_ERR_TIMEOUT);
       // Let the last copies land before the CTA can exit.
-      for (int i = max(0, g - C::NST); i < g; ++i)
-        mbar_wait(bar(C::B_F + i % C::NST), (i / C::NST) & 1, kWaitTimeoutNs);
+      if (rank == 0)
+        for (int i = max(0, g - C::NST); i < g; ++i)
+          mbar_wait(bar(C::B_F + i % C::NST), (i / C::NST) & 1, kWaitTimeoutNs);
     }
+    __syncwarp();
   } else if (warp == kIssuer) {
     // The whole warp runs the loop; one elected lane issues each MMA.  B's rows are
     // the contraction's in kApply (MN-major), its columns in the others (K-major).
-    constexpr uint32_t id = idesc_fp16(kTR, BN, false, KIND == kApply);
+    constexpr uint32_t id = idesc_fp16(kTR * CG, BN, false, KIND == kApply);
+    auto commit = [&](int i) {
+      if constexpr (CG == 2) warp_commit_pair(bar(i));
+      else warp_commit(bar(i));
+    };
     bool ok = true;
     int g = 0, q = 0, odd = 0;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, odd ^= 1) {
-      const GemmTile w = gemm_tile<BN, KIND>(sb, t);
+    for (int t = first_tile; rank == 0 && ok && t < p.tiles; t += stride, odd ^= 1) {
+      const GemmTile w = gemm_tile<CG, EXACT, KIND>(sb, t);
       const uint32_t cross = tmem + (2 + odd) * BN;
       for (int k0 = 0; ok && k0 < w.steps; k0 += min(C::kChunk, w.steps - k0), ++q) {
         const int buf = q & 1;
-        if (q >= 2 && !warp_wait(bar(C::B_AE + buf), ((q >> 1) - 1) & 1)) {
+        if (q >= 2 && !warp_wait_cluster(bar(C::B_AE + buf), ((q >> 1) - 1) & 1)) {
           ok = false;
           break;
         }
@@ -573,38 +632,50 @@ __global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
             const uint64_t db = sdesc_sw128(sbb + (pr == 1 ? C::kB : 0),
                                             KIND == kApply ? kTile / 2 : 16, 1024);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              warp_mma_bf16(pr > 0 ? cross : d, sdesc_add(da, kk * 32),
-                            sdesc_add(db, KIND == kApply ? kk * 2048 : kk * 32), id,
-                            (k > 0 || pr > 1 || kk > 0 || (pr == 1 && k0 > 0)) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t dak = sdesc_add(da, kk * 32);
+              const uint64_t dbk = sdesc_add(db, KIND == kApply ? kk * 2048 : kk * 32);
+              const uint32_t add = (k > 0 || pr > 1 || kk > 0 || (pr == 1 && k0 > 0)) ? 1u : 0u;
+              if constexpr (CG == 2) warp_mma_f16_pair(pr > 0 ? cross : d, dak, dbk, id, add);
+              else warp_mma_bf16(pr > 0 ? cross : d, dak, dbk, id, add);
+            }
           }
-          warp_commit(bar(C::B_E + st));
+          commit(C::B_E + st);
         }
-        if (ok) warp_commit(bar(C::B_AF + buf));
+        if (ok) commit(C::B_AF + buf);
       }
     }
     if (!ok && lane == 0) report_error(p.status, SPARGE_ERR_TIMEOUT);
-    warp_commit(bar(C::B_DONE));
-    warp_wait(bar(C::B_DONE), 0);
+    if (rank == 0) {
+      commit(C::B_DONE);
+      warp_wait(bar(C::B_DONE), 0);
+    }
   } else {
-    // Thread = row r (TMEM lane); the two warps of a quarter take every other
-    // 64-column tile.
+    // Thread = row r of the CTA's block (TMEM lane); the two warps of a quarter take
+    // every other 64-column tile.  A warp's 32 rows of a tile are 4 KB in a row: they
+    // come into what the warp holds, are changed there row by row, and go out again,
+    // by bulk copies.
     const int quarter = warp & 3, half = warp >> 2;
     const int r = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint8_t* hold = smem_raw + C::off_hold + warp * C::kHold;
+    const uint32_t hold_at = s0 + C::off_hold + warp * C::kHold;
+    const uint32_t full = bar(C::B_H + warp);
+    const uint32_t read_out = CG == 2 ? cluster_addr(bar(C::B_AE), 0) : bar(C::B_AE);
+    constexpr uint32_t kPlane = kTile / 4;  // bytes of a warp's rows
     bool ok = true;
-    int q = 0, odd = 0;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, odd ^= 1) {
-      const GemmTile w = gemm_tile<BN, KIND>(sb, t);
+    int q = 0, odd = 0, held = 0;
+    for (int t = first_tile; ok && t < p.tiles; t += stride, odd ^= 1) {
+      const GemmTile w = gemm_tile<CG, EXACT, KIND>(sb, t);
       const Shape& s = *w.s;
-      const int mb = s.mb, xt = 2 * s.nb, at = 2 * mb;
+      const int mb = s.mb, xt = 2 * s.nb, at = 2 * mb, rb = w.rb + rank;
+      const int across = KIND == kApply ? xt : at;
       const int64_t x_plane = static_cast<int64_t>(mb) * xt * kTile;
       const int64_t a_plane = static_cast<int64_t>(mb) * at * kTile;
       const uint8_t* A = p.base + static_cast<int64_t>(s.a) * kTile;
       uint8_t* G = p.base + static_cast<int64_t>(KIND == kGram ? s.a : s.b) * kTile;
       const uint8_t* X = p.base + static_cast<int64_t>(s.x[x_in]) * kTile;
       uint8_t* Y = p.base + static_cast<int64_t>(s.x[x_out]) * kTile;
-      const int cols = min(BN / 64, (KIND == kApply ? xt : at) - w.cb);
       // A = X X^T comes scaled by 4^kx, A A by kScaleA^2, B X by kScaleA.
       const float f = KIND == kGram     ? scalbnf(kScaleA, -2 * s.kx)
                       : KIND == kSquare ? p.c / kScaleA
@@ -613,68 +684,204 @@ __global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
       const int64_t rows = static_cast<int64_t>(mb) * kTR;
       float* dA = vec + static_cast<int64_t>(xt) * rows;
       float* dB = dA + rows;
-      const int row = w.rb * kTR + r;
-      const float d_row = KIND == kSquare ? __ldcg(dA + row) : 0.f;
-      const float a_row = KIND == kApply ? p.a + __ldcg(dB + row) : 0.f;
-      // Eight products' sums (piece ch of the thread's row in the j-th tile) to their
-      // place; returns the sum of X's squares.
-      const int64_t first = static_cast<int64_t>(w.rb) * (KIND == kApply ? xt : at) + w.cb;
-      auto put = [&](int j, int ch, float (&y)[8]) -> float {
-        const int64_t tile = first + j;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= f;
-        if constexpr (KIND == kApply) {
-          float x[8], squares = 0.f;
-          load_x<EXACT>(X, tile, x_plane, r, ch, x);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            y[i] = fmaf(a_row, x[i], y[i]);
-            squares = fmaf(y[i], y[i], squares);
-          }
-          store_x<EXACT>(Y, tile, x_plane, r, ch, y);
-          return squares;
-        } else {
-          const int64_t at_byte = tile * kTile + piece(r, ch);
-          const int col = (w.cb + j) * kTC + ch * 8;
-          if constexpr (KIND == kSquare) {
-            float e[8];
-            unpack_half8(__ldcg(reinterpret_cast<const uint4*>(A + at_byte)), e);
+      const int row = rb * kTR + r;
+
+      // Whether the j-th 64-column tile is there and this warp's to write.
+      auto wanted = [&](int j) {
+        return rb < mb && 2 * w.cb + j < across && (KIND == kApply || w.cb + j / 2 >= rb);
+      };
+      auto tile_of = [&](int j) { return static_cast<int64_t>(rb) * across + 2 * w.cb + j; };
+      // What the warp holds is free again; the j-th tile's values on their way in.
+      auto fetch = [&](int j) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_wait_read();
+          if constexpr (KIND == kApply) {
+            mbar_arrive_expect_tx(full, 2 * kPlane);
             if constexpr (EXACT) {
-              float lo[8];
-              unpack_half8(__ldcg(reinterpret_cast<const uint4*>(A + a_plane + at_byte)), lo);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) e[i] += lo[i];
+              bulk_load(hold_at, X + 2 * x_plane + tile_of(j) * 2 * kTile + quarter * 2 * kPlane,
+                        2 * kPlane, full);
+            } else {
+              const uint8_t* src = X + tile_of(j) * kTile + quarter * kPlane;
+              bulk_load(hold_at, src, kPlane, full);
+              bulk_load(hold_at + kPlane, src + x_plane, kPlane, full);
             }
-            const float4 d0 = __ldcg(reinterpret_cast<const float4*>(dA + col));
-            const float4 d1 = __ldcg(reinterpret_cast<const float4*>(dA + col) + 1);
-            const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = fmaf(e[i], fmaf(p.c, d_row + d[i], p.b), y[i]);
+          } else if constexpr (KIND == kSquare) {
+            mbar_arrive_expect_tx(full, C::kPlanes * kPlane);
+            const uint8_t* src = A + tile_of(j) * kTile + quarter * kPlane;
+            bulk_load(hold_at, src, kPlane, full);
+            if constexpr (EXACT) bulk_load(hold_at + kPlane, src + a_plane, kPlane, full);
           }
-          if (row >= col && row < col + 8) {  // the diagonal
+        }
+        __syncwarp();
+      };
+      auto held_piece = [&](int plane, int ch) -> uint4& {
+        return *reinterpret_cast<uint4*>(hold + plane * kPlane + piece(lane, ch));
+      };
+      // The held planes are written: out with them.
+      auto put_out = [&](uint8_t* dst, uint32_t from, uint32_t bytes) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_store(dst, hold_at + from, bytes);
+          bulk_commit();
+        }
+      };
+      // The products' sums of the j-th tile to its results.
+      auto process = [&](int j, float (&y)[64]) {
+        const int64_t tile = tile_of(j);
+        const int64_t at_byte = tile * kTile + quarter * kPlane;
+        const int col0 = (2 * w.cb + j) * kTC;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) y[i] *= f;
+        if constexpr (KIND != kGram) {
+          if (!warp_wait(full, held & 1)) ok = false;
+          ++held;
+        }
+        if constexpr (KIND == kApply) {
+          const float a_row = p.a + __ldcg(dB + row);
+          float squares = 0.f;
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) {
+            float x[8], v[8];
+            if constexpr (EXACT) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float4 u = *reinterpret_cast<float4*>(hold + piece32(lane, 2 * ch + e));
+                x[4 * e] = u.x, x[4 * e + 1] = u.y, x[4 * e + 2] = u.z, x[4 * e + 3] = u.w;
+              }
+            } else {
+              float lo[8];
+              unpack_half8(held_piece(0, ch), x);
+              unpack_half8(held_piece(1, ch), lo);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] += lo[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              v[i] = y[8 * ch + i] = fmaf(a_row, x[i], y[8 * ch + i]);
+              squares = fmaf(v[i], v[i], squares);
+            }
+            if constexpr (EXACT) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float4*>(hold + piece32(lane, 2 * ch + e)) =
+                    make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            } else {
+              split_half8(v, held_piece(0, ch), held_piece(1, ch));
+            }
+          }
+          vec[(2 * w.cb + j) * rows + row] = squares;
+          if constexpr (EXACT) {
+            put_out(Y + 2 * x_plane + tile * 2 * kTile + quarter * 2 * kPlane, 0, 2 * kPlane);
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+              float v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = y[8 * ch + i];
+              split_half8(v, held_piece(0, ch), held_piece(1, ch));
+            }
+          }
+          put_out(Y + at_byte, 0, kPlane);
+          put_out(Y + x_plane + at_byte, kPlane, kPlane);
+        } else {
+          if constexpr (KIND == kSquare) {
+            const float d_row = __ldg(dA + row);
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+              float e[8];
+              unpack_half8(held_piece(0, ch), e);
+              if constexpr (EXACT) {
+                float lo[8];
+                unpack_half8(held_piece(1, ch), lo);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i] += lo[i];
+              }
+              const float4 d0 = __ldg(reinterpret_cast<const float4*>(dA + col0 + 8 * ch));
+              const float4 d1 = __ldg(reinterpret_cast<const float4*>(dA + col0 + 8 * ch) + 1);
+              const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                y[8 * ch + i] = fmaf(e[i], fmaf(p.c, d_row + d[i], p.b), y[8 * ch + i]);
+            }
+          }
+          if (row - lane >= col0 && row - lane < col0 + kTC) {  // a tile on the diagonal
             if constexpr (KIND == kGram) {
               float sum = 0.f;
+#pragma unroll 8
               for (int i = 0; i < xt; ++i) sum += __ldcg(vec + i * rows + row);
               dA[row] = scalbnf(sum, -2 * s.kx);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (col + i != row) continue;
-              if constexpr (KIND == kSquare)
+            for (int i = 0; i < 64; ++i) {
+              if (col0 + i != row) continue;
+              if constexpr (KIND == kSquare) {
+                const float d_row = __ldg(dA + row);
                 dB[row] = fmaf(d_row, fmaf(p.c, d_row, p.b), y[i] / kScaleA);
+              }
               y[i] = 0.f;
             }
           }
-          uint4 hi, lo;
-          split_half8(y, hi, lo);
-          *reinterpret_cast<uint4*>(G + at_byte) = hi;
-          if constexpr (EXACT) *reinterpret_cast<uint4*>(G + a_plane + at_byte) = lo;
-          return 0.f;
+          const int cbk = w.cb + j / 2;  // the tile's block of columns
+#pragma unroll
+          for (int pl = 0; pl < C::kPlanes; ++pl) {
+            if (pl > 0 && lane == 0) bulk_wait_read();
+            __syncwarp();  // every lane has read what it held
+            uint32_t bits[32];
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+              float v[8];
+              uint4 hi, lo;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = y[8 * ch + i];
+              split_half8(v, hi, lo);
+              const uint4 u = pl == 0 ? hi : lo;
+              held_piece(0, ch) = u;
+              bits[4 * ch] = u.x, bits[4 * ch + 1] = u.y, bits[4 * ch + 2] = u.z, bits[4 * ch + 3] = u.w;
+            }
+            put_out(G + pl * a_plane + at_byte, 0, kPlane);
+            if (cbk > rb) {
+              // The same transposed, 32 columns at a time: each becomes 64 bytes of a row.
+              constexpr int kPitch16 = 80;
+              uint8_t* turn = hold + kPlane;
+#pragma unroll
+              for (int c0 = 0; c0 < 64; c0 += 32) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                  const uint32_t u = bits[(c0 + c) / 2];
+                  *reinterpret_cast<uint16_t*>(turn + c * kPitch16 + lane * 2) = u & 0xffffu;
+                  *reinterpret_cast<uint16_t*>(turn + (c + 1) * kPitch16 + lane * 2) = u >> 16;
+                }
+                __syncwarp();
+                uint8_t* dst = G + pl * a_plane +
+                               (static_cast<int64_t>(cbk) * at + 2 * rb + quarter / 2) * kTile;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  *reinterpret_cast<uint4*>(
+                      dst + piece((j & 1) * 64 + c0 + lane, (quarter & 1) * 4 + e)) =
+                      *reinterpret_cast<const uint4*>(turn + lane * kPitch16 + e * 16);
+                __syncwarp();
+              }
+            }
+          }
         }
       };
+      // An accumulator was read.
+      auto release = [&](int buf) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) mbar_arrive_cluster(read_out + 8u * buf);
+          else mbar_arrive(bar(C::B_AE + buf));
+        }
+      };
+
+      float acc[64];
       if constexpr (EXACT) {
-        static_assert(BN == 128, "a thread's sums are those of one tile");
-        float acc[64];
+        if (wanted(half)) fetch(half);
         for (int k0 = 0; k0 < w.steps; k0 += C::kChunk, ++q) {
           const int buf = q & 1;
           if (!warp_wait(bar(C::B_AF + buf), (q >> 1) & 1)) {
@@ -695,56 +902,47 @@ __global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
               for (int i = 0; i < 32; ++i) acc[c0 + i] += v[i];
             }
           }
-          tc_fence_before();
-          mbar_arrive(bar(C::B_AE + buf));
+          release(buf);
         }
-        if (ok && half < cols) {
-          float squares = 0.f;
-#pragma unroll
-          for (int ch = 0; ch < 8; ++ch) {
-            float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = acc[8 * ch + i];
-            squares += put(half, ch, y);
-          }
-          if (KIND == kApply) vec[(w.cb + half) * rows + row] = squares;
-        }
+        if (ok && wanted(half)) process(half, acc);
       } else {
         const int buf = q & 1;
+        if (wanted(half)) fetch(half);
         if (!warp_wait(bar(C::B_AF + buf), (q >> 1) & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        for (int j = half; j < cols; j += 2) {
-          float squares = 0.f;
+#pragma unroll 1
+        for (int j = half; j < BN / 64; j += 2) {
+          if (wanted(j)) {
+            if (j != half) fetch(j);
 #pragma unroll
-          for (int c0 = 0; c0 < 64; c0 += 32) {
-            float v[32];
-            tmem_ld32(lanes + buf * BN + j * 64 + c0, v);
+            for (int c0 = 0; c0 < 64; c0 += 32) {
+              float v[32];
+              tmem_ld32(lanes + buf * BN + j * 64 + c0, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float y[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = v[8 * e + i];
-              squares += put(j, c0 / 8 + e, y);
+              for (int i = 0; i < 32; ++i) acc[c0 + i] = v[i];
             }
           }
-          if (KIND == kApply) vec[(w.cb + j) * rows + row] = squares;
+          if (j + 2 >= BN / 64) release(buf);
+          if (wanted(j)) process(j, acc);
         }
-        tc_fence_before();
-        mbar_arrive(bar(C::B_AE + buf));
         ++q;
       }
     }
     if (!ok) report_error(p.status, SPARGE_ERR_TIMEOUT);
+    if (lane == 0) bulk_wait();  // every result is out
+    __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // neither CTA's memory is in use any more
   if (warp == kIssuer) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::tmem_cols);
+    if constexpr (CG == 2) tmem_dealloc_pair(tmem, C::tmem_cols);
+    else tmem_dealloc(tmem, C::tmem_cols);
   }
 }
 
@@ -752,7 +950,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, EXACT>::kThreads, 1)
 // A launch that may start while the kernel before it on the stream ends
 // (programmatic dependent launch); every kernel here waits before it reads.
 template <typename... Params>
-cudaError_t launch_chained(void (*kernel)(Params...), int grid, int threads, uint32_t smem,
+cudaError_t launch_chained(void (*kernel)(Params...), int grid, int threads, uint32_t smem, int cluster,
                            cudaStream_t st, const Params&... params) {
   if (smem > 48 * 1024) {
     const cudaError_t e =
@@ -764,11 +962,14 @@ cudaError_t launch_chained(void (*kernel)(Params...), int grid, int threads, uin
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, params...);
 }
 
@@ -780,10 +981,25 @@ struct Batch {
   ShapeBatch shapes;
   MatrixBatch mats;
   size_t bytes;        // tiles, then the partial sums
-  int norm_ctas, tiles, tiles_a, tiles_x;
+  int norm_ctas, tiles;
 };
 
-Batch make_batch(const sparge_ortho& a, int at, int BN) {
+// Running counts of the output tiles; their totals for A and for X.
+template <int CG, bool EXACT>
+void count_tiles(ShapeBatch& sb, int& tiles_a, int& tiles_x) {
+  tiles_a = tiles_x = 0;
+  for (int k = 0; k < sb.n; ++k) {
+    Shape& s = sb.s[k];
+    const int down = row_tiles<CG, EXACT>(s.mb);
+    for (int i = 0; i < down; ++i)
+      tiles_a += col_tiles<CG, EXACT>(s.mb) - first_col<CG, EXACT>(i);
+    tiles_x += down * col_tiles<CG, EXACT>(s.nb);
+    s.end_a = tiles_a;
+    s.end_x = tiles_x;
+  }
+}
+
+Batch make_batch(const sparge_ortho& a, int at) {
   Batch b = {};
   const bool exact = !a.half;
   int64_t values = 0;
@@ -814,10 +1030,6 @@ Batch make_batch(const sparge_ortho& a, int at, int BN) {
     h.v = used;
     used += (static_cast<uint32_t>(h.mb) * (2 * h.nb + 2) * kTR * sizeof(float) + kTile - 1) / kTile;
     m.v = h.v;
-    b.tiles_a += h.mb * ((h.mb * 128 + BN - 1) / BN);
-    b.tiles_x += h.mb * ((h.nb * 128 + BN - 1) / BN);
-    h.end_a = b.tiles_a;
-    h.end_x = b.tiles_x;
     m.grad = s.grad;
     m.mom = s.momentum;
     m.out = s.out;
@@ -854,37 +1066,56 @@ Batch make_batch(const sparge_ortho& a, int at, int BN) {
   return b;
 }
 
-constexpr int kBN = 128;
-
-template <bool EXACT>
-cudaError_t run_batch(const sparge_ortho& a, Batch& b, uint8_t* ws, cudaStream_t st) {
-  using C = GemmCfg<kBN, EXACT>;
-  b.mats.base = ws;
-  b.mats.partial = reinterpret_cast<double*>(ws + reinterpret_cast<uintptr_t>(b.mats.partial));
 #define ORTHO_RUN(...)                      \
   do {                                      \
     const cudaError_t e_ = (__VA_ARGS__);   \
     if (e_ != cudaSuccess) return e_;       \
   } while (0)
-  ORTHO_RUN(launch_chained(ortho_norm_kernel, b.norm_ctas, 256, 0, st, b.mats));
-  ORTHO_RUN(launch_chained(ortho_start_kernel<EXACT>, b.tiles, 256, 0, st, b.mats));
+
+template <int CG, bool EXACT>
+cudaError_t run_products(const sparge_ortho& a, Batch& b, uint8_t* ws, cudaStream_t st) {
+  using C = GemmCfg<CG, EXACT>;
+  CUtensorMap tm128, tm64;
+  const int64_t bytes = reinterpret_cast<uint8_t*>(b.mats.partial) - ws;
+  if (make_tmap_rows(&tm128, ws, bytes, 128) != 0 || make_tmap_rows(&tm64, ws, bytes, 64) != 0)
+    return cudaErrorInvalidValue;
+  int tiles_a = 0, tiles_x = 0;
+  count_tiles<CG, EXACT>(b.shapes, tiles_a, tiles_x);
+  const int grid_a = CG * std::min(tiles_a, kSMs / CG), grid_x = CG * std::min(tiles_x, kSMs / CG);
   GemmParams p = {ws, 0, 0, a.a, a.b, a.c, a.status};
   for (int i = 0; i < a.steps; ++i) {
     p.from = i & 1;
-    p.tiles = b.tiles_a;
-    const int grid_a = std::min(b.tiles_a, kSMs), grid_x = std::min(b.tiles_x, kSMs);
-    ORTHO_RUN(launch_chained(ortho_gemm_kernel<kBN, EXACT, kGram>, grid_a, C::kThreads, C::bytes, st,
-                             b.shapes, p));
-    ORTHO_RUN(launch_chained(ortho_gemm_kernel<kBN, EXACT, kSquare>, grid_a, C::kThreads, C::bytes,
-                             st, b.shapes, p));
-    p.tiles = b.tiles_x;
-    ORTHO_RUN(launch_chained(ortho_gemm_kernel<kBN, EXACT, kApply>, grid_x, C::kThreads, C::bytes,
-                             st, b.shapes, p));
+    p.tiles = tiles_a;
+    ORTHO_RUN(launch_chained(ortho_gemm_kernel<CG, EXACT, kGram>, grid_a, C::kThreads, C::bytes, CG,
+                             st, tm128, tm64, b.shapes, p));
+    ORTHO_RUN(launch_chained(ortho_gemm_kernel<CG, EXACT, kSquare>, grid_a, C::kThreads, C::bytes, CG,
+                             st, tm128, tm64, b.shapes, p));
+    p.tiles = tiles_x;
+    ORTHO_RUN(launch_chained(ortho_gemm_kernel<CG, EXACT, kApply>, grid_x, C::kThreads, C::bytes, CG,
+                             st, tm128, tm64, b.shapes, p));
   }
-  ORTHO_RUN(launch_chained(ortho_finish_kernel<EXACT>, b.tiles, 256, 0, st, b.mats));
-#undef ORTHO_RUN
   return cudaSuccess;
 }
+
+// Pairs of CTAs where their tiles fill half of the machine, single CTAs else.
+constexpr int kPairTiles = kSMs / 4;
+
+template <bool EXACT>
+cudaError_t run_batch(const sparge_ortho& a, Batch& b, uint8_t* ws, cudaStream_t st) {
+  b.mats.base = ws;
+  b.mats.partial = reinterpret_cast<double*>(ws + reinterpret_cast<uintptr_t>(b.mats.partial));
+  ORTHO_RUN(launch_chained(ortho_norm_kernel, b.norm_ctas, 256, 0, 1, st, b.mats));
+  ORTHO_RUN(launch_chained(ortho_start_kernel<EXACT>, b.tiles, 256, 0, 1, st, b.mats));
+  int tiles_a = 0, tiles_x = 0;
+  count_tiles<2, EXACT>(b.shapes, tiles_a, tiles_x);
+  if (tiles_x >= kPairTiles)
+    ORTHO_RUN(run_products<2, EXACT>(a, b, ws, st));
+  else
+    ORTHO_RUN(run_products<1, EXACT>(a, b, ws, st));
+  ORTHO_RUN(launch_chained(ortho_finish_kernel<EXACT>, b.tiles, 256, 0, 1, st, b.mats));
+  return cudaSuccess;
+}
+#undef ORTHO_RUN
 
 #define ORTHO_TRY(expr)               \
   do {                                \
@@ -975,7 +1206,7 @@ int check_ortho(const sparge_ortho* a) {
 size_t workspace_of(const sparge_ortho& a) {
   size_t most = 0;
   for (int at = 0; at < a.n;) {
-    const Batch b = make_batch(a, at, kBN);
+    const Batch b = make_batch(a, at);
     most = std::max(most, b.bytes);
     at = b.end;
   }
@@ -1003,7 +1234,7 @@ int sparge_orthogonalize(const sparge_ortho* args, void* workspace, size_t ws_by
   if (workspace == nullptr || ws_bytes < workspace_of(*args)) return SPARGE_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return SPARGE_ERR_MISALIGNED;
   for (int at = 0; at < args->n;) {
-    Batch b = make_batch(*args, at, kBN);
+    Batch b = make_batch(*args, at);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const cudaError_t e = args->half ? run_batch<false>(*args, b, ws, stream)
                                      : run_batch<true>(*args, b, ws, stream);

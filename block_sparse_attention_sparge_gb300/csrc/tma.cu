@@ -72,4 +72,20 @@ int make_tmap_bf16_4d(void* tmap_out, const void* base, int batch, int heads, in
   return r == CUDA_SUCCESS ? 0 : -1;
 }
 
+// Rows of 128 bytes, as they stand: boxes of box_rows of them.  `bytes` is a multiple
+// of 128.
+int make_tmap_rows(void* tmap_out, const void* base, int64_t bytes, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return -1;
+  cuuint64_t dims[2] = {64, static_cast<cuuint64_t>(bytes / 128)};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1u, 1u};
+  CUresult r = fn(static_cast<CUtensorMap*>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                  const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -1;
+}
+
 }  // namespace sparge
