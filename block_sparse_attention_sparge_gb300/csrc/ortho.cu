@@ -227,9 +227,24 @@ SPARGE_DEV int find(int n, int at, End end) {  // the first i with at < end(i)
 }
 
 // Squares of any size: those of values near one as they are, the others scaled.
+// At most kSquares of them, then out into fp64, whose additions run at 1 / 64 of fp32's
+// rate.
+constexpr int kSquares = 64;
 struct Squares {
   float big = 0.f, mid = 0.f, small = 0.f;
-  SPARGE_DEV void add(float x) {
+  SPARGE_DEV void add(const float (&x)[8]) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+    if (top >= 0x1p-40f && top <= 0x1p40f) {  // what is far below the largest may vanish
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mid = fmaf(x[i], x[i], mid);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) add_any(x[i]);
+    }
+  }
+  SPARGE_DEV void add_any(float x) {
     const float a = fabsf(x);
     if (a > 0x1p40f) {
       big = fmaf(x * 0x1p-70f, x * 0x1p-70f, big);
@@ -239,27 +254,32 @@ struct Squares {
       mid = fmaf(x, x, mid);  // NaN too
     }
   }
-  SPARGE_DEV double total() const {
-    return static_cast<double>(big) * 0x1p140 + mid + static_cast<double>(small) * 0x1p-200;
+  SPARGE_DEV void out(double& sum) {
+    sum += mid;
+    if (big != 0.f) sum += static_cast<double>(big) * 0x1p140;
+    if (small != 0.f) sum += static_cast<double>(small) * 0x1p-200;
+    big = mid = small = 0.f;
   }
 };
 
-// Sum over the 256 threads of a CTA, in a fixed order; all of them get it.
+// Sum over the 256 threads of a CTA, in a fixed order, for thread 0.
 SPARGE_DEV double cta_sum(double v) {
   __shared__ double part[8];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();  // the last call's were read
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   double s = 0.0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s += part[i];
+  if (threadIdx.x == 0)
+    for (int i = 0; i < 8; ++i) s += part[i];
   return s;
 }
 
 // The momentum's step and the partial sums of U^2.  A CTA takes every parts-th
-// piece of 16 rows x 128 columns.
-__global__ void __launch_bounds__(256) ortho_norm_kernel(const __grid_constant__ MatrixBatch p) {
+// piece of 16 rows x 128 columns, kAtOnce of them in flight.
+constexpr int kAtOnce = 2;
+__global__ void __launch_bounds__(256, 4) ortho_norm_kernel(const __grid_constant__ MatrixBatch p) {
   grid_launch_dependents();
   grid_wait();
   const int i = find(p.n, blockIdx.x, [&](int k) { return p.m[k].end_p; });
@@ -268,85 +288,119 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const __grid_constant__
   const int across = (m.cols + 127) / 128;
   const int pieces = (m.rows + 15) / 16 * across;
   double sum = 0.0;
-  for (int q = part; q < pieces; q += m.parts) {
-    const int r = q / across * 16 + threadIdx.x / 16, c = q % across * 128 + threadIdx.x % 16 * 8;
-    if (r >= m.rows || c >= m.cols) continue;
-    float u[8];
-    read_any(m.grad, m.grad_f32, r * m.gs, c, m.cols, u);
-    if (m.mom != nullptr) {
-      float v[8];
-      read8(m.mom + r * m.ms, c, m.cols, v);
+  Squares s;
+  int n = 0;
+  for (int q0 = part; q0 < pieces; q0 += kAtOnce * m.parts) {
+    float u[kAtOnce][8], v[kAtOnce][8];
+    int r[kAtOnce], c[kAtOnce];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[k] = fmaf(p.mu, v[k], u[k]);
-        u[k] = p.nesterov ? fmaf(p.mu, v[k], u[k]) : v[k];
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int q = q0 + k * m.parts;
+      r[k] = q / across * 16 + threadIdx.x / 16;
+      c[k] = q % across * 128 + threadIdx.x % 16 * 8;
+      if (q >= pieces || r[k] >= m.rows) c[k] = m.cols;  // nothing there
+      if (c[k] < m.cols) {
+        read_any(m.grad, m.grad_f32, r[k] * m.gs, c[k], m.cols, u[k]);
+        if (m.mom != nullptr) read8(m.mom + r[k] * m.ms, c[k], m.cols, v[k]);
       }
-      write8(m.mom + r * m.ms, c, m.cols, v);
     }
-    Squares s;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s.add(u[k]);
-    sum += s.total();
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (c[k] >= m.cols) continue;
+      if (m.mom != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[k][j] = fmaf(p.mu, v[k][j], u[k][j]);
+          u[k][j] = p.nesterov ? fmaf(p.mu, v[k][j], u[k][j]) : v[k][j];
+        }
+        write8(m.mom + r[k] * m.ms, c[k], m.cols, v[k]);
+      }
+      s.add(u[k]);
+    }
+    n += 8 * kAtOnce;
+    if (n >= kSquares) s.out(sum), n = 0;
   }
+  s.out(sum);
   sum = cta_sum(sum);
   if (threadIdx.x == 0) p.partial[m.part0 + part] = sum;
 }
 
 constexpr int kPitch = kTC + 1;  // floats of a row of a transposed tile in shared memory
 
-// X of the start: U / (|U| + eps) in its tiles.  One CTA to a tile.
+// X of the start: U / (|U| + eps) in its tiles.  A CTA takes tiles side by side, of
+// one matrix mostly, whose factor it works out once.
+constexpr int kStartCtas = 8 * kSMs;
 template <bool EXACT>
 __global__ void __launch_bounds__(256) ortho_start_kernel(const __grid_constant__ MatrixBatch p) {
   __shared__ float t[kTR * kPitch];
+  __shared__ float factor[2];
   grid_launch_dependents();
   grid_wait();
-  const int i = find(p.n, blockIdx.x, [&](int k) { return p.m[k].end_t; });
-  const Matrix& m = p.m[i];
-  double sum = 0.0;
-  for (int k = threadIdx.x; k < m.parts; k += 256) sum += __ldcg(p.partial + m.part0 + k);
-  sum = cta_sum(sum);
-  // 2^kx / (|U| + eps) as two factors, neither of which leaves fp32's range.
-  const double inv = scalbn(1.0, m.kx) / (sqrt(sum) + static_cast<double>(p.eps));
-  int e = 0;
-  const double frac = frexp(inv, &e);
-  const bool fine = inv > 0.0 && inv < 1e300;
-  const float f1 = fine ? scalbnf(1.f, e / 2) : 1.f;
-  const float f2 = fine ? scalbnf(static_cast<float>(frac), e - e / 2) : static_cast<float>(inv);
-  const int tiles = m.end_t - (i > 0 ? p.m[i - 1].end_t : 0);
-  const int tile = blockIdx.x - (m.end_t - tiles);
-  const int64_t plane = static_cast<int64_t>(tiles) * kTile;
-  const int r0 = tile / (2 * m.nb) * kTR, c0 = tile % (2 * m.nb) * kTC;
-  uint8_t* x = p.base + static_cast<int64_t>(m.x0) * kTile;
-  if (m.tall) {
-    // Rows of the tile are columns of the matrix: 64 rows of it, 128 columns.
-    for (int k = threadIdx.x; k < kTC * 16; k += 256) {
-      const int r = c0 + k / 16, c = r0 + k % 16 * 8;
-      float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (r < m.rows && c < m.cols) read_u(p, m, r, c, u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t[(k % 16 * 8 + j) * kPitch + k / 16] = u[j];
+  const int64_t all = p.m[p.n - 1].end_t;
+  const int first = static_cast<int>(all * blockIdx.x / gridDim.x);
+  const int last = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
+  int i = -1;
+  float f1 = 0.f, f2 = 0.f;
+  for (int at = first; at < last; ++at) {
+    if (i < 0 || at >= p.m[i].end_t) {
+      i = find(p.n, at, [&](int k) { return p.m[k].end_t; });
+      const Matrix& m = p.m[i];
+      double sum = 0.0;
+      for (int k = threadIdx.x; k < m.parts; k += 256) sum += __ldcg(p.partial + m.part0 + k);
+      sum = cta_sum(sum);
+      if (threadIdx.x == 0) {
+        // 2^kx / (|U| + eps) as two factors, neither of which leaves fp32's range.
+        const double inv = scalbn(1.0, m.kx) / (sqrt(sum) + static_cast<double>(p.eps));
+        int e = 0;
+        const double frac = frexp(inv, &e);
+        const bool fine = inv > 0.0 && inv < 1e300;
+        factor[0] = fine ? scalbnf(1.f, e / 2) : 1.f;
+        factor[1] = fine ? scalbnf(static_cast<float>(frac), e - e / 2) : static_cast<float>(inv);
+      }
+      __syncthreads();
+      f1 = factor[0], f2 = factor[1];
     }
-    __syncthreads();
-  }
-  for (int k = threadIdx.x; k < kTR * 8; k += 256) {
-    const int r = k / 8, ch = k % 8;
-    float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const Matrix& m = p.m[i];
+    const int tiles = m.end_t - (i > 0 ? p.m[i - 1].end_t : 0);
+    const int tile = at - (m.end_t - tiles);
+    const int64_t plane = static_cast<int64_t>(tiles) * kTile;
+    const int r0 = tile / (2 * m.nb) * kTR, c0 = tile % (2 * m.nb) * kTC;
+    uint8_t* x = p.base + static_cast<int64_t>(m.x0) * kTile;
     if (m.tall) {
+      // Rows of the tile are columns of the matrix: 64 rows of it, 128 columns.
+      __syncthreads();  // the last tile was read
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = t[r * kPitch + ch * 8 + j];
-    } else if (r0 + r < m.rows && c0 + ch * 8 < m.cols) {
-      read_u(p, m, r0 + r, c0 + ch * 8, u);
+      for (int k = threadIdx.x; k < kTC * 16; k += 256) {
+        const int r = c0 + k / 16, c = r0 + k % 16 * 8;
+        float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (r < m.rows && c < m.cols) read_u(p, m, r, c, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[(k % 16 * 8 + j) * kPitch + k / 16] = u[j];
+      }
+      __syncthreads();
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = u[j] * f1 * f2;
-    store_x<EXACT>(x, tile, plane, r, ch, u);
-    float squares = 0.f;
+    for (int k = threadIdx.x; k < kTR * 8; k += 256) {
+      const int r = k / 8, ch = k % 8;
+      float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (m.tall) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) squares = fmaf(u[j], u[j], squares);
-    squares = sum_of_8(squares);  // the eight threads of a row
-    if (ch == 0)
-      vectors(p.base, m.v)[static_cast<int64_t>(tile % (2 * m.nb)) * (tiles / (2 * m.nb) * kTR) + r0 + r] =
-          squares;
+        for (int j = 0; j < 8; ++j) u[j] = t[r * kPitch + ch * 8 + j];
+      } else if (r0 + r < m.rows && c0 + ch * 8 < m.cols) {
+        read_u(p, m, r0 + r, c0 + ch * 8, u);
+      }
+      float squares = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u[j] = u[j] * f1 * f2;
+        squares = fmaf(u[j], u[j], squares);
+      }
+      store_x<EXACT>(x, tile, plane, r, ch, u);
+      squares = sum_of_8(squares);  // the eight threads of a row
+      if (ch == 0)
+        vectors(p.base, m.v)[static_cast<int64_t>(tile % (2 * m.nb)) *
+                                 (tiles / (2 * m.nb) * kTR) + r0 + r] = squares;
+    }
   }
 }
 
@@ -1105,7 +1159,7 @@ cudaError_t run_batch(const sparge_ortho& a, Batch& b, uint8_t* ws, cudaStream_t
   b.mats.base = ws;
   b.mats.partial = reinterpret_cast<double*>(ws + reinterpret_cast<uintptr_t>(b.mats.partial));
   ORTHO_RUN(launch_chained(ortho_norm_kernel, b.norm_ctas, 256, 0, 1, st, b.mats));
-  ORTHO_RUN(launch_chained(ortho_start_kernel<EXACT>, b.tiles, 256, 0, 1, st, b.mats));
+  ORTHO_RUN(launch_chained(ortho_start_kernel<EXACT>, std::min(b.tiles, kStartCtas), 256, 0, 1, st, b.mats));
   int tiles_a = 0, tiles_x = 0;
   count_tiles<2, EXACT>(b.shapes, tiles_a, tiles_x);
   if (tiles_x >= kPairTiles)
