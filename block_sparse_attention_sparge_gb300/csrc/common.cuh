@@ -163,6 +163,16 @@ SPARGE_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "
 SPARGE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 SPARGE_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// 4-D tiled store out of shared memory, in the thread's bulk group (what lies outside
+// the tensor is left out).
+SPARGE_DEV void tma_store_4d(const void* tmap, uint32_t src, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(tmap)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
 // ----------------------------------------------------------------- CTA pairs
 // Two CTAs of a cluster whose tensor cores work on one tile (cta_group::2): the
 // even one issues, each holds its half of the rows of A and D and of the columns of B.

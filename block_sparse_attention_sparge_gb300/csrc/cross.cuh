@@ -49,6 +49,8 @@ SPARGE_DEV void zero_tile_rows(uint8_t* tile, int chunks, uint32_t chunk_bytes, 
 size_t cross_fwd_workspace_bytes(const CrossGeom& g);
 cudaError_t launch_cross_fwd(const CrossGeom& g, const sparge_cross& a, void* workspace,
                              cudaStream_t st);
+// cross_fwd_wide.cu: the form for query tiles that fill the machine (no workspace).
+cudaError_t launch_cross_fwd_wide(const CrossGeom& g, const sparge_cross& a, cudaStream_t st);
 // cross_bwd.cu
 size_t cross_bwd_workspace_bytes(const CrossGeom& g);
 cudaError_t launch_cross_bwd(const CrossGeom& g, const sparge_cross& a, void* workspace,

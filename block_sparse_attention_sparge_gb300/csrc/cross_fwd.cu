@@ -494,6 +494,8 @@ cudaError_t launch_fwd_impl(const CrossGeom& g, const sparge_cross& a, void* wor
 
 }  // namespace
 
+constexpr int kWideTiles = 2 * kSMs;
+
 size_t cross_fwd_workspace_bytes(const CrossGeom& g) {
   const int parts = fwd_parts(g);
   if (parts == 1) return 0;
@@ -502,6 +504,7 @@ size_t cross_fwd_workspace_bytes(const CrossGeom& g) {
 
 cudaError_t launch_cross_fwd(const CrossGeom& g, const sparge_cross& a, void* workspace,
                              cudaStream_t st) {
+  if (static_cast<int64_t>(g.B) * g.H * g.Mq >= kWideTiles) return launch_cross_fwd_wide(g, a, st);
   return g.d == 128 ? launch_fwd_impl<128>(g, a, workspace, st)
                     : launch_fwd_impl<64>(g, a, workspace, st);
 }

@@ -56,7 +56,15 @@ CASES = [
     ((1, 1, 1, 1, 64, 9000, 64), None),
     ((3, 1, 1, 1, 7, 3001, 128), [3001, 0, 260]),
     ((1, 1, 1, 1, 20000, 40, 64), None),
-    ((40, 40, 4, 4, 129, 66, 64), None),            # more query tiles than the machine holds
+    # query tiles that fill the machine
+    ((40, 40, 4, 4, 129, 66, 64), None),
+    ((1, 1, 12, 12, 3500, 512, 128), None),
+    ((3, 3, 12, 3, 1200, 300, 128), [300, 0, 129]),
+    ((7, 1, 6, 2, 1000, 400, 64), [400, 1, 0, 128, 257, 399, 3]),
+    ((80, 80, 4, 2, 1, 200, 64), None),
+    ((80, 80, 5, 1, 2, 129, 128), [129 - (i * 7) % 130 for i in range(80)]),
+    ((1, 1, 3, 3, 13100, 700, 64), None),
+    ((311, 1, 1, 1, 100, 130, 128), None),
 ]
 
 
@@ -86,7 +94,7 @@ def test_backward(k, layout):
 
 
 @pytest.mark.parametrize("garbage", [float("nan"), float("inf"), -3.3e38])
-@pytest.mark.parametrize("k", [4, 5, 6, 7, 8, 10, 14, 16])
+@pytest.mark.parametrize("k", [4, 5, 6, 7, 8, 10, 14, 16, 20, 21, 23])
 def test_what_lies_behind_the_lengths_is_not_used(k, garbage):
     shape, lens = CASES[k]
     q, kk, v, do = _make(shape, k, "tokens", garbage, lens)
@@ -114,15 +122,17 @@ def test_scales(scale):
           ("dq", "dk", "dv"))
 
 
-def test_logits_that_grow_from_step_to_step():
+@pytest.mark.parametrize("batch", [1, 80])
+@pytest.mark.parametrize("d", [64, 128])
+def test_logits_that_grow_from_step_to_step(batch, d):
     """The running maximum moves by more than the kernel's bound for rescaling, both
     ways, and a last key outweighs all before."""
-    q, k, v, _ = _make((1, 1, 2, 2, 140, 700, 64), 5)
+    q, k, v, _ = _make((batch, 1, 2, 2, 140, 700, d), 5)
     ramp = torch.linspace(-3, 3, 700, device=DEV)
-    k = k * 0.1 + (ramp[:, None] * torch.ones(64, device=DEV)).to(BF)
+    k = k * 0.1 + (ramp[:, None] * torch.ones(d, device=DEV)).to(BF)
     q = (q * 0.1 + 1.0).to(BF)
     q[:, :, ::2] *= -1
-    for lens in (None, [651]):
+    for lens in (None, [651] * batch):
         o, lse = B.sparge_cross_fwd(q, k, v, _lens(lens))
         out, lim = reference(q, k, v, lens)
         check((o, lse), out, lim, ("o", "lse"))
