@@ -46,6 +46,10 @@ constexpr int kNormParts = 256;                   // partial sums of a matrix
 struct Shape {
   int mb, nb;        // blocks of 128 rows and columns of X
   int end_a, end_x;  // running count of output tiles: of A and B, of X
+  int end_g;         // running count of the items of A = X X^T: tiles times parts
+  int parts;         // of the contraction of A = X X^T
+  uint32_t slot;     // its first partial sum, where there are several parts
+  uint32_t count;    // and its first counter
   uint32_t x[2], a, b;
   uint32_t v;        // fp32 vectors: see below
   int kx;            // exponent of X's scale
@@ -75,6 +79,8 @@ struct MatrixBatch {
   int n;
   uint8_t* base;
   double* partial;
+  int* counts;  // of the parts of A = X X^T that are done
+  int n_counts;
   float mu, eps;
   int nesterov, update;
   Matrix m[kMaxBatch];
@@ -336,6 +342,7 @@ __global__ void __launch_bounds__(256) ortho_start_kernel(const __grid_constant_
   __shared__ float factor[2];
   grid_launch_dependents();
   grid_wait();
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < p.n_counts; i += gridDim.x * 256) p.counts[i] = 0;
   const int64_t all = p.m[p.n - 1].end_t;
   const int first = static_cast<int>(all * blockIdx.x / gridDim.x);
   const int last = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
@@ -461,6 +468,13 @@ enum Product { kGram, kSquare, kApply };  // A = X X^T;  B = b A + c A A;  X = a
 // runs in steps of 64.  A and B are symmetric: tiles below the diagonal's blocks are
 // not computed, the others are written twice, as they are and transposed.
 // Eight epilogue warps read one accumulator while the products fill the other.
+//
+// The contraction of A = X X^T runs over the long side.  Where the tiles are few for
+// the machine it is cut into parts (plan_parts): an epilogue warp writes its 32 x 64
+// sums, and the one that finds by its counter that it is the last reads those of all
+// parts, adds them in the parts' order (so the result does not depend on which came
+// last) and goes on with the tile.  Six odd matrices, the longest 16 x 5120, fp32:
+// A takes 21 us a step, 55 without parts; the whole call 244 us and 387.
 template <int CG, bool EXACT>
 struct GemmCfg {
   static constexpr int BN = CG == 2 && !EXACT ? 256 : 128;
@@ -472,6 +486,7 @@ struct GemmCfg {
   static constexpr uint32_t kStage = kPlanes * (kA + kB);
   // An epilogue warp's own: 32 rows of a tile, in two planes of fp16 or one of fp32.
   static constexpr uint32_t kHold = 8192;
+  static constexpr int kUnits = CG * BN / 64 * 4;  // partial sums of a tile
   static constexpr int NST = static_cast<int>((226 * 1024 - kWarps * kHold) / kStage);
   static constexpr uint32_t off_hold = NST * kStage;
   static constexpr uint32_t off_bar = off_hold + kWarps * kHold;
@@ -492,9 +507,13 @@ struct GemmCfg {
   static constexpr uint32_t tmem_cols = (EXACT ? 4 : 2) * BN;
 };
 
+constexpr int kUnit = 32 * 65;  // values of a partial sum: those of a warp, and the diagonal's
+
 struct GemmParams {
   uint8_t* base;
-  int tiles;
+  float* sums;       // partial sums
+  int* counts;       // and how many of a tile's parts are there
+  int tiles;         // or items
   int from;          // which of a matrix's two X is read; the other is written
   float a, b, c;
   int32_t* status;
@@ -503,7 +522,10 @@ struct GemmParams {
 struct GemmTile {
   const Shape* s;
   int rb, cb;   // first block of 128 rows, of 128 columns
-  int steps;    // of the contraction
+  int from;     // first step of the contraction
+  int steps;    // and their number
+  int index;    // of the tile in its matrix
+  int part;
 };
 // Output tiles of a matrix: all of X's, those of A that reach the diagonal or above.
 template <int CG, bool EXACT>
@@ -520,12 +542,23 @@ __host__ __device__ inline int first_col(int i) {  // of row i of A's tiles
 template <int CG, bool EXACT, Product KIND>
 SPARGE_DEV GemmTile gemm_tile(const ShapeBatch& sb, int t) {
   constexpr int CU = GemmCfg<CG, EXACT>::BN / 128;
-  const int i = find(sb.n, t, [&](int k) { return KIND == kApply ? sb.s[k].end_x : sb.s[k].end_a; });
+  auto end = [&](int k) {
+    return KIND == kApply ? sb.s[k].end_x : KIND == kGram ? sb.s[k].end_g : sb.s[k].end_a;
+  };
+  const int i = find(sb.n, t, end);
   const Shape& s = sb.s[i];
-  t -= i == 0 ? 0 : KIND == kApply ? sb.s[i - 1].end_x : sb.s[i - 1].end_a;
+  t -= i == 0 ? 0 : end(i - 1);
   GemmTile g;
   g.s = &s;
+  g.from = g.part = 0;
   g.steps = 2 * (KIND == kGram ? s.nb : s.mb);
+  if (KIND == kGram) {
+    g.part = t % s.parts;
+    t /= s.parts;
+    g.from = g.steps * g.part / s.parts;
+    g.steps = g.steps * (g.part + 1) / s.parts - g.from;
+  }
+  g.index = t;
   const int across = col_tiles<CG, EXACT>(KIND == kApply ? s.nb : s.mb);
   int row = 0;
   if (KIND == kApply) {
@@ -599,7 +632,7 @@ __global__ void __launch_bounds__(GemmCfg<CG, EXACT>::kThreads, 1)
         const int both = min(CG, mb - w.rb);                   // CTAs with rows
         const int wide = min(BN / 128, nb - w.cb);             // blocks with columns
         const uint32_t bytes = C::kPlanes * (both * kTile + wide * kTile);
-        for (int k = 0; k < w.steps; ++k, ++g) {
+        for (int k = w.from; k < w.from + w.steps; ++k, ++g) {
           const int st = g % C::NST;
           if (g >= C::NST && !mbar_wait(bar(C::B_E + st), ((g / C::NST) - 1) & 1, kWaitTimeoutNs)) {
             ok = false;
@@ -782,8 +815,56 @@ __global__ void __launch_bounds__(GemmCfg<CG, EXACT>::kThreads, 1)
           bulk_commit();
         }
       };
+      auto diagonal = [&](int j) {  // whether the warp's rows of the j-th tile meet it
+        const int col0 = (2 * w.cb + j) * kTC;
+        return row - lane >= col0 && row - lane < col0 + kTC;
+      };
+      // A's diagonal, of this part's columns of X.
+      auto squares_of = [&](int j) {
+        float sum = 0.f;
+        if (KIND == kGram && diagonal(j)) {
+#pragma unroll 8
+          for (int i = w.from; i < w.from + w.steps; ++i) sum += __ldcg(vec + i * rows + row);
+        }
+        return sum;
+      };
+      // A part's sums of the j-th tile to those of the whole contraction; false where
+      // other parts are still to come.
+      auto join = [&](int j, float (&y)[64], float& squares) {
+        if (KIND != kGram || s.parts == 1) return true;
+        const int64_t unit = (rank * (BN / 64) + j) * 4 + quarter;
+        float* mine = p.sums + (s.slot + static_cast<int64_t>(w.index) * s.parts * C::kUnits + unit) *
+                                   kUnit;
+        constexpr int64_t kNext = static_cast<int64_t>(C::kUnits) * kUnit;
+        float4* dst = reinterpret_cast<float4*>(mine + w.part * kNext);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          __stcg(dst + e * 32 + lane, make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]));
+        __stcg(mine + w.part * kNext + 64 * 32 + lane, squares);
+        __threadfence();
+        __syncwarp();
+        int* count = p.counts + s.count + static_cast<int64_t>(w.index) * C::kUnits + unit;
+        int before = lane == 0 ? atomicAdd(count, 1) : 0;
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before != s.parts - 1) return false;
+        __threadfence();
+        if (lane == 0) *count = 0;  // for the next step
+        squares = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) y[i] = 0.f;
+        for (int q = 0; q < s.parts; ++q) {
+          const float4* src = reinterpret_cast<const float4*>(mine + q * kNext);
+          squares += __ldcg(mine + q * kNext + 64 * 32 + lane);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float4 u = __ldcg(src + e * 32 + lane);
+            y[4 * e] += u.x, y[4 * e + 1] += u.y, y[4 * e + 2] += u.z, y[4 * e + 3] += u.w;
+          }
+        }
+        return true;
+      };
       // The products' sums of the j-th tile to its results.
-      auto process = [&](int j, float (&y)[64]) {
+      auto process = [&](int j, float (&y)[64], float diag) {
         const int64_t tile = tile_of(j);
         const int64_t at_byte = tile * kTile + quarter * kPlane;
         const int col0 = (2 * w.cb + j) * kTC;
@@ -862,13 +943,8 @@ __global__ void __launch_bounds__(GemmCfg<CG, EXACT>::kThreads, 1)
                 y[8 * ch + i] = fmaf(e[i], fmaf(p.c, d_row + d[i], p.b), y[8 * ch + i]);
             }
           }
-          if (row - lane >= col0 && row - lane < col0 + kTC) {  // a tile on the diagonal
-            if constexpr (KIND == kGram) {
-              float sum = 0.f;
-#pragma unroll 8
-              for (int i = 0; i < xt; ++i) sum += __ldcg(vec + i * rows + row);
-              dA[row] = scalbnf(sum, -2 * s.kx);
-            }
+          if (diagonal(j)) {
+            if constexpr (KIND == kGram) dA[row] = scalbnf(diag, -2 * s.kx);
 #pragma unroll
             for (int i = 0; i < 64; ++i) {
               if (col0 + i != row) continue;
@@ -958,7 +1034,10 @@ __global__ void __launch_bounds__(GemmCfg<CG, EXACT>::kThreads, 1)
           }
           release(buf);
         }
-        if (ok && wanted(half)) process(half, acc);
+        if (ok && wanted(half)) {
+          float diag = squares_of(half);
+          if (join(half, acc, diag)) process(half, acc, diag);
+        }
       } else {
         const int buf = q & 1;
         if (wanted(half)) fetch(half);
@@ -980,7 +1059,10 @@ __global__ void __launch_bounds__(GemmCfg<CG, EXACT>::kThreads, 1)
             }
           }
           if (j + 2 >= BN / 64) release(buf);
-          if (wanted(j)) process(j, acc);
+          if (wanted(j)) {
+            float diag = squares_of(j);
+            if (join(j, acc, diag)) process(j, acc, diag);
+          }
         }
         ++q;
       }
@@ -1034,8 +1116,11 @@ struct Batch {
   int end;
   ShapeBatch shapes;
   MatrixBatch mats;
-  size_t bytes;        // tiles, then the partial sums
+  size_t bytes;        // tiles, then the partial sums of the norms, counters, those of A
+  size_t sums;         // where the last begin
   int norm_ctas, tiles;
+  int pairs;           // whether pairs of CTAs compute the products
+  int tiles_a, tiles_x, items_g;
 };
 
 // Running counts of the output tiles; their totals for A and for X.
@@ -1051,6 +1136,61 @@ void count_tiles(ShapeBatch& sb, int& tiles_a, int& tiles_x) {
     s.end_a = tiles_a;
     s.end_x = tiles_x;
   }
+}
+
+// Pairs of CTAs where their tiles fill half of the machine, single CTAs else.
+constexpr int kPairTiles = kSMs / 4;
+
+// Cuts the contractions of A = X X^T: into parts of a number of steps for which the
+// busiest CTA (items go round) is done first.  In steps of the products: an item
+// costs kItemSteps beside its own, a join kJoinSteps for each part (reading 8 KB of
+// sums a warp takes 0.7 us; a step 0.7 us in the exact form, 0.25 us in the other).
+constexpr int kItemSteps = 4, kMaxParts = 64;
+template <int CG, bool EXACT>
+void plan_parts(Batch& b) {
+  count_tiles<CG, EXACT>(b.shapes, b.tiles_a, b.tiles_x);
+  constexpr int kJoinSteps = EXACT ? 1 : 3, kSlots = kSMs / CG;
+  auto tiles_of = [&](int k) { return b.shapes.s[k].end_a - (k > 0 ? b.shapes.s[k - 1].end_a : 0); };
+  auto parts_of = [&](int k, int steps) {
+    return std::max(1, std::min(kMaxParts, (2 * b.shapes.s[k].nb + steps - 1) / steps));
+  };
+  int longest = 0;
+  for (int k = 0; k < b.shapes.n; ++k) longest = std::max(longest, 2 * b.shapes.s[k].nb);
+  int chosen = longest;
+  if (b.tiles_a <= 2 * kSlots) {
+    int64_t least = INT64_MAX;
+    for (int steps = longest; steps >= 4; steps = steps * 3 / 4) {
+      int load[kSlots] = {};
+      int at = 0, items = 0;
+      for (int k = 0; k < b.shapes.n; ++k) {
+        const int parts = parts_of(k, steps);
+        const int each = (2 * b.shapes.s[k].nb + parts - 1) / parts + kItemSteps +
+                         (parts > 1 ? parts * kJoinSteps : 0);
+        items += tiles_of(k) * parts;
+        if (items > 2 * kSlots + b.tiles_a) break;
+        for (int i = tiles_of(k) * parts; i > 0; --i, at = at + 1 < kSlots ? at + 1 : 0) load[at] += each;
+      }
+      if (items > 2 * kSlots + b.tiles_a) break;
+      const int64_t most = *std::max_element(load, load + kSlots);
+      if (most < least) least = most, chosen = steps;
+    }
+  }
+  uint32_t slots = 0, counts = 0;
+  for (int k = 0; k < b.shapes.n; ++k) {
+    Shape& s = b.shapes.s[k];
+    s.parts = parts_of(k, chosen);
+    s.slot = slots;
+    s.count = counts;
+    b.items_g += tiles_of(k) * s.parts;
+    s.end_g = b.items_g;
+    if (s.parts == 1) continue;
+    counts += tiles_of(k) * GemmCfg<CG, EXACT>::kUnits;
+    slots += tiles_of(k) * s.parts * GemmCfg<CG, EXACT>::kUnits;
+  }
+  b.mats.n_counts = static_cast<int>(counts);
+  b.sums = (b.bytes + counts * sizeof(int) + 255) / 256 * 256;
+  b.mats.counts = reinterpret_cast<int*>(b.bytes);  // an offset, too
+  b.bytes = b.sums + static_cast<size_t>(slots) * kUnit * sizeof(float);
 }
 
 Batch make_batch(const sparge_ortho& a, int at) {
@@ -1117,6 +1257,12 @@ Batch make_batch(const sparge_ortho& a, int at) {
   const size_t tiles = static_cast<size_t>(used) * kTile;
   b.mats.partial = reinterpret_cast<double*>(tiles);  // an offset until the base is known
   b.bytes = tiles + static_cast<size_t>(partials) * sizeof(double);
+  int tiles_a = 0, tiles_x = 0;
+  if (exact) count_tiles<2, true>(b.shapes, tiles_a, tiles_x);
+  else count_tiles<2, false>(b.shapes, tiles_a, tiles_x);
+  b.pairs = tiles_x >= kPairTiles;
+  if (exact) b.pairs ? plan_parts<2, true>(b) : plan_parts<1, true>(b);
+  else b.pairs ? plan_parts<2, false>(b) : plan_parts<1, false>(b);
   return b;
 }
 
@@ -1133,36 +1279,33 @@ cudaError_t run_products(const sparge_ortho& a, Batch& b, uint8_t* ws, cudaStrea
   const int64_t bytes = reinterpret_cast<uint8_t*>(b.mats.partial) - ws;
   if (make_tmap_rows(&tm128, ws, bytes, 128) != 0 || make_tmap_rows(&tm64, ws, bytes, 64) != 0)
     return cudaErrorInvalidValue;
-  int tiles_a = 0, tiles_x = 0;
-  count_tiles<CG, EXACT>(b.shapes, tiles_a, tiles_x);
-  const int grid_a = CG * std::min(tiles_a, kSMs / CG), grid_x = CG * std::min(tiles_x, kSMs / CG);
-  GemmParams p = {ws, 0, 0, a.a, a.b, a.c, a.status};
+  auto grid = [](int items) { return CG * std::min(items, kSMs / CG); };
+  const int grid_g = grid(b.items_g), grid_a = grid(b.tiles_a), grid_x = grid(b.tiles_x);
+  GemmParams p = {ws, reinterpret_cast<float*>(ws + b.sums), b.mats.counts, 0, 0, a.a, a.b, a.c,
+                  a.status};
   for (int i = 0; i < a.steps; ++i) {
     p.from = i & 1;
-    p.tiles = tiles_a;
-    ORTHO_RUN(launch_chained(ortho_gemm_kernel<CG, EXACT, kGram>, grid_a, C::kThreads, C::bytes, CG,
+    p.tiles = b.items_g;
+    ORTHO_RUN(launch_chained(ortho_gemm_kernel<CG, EXACT, kGram>, grid_g, C::kThreads, C::bytes, CG,
                              st, tm128, tm64, b.shapes, p));
+    p.tiles = b.tiles_a;
     ORTHO_RUN(launch_chained(ortho_gemm_kernel<CG, EXACT, kSquare>, grid_a, C::kThreads, C::bytes, CG,
                              st, tm128, tm64, b.shapes, p));
-    p.tiles = tiles_x;
+    p.tiles = b.tiles_x;
     ORTHO_RUN(launch_chained(ortho_gemm_kernel<CG, EXACT, kApply>, grid_x, C::kThreads, C::bytes, CG,
                              st, tm128, tm64, b.shapes, p));
   }
   return cudaSuccess;
 }
 
-// Pairs of CTAs where their tiles fill half of the machine, single CTAs else.
-constexpr int kPairTiles = kSMs / 4;
-
 template <bool EXACT>
 cudaError_t run_batch(const sparge_ortho& a, Batch& b, uint8_t* ws, cudaStream_t st) {
   b.mats.base = ws;
   b.mats.partial = reinterpret_cast<double*>(ws + reinterpret_cast<uintptr_t>(b.mats.partial));
+  b.mats.counts = reinterpret_cast<int*>(ws + reinterpret_cast<uintptr_t>(b.mats.counts));
   ORTHO_RUN(launch_chained(ortho_norm_kernel, b.norm_ctas, 256, 0, 1, st, b.mats));
   ORTHO_RUN(launch_chained(ortho_start_kernel<EXACT>, std::min(b.tiles, kStartCtas), 256, 0, 1, st, b.mats));
-  int tiles_a = 0, tiles_x = 0;
-  count_tiles<2, EXACT>(b.shapes, tiles_a, tiles_x);
-  if (tiles_x >= kPairTiles)
+  if (b.pairs)
     ORTHO_RUN(run_products<2, EXACT>(a, b, ws, st));
   else
     ORTHO_RUN(run_products<1, EXACT>(a, b, ws, st));
