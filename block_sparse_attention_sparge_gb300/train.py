@@ -256,13 +256,13 @@ class AttentionBlock(torch.nn.Module):
             self.norm_q, self.norm_k = (torch.nn.Parameter(torch.ones(width, device=device))
                                         for _ in range(2))
 
-    modulated = True  # takes a row of run_blocks' modulation
+    crosses = False  # whether run_blocks' context goes to it, and no row of its modulation
 
     def _heads(self, t, b, n):
         return (t.reshape(b, n, self.heads, self.head_dim).permute(0, 2, 1, 3)
                 .to(torch.bfloat16).contiguous())
 
-    def attend(self, x, grid=None, context=None, kv_len=None):
+    def attend(self, x, grid=None):
         """The attention of tokens x, without the residual and its norm."""
         b, n, _ = x.shape
         if self.rope is None and self.qk_norm is None:
@@ -297,7 +297,7 @@ class CrossAttentionBlock(torch.nn.Module):
     is residual: x + attention(norm(x)). ``kv_len`` (int32 [B]) counts the valid
     context tokens of each sample."""
 
-    modulated = False
+    crosses = True
 
     def __init__(self, channels: int, heads: int, head_dim: int, context_channels: int,
                  kv_heads: int | None = None, generator: torch.Generator | None = None,
@@ -348,10 +348,11 @@ def run_blocks(blocks, x, grid=None, modulation=None, context=None, kv_len=None)
     next block's norm. ``modulation`` is fp32 [B, F, blocks, 3, C]: shift, scale
     and gate of each block that takes one (attention over a context does not), or
     None. ``context`` and ``kv_len`` go to the blocks that attend to one."""
+    crosses = [getattr(block, "crosses", False) for block in blocks]
     rows, count = [], 0
-    for block in blocks:
-        rows.append(count if block.modulated else None)
-        count += block.modulated
+    for cross in crosses:
+        rows.append(None if cross else count)
+        count += not cross
 
     def mod(i, k):
         if modulation is None or rows[i] is None:
@@ -360,7 +361,7 @@ def run_blocks(blocks, x, grid=None, modulation=None, context=None, kv_len=None)
 
     _, h = residual_norm(x, None, None, mod(0, 1), mod(0, 0), blocks[0].norm)
     for i, block in enumerate(blocks):
-        o = block.attend(h, grid, context, kv_len)
+        o = block.attend(h, grid, context, kv_len) if crosses[i] else block.attend(h, grid)
         if i + 1 < len(blocks):
             x, h = residual_norm(x, o, mod(i, 2), mod(i + 1, 1), mod(i + 1, 0),
                                  blocks[i + 1].norm)
