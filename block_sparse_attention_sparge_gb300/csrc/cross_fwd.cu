@@ -452,11 +452,22 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
 }
 
 // Parts of a query tile's keys: one, unless the tiles fill less than half of the
-// CTAs that the machine holds; then as many as fill it, of four steps at least.
+// CTAs that the machine holds; then as many, up to what fills it, as shorten the call,
+// where the partial results and their join cost kJoinSteps steps of 64 keys and half of
+// one for each part.  (152 tiles, d = 128: 512 keys 12.5 us, in two parts 18.6; 1500
+// keys 24.9 and 24.7; at d = 64 10.4 and 12.4, 21.5 and 17.8.)
+constexpr int kJoinSteps = 9;
 int fwd_parts(const CrossGeom& g) {
   const int64_t items = static_cast<int64_t>(g.B) * g.H * g.Mq, slots = kSMs * kFwdCtasPerSm;
   const int64_t steps = (g.M + kBN - 1) / kBN;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({slots / items, steps / 4, 64})));
+  const int most = static_cast<int>(std::min<int64_t>({slots / items, steps, 64}));
+  int best = 1;
+  int64_t least = 2 * steps;
+  for (int P = 2; P <= most; ++P) {
+    const int64_t cost = 2 * ((steps + P - 1) / P) + 2 * kJoinSteps + P;
+    if (cost < least) least = cost, best = P;
+  }
+  return best;
 }
 
 template <int D>
@@ -492,9 +503,22 @@ cudaError_t launch_fwd_impl(const CrossGeom& g, const sparge_cross& a, void* wor
   return cudaGetLastError();
 }
 
-}  // namespace
+// Which form: the persistent one where more query tiles than CTAs fit at once wait
+// their turn.  Measured, us, one CTA to a tile / persistent, at 304, 376, 608, 1216 tiles:
+//   d = 128, 128 keys   8.1 /  8.9   12.0 / 10.1   14.2 / 11.4   26.6 / 19.8
+//            512       13.0 / 14.0   19.6 / 18.9   23.0 / 21.2   43.6 / 36.5
+//            1500      25.3 / 26.9   40.1 / 41.8   47.8 / 48.1   92.5 / 88.6
+//   d = 64,  128 keys   6.5 /  8.9    9.1 /  9.8   10.8 / 10.8   19.0 / 16.6
+//            512       10.7 / 13.6   16.1 / 18.4   18.6 / 20.3   35.2 / 34.2
+//            1500      21.5 / 26.3   34.6 / 40.5   40.8 / 45.5   77.9 / 84.4
+// At d = 64 a step has half the products for the same exponents, which are what
+// bounds it, so the persistent form's other gains show late and not over long contexts.
+bool wide_form(const CrossGeom& g) {
+  const int64_t tiles = static_cast<int64_t>(g.B) * g.H * g.Mq;
+  return g.d == 128 ? tiles > kFwdCtasPerSm * kSMs : tiles > 4 * kSMs && g.M <= 768;
+}
 
-constexpr int kWideTiles = 2 * kSMs;
+}  // namespace
 
 size_t cross_fwd_workspace_bytes(const CrossGeom& g) {
   const int parts = fwd_parts(g);
@@ -504,7 +528,7 @@ size_t cross_fwd_workspace_bytes(const CrossGeom& g) {
 
 cudaError_t launch_cross_fwd(const CrossGeom& g, const sparge_cross& a, void* workspace,
                              cudaStream_t st) {
-  if (static_cast<int64_t>(g.B) * g.H * g.Mq >= kWideTiles) return launch_cross_fwd_wide(g, a, st);
+  if (wide_form(g)) return launch_cross_fwd_wide(g, a, st);
   return g.d == 128 ? launch_fwd_impl<128>(g, a, workspace, st)
                     : launch_fwd_impl<64>(g, a, workspace, st);
 }

@@ -2,15 +2,14 @@
 // softmax(scale Q K^T) V, the first kv_len[b] of M keys valid.
 //
 // Persistent, one CTA an SM.  A CTA works on two tiles of 128 queries that read the
-// same keys (of one head, or of two heads of a group) in steps of 128 keys: while the
-// softmax of one tile runs, the tensor cores work on the other's, so each tile needs one
-// S tile in tensor memory only (2 x 128 columns, and 2 x d for the outputs: all 512).
-// A warp to a tile issues its products, PV(t) and then S(t + 1), where step t + 1 after
-// an item's last is the next item's first: the pipe does not drain between items, whose
-// queries come into a second buffer meanwhile.  A thread's products run in their order
-// and a commit stands for all of them so far, so S(t + 1) takes the place of P(t), and
-// its being there means that PV(t) is.  (One warp for both tiles spent 4600 cycles a
-// step on issuing 2080 cycles of products.)
+// same keys (of one head, or of two heads of a group) in steps of 64 keys, with two S
+// tiles to each (4 x 64 columns of tensor memory, and 2 x d for the outputs: all 512 at
+// d = 128).  A warp to a tile issues its products, S two steps ahead of PV, where the
+// step after an item's last is the next item's first: the pipe does not drain between
+// items, whose queries come into a second buffer meanwhile.  A thread's products run in
+// their order and a commit stands for all of them so far, so S(t + 2) takes the place of
+// P(t), and its being there means that PV(t) is.  (One warp for both tiles spent 4600
+// cycles a step of 128 keys on issuing 2080 cycles of products.)
 //
 // Softmax (a thread to a row): the exponents are taken against the maximum that the row
 // had before the step, in one pass over the step's scores, which also finds whether one
