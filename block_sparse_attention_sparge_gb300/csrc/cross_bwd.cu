@@ -988,11 +988,24 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     bool ok = true;
-    int g = 0, j = 0;
-    for (int seq = 0;; ++seq) {
-      const int it = next_item(seq, ok);
+    int g = 0, seq = 0;
+    // The next item, its log-sum-exp and D on their way while this one's epilogue runs
+    // (480p 390 -> 373 us for the whole backward).
+    int it;
+    float lse, delta;
+    auto fetch = [&] {
+      it = next_item(seq, ok);
       __syncwarp();
       if (lane == 0) release_item(seq);
+      ++seq;
+      if (it < 0) return;
+      const int rest = it / p.q_parts, n = rest % p.g.Mq * kBM + r;
+      const int64_t stat = static_cast<int64_t>(rest / p.g.Mq) * N + n;
+      lse = n < N ? __ldg(p.lse + stat) : 0.f;
+      delta = n < N ? __ldg(p.delta + stat) : 0.f;
+    };
+    fetch();
+    while (true) {
       if (it < 0) {
         if (it == -2) ok = false;
         break;
@@ -1016,11 +1029,10 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
             }
           }
         }
+        fetch();
         continue;
       }
-      const int64_t stat = (static_cast<int64_t>(x.b) * p.g.H + x.h) * N + row;
-      const float lse2 = rv ? __ldg(p.lse + stat) * kLog2e : 0.f;
-      const float drow = rv ? __ldg(p.delta + stat) : 0.f;
+      const float lse2 = lse * kLog2e, drow = delta;
       for (int u = 0; ok && u < x.n; ++u, ++g) {
         const int b = g & 1;
         // Valid keys among this thread's 32 (warp-uniform).
@@ -1078,6 +1090,7 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
         mbar_arrive(bar(C::B_DSF + 4 * b + cg));
       }
       if (!ok) break;
+      fetch();
       // Epilogue: read this warp's dQ columns, release the accumulator to the
       // next q-block's dQ MMAs, then scale, convert and store.
       const int gl = g - 1;
@@ -1093,7 +1106,6 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
       for (int c = 0; c < D / 4; c += 16) SPARGE_TMEM_WAIT_LD16((ro + c));
       tc_fence_before();
       mbar_arrive(bar(C::B_DQE));
-      ++j;
       if (rv && split) {
 #pragma unroll
         for (int c = 0; c < D / 4; c += 4)
@@ -1148,6 +1160,7 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(const __grid_constant__ 
   const float* src = (keys ? p.k_part : p.q_part) + (tile * parts * kPair + n % kPair) * width +
                      which * D + c;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int q = 0; q < parts; ++q) {
     const float4* s = reinterpret_cast<const float4*>(src + static_cast<int64_t>(q) * kPair * width);
     const float4 x = __ldcg(s), y = __ldcg(s + 1);

@@ -521,8 +521,8 @@ typedef struct sparge_ortho {
                               runs out */
 } sparge_ortho;
 
-/* Workspace: X, A and B of as many matrices as are worked on at once.  Sizes alone
- * decide. */
+/* Workspace: X, A and B of as many matrices as are worked on at once, partial sums
+ * of A where sides are long and matrices few.  Sizes and `half` alone decide. */
 int sparge_orthogonalize_workspace_bytes(const sparge_ortho* args, size_t* bytes);
 
 /*
