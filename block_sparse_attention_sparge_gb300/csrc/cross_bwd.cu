@@ -20,37 +20,50 @@ constexpr int kBM = kCrossQ;    // queries of a tile
 constexpr int kPair = kCrossK;  // keys of a tile
 
 // ---------------------------------------------------------------- D = rowsum(dO * O)
-// D / 8 threads to a row, 16-byte streaming loads.  The first CTA also starts the
-// item counters of the gradient kernels at zero.
+// D / 8 threads to a row, kDeltaRows rows of a head to a thread with all their 16-byte
+// loads in flight; one division finds a CTA's head (a row to a thread, found by 64-bit
+// divisions: 41 us at 480p, and 34).  The first CTA also starts the item counters of the
+// gradient kernels at zero.
+constexpr int kDeltaRows = 4;
 template <int D>
 __global__ void __launch_bounds__(256) cross_delta_kernel(HeadsView o, HeadsView dout, int H, int N,
-                                                          int64_t rows, float* __restrict__ delta,
+                                                          int blocks,  // of a head
+                                                          float* __restrict__ delta,
                                                           int32_t* __restrict__ work) {
   constexpr int CH = D / 8;      // 16-byte pieces of a row
-  constexpr int RPB = 256 / CH;  // rows of a CTA
+  constexpr int RPB = 256 / CH;  // rows that a CTA takes at a time
   if (blockIdx.x == 0 && threadIdx.x < 2) work[threadIdx.x] = 0;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / CH;
+  const unsigned bh = blockIdx.x / static_cast<unsigned>(blocks), b = bh / static_cast<unsigned>(H);
+  const int64_t h = bh - b * static_cast<unsigned>(H);
+  const int first = static_cast<int>(blockIdx.x - bh * blocks) * (RPB * kDeltaRows) + threadIdx.x / CH;
   const int c = threadIdx.x % CH;
-  float s = 0.f;
-  if (r < rows) {
-    const int64_t bh = r / N, n = r - bh * N, b = bh / H, h = bh - b * H;
-    auto at = [&](const HeadsView& v) {
-      return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(v.p) + b * v.sb +
-                                            h * v.sh + n * v.sn) + c;
-    };
-    const uint4 x = ldg_no_l1(at(o)), y = ldg_no_l1(at(dout));
-    const __nv_bfloat162* hx = reinterpret_cast<const __nv_bfloat162*>(&x);
-    const __nv_bfloat162* hy = reinterpret_cast<const __nv_bfloat162*>(&y);
+  auto at = [&](const HeadsView& v, int n) {
+    return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(v.p) + b * v.sb +
+                                          h * v.sh + n * v.sn) + c;
+  };
+  uint4 x[kDeltaRows], y[kDeltaRows];
+#pragma unroll
+  for (int i = 0; i < kDeltaRows; ++i) {
+    const int n = first + i * RPB;
+    x[i] = n < N ? ldg_no_l1(at(o, n)) : make_uint4(0u, 0u, 0u, 0u);
+    y[i] = n < N ? ldg_no_l1(at(dout, n)) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < kDeltaRows; ++i) {
+    const __nv_bfloat162* hx = reinterpret_cast<const __nv_bfloat162*>(&x[i]);
+    const __nv_bfloat162* hy = reinterpret_cast<const __nv_bfloat162*>(&y[i]);
+    float s = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 fx = __bfloat1622float2(hx[e]), fy = __bfloat1622float2(hy[e]);
       s = fmaf(fx.x, fy.x, s);
       s = fmaf(fx.y, fy.y, s);
     }
-  }
 #pragma unroll
-  for (int off = CH / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  if (c == 0 && r < rows) delta[r] = s;
+    for (int off = CH / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    const int n = first + i * RPB;
+    if (c == 0 && n < N) delta[static_cast<int64_t>(bh) * N + n] = s;
+  }
 }
 
 // Loads 32 consecutive fp32 TMEM columns of this thread's lane.
@@ -1139,12 +1152,13 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
 }
 
 // Sums of the parts, in their order: dV | dK of the key tiles, dQ of the query
-// tiles.  A thread takes eight values of a row.
+// tiles.  A thread takes eight values of a row; there are parts only where tiles are few
+// for the machine, so 32 bits count the threads.
 template <int D>
 __global__ void __launch_bounds__(256) cross_sum_kernel(const __grid_constant__ CrossBwdParams p,
-                                                        int64_t key_work, int64_t query_work) {
-  constexpr int TPR = D / 8;
-  int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+                                                        uint32_t key_work, uint32_t query_work) {
+  constexpr uint32_t TPR = D / 8;
+  uint32_t i = blockIdx.x * 256u + threadIdx.x;
   if (i >= key_work + query_work) return;
   const bool keys = i < key_work;
   if (!keys) i -= key_work;
@@ -1152,10 +1166,11 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(const __grid_constant__ 
   i /= TPR;
   const int which = keys ? static_cast<int>(i & 1) : 0;  // dV, dK
   if (keys) i >>= 1;
-  const int len = keys ? p.g.M : p.g.N, heads = keys ? p.g.Hk : p.g.H;
+  const uint32_t len = keys ? p.g.M : p.g.N, heads = keys ? p.g.Hk : p.g.H;
   const int tiles = keys ? p.g.Mt : p.g.Mq, parts = keys ? p.k_parts : p.q_parts;
-  const int64_t bh = i / len, n = i - bh * len, b = bh / heads, h = bh - b * heads;
-  const int64_t tile = bh * tiles + n / kPair;
+  const uint32_t bh = i / len;
+  const int64_t n = i - bh * len, b = bh / heads, h = bh % heads;
+  const int64_t tile = static_cast<int64_t>(bh) * tiles + n / kPair;
   const int width = keys ? 2 * D : D;
   const float* src = (keys ? p.k_part : p.q_part) + (tile * parts * kPair + n % kPair) * width +
                      which * D + c;
@@ -1249,9 +1264,9 @@ cudaError_t launch_bwd_impl(const CrossGeom& g, const sparge_cross& a, void* wor
       make_tmap_bf16_4d(&tv, a.v, g.Bk, g.Hk, g.M, D, a.v_stride, kPair) != 0)
     return cudaErrorInvalidValue;
 
-  const int64_t rows = static_cast<int64_t>(g.B) * g.H * g.N, per = 256 / (D / 8);
-  cross_delta_kernel<D><<<static_cast<unsigned>((rows + per - 1) / per), 256, 0, st>>>(
-      view(a.o, a.o_stride), view(a.dout, a.dout_stride), g.H, g.N, rows, delta, p.work);
+  const int per = 256 / (D / 8) * kDeltaRows, blocks = (g.N + per - 1) / per;
+  cross_delta_kernel<D><<<static_cast<unsigned>(g.B) * g.H * blocks, 256, 0, st>>>(
+      view(a.o, a.o_stride), view(a.dout, a.dout_stride), g.H, g.N, blocks, delta, p.work);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
@@ -1286,10 +1301,11 @@ cudaError_t launch_bwd_impl(const CrossGeom& g, const sparge_cross& a, void* wor
   if (e != cudaSuccess) return e;
 
   const int64_t key_work = p.k_parts > 1 ? static_cast<int64_t>(g.Bk) * g.Hk * g.M * 2 * (D / 8) : 0;
-  const int64_t query_work = p.q_parts > 1 ? rows * (D / 8) : 0;
+  const int64_t query_work =
+      p.q_parts > 1 ? static_cast<int64_t>(g.B) * g.H * g.N * (D / 8) : 0;
   if (key_work + query_work == 0) return cudaSuccess;
   cross_sum_kernel<D><<<static_cast<unsigned>((key_work + query_work + 255) / 256), 256, 0, st>>>(
-      p, key_work, query_work);
+      p, static_cast<uint32_t>(key_work), static_cast<uint32_t>(query_work));
   return cudaGetLastError();
 }
 
