@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtasPerSm)
     const bool have = ok && n > 0 && warp_wait(bar(C::B_PV + ((n - 1) & 1)), ((n - 1) >> 1) & 1);
     if (ok && n > 0 && !have) report_error(status, SPARGE_ERR_TIMEOUT);
     tc_fence_after();
-    const bool good = have && l > 0.f;
+    const bool good = have && !(l <= 0.f);  // (a sum that is NaN stays one)
     const float inv_l = good ? 1.f / l : 0.f;
     const bool in_range = row < N;
     const bool split = p.parts > 1;
@@ -426,9 +426,14 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
   const int64_t item = bh * p.g.Mq + row / kBM;
   const int64_t first = item * p.parts * kBM + row % kBM;
   float top = -INFINITY;
-  for (int i = 0; i < p.parts; ++i) top = fmaxf(top, __ldg(p.l_part + first + i * kBM));
+  bool some = false;  // parts with keys; NaN, which the maximum leaves out, is one
+  for (int i = 0; i < p.parts; ++i) {
+    const float l = __ldg(p.l_part + first + i * kBM);
+    top = fmaxf(top, l);
+    some |= !(l <= -INFINITY);
+  }
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-  if (top > -INFINITY) {
+  if (some) {
     for (int i = 0; i < p.parts; ++i) {
       const float w = exp2f(__ldg(p.l_part + first + i * kBM) - top);
       const float4* src =
@@ -441,14 +446,14 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
       acc[6] = fmaf(w, b.z, acc[6]), acc[7] = fmaf(w, b.w, acc[7]);
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum <= 0.f ? 0.f : 1.f / sum;
   const int64_t b = bh / p.g.H, h = bh - b * p.g.H;
   __nv_bfloat16* out =
       static_cast<__nv_bfloat16*>(p.o.p) + b * p.o.sb + h * p.o.sh + row * p.o.sn + c;
   *reinterpret_cast<uint4*>(out) =
       make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
                  pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
-  if (c == 0 && p.lse != nullptr) p.lse[at] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  if (c == 0 && p.lse != nullptr) p.lse[at] = sum <= 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // Parts of a query tile's keys: one, unless the tiles fill less than half of the

@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++done[i];
         tc_fence_after();
         const float2 ml = stats[i * kBM + r];
-        const bool good = ml.y > 0.f;
+        const bool good = !(ml.y <= 0.f);  // (a sum that is NaN stays one)
         const float inv = good ? 1.f / ml.y : 0.f;
         // The output goes where the tile's queries were, and from there to memory.
         const uint32_t stage = C::off_q + (2 * qb + i) * C::kQ;
