@@ -424,7 +424,8 @@ struct DkdvCfg {
   static constexpr int B_DKE = B_RKF + 2;     // all compute threads: dV, dK read out
   static constexpr int B_IF = B_DKE + 1;      // NRING: key tile handed out
   static constexpr int B_IE = B_IF + NRING;   // NRING: read by both issuers and every compute warp
-  static constexpr int B_DONE = B_IE + NRING; // count 2
+  static constexpr int B_ACC = B_IE + NRING;  // every gradient MMA of a key tile done
+  static constexpr int B_DONE = B_ACC + 1;    // count 2
   static constexpr int NBAR = B_DONE + 1;
   static constexpr uint32_t off_slot = off_bar + NBAR * 8;
   static constexpr uint32_t bytes = off_slot + 16;
@@ -792,6 +793,8 @@ __global__ void __launch_bounds__(Roles<kDkdvWarps>::kThreads, 1)
           warp_commit(bar(C::B_QE + sl));
         }
       }
+      if (!ok) break;
+      warp_commit(bar(C::B_ACC));
       ++j;
     }
     if (!ok && lane == 0) report_error(status, SPARGE_ERR_TIMEOUT);
@@ -810,7 +813,7 @@ __global__ void __launch_bounds__(Roles<kDkdvWarps>::kThreads, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int flag_bit = r < kBN ? 1 : 2;  // warp-uniform (quarters 0-1 vs 2-3)
     bool ok = true;
-    int t = 0;
+    int t = 0, j = 0;  // entries and tiles with work so far
     for (int seq = 0;; ++seq) {
       int n = 0, pw = 0;
       const int it = next_tile(seq, ok, &n, &pw);
@@ -977,15 +980,11 @@ __global__ void __launch_bounds__(Roles<kDkdvWarps>::kThreads, 1)
       if (!ok) break;
       // Epilogue: lane r holds key r of dV and dK; warp group cg writes its
       // share of the features, then releases the accumulators to the next
-      // tile's first MMAs.  Every gradient MMA of the tile is done once dK of
-      // the last entry's second half is (the pipe runs them in order).  The
-      // warps of the first half get here as soon as their own last half is
-      // done, when that barrier may still be one phase short of the last
-      // entry's previous phase (its dP^T had to wait only for the one before),
-      // so the wait takes the previous phase first: a parity wait is exact
-      // only within one phase of the barrier.
-      if ((t >= 2 && !warp_wait(bar(C::B_RKF + 1), (t - 2) & 1)) ||
-          !warp_wait(bar(C::B_RKF + 1), (t - 1) & 1)) {
+      // tile's first MMAs.  A barrier of its own says that the tile's gradient MMAs are
+      // done: one phase a tile, each waited for by every warp.  (The halves' barriers
+      // would not do: a warp may come here one phase before the last entry's, or when
+      // that is over already, and a parity cannot tell these apart.)
+      if (!warp_wait(bar(C::B_ACC), j++ & 1)) {
         ok = false;
         break;
       }
