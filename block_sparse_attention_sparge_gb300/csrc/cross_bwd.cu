@@ -122,7 +122,8 @@ struct DkdvCfg {
   static constexpr int B_DKE = B_RKF + 2;     // all compute threads: dV, dK read out
   static constexpr int B_IF = B_DKE + 1;      // NRING: key tile handed out
   static constexpr int B_IE = B_IF + NRING;   // NRING: read by both issuers and every compute warp
-  static constexpr int B_DONE = B_IE + NRING; // count 2
+  static constexpr int B_ACC = B_IE + NRING;  // every gradient MMA of a key tile done
+  static constexpr int B_DONE = B_ACC + 1;    // count 2
   static constexpr int NBAR = B_DONE + 1;
   static constexpr uint32_t off_slot = off_bar + NBAR * 8;
   static constexpr uint32_t bytes = off_slot + 16;
@@ -144,7 +145,7 @@ struct DkdvCfg {
 struct CrossBwdParams {
   CrossGeom g;
   const float* lse;
-  const float* delta;  // [B, H, N]
+  float* delta;        // [B, H, N]
   int32_t* work;       // item counters: dQ, dK/dV
   HeadsView dq, dk, dv;
   int q_parts;         // of a query tile's keys
@@ -458,6 +459,8 @@ __global__ void __launch_bounds__(Roles<kDkdvWarps>::kThreads, 1)
           warp_commit(bar(C::B_QE + sl));
         }
       }
+      if (!ok) break;
+      warp_commit(bar(C::B_ACC));
       ++j;
     }
     if (!ok && lane == 0) report_error(status, SPARGE_ERR_TIMEOUT);
@@ -475,7 +478,7 @@ __global__ void __launch_bounds__(Roles<kDkdvWarps>::kThreads, 1)
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     bool ok = true;
-    int t = 0;
+    int t = 0, j = 0;  // entries and tiles with work so far
     for (int seq = 0;; ++seq) {
       int n = 0;
       const int it = next_tile(seq, ok, &n);
@@ -618,15 +621,11 @@ __global__ void __launch_bounds__(Roles<kDkdvWarps>::kThreads, 1)
       if (!ok) break;
       // Epilogue: lane r holds key r of dV and dK; warp group cg writes its
       // share of the features, then releases the accumulators to the next
-      // tile's first MMAs.  Every gradient MMA of the tile is done once dK of
-      // the last entry's second half is (the pipe runs them in order).  The
-      // warps of the first half get here as soon as their own last half is
-      // done, when that barrier may still be one phase short of the last
-      // entry's previous phase (its dP^T had to wait only for the one before),
-      // so the wait takes the previous phase first: a parity wait is exact
-      // only within one phase of the barrier.
-      if ((t >= 2 && !warp_wait(bar(C::B_RKF + 1), (t - 2) & 1)) ||
-          !warp_wait(bar(C::B_RKF + 1), (t - 1) & 1)) {
+      // tile's first MMAs.  A barrier of its own says that the tile's gradient MMAs are
+      // done: one phase a tile, each waited for by every warp.  (The halves' barriers
+      // would not do: a warp may come here one phase before the last entry's, or when
+      // that is over already, and a parity cannot tell these apart.)
+      if (!warp_wait(bar(C::B_ACC), j++ & 1)) {
         ok = false;
         break;
       }
@@ -702,7 +701,8 @@ struct DqCfg {
   static constexpr uint32_t off_do = off_q + kQ;
   static constexpr uint32_t off_k = off_do + kQ;        // NSK slots of K
   static constexpr uint32_t off_v = off_k + NSK * kKP;  // NSV slots of V
-  static constexpr uint32_t off_ring = off_v + NSV * kKP;  // NRING q-block ids
+  static constexpr uint32_t off_sum = off_v + NSV * kKP;   // 4 x {sum of P dP [128]}
+  static constexpr uint32_t off_ring = off_sum + 4 * kBM * 4;  // NRING q-block ids
   static constexpr uint32_t off_bar = off_ring + 64;
   static constexpr int B_Q = 0;            // Q, dO of a q-block landed
   static constexpr int B_QE = 1;           // its S and dP MMAs done: Q, dO slots free
@@ -718,11 +718,14 @@ struct DqCfg {
   static constexpr int B_DQE = B_DPE + 1;  // all compute threads: dQ accumulator read out
   static constexpr int B_IF = B_DQE + 1;   // NRING: q-block id written
   static constexpr int B_IE = B_IF + NRING;  // NRING: id read by both issuers and every compute warp
-  static constexpr int B_DONE = B_IE + NRING;  // count 2
+  static constexpr int B_DS = B_IE + NRING;  // every compute warp: sums of P dP written
+  static constexpr int B_DR = B_DS + 1;      // every compute warp: and read
+  static constexpr int B_DONE = B_DR + 1;    // count 2
   static constexpr int NBAR = B_DONE + 1;
   static constexpr uint32_t off_slot = off_bar + NBAR * 8;
   static constexpr uint32_t bytes = off_slot + 16;
-  static constexpr uint32_t smem_alloc = bytes + 1024;
+  // (Starts 1024-byte aligned, see above.)
+  static constexpr uint32_t smem_alloc = bytes;
   // TMEM: dQ [0, D), S of step g in buffer g % 2 at 128 + 128 * (g % 2) (128
   // keys; dS of keys 32c .. 32c + 31 written over its columns 32c .. 32c + 15
   // as bf16 pairs), dP at 384.
@@ -739,7 +742,15 @@ struct DqCfg {
 // the next item overlap the current one's last steps and epilogue.  The
 // steps of successive items share one running step count g, which indexes
 // the slot rings and barrier phases.
-template <int D>
+// OWN: the context is one key tile, so a step has all keys of its rows and D is summed
+// here as sum_j P dP, in fp32, and written for the dK/dV kernel, which runs after this
+// one; O is not read.  With few keys O is as large as V, and what its rounding does to D
+// is what dQ and dK are off by beside the roundings of dS and of the result: in the 2-norm
+// 0.0038 with 2 keys, 0.0026 with 10, 0.0025 with 30, 0.0024 with 100; summed here 0.0024
+// throughout.  It costs a longer chain and the overlap of the two kernels (30000 queries
+// of 12 heads: 163 -> 185 us at d = 128, 121 -> 145 at d = 64), so up to kOwnKeys keys.
+constexpr int kOwnKeys = 64;
+template <int D, bool OWN>
 __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
     cross_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -748,10 +759,13 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
   using R = Roles<kDqWarps>;
   int32_t* status = p.status;
   const int N = p.g.N;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw;
   const uint32_t s0 = smem_u32(sm);
+  if ((s0 & 1023u) != 0u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) report_error(status, SPARGE_ERR_CUDA);
+    return;
+  }
   auto bar = [&](int i) -> uint32_t { return s0 + C::off_bar + 8u * i; };
   uint32_t* slot = reinterpret_cast<uint32_t*>(sm + C::off_slot);
   volatile int32_t* ring = reinterpret_cast<volatile int32_t*>(sm + C::off_ring);
@@ -764,6 +778,7 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
       if (i == C::B_DPE || i == C::B_DQE) cnt = 32 * R::kCompute;
       if (i >= C::B_DSF && i < C::B_DSF + 8) cnt = 32 * (R::kCompute / 4);
       if (i >= C::B_IE && i < C::B_IE + C::NRING) cnt = 2 + R::kCompute;
+      if (i == C::B_DS || i == C::B_DR) cnt = R::kCompute;
       if (i == C::B_DONE) cnt = 2;
       mbar_init(bar(i), cnt);
     }
@@ -1005,7 +1020,9 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
     // The next item, its log-sum-exp and D on their way while this one's epilogue runs
     // (480p 390 -> 373 us for the whole backward).
     int it;
-    float lse, delta;
+    float lse, delta = 0.f;
+    int items = 0;  // that summed D
+    float* sums = reinterpret_cast<float*>(sm + C::off_sum);
     auto fetch = [&] {
       it = next_item(seq, ok);
       __syncwarp();
@@ -1015,7 +1032,7 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
       const int rest = it / p.q_parts, n = rest % p.g.Mq * kBM + r;
       const int64_t stat = static_cast<int64_t>(rest / p.g.Mq) * N + n;
       lse = n < N ? __ldg(p.lse + stat) : 0.f;
-      delta = n < N ? __ldg(p.delta + stat) : 0.f;
+      if constexpr (!OWN) delta = n < N ? __ldg(p.delta + stat) : 0.f;
     };
     fetch();
     while (true) {
@@ -1045,7 +1062,8 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
         fetch();
         continue;
       }
-      const float lse2 = lse * kLog2e, drow = delta;
+      const float lse2 = lse * kLog2e;
+      float drow = delta;
       for (int u = 0; ok && u < x.n; ++u, ++g) {
         const int b = g & 1;
         // Valid keys among this thread's 32 (warp-uniform).
@@ -1064,6 +1082,33 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
         const uint32_t sb = lane_base + C::col_s + 128 * b + 32 * cg;
         tmem_ld32u(sb, sr, sr2);
         uint32_t pk[16];
+        if constexpr (OWN) {
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float pe = ex2_approx(
+                fmaf(__uint_as_float(e < 16 ? sr[e] : sr2[e - 16]), p.scale_log2, -lse2));
+            sum += e < valid ? pe * __uint_as_float(e < 16 ? dr[e] : dr2[e - 16]) : 0.f;
+          }
+          // (the last item's sums were read by all)
+          if (items > 0 && !warp_wait(bar(C::B_DR), (items - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          sums[cg * kBM + r] = sum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_DS));
+          if (!warp_wait(bar(C::B_DS), items & 1)) {
+            ok = false;
+            break;
+          }
+          drow = (sums[r] + sums[kBM + r]) + (sums[2 * kBM + r] + sums[3 * kBM + r]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_DR));
+          ++items;
+          if (cg == 0 && rv)
+            p.delta[(static_cast<int64_t>(x.b) * p.g.H + x.h) * N + row] = drow;
+        }
         if (rv && valid == 32) {
           // Two columns per packed instruction: P = 2^(S * scale*log2e - lse*log2e),
           // dS = P * (dP - D).
@@ -1264,40 +1309,52 @@ cudaError_t launch_bwd_impl(const CrossGeom& g, const sparge_cross& a, void* wor
       make_tmap_bf16_4d(&tv, a.v, g.Bk, g.Hk, g.M, D, a.v_stride, kPair) != 0)
     return cudaErrorInvalidValue;
 
-  const int per = 256 / (D / 8) * kDeltaRows, blocks = (g.N + per - 1) / per;
-  cross_delta_kernel<D><<<static_cast<unsigned>(g.B) * g.H * blocks, 256, 0, st>>>(
-      view(a.o, a.o_stride), view(a.dout, a.dout_stride), g.H, g.N, blocks, delta, p.work);
-  cudaError_t e = cudaGetLastError();
+  // Few keys: D is the dQ kernel's, which runs first.
+  const bool own = g.M <= kOwnKeys;
+  cudaError_t e;
+  if (own) {
+    e = cudaMemsetAsync(p.work, 0, 2 * sizeof(int32_t), st);
+  } else {
+    const int per = 256 / (D / 8) * kDeltaRows, blocks = (g.N + per - 1) / per;
+    cross_delta_kernel<D><<<static_cast<unsigned>(g.B) * g.H * blocks, 256, 0, st>>>(
+        view(a.o, a.o_stride), view(a.dout, a.dout_stride), g.H, g.N, blocks, delta, p.work);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
 
   // Both gradient kernels are persistent: one CTA per SM (or per item when there
   // are fewer), taking items from their counters.
-  const int k_items = g.Bk * g.Hk * g.Mt * p.k_parts;
-  e = cudaFuncSetAttribute(cross_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           DkdvCfg<D>::smem_alloc);
+  auto run_dkdv = [&]() -> cudaError_t {
+    const int k_items = g.Bk * g.Hk * g.Mt * p.k_parts;
+    const cudaError_t r = cudaFuncSetAttribute(
+        cross_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::smem_alloc);
+    if (r != cudaSuccess) return r;
+    cross_dkdv_kernel<D><<<std::min(k_items, kSMs), Roles<kDkdvWarps>::kThreads,
+                           DkdvCfg<D>::smem_alloc, st>>>(tq64, tk, tv, tdo64, p, k_items);
+    return cudaGetLastError();
+  };
+  auto run_dq = [&](auto* kernel) -> cudaError_t {
+    const int q_items = g.B * g.H * g.Mq * p.q_parts;
+    const cudaError_t r = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::smem_alloc);
+    if (r != cudaSuccess) return r;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(std::min(q_items, kSMs));
+    cfg.blockDim = dim3(Roles<kDqWarps>::kThreads);
+    cfg.dynamicSmemBytes = DqCfg<D>::smem_alloc;
+    cfg.stream = st;
+    // Programmatic dependent launch: the dQ CTAs may start while the last dK/dV
+    // CTAs run (D and the counters were complete before dK/dV started).
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = own ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, tdo, p, q_items);
+  };
+  e = own ? run_dq(cross_dq_kernel<D, true>) : run_dkdv();
   if (e != cudaSuccess) return e;
-  cross_dkdv_kernel<D><<<std::min(k_items, kSMs), Roles<kDkdvWarps>::kThreads,
-                         DkdvCfg<D>::smem_alloc, st>>>(tq64, tk, tv, tdo64, p, k_items);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-
-  // Programmatic dependent launch: the dQ CTAs may start while the last dK/dV
-  // CTAs run (D and the counters were complete before dK/dV started).
-  const int q_items = g.B * g.H * g.Mq * p.q_parts;
-  e = cudaFuncSetAttribute(cross_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           DqCfg<D>::smem_alloc);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min(q_items, kSMs));
-  cfg.blockDim = dim3(Roles<kDqWarps>::kThreads);
-  cfg.dynamicSmemBytes = DqCfg<D>::smem_alloc;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, cross_dq_kernel<D>, tq, tk, tv, tdo, p, q_items);
+  e = own ? run_dkdv() : run_dq(cross_dq_kernel<D, false>);
   if (e != cudaSuccess) return e;
 
   const int64_t key_work = p.k_parts > 1 ? static_cast<int64_t>(g.Bk) * g.Hk * g.M * 2 * (D / 8) : 0;
