@@ -332,7 +332,10 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtasPerSm)
       // Eight partial row sums held as four packed pairs; the exponent
       // arguments two columns per packed FMA.
       const uint64_t sl2 = f32x2(scale_log2, scale_log2);
-      const uint64_t nm2 = f32x2(-m_used, -m_used);
+      // (Against a maximum of -inf, scores of -inf would have NaN for 0: any finite
+      // reference will do until there is a score.)
+      const float ref = m_used == -INFINITY ? 0.f : m_used;
+      const uint64_t nm2 = f32x2(-ref, -ref);
       uint64_t rs2[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) rs2[e] = f32x2(0.f, 0.f);

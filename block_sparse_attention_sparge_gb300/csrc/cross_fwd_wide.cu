@@ -15,7 +15,9 @@
 // had before the step, in one pass over the step's scores, which also finds whether one
 // of them passes it by more than 2^8.  Only then (and in the first step) the maximum
 // moves, sum and output are rescaled and the pass is repeated; the results are exact
-// either way, because sum and output share the reference.
+// either way, because sum and output share the reference.  A maximum of -inf (all scores
+// so far) stands for no reference: the pass takes 0, and moves to the first score that is
+// there, however small.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -431,7 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint32_t pk[32];
         for (int pass = 0;; ++pass) {
-          const uint64_t nm2 = f32x2(-m, -m);
+          const bool none = m == -INFINITY;
+          const float ref = none ? 0.f : m;
+          const uint64_t nm2 = f32x2(-ref, -ref);
           uint64_t rs[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
           float top[2] = {-INFINITY, -INFINITY};
           uint32_t s[2][16];
@@ -461,14 +465,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Decided for the whole warp: tensor memory is read and written by warps.  One
           // repetition is enough, and all there is: scores past 2^30 or so could not move
           // the reference by their distance to it.
-          if (pass > 0 || !__any_sync(0xffffffffu, over > kSlack)) {
+          const bool move = over > (none ? -INFINITY : kSlack);
+          if (pass > 0 || !__any_sync(0xffffffffu, move)) {
             const uint64_t sum = fadd2(rs[0], rs[1]);
             l += f32x2_lo(sum) + f32x2_hi(sum);
             break;
           }
-          const float up = over > kSlack ? over : 0.f;
-          const float alpha = exp2f(-up);
-          m += up;
+          const float up = move ? over : 0.f;
+          const float alpha = none ? 1.f : exp2f(-up);  // (1 for a sum and an output of 0)
+          if (move) m = ref + up;
           l *= alpha;
           if (t > 0) {
             // O holds the steps before this one once the last of them is done.  (S of

@@ -430,7 +430,9 @@ int sparge_clip_grads(const sparge_tensor* grads, void* const* out, int32_t n, f
  *   LSE = log sum exp S,  O = exp(S - LSE) V.
  * All tensors are bf16 [batch, heads, tokens, d], d contiguous, with strides of
  * their own: as the attention lays them out or as projections do ([batch, tokens,
- * heads, d]).  Query head h reads key head h / (H / Hk).
+ * heads, d]).  Query head h reads key head h / (H / Hk).  A score of -inf (also of
+ * products that leave fp32) leaves its key out, and a row of such scores alone is one
+ * without keys: O = 0, LSE = -inf.
  */
 typedef struct sparge_cross {
   int32_t B, Bk;           /* samples of Q; contexts: B, or 1 for all samples */
