@@ -66,6 +66,10 @@ __global__ void __launch_bounds__(256) cross_delta_kernel(HeadsView o, HeadsView
   }
 }
 
+// What is added to a row's scores for its probabilities' exponents: -lse * log2(e); -inf
+// for a row without keys (its scores, if any, are all -inf), whose probabilities are 0.
+SPARGE_DEV float minus_lse_log2(float lse) { return lse == -INFINITY ? lse : -lse * kLog2e; }
+
 // Loads 32 consecutive fp32 TMEM columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld32u(uint32_t addr, uint32_t (&a)[16], uint32_t (&b)[16]) {
   SPARGE_TMEM_LD_X16(addr, a);
@@ -324,8 +328,8 @@ __global__ void __launch_bounds__(Roles<kDkdvWarps>::kThreads, 1)
           // -inf and 0, so that their P and dS are 0).
           float2 l2, d2;
           const int tok = row0 + lane * 2;
-          l2.x = tok < N ? -__ldg(lse_h + tok) * kLog2e : -INFINITY;
-          l2.y = tok + 1 < N ? -__ldg(lse_h + tok + 1) * kLog2e : -INFINITY;
+          l2.x = tok < N ? minus_lse_log2(__ldg(lse_h + tok)) : -INFINITY;
+          l2.y = tok + 1 < N ? minus_lse_log2(__ldg(lse_h + tok + 1)) : -INFINITY;
           d2.x = tok < N ? -__ldg(del_h + tok) : 0.f;
           d2.y = tok + 1 < N ? -__ldg(del_h + tok + 1) : 0.f;
           float* rowv = reinterpret_cast<float*>(sm + C::off_row + sl * (2 * 64 * 4));
@@ -1062,7 +1066,7 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
         fetch();
         continue;
       }
-      const float lse2 = lse * kLog2e;
+      const float nlse2 = minus_lse_log2(lse);
       float drow = delta;
       for (int u = 0; ok && u < x.n; ++u, ++g) {
         const int b = g & 1;
@@ -1087,7 +1091,7 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const float pe = ex2_approx(
-                fmaf(__uint_as_float(e < 16 ? sr[e] : sr2[e - 16]), p.scale_log2, -lse2));
+                fmaf(__uint_as_float(e < 16 ? sr[e] : sr2[e - 16]), p.scale_log2, nlse2));
             sum += e < valid ? pe * __uint_as_float(e < 16 ? dr[e] : dr2[e - 16]) : 0.f;
           }
           // (the last item's sums were read by all)
@@ -1113,7 +1117,7 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
           // Two columns per packed instruction: P = 2^(S * scale*log2e - lse*log2e),
           // dS = P * (dP - D).
           const uint64_t sl2 = f32x2(p.scale_log2, p.scale_log2);
-          const uint64_t nl2 = f32x2(-lse2, -lse2);
+          const uint64_t nl2 = f32x2(nlse2, nlse2);
           const uint64_t nd2 = f32x2(-drow, -drow);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
@@ -1131,9 +1135,9 @@ __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float p0 = ex2_approx(
-                fmaf(__uint_as_float(e < 16 ? sr[e] : sr2[e - 16]), p.scale_log2, -lse2));
+                fmaf(__uint_as_float(e < 16 ? sr[e] : sr2[e - 16]), p.scale_log2, nlse2));
             const float p1 = ex2_approx(
-                fmaf(__uint_as_float(e < 16 ? sr[e + 1] : sr2[e - 15]), p.scale_log2, -lse2));
+                fmaf(__uint_as_float(e < 16 ? sr[e + 1] : sr2[e - 15]), p.scale_log2, nlse2));
             const float d_a = __uint_as_float(e < 16 ? dr[e] : dr2[e - 16]);
             const float d_b = __uint_as_float(e < 16 ? dr[e + 1] : dr2[e - 15]);
             // (V behind the length may hold NaN: 0, not 0 * dP.)

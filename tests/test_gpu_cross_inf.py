@@ -90,3 +90,25 @@ def test_masked_keys_under_a_negative_scale(k):
     got = B.sparge_cross_fwd(q, kk, v, softmax_scale=-0.1, check_status=True)
     out, lim = _reference(q, kk, v, do, mask, -0.1)
     check(got, out, lim, ("o", "lse"))
+
+
+@pytest.mark.parametrize("rows", ["all", "half"])
+@pytest.mark.parametrize("name", ["step", "every other step", "all but the last", "all"])
+@pytest.mark.parametrize("shape", SHAPES + [(1, 2, 150, 40, 64), (1, 1, 150, 64, 128)])
+def test_gradients_of_masked_keys(shape, name, rows):
+    """Rows whose keys are all masked add nothing to any gradient."""
+    (q, kk, v, do), mask = _make(shape, name, -1e30, 0.0, rows, 3)
+    o, lse = B.sparge_cross_fwd(q, kk, v)
+    got = B.sparge_cross_bwd(q, kk, v, o, lse, do, check_status=True)
+    out, lim = _reference(q, kk, v, do, mask)
+    # Channel 0 of dQ is -1e30 scale times the sum of dS over the masked keys. In a row that
+    # they are not masked for, that is minus the sum over the others (all of them add up to 0):
+    # with one other of 130 keys, 129 terms of the size of the one that is left, each rounded
+    # (2^-9 / sqrt(3), sqrt(129) of them), and D's rounding 129 times over: 0.01 and more of
+    # the result. So it has its bound alone, element by element, and no 2-norm beside it.
+    e = (got[0][..., 0].double() - out["dq"][..., 0]).abs()
+    assert (e <= lim["dq"][..., 0]).all()
+    check((got[0][..., 1:],), *({"dq": t["dq"][..., 1:]} for t in (out, lim)), ("dq",))
+    check(got[1:], out, lim, ("dk", "dv"))
+    alone = mask.all(-1)
+    assert (got[0][:, :, alone] == 0).all()
