@@ -389,6 +389,8 @@ class Muon(torch.optim.Optimizer):
     ``half`` (the default) takes the products in fp16, which leaves the update off by
     some 2^-9 of its size; None goes by the parameters' type."""
 
+    _HOW = ("lr", "momentum", "nesterov", "weight_decay", "rms", "steps", "half")
+
     def __init__(self, params, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,
                  weight_decay: float = 0.0, rms: float | None = None, steps: int = 5,
                  half: bool | None = True):
@@ -418,7 +420,7 @@ class Muon(torch.optim.Optimizer):
                 for at, t in zip(places.setdefault(p.device, ([], [], [])),
                                  (p, g, state["momentum"])):
                     at.append(t)
-            how = {k: v for k, v in group.items() if k != "params"}
+            how = {k: group[k] for k in self._HOW}  # (schedules and users add keys of their own)
             for weights, grads, momenta in places.values():
                 B.sparge_muon_step(weights, grads, momenta, **how)
         return loss
