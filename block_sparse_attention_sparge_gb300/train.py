@@ -353,6 +353,9 @@ def run_blocks(blocks, x, grid=None, modulation=None, context=None, kv_len=None)
     for cross in crosses:
         rows.append(None if cross else count)
         count += not cross
+    if modulation is not None and count < len(blocks) and modulation.shape[2] != count:
+        raise ValueError(f"expected a modulation of {count} rows: {count} blocks take one, those "
+                         "that attend to a context none")
 
     def mod(i, k):
         if modulation is None or rows[i] is None:
