@@ -176,6 +176,7 @@ _SIGNATURES = {
     "sparge_cross_bwd_workspace_bytes": ([_P, ctypes.POINTER(_SZ)], _I),
     "sparge_cross_bwd": ([_P, _P, _SZ, _P], _I),
     "sparge_orthogonalize_workspace_bytes": ([_P, ctypes.POINTER(_SZ)], _I),
+    "sparge_orthogonalize_check": ([_P], _I),
     "sparge_orthogonalize": ([_P, _P, _SZ, _P], _I),
     "sparge_status_copy_async": ([_P, _P, _P], _I),
     "sparge_read_status": ([_P, _P, ctypes.POINTER(ctypes.c_int32)], _I),
@@ -989,14 +990,28 @@ def _orthogonalize(grads, outs, momenta, factors, steps, coefficients, eps, mu, 
         rows[o.dtype is torch.bfloat16 if half is None else bool(half)].append(packed)
     lib = load_library()
     status = _cross_status(status, check_status, device)
-    for fast, part in rows.items():
-        if not part:
-            continue
+
+    def pack(part, fast):
         table = ctypes.create_string_buffer(b"".join(part))
-        args = _ORTHO.pack(ctypes.addressof(table), len(part), steps, a, b, c, eps, mu,
-                           bool(nesterov), factors is not None, fast, _addr(status))
-        ws, size, _hold = _workspace(lib.sparge_orthogonalize_workspace_bytes,
-                                     "sparge_orthogonalize", args, device, workspace)
+        return table, _ORTHO.pack(ctypes.addressof(table), len(part), steps, a, b, c, eps, mu,
+                                  bool(nesterov), factors is not None, fast, _addr(status))
+
+    calls = [pack(part, fast) for fast, part in rows.items() if part]
+    if len(calls) > 1:
+        # One list to its caller: refused, if at all, before the first of two calls. (With
+        # a workspace too small for either, that is the one that needs more.)
+        _table, args = pack(rows[False] + rows[True], False)
+        _check(lib.sparge_orthogonalize_check(args), where)
+        need = _SZ(0)
+
+        def bytes_of(call):
+            _check(lib.sparge_orthogonalize_workspace_bytes(call[1], ctypes.byref(need)), where)
+            return need.value
+
+        calls.sort(key=bytes_of, reverse=True)
+    ws, size, _hold = _workspace(lib.sparge_orthogonalize_workspace_bytes, "sparge_orthogonalize",
+                                 calls[0][1], device, workspace)
+    for _table, args in calls:
         _call(lib.sparge_orthogonalize, where, index, args, ws, size)
     if check_status:
         _finish(status, True, where)

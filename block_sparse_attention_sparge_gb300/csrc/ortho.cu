@@ -1425,6 +1425,12 @@ int sparge_orthogonalize_workspace_bytes(const sparge_ortho* args, size_t* bytes
   return SPARGE_OK;
 }
 
+int sparge_orthogonalize_check(const sparge_ortho* args) try {
+  return check_ortho(args);
+} catch (...) {  // no memory for the list on the host
+  return SPARGE_ERR_INVALID_ARG;
+}
+
 int sparge_orthogonalize(const sparge_ortho* args, void* workspace, size_t ws_bytes,
                          sparge_stream_t stream) try {
   ORTHO_TRY(check_ortho(args));

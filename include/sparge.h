@@ -527,6 +527,10 @@ typedef struct sparge_ortho {
  * of A where sides are long and matrices few.  Sizes and `half` alone decide. */
 int sparge_orthogonalize_workspace_bytes(const sparge_ortho* args, size_t* bytes);
 
+/* The checks of the call below but for its workspace's, on the host alone: for a list
+ * that is to be worked on in two calls, one of each form (`half`). */
+int sparge_orthogonalize_check(const sparge_ortho* args);
+
 /*
  * sparge_orthogonalize -- all matrices of a list at once: 3 + 3 * steps launches
  * for up to 64 matrices (of up to 2^27 values).  Matrices of which one is written
