@@ -176,13 +176,14 @@ SPARGE_DEV void store_x(uint8_t* tiles, int64_t tile, int64_t plane, int r, int 
 
 // --------------------------------------------------- the matrices themselves
 // Eight values of a row from column c on (0 behind the last); 16-byte loads where
-// the place allows them.
+// the place allows them.  (Not through the read-only path: a momentum is written by the kernel
+// before, which still runs when this one comes onto the machine, and a weight by this one.)
 template <typename T>
 SPARGE_DEV void read8(const T* row, int c, int cols, float (&f)[8]) {
   if (c + 8 <= cols && reinterpret_cast<uintptr_t>(row + c) % 16 == 0) {
     Raw8<T> r;
 #pragma unroll
-    for (int i = 0; i < pieces8<T>(); ++i) r.v[i] = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
+    for (int i = 0; i < pieces8<T>(); ++i) r.v[i] = reinterpret_cast<const uint4*>(row + c)[i];
     unpack8(r, f);
   } else {
 #pragma unroll
@@ -924,7 +925,7 @@ __global__ void __launch_bounds__(GemmCfg<CG, EXACT>::kThreads, 1)
           put_out(Y + x_plane + at_byte, kPlane, kPlane);
         } else {
           if constexpr (KIND == kSquare) {
-            const float d_row = __ldg(dA + row);
+            const float d_row = dA[row];
 #pragma unroll
             for (int ch = 0; ch < 8; ++ch) {
               float e[8];
@@ -935,8 +936,8 @@ __global__ void __launch_bounds__(GemmCfg<CG, EXACT>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) e[i] += lo[i];
               }
-              const float4 d0 = __ldg(reinterpret_cast<const float4*>(dA + col0 + 8 * ch));
-              const float4 d1 = __ldg(reinterpret_cast<const float4*>(dA + col0 + 8 * ch) + 1);
+              const float4 d0 = *reinterpret_cast<const float4*>(dA + col0 + 8 * ch);
+              const float4 d1 = *reinterpret_cast<const float4*>(dA + col0 + 8 * ch + 4);
               const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
 #pragma unroll
               for (int i = 0; i < 8; ++i)
@@ -949,7 +950,7 @@ __global__ void __launch_bounds__(GemmCfg<CG, EXACT>::kThreads, 1)
             for (int i = 0; i < 64; ++i) {
               if (col0 + i != row) continue;
               if constexpr (KIND == kSquare) {
-                const float d_row = __ldg(dA + row);
+                const float d_row = dA[row];
                 dB[row] = fmaf(d_row, fmaf(p.c, d_row, p.b), y[i] / kScaleA);
               }
               y[i] = 0.f;
