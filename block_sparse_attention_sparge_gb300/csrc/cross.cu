@@ -71,10 +71,13 @@ int check_cross(const sparge_cross* a, bool bwd) {
   CROSS_TRY(check_word(a->kv_len));
   CROSS_TRY(check_word(a->lse));
   CROSS_TRY(check_word(a->status));
-  Layout in[5] = {t.at(a->q, a->q_stride, false), t.at(a->k, a->k_stride, true),
+  Layout in[7] = {t.at(a->q, a->q_stride, false), t.at(a->k, a->k_stride, true),
                   t.at(a->v, a->v_stride, true)};
   Layout out[3];
   int n_in = 3, n_out = 0;
+  auto words = [](const void* p, int64_t n) { return layout_of(p, {1, 1, 1}, {0, 0, 0}, 4 * n, 1); };
+  if (a->kv_len != nullptr) in[n_in++] = words(a->kv_len, a->B);
+  const Layout lse = words(a->lse, static_cast<int64_t>(a->B) * a->H * a->N);
   if (bwd) {
     if (a->lse == nullptr) return SPARGE_ERR_INVALID_ARG;
     CROSS_TRY(check_heads_tensor(a->dout, a->dout_stride, t.nq));
@@ -83,11 +86,13 @@ int check_cross(const sparge_cross* a, bool bwd) {
     CROSS_TRY(check_heads_tensor(a->dv, a->dv_stride, t.nk));
     in[n_in++] = t.at(a->o, a->o_stride, false);
     in[n_in++] = t.at(a->dout, a->dout_stride, false);
+    in[n_in++] = lse;
     out[n_out++] = t.at(a->dq, a->dq_stride, false);
     out[n_out++] = t.at(a->dk, a->dk_stride, true);
     out[n_out++] = t.at(a->dv, a->dv_stride, true);
   } else {
     out[n_out++] = t.at(a->o, a->o_stride, false);
+    if (a->lse != nullptr) out[n_out++] = lse;
   }
   for (int i = 0; i < n_out; ++i) {
     if (meets_itself(out[i])) return SPARGE_ERR_INVALID_ARG;

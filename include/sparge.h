@@ -464,8 +464,8 @@ typedef struct sparge_cross {
 int sparge_cross_fwd_workspace_bytes(const sparge_cross* args, size_t* bytes);
 
 /*
- * One launch; a second joins partial results where there are some.  The output may
- * not share memory with an input (SPARGE_ERR_INVALID_ARG).
+ * One launch; a second joins partial results where there are some.  O and LSE may
+ * not share memory with an input or with one another (SPARGE_ERR_INVALID_ARG).
  */
 int sparge_cross_fwd(const sparge_cross* args, void* workspace, size_t ws_bytes,
                      sparge_stream_t stream);
@@ -479,6 +479,8 @@ int sparge_cross_bwd_workspace_bytes(const sparge_cross* args, size_t* bytes);
  * dK and dV summed over the query heads that read the key head and, with one
  * context for all, over the samples; 0 where no query reads a token.  Sums are
  * taken in a fixed order: repeated calls give the same bits.
+ * The gradients may not share memory with an input or with one another
+ * (SPARGE_ERR_INVALID_ARG).
  */
 int sparge_cross_bwd(const sparge_cross* args, void* workspace, size_t ws_bytes,
                      sparge_stream_t stream);
