@@ -26,7 +26,7 @@ int check_sizes(const sparge_cross* a) {
   if (a->B < 1 || a->H < 1 || a->Hk < 1 || a->N < 1 || a->M < 1 || a->d < 1)
     return SPARGE_ERR_INVALID_ARG;
   if ((a->Bk != 1 && a->Bk != a->B) || a->H % a->Hk != 0) return SPARGE_ERR_INVALID_ARG;
-  if (!isfinite(a->softmax_scale)) return SPARGE_ERR_INVALID_ARG;
+  if (!isfinite(a->softmax_scale * kLog2e)) return SPARGE_ERR_INVALID_ARG;  // (the exponents' factor)
   if (a->d != 64 && a->d != 128) return SPARGE_ERR_UNSUPPORTED;
   if (a->N > kMaxTokens || a->M > kMaxTokens) return SPARGE_ERR_UNSUPPORTED;
   const int64_t heads = static_cast<int64_t>(a->B) * a->H;

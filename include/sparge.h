@@ -438,7 +438,7 @@ typedef struct sparge_cross {
   int32_t B, Bk;           /* samples of Q; contexts: B, or 1 for all samples */
   int32_t H, Hk;           /* heads of Q; of K and V, a divisor of H */
   int32_t N, M, d;         /* query tokens, context tokens (each 1 .. 524288); 64 or 128 */
-  float softmax_scale;     /* 0 = 1/sqrt(d) */
+  float softmax_scale;     /* 0 = 1/sqrt(d); times log2(e) finite */
   const int32_t* kv_len;   /* [B] (device): valid context tokens of each sample, taken
                               into [0, M]; NULL: all.  K and V behind them are not
                               used, whatever they hold.  0: O = 0, LSE = -inf */
