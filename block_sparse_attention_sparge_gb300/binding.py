@@ -917,6 +917,8 @@ def sparge_cross_bwd(q, k, v, o, lse, dout, kv_len=None, softmax_scale: float = 
     """Gradients (dQ, dK, dV) of ``sparge_cross_fwd``: o and lse as it returned
     them, dout of o's shape.  dK and dV are summed over the heads of a group and,
     with one context, over the samples; they are 0 behind the samples' lengths.
+    With more than 64 context tokens they are less exact where the values' mean is
+    large beside their spread (``include/sparge.h`` has the figures).
     ``out``: three tensors to write them into, of any order of the first three
     dimensions (slices of one buffer, say)."""
     index = _cuda_index(q, k, v, o, lse, dout)

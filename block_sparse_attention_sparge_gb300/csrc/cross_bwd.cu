@@ -748,11 +748,17 @@ struct DqCfg {
 // the slot rings and barrier phases.
 // OWN: the context is one key tile, so a step has all keys of its rows and D is summed
 // here as sum_j P dP, in fp32, and written for the dK/dV kernel, which runs after this
-// one; O is not read.  With few keys O is as large as V, and what its rounding does to D
-// is what dQ and dK are off by beside the roundings of dS and of the result: in the 2-norm
-// 0.0038 with 2 keys, 0.0026 with 10, 0.0025 with 30, 0.0024 with 100; summed here 0.0024
+// one; O is not read.  Above kOwnKeys keys D is dO . O of O as the forward rounded it, and a
+// row's dS is off by P times what that rounding (and that of P before its product with V)
+// makes of D.  With values of mean 0 this shows where few keys are valid: dQ off by 0.0039 in
+// the 2-norm with 2 of them, 0.0026 with 10, 0.0024 with 100, which the roundings of dS and of
+// the result give alone.  dS depends on the differences of values, but O's rounding on their
+// size: where the rows of V share a mean of c times their spread, dQ is off by 0.0037, 0.0088
+// and 0.029 for c = 1, 3 and 10 (300 keys, d = 64; 0.0105 and 0.033 for c = 3 and 10 with 2
+// valid keys), dK by 0.0029, 0.0057 and 0.019.  Summed here both are off by 0.0024
 // throughout.  It costs a longer chain and the overlap of the two kernels (30000 queries
-// of 12 heads: 163 -> 185 us at d = 128, 121 -> 145 at d = 64), so up to kOwnKeys keys.
+// of 12 heads: 163 -> 185 us at d = 128, 121 -> 145 at d = 64), and with more key tiles a
+// pass over S and dP of its own, so up to kOwnKeys keys.
 constexpr int kOwnKeys = 64;
 template <int D, bool OWN>
 __global__ void __launch_bounds__(Roles<kDqWarps>::kThreads, 1)
