@@ -389,8 +389,11 @@ class BlockStack(torch.nn.Module):
 class Muon(torch.optim.Optimizer):
     """Optimiser of matrices by orthogonalised momenta: ``sparge_muon_step`` over all
     parameters of a group at once. Momenta are fp32 whatever the parameters' type.
-    ``half`` (the default) takes the products in fp16, which leaves the update off by
-    some 2^-9 of its size; None goes by the parameters' type."""
+    ``half`` (the default here, where the binding goes by the parameters' type, as None
+    does) takes the products in fp16: the update is off by some 2^-9 of its size, by more for
+    narrow matrices with few strong directions (``include/sparge.h`` has the figures), whose
+    groups may be given ``half=False``. A captured step keeps the learning rate and the other
+    numbers of its capture."""
 
     _HOW = ("lr", "momentum", "nesterov", "weight_decay", "rms", "steps", "half")
 

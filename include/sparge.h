@@ -498,6 +498,15 @@ int sparge_cross_bwd(const sparge_cross* args, void* workspace, size_t ws_bytes,
  * optimiser):
  *   X = U / (|U| + eps),   `steps` times  X <- a X + (b A + c A A) X,  A = X X^T
  * (X^T X for tall matrices), |U| the 2-norm of all values.
+ *
+ * Errors, of the result's 2-norm: some 2^-9 with fp16 products (`half`) and 2^-20 with
+ * pairs, where the singular values are spread evenly over two orders (2^-8 and 2^-18 with a
+ * short side of 2) or, with sides of 64 and more, over six (2^-18 with pairs).  What is rounded reaches the weak directions and
+ * grows with them, by up to |a| a step.  One or two strong directions with all others
+ * 10^3 and more below: 2^-4 with a short side up to 16, 2^-7 with 64, 2^-8 with 128, less
+ * beyond; 2^-15 with pairs and 2^-14 from 128 on.  The values that the products take (X
+ * times the root of its long side, 256 A and 256 B) have to stay below fp16's 65504, which
+ * they do where the polynomial keeps singular values in [0, 1] near there.
  */
 typedef struct sparge_matrix {
   int32_t rows, cols;      /* each 1 .. 65536 */
@@ -524,8 +533,8 @@ typedef struct sparge_ortho {
   int32_t nesterov;
   int32_t update;
   int32_t half;            /* nonzero: products of fp16 values (X itself is kept in 22
-                              bits, so X is off by some 2^-9 of its size); 0: of fp16
-                              pairs, three products for each (some 2^-20) */
+                              bits); 0: of fp16 pairs, three products for each.  How far
+                              off X is: see below */
   int32_t* status;         /* nullable; records SPARGE_ERR_TIMEOUT if a bounded wait
                               runs out */
 } sparge_ortho;
