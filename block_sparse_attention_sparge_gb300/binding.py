@@ -1053,11 +1053,13 @@ def sparge_orthogonalize(mats, out=None, steps: int = 5, coefficients=_NEWTON_SC
 def sparge_muon_step(weights, grads, momenta, lr: float, momentum: float = 0.95,
                      nesterov: bool = True, weight_decay: float = 0.0, rms: float | None = None,
                      steps: int = 5, coefficients=_NEWTON_SCHULZ, eps: float = 1e-7,
-                     half: bool | None = None, workspace=None, status=None, check_status=False):
+                     half: bool | None = None, workspace=None, status=None, check_status=False,
+                     inputs_first: bool = False):
     """One optimiser step on matrices, in place: m <- momentum * m + g; U = g +
     momentum * m (``nesterov``) or m; w <- (1 - lr * weight_decay) * w - lr * gain *
-    O, O the orthogonalised U (``sparge_orthogonalize``).  gain is sqrt(max(1, rows /
-    columns)), or with ``rms`` what gives the update about that root mean square:
+    O, O the orthogonalised U (``sparge_orthogonalize``).  gain is sqrt(max(1, outputs /
+    inputs)) of weights [outputs, inputs], or with ``inputs_first`` [inputs, outputs] (those
+    of ``x @ w``), or with ``rms`` what gives the update about that root mean square:
     rms * sqrt(max(rows, columns)).  Weights and gradients are bf16 or fp32, momenta
     fp32 (``momenta`` None: U = g).  ``half`` None: as the weights are bf16 or fp32."""
     weights, grads = list(weights), list(grads)
@@ -1071,6 +1073,8 @@ def sparge_muon_step(weights, grads, momenta, lr: float, momentum: float = 0.95,
         if w.dim() != 2 or 0 in w.shape:
             raise ValueError("expected matrices")
         r, c = w.shape
+        if inputs_first:
+            r, c = c, r
         gain = math.sqrt(max(1.0, r / c)) if rms is None else rms * math.sqrt(max(r, c))
         factors.append((1.0 - lr * weight_decay, lr * gain))
     _orthogonalize(grads, weights, momenta, factors, steps, coefficients, eps, momentum, nesterov,

@@ -393,18 +393,27 @@ class Muon(torch.optim.Optimizer):
     does) takes the products in fp16: the update is off by some 2^-9 of its size, by more for
     narrow matrices with few strong directions (``include/sparge.h`` has the figures), whose
     groups may be given ``half=False``. A captured step keeps the learning rate and the other
-    numbers of its capture."""
+    numbers of its capture.
 
-    _HOW = ("lr", "momentum", "nesterov", "weight_decay", "rms", "steps", "half")
+    The gain sqrt(max(1, outputs / inputs)) takes parameters as [outputs, inputs]; those of
+    this module's blocks are [inputs, outputs] (x @ w) and want ``inputs_first=True``."""
+
+    _HOW = ("lr", "momentum", "nesterov", "weight_decay", "rms", "steps", "half", "inputs_first")
 
     def __init__(self, params, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,
                  weight_decay: float = 0.0, rms: float | None = None, steps: int = 5,
-                 half: bool | None = True):
+                 half: bool | None = True, inputs_first: bool = False):
         super().__init__(params, dict(lr=lr, momentum=momentum, nesterov=nesterov,
-                                      weight_decay=weight_decay, rms=rms, steps=steps, half=half))
+                                      weight_decay=weight_decay, rms=rms, steps=steps, half=half,
+                                      inputs_first=inputs_first))
         for group in self.param_groups:
             if any(p.dim() != 2 for p in group["params"]):
                 raise ValueError("Muon takes matrices; give other parameters to another optimiser")
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        for group in self.param_groups:
+            group.setdefault("inputs_first", False)  # (a checkpoint from before there was one)
 
     @torch.no_grad()
     def step(self, closure=None):

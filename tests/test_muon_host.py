@@ -57,3 +57,16 @@ def test_named_parameters_and_keys_of_the_users_own(calls):
         pytest.skip("this torch takes no named parameters")
     opt.step()
     assert len(calls) == 2 and calls[-1]["weights"][0] is module.weight
+
+
+def test_which_side_of_a_weight_its_inputs_are(calls):
+    a, b = _weights()
+    opt = T.Muon([dict(params=[a]), dict(params=[b], inputs_first=True)])
+    opt.step()
+    assert [c["inputs_first"] for c in calls] == [False, True]
+    state = opt.state_dict()
+    for group in state["param_groups"]:
+        del group["inputs_first"]
+    opt.load_state_dict(state)
+    opt.step()
+    assert [c["inputs_first"] for c in calls[2:]] == [False, False]
