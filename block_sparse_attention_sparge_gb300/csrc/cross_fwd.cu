@@ -519,8 +519,9 @@ cudaError_t launch_fwd_impl(const CrossGeom& g, const sparge_cross& a, void* wor
 //   d = 64,  128 keys   6.5 /  8.9    9.1 /  9.8   10.8 / 10.8   19.0 / 16.6
 //            512       10.7 / 13.6   16.1 / 18.4   18.6 / 20.3   35.2 / 34.2
 //            1500      21.5 / 26.3   34.6 / 40.5   40.8 / 45.5   77.9 / 84.4
-// At d = 64 a step has half the products for the same exponents, which are what
-// bounds it, so the persistent form's other gains show late and not over long contexts.
+// At d = 64 a step has half the products for the same softmax, whose chain is what it takes
+// (0.78 us a step of two tiles by these times, 0.81 at d = 128), so the persistent form's
+// other gains show late and not over long contexts.
 bool wide_form(const CrossGeom& g) {
   const int64_t tiles = static_cast<int64_t>(g.B) * g.H * g.Mq;
   return g.d == 128 ? tiles > kFwdCtasPerSm * kSMs : tiles > 4 * kSMs && g.M <= 768;

@@ -457,7 +457,7 @@ def distillation_step(student, teacher, x: torch.Tensor, optimizer: torch.optim.
     teacher: loss = mean((student(x) - teacher(x))^2); backward through the
     library's sparse attention backward; gradients clipped to the global norm
     ``max_grad_norm`` where that is given; optimiser step. ``inputs`` (grid,
-    modulation) go to both. Returns the loss."""
+    modulation, context, kv_len) go to both. Returns the loss."""
     with torch.no_grad():
         target = teacher(x, **inputs)
     optimizer.zero_grad(set_to_none=True)
